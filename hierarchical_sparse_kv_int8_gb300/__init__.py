@@ -19,7 +19,8 @@ import numpy as np
 from . import _build
 
 __all__ = ["Arenas", "Config", "Context", "DhsError", "build", "load", "LOC_RING", "LOC_OPT",
-           "LOC_HOT", "LOC_STAGE", "BUF", "ROLE_FULL", "ROLE_FOLLOWER"]
+           "LOC_HOT", "LOC_STAGE", "BUF", "ROLE_FULL", "ROLE_FOLLOWER", "PageCache", "PAGE_BF16",
+           "PAGE_INT8", "PAGE_E4M3", "prompt_attend", "prompt_workspace", "check_errors"]
 
 LOC_RING, LOC_OPT, LOC_HOT, LOC_STAGE = 0, 1, 2, 3
 LOC_TIER_SHIFT = 28
@@ -124,6 +125,17 @@ _SIGS = {
                             ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p],
                            ctypes.c_int),
 }
+_P, _I32, _I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+_SIGS.update({
+    "dhs_page_write": ([_P, _P, _P, _P, _I64, _P, _P, _P, _I32, _I32, _P, _P], ctypes.c_int),
+    "dhs_page_read": ([_P, _P, _P, _P, _I64, _P, _P, _P, _I32, _I32, _P, _P], ctypes.c_int),
+    "dhs_page_attend": ([_P] * 5 + [_I32] * 4 + [ctypes.c_float, _P, _P, _P, _I64, _P, _P],
+                        ctypes.c_int),
+    "dhs_page_attend_workspace": ([_P, _I32, _I32, _I32], _I64),
+    "dhs_prompt_attend": ([_P] * 4 + [_I64] * 2 + [_P] * 2 + [_I32] * 4 +
+                          [ctypes.c_float, _P, _P, _P, _I64, _P, _P], ctypes.c_int),
+    "dhs_prompt_attend_workspace": ([_I64, _I64, _I32, _I32, _I32, _I32], _I64),
+})
 
 
 def build(force: bool = False) -> str:
@@ -518,3 +530,16 @@ class Context:
         self._check(self._lib.dhs_round_host(self.h, _dptr(q_idx), _host_ptr(kr), _dptr(q),
                                              _dptr(block_kv), _host_ptr(a), _dptr(out),
                                              _dptr(lse), _stream(stream)), "dhs_round_host")
+
+
+_DENSE = ("PageCache", "PAGE_BF16", "PAGE_INT8", "PAGE_E4M3", "prompt_attend", "prompt_workspace",
+          "check_errors")
+
+
+def __getattr__(name):
+    # the dense operators take torch tensors only, so torch is imported with them
+    if name in _DENSE:
+        from . import dense
+        globals().update((n, getattr(dense, n)) for n in _DENSE)
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))

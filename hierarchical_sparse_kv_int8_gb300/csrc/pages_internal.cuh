@@ -1,0 +1,71 @@
+// Shared by the paged-cache and prompt operators: the cache as kernels see it,
+// where a position lives in it, and which sequence a packed token belongs to.
+#pragma once
+#include "dhs_internal.cuh"
+#include "ptx_util.cuh"
+
+namespace dhs {
+
+constexpr int kPageMaxHeads = 1024;
+
+// The cache, by value.  A "row" is one (page, kv head, page row): head_dim
+// elements at row * head_dim and one scale at `row` of the scale arrays.
+struct PageView {
+  unsigned char *k, *v;
+  float *ks, *vs;
+  int64_t n_pages;
+  int rows, hkv, d, kind;
+};
+
+inline bool page_view(const dhs_pages *p, PageView *out) {
+  if (!p || !p->k || !p->v || ((uintptr_t)p->k & 15u) || ((uintptr_t)p->v & 15u)) return false;
+  if (p->kind < DHS_PAGE_BF16 || p->kind > DHS_PAGE_E4M3) return false;
+  if (p->kind != DHS_PAGE_BF16 && (!p->k_scale || !p->v_scale)) return false;
+  if (p->page_rows < 1 || p->kv_heads < 1 || p->kv_heads > kPageMaxHeads || p->n_pages < 1 ||
+      p->n_pages > INT32_MAX || (p->head_dim != 64 && p->head_dim != 128))
+    return false;
+  out->k = static_cast<unsigned char *>(p->k);
+  out->v = static_cast<unsigned char *>(p->v);
+  out->ks = p->k_scale;
+  out->vs = p->v_scale;
+  out->n_pages = p->n_pages;
+  out->rows = p->page_rows;
+  out->hkv = p->kv_heads;
+  out->d = p->head_dim;
+  out->kind = p->kind;
+  return true;
+}
+
+__device__ __forceinline__ void page_error(int32_t *err, int code, int site) {
+  if (err) record_error(err, code, site);
+}
+
+// Row (of kv head 0) that holds position `pos` of the sequence whose table
+// starts at `tab`, or -1 (recorded) where the table names no page; kv head h's
+// row is h * rows further on.  The caller has checked 0 <= pos < width * rows.
+__device__ __forceinline__ int64_t page_row(const PageView &p, const int32_t *tab, int pos,
+                                            int32_t *err, int site) {
+  const int pg = pos / p.rows, in = pos - pg * p.rows;
+  const int32_t page = tab[pg];
+  if (page < 0 || page >= p.n_pages) {
+    page_error(err, DC_LOC_RANGE, site);
+    return -1;
+  }
+  return (int64_t)page * p.hkv * p.rows + in;
+}
+
+// Sequence of packed token `tok`: the i with cu[i] <= tok < cu[i + 1], or -1
+// (padding).  For offsets that do not ascend some i or -1 comes back; the
+// caller checks what it derives from it.
+__device__ __forceinline__ int seq_of(const int32_t *cu, int n, int64_t tok) {
+  if (tok < cu[0]) return -1;
+  int lo = 0, hi = n;  // cu[lo] <= tok; hi is n or cu[hi] > tok
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (cu[mid] <= tok) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo < n ? lo : -1;
+}
+
+}  // namespace dhs

@@ -589,6 +589,130 @@ int dhs_policy_query(const dhs_policy *p, int32_t request, int64_t *required_pag
 /* total - reserve - required - optional pages; -1 for NULL. */
 int64_t dhs_policy_free_pages(const dhs_policy *p);
 
+/* ------------------------------------------------------------------------
+ * Dense attention over a paged cache (no counterpart in the paper's method;
+ * its models put such layers between the sparse ones, and a sparse layer's
+ * history starts as a prompt that is attended densely).  A serving loop calls
+ *   dhs_prompt_attend  the prompt's causal attention, packed sequences
+ *   dhs_page_write     the new tokens' keys and values into the pages
+ *   dhs_page_attend    the newest 1-8 tokens of every sequence over the pages
+ *   dhs_page_read      cached rows back, for the next chunk of a long prompt
+ * The calls need no context, allocate nothing, synchronise nothing and can be
+ * captured into a CUDA graph; lengths, offsets and page tables are read on the
+ * device, so a captured graph follows them.  Pointers and stream belong to the
+ * current device.  head_dim is 64 or 128; q, k, v and out are bf16.
+ *
+ * `err` of every call is a device int32[2] or NULL: a kernel that finds a bad
+ * page, length or offset leaves the rows in question out, never follows them,
+ * and records what it found unless err[0] already holds a record: err[0] = 1
+ * for a length or offset outside its range, 2 for a page outside [0, n_pages),
+ * 4 for a bounded wait that ran out; err[1] = the call, DHS_SITE_*. */
+enum { DHS_PAGE_BF16 = 0, DHS_PAGE_INT8 = 1, DHS_PAGE_E4M3 = 2 };
+enum { DHS_SITE_PAGE_WRITE = 1, DHS_SITE_PAGE_READ = 2, DHS_SITE_PAGE_ATTEND = 3,
+       DHS_SITE_PROMPT_ATTEND = 4 };
+
+/* The cache: caller-owned device memory, k and v 16-byte aligned.
+ *   k, v              [n_pages][kv_heads][page_rows][head_dim] elements of
+ *                     `kind`: bf16, int8, or e4m3 (finite codes)
+ *   k_scale, v_scale  fp32 [n_pages][kv_heads][page_rows], what a row's codes
+ *                     are multiplied by; NULL for DHS_PAGE_BF16
+ * A page table is device int32 [n_seqs][table_width]: position t of sequence
+ * i is row t % page_rows of page table[i][t / page_rows].  Entries past a
+ * sequence's length are not read. */
+typedef struct {
+  void *k, *v;
+  float *k_scale, *v_scale;
+  int64_t n_pages;
+  int32_t page_rows; /* >= 1 */
+  int32_t kv_heads;  /* 1 .. 1024 */
+  int32_t head_dim;  /* 64 or 128 */
+  int32_t kind;      /* DHS_PAGE_* */
+} dhs_pages;
+
+/* Quantise (or copy) the rows of new tokens into the cache.
+ *   k, v        device bf16, n_tokens packed tokens of kv_heads rows, 16-byte
+ *               aligned.  strides: host int64[4], in elements, of a token and
+ *               a head of k, then of v, multiples of 8; NULL means contiguous
+ *               [n_tokens][kv_heads][head_dim]
+ *   cu          device int32 [n_seqs + 1]: sequence i's tokens are cu[i] ..
+ *               cu[i + 1] - 1, ascending from cu[0] >= 0; tokens before
+ *               cu[0] or from cu[n_seqs] on are padding and not stored
+ *   seq_lens    device int32 [n_seqs]: length of sequence i with its new
+ *               tokens, which are its last ones: token cu[i] + u is position
+ *               seq_lens[i] - (cu[i + 1] - cu[i]) + u
+ * Rows no token names are left as they were.  A page that is written belongs to
+ * one sequence: two tokens of one call that name the same row race.
+ * 8-bit kinds: per token and head, scale = max|x| / Q in fp32 (Q = 127 for
+ * int8, 448 for e4m3), code = x / scale rounded to nearest, ties to even,
+ * exactly (as in real numbers).  A row whose max|x| is below 2^-100 is stored
+ * as zero codes with scale 0; a row with an infinity or a NaN as zero codes with
+ * scale NaN, so that all of it reads back as NaN. */
+int dhs_page_write(const dhs_pages *pages, const void *k, const void *v, const int64_t *strides,
+                   int64_t n_tokens, const int32_t *cu, const int32_t *seq_lens,
+                   const int32_t *page_table, int32_t table_width, int32_t n_seqs, int32_t *err,
+                   dhs_stream stream);
+
+/* The inverse: packed token cu[i] + u of k and v (addressed as in
+ * dhs_page_write) receives the cached row, code * scale rounded to bf16.
+ * Padding tokens are left as they were; rows that cannot be read (see err)
+ * become zeros. */
+int dhs_page_read(const dhs_pages *pages, void *k, void *v, const int64_t *strides,
+                  int64_t n_tokens, const int32_t *cu, const int32_t *seq_lens,
+                  const int32_t *page_table, int32_t table_width, int32_t n_seqs, int32_t *err,
+                  dhs_stream stream);
+
+/* Attention of the newest tokens of every sequence over its cached rows, for
+ * head h (kv head h / (q_heads / kv_heads)) and query j < n_i:
+ *   out = softmax(scale * K q) V over positions 0 .. seq_lens[i] - n_i + j.
+ *   q         device bf16 [n_seqs][q_len][q_heads][head_dim], 16-byte aligned
+ *   q_lens    device int32 [n_seqs] or NULL: n_i, queries of sequence i
+ *             (0 <= n_i <= q_len; NULL: all q_len); rows of q, out and lse from
+ *             n_i on are not touched
+ *   seq_lens  device int32 [n_seqs], the queries' own positions included
+ *             (write their rows first); 0 for an idle slot
+ *   scale     0 = 1/sqrt(head_dim); finite and not negative
+ *   out       device bf16 like q
+ *   lse       device fp32 [n_seqs][q_len][q_heads] natural-log sum-exp, or NULL
+ * A query that sees no position has out = 0 and lse = -inf.  q_len * (q_heads
+ * / kv_heads) <= 128, q_len <= 8.  The result does not depend on the other
+ * sequences' values.
+ *   workspace  device, 16-byte aligned, at least dhs_page_attend_workspace()
+ *              bytes; its first workspace_bytes are zero before the first call
+ *              that uses it, and each call leaves ready for the next.  Calls
+ *              that may overlap on the GPU (other streams, graphs replayed at the
+ *              same time) each take one of their own. */
+int dhs_page_attend(const dhs_pages *pages, const void *q, const int32_t *q_lens,
+                    const int32_t *seq_lens, const int32_t *page_table, int32_t table_width,
+                    int32_t n_seqs, int32_t q_len, int32_t q_heads, float scale, void *out,
+                    float *lse, void *workspace, int64_t workspace_bytes, int32_t *err,
+                    dhs_stream stream);
+/* Bytes the call needs on the current device, -1 for arguments it refuses. */
+int64_t dhs_page_attend_workspace(const dhs_pages *pages, int32_t n_seqs, int32_t q_len,
+                                  int32_t q_heads);
+
+/* Causal attention of packed sequences.  Sequence i has queries cu_q[i] ..
+ * cu_q[i + 1] - 1 and keys cu_k[i] .. cu_k[i + 1] - 1; its queries are its last
+ * positions, so query u of n_q sees keys 0 .. n_k - n_q + u (a whole prompt has
+ * n_q = n_k, a chunk of one n_q < n_k).
+ *   q, k, v    device bf16, n_q tokens of q_heads rows and n_k tokens of kv_heads
+ *              rows, 16-byte aligned.  strides: host int64[6], in elements, of a
+ *              token and a head of q, k, v, multiples of 8; NULL: contiguous
+ *   cu_q, cu_k device int32 [n_seqs + 1], ascending from >= 0, at most n_q and
+ *              n_k; query rows outside every sequence are not touched
+ *   out        device bf16 [n_q][q_heads][head_dim], 16-byte aligned
+ *   lse        device fp32 [n_q][q_heads] natural-log sum-exp, or NULL
+ * q_heads / kv_heads <= 128.  A query that sees no key has out = 0 and lse = -inf;
+ * what a key that a query does not see holds (infinities, NaN) never reaches it.
+ *   workspace  as in dhs_page_attend, of dhs_prompt_attend_workspace() bytes;
+ *              NULL with 0 bytes where that is 0 */
+int dhs_prompt_attend(const void *q, const void *k, const void *v, const int64_t *strides,
+                      int64_t n_q, int64_t n_k, const int32_t *cu_q, const int32_t *cu_k,
+                      int32_t n_seqs, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                      float scale, void *out, float *lse, void *workspace,
+                      int64_t workspace_bytes, int32_t *err, dhs_stream stream);
+int64_t dhs_prompt_attend_workspace(int64_t n_q, int64_t n_k, int32_t n_seqs, int32_t q_heads,
+                                    int32_t kv_heads, int32_t head_dim);
+
 #ifdef __cplusplus
 }
 #endif
