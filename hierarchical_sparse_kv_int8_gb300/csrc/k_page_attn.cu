@@ -1,87 +1,737 @@
 // Attention of the newest tokens of every sequence over its paged cache.
 //
-// One warp per (sequence, query, head): it walks the visible positions one by
-// one with the running maximum m and sum l of an online softmax in log2 units,
-//   m' = max(m, x),  o = o 2^(m - m') + 2^(x - m') v,  l likewise.
+// For sequence i and kv head h the R = q_len x G (query, head) pairs, G = q_heads
+// / kv_heads, are the rows of one small matrix; S = Q K^T and O = P V run on
+// mma.sync m16n8k16 tiles of 16 rows (R is 1 to 128, and what bounds the work is
+// the cache's bytes: 16 rows take 4 cycles of tensor core per cached token and
+// head against 22 cycles of HBM for its 512 bytes in bf16, 11 in 8 bits).
+// The softmax is online in log2 units: with the running maximum m of a row,
+//   l = sum 2^(x - m),  O = sum 2^(x - m) v,
+// and O and l are rescaled only when m grows by more than kRescale, so weights
+// stay below 2^kRescale.
+//
+// Work split: the positions of every (sequence, kv head) item are cut into
+// blocks, all items' blocks are laid end to end, and CTA b of n takes blocks
+// [b T / n, (b + 1) T / n) of the T.  Every CTA so reads the same number of rows
+// whatever the lengths are, and an item lies in as many CTAs as its length asks
+// for.  An item inside one CTA is finished there; otherwise each CTA leaves (m,
+// l, O) of its part in the workspace, and the last one to arrive (a counter per
+// item, which it sets back) joins the parts in CTA order, so bits repeat.  The
+// lengths are read on the device: every CTA adds up the block counts itself.
+//
+// Inside a CTA four warps form WT token groups of WM warps.  A group streams
+// tiles of TN positions through a ring of NS stages of shared memory with
+// 16-byte cp.async (a row's page is looked up two tiles before its copy is
+// waited for, so neither latency is exposed); its warps share the tile, each
+// with its own 16 MT rows of Q and O in registers.  Groups need no barrier but
+// their own until the item's end, where they are merged through shared memory.
+//
+// 8-bit rows: the codes are turned into bf16 in registers (exactly), a key's
+// scale multiplies its column of scores, a value's scale its column of weights.
+// The fragments are read so that no transposition is needed: a thread's 16
+// bytes of a key are 16 consecutive dims, which Q's fragments are loaded to
+// match, and of a value 16 (8) consecutive output columns of two positions,
+// paired by byte permutes.
+//
+// Positions that a query does not see have weight 0.  0 times an infinity or a
+// NaN is not 0, so among the last q_len - 1 positions, the only ones that some
+// queries of a sequence see and others do not, values that are not finite are
+// set to 0 in shared memory and added afterwards to the queries that see them.
 #include "pages_internal.cuh"
+#include "tc_util.cuh"
 
 #include <math_constants.h>
+
+#include <algorithm>
+#include <atomic>
 
 namespace dhs {
 namespace {
 
 constexpr int kPaWarps = 4;
+constexpr int kPaThreads = kPaWarps * 32;
+constexpr float kRescale = 8.f;
 
-template <int D, int KIND>
-__device__ __forceinline__ void row_values(const unsigned char *base, const float *sc, int64_t row,
-                                           int lane, float (&x)[D / 32]) {
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    const int64_t at = row * D + lane * (D / 32) + i;
-    if (KIND == DHS_PAGE_BF16)
-      x[i] = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(base)[at]);
-    else if (KIND == DHS_PAGE_INT8)
-      x[i] = (float)reinterpret_cast<const int8_t *>(base)[at] * sc[row];
-    else {
-      const uint32_t c = base[at];
-      const float m = __uint_as_float((c & 0x7Fu) << 20) * 1.329227995784916e36f;
-      x[i] = (c & 0x80u ? -m : m) * sc[row];
-    }
-  }
+// ------------------------------------------------------------ 8-bit to bf16 pairs
+// int8 x in the low byte of each half (other bytes ignored): 128 + (x & 127) and
+// 128 + (x & 128) are bf16 numbers of the same exponent pattern, and their
+// difference is x, exactly.
+__device__ __forceinline__ uint32_t int8_pair(uint32_t t) {
+  uint32_t a = (t & 0x007F007Fu) | 0x43004300u, b = (t & 0x00800080u) | 0x43004300u, r;
+  asm("sub.rn.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// e4m3 x in the high byte of each half: its seven lower bits at bf16's exponent
+// and mantissa are x times 2^-120 (subnormals too); the product is exact.
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t t) {
+  uint32_t a = ((t >> 4) & 0x07F007F0u) | (t & 0x80008000u), r;
+  asm("mul.rn.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(0x7B807B80u));
+  return r;
+}
+// bytes `i` of a and of b, as a pair of bf16
+template <int KIND>
+__device__ __forceinline__ uint32_t byte_pair(uint32_t a, uint32_t b, int i) {
+  if (KIND == DHS_PAGE_INT8) return int8_pair(__byte_perm(a, b, 0x0400u + 0x0101u * i));
+  return e4m3_pair(__byte_perm(a, b, 0x4000u + 0x1010u * i));
+}
+// bytes `i` and i + 1 of a
+template <int KIND>
+__device__ __forceinline__ uint32_t next_pair(uint32_t a, int i) {
+  if (KIND == DHS_PAGE_INT8) return int8_pair(__byte_perm(a, 0u, 0x0100u + 0x0101u * i));
+  return e4m3_pair(__byte_perm(a, 0u, 0x1000u + 0x1010u * i));
 }
 
-template <int D, int KIND>
-__global__ void __launch_bounds__(kPaWarps * 32)
-k_page_attn(const PageView pg, const __nv_bfloat16 *__restrict__ q,
-            const int32_t *__restrict__ q_lens, const int32_t *__restrict__ seq_lens,
-            const int32_t *__restrict__ table, int width, int n_seqs, int q_len, int hq,
-            float scale_log2, __nv_bfloat16 *__restrict__ out, float *__restrict__ lse,
-            int32_t *err) {
-  const int64_t item = (int64_t)blockIdx.x * kPaWarps + threadIdx.x / 32;
-  const int lane = threadIdx.x & 31;
-  if (item >= (int64_t)n_seqs * q_len * hq) return;
-  const int h = (int)(item % hq), j = (int)(item / hq % q_len), i = (int)(item / hq / q_len);
-  const int kvh = h / (hq / pg.hkv);
-  int nq = q_lens ? q_lens[i] : q_len, len = seq_lens[i];
-  if (nq < 0 || nq > q_len || len < 0 || len > (int64_t)width * pg.rows) {
-    page_error(err, DC_ROW_RANGE, DHS_SITE_PAGE_ATTEND);
-    nq = max(0, min(nq, q_len));
-    len = (int)max((int64_t)0, min((int64_t)len, (int64_t)width * pg.rows));
+__device__ __forceinline__ void cp_async_4_zfill(void *dst, const void *src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(bytes));
+}
+
+template <int D_, int KIND_, int WM_, int MT_>
+struct Cfg {
+  static constexpr int D = D_, KIND = KIND_, WM = WM_, MT = MT_;
+  static constexpr int WT = kPaWarps / WM;
+  static constexpr int W = KIND == DHS_PAGE_BF16 ? 2 : 1;
+  static constexpr int RB = D * W;                       // bytes of a row
+  static constexpr int CH = RB / 16;                     // 16-byte chunks of a row
+  // positions of a group's tile: 8 KB of keys and values per warp of the group
+  static constexpr int TN0 = 8192 * WM / (2 * RB);
+  static constexpr int TN = TN0 > 64 ? 64 : TN0;
+  static constexpr int SUB = MT == 1 && TN >= 32 ? 32 : 16;  // positions scored at a time
+  static constexpr int KV = TN * RB;
+  static constexpr int STAGE = 2 * KV + (W == 1 ? 2 * TN * 4 : 0);  // keys, values, scales
+  static constexpr int NS = 3;
+  static constexpr int GROUP = NS * STAGE;
+  static constexpr int ROWS = WM * MT * 16;              // rows of Q that fit
+  static constexpr int OPAD = D + 4;
+  static constexpr int MERGE = WT * ROWS * OPAD * 4;
+  static constexpr int DATA = WT * GROUP > MERGE ? WT * GROUP : MERGE;
+  static constexpr int SLOTS = NS + 1;
+  static constexpr int OFF_ROW = DATA;                           // int64 [WT][SLOTS][TN]
+  static constexpr int OFF_MASK = OFF_ROW + WT * SLOTS * TN * 8; // uint32 [WT][SLOTS][2]
+  static constexpr int OFF_ML = OFF_MASK + WT * SLOTS * 8;       // float [WT][ROWS][2]
+  static constexpr int SMEM = OFF_ML + WT * ROWS * 8;
+  static constexpr int OCC = SMEM * 2 <= 226 * 1024 ? 2 : 1;
+  static constexpr int BLOCK = WT * TN;                  // positions of a block
+};
+
+// Physical 16-byte chunk of a row's chunk `c` in shared memory, such that the
+// reads below meet no bank twice (ldmatrix takes the same chunk of 8 rows; 8-bit
+// keys 4 neighbouring chunks of rows 2i and 2i + 1; 8-bit values 2 chunks of
+// every other row).
+template <class C>
+__device__ __forceinline__ int kchunk(int row, int c) {
+  if (C::W == 2) return c ^ (row & 7);
+  return C::D == 128 ? c ^ ((row & 1) << 2) : c;
+}
+template <class C>
+__device__ __forceinline__ int vchunk(int row, int c) {
+  if (C::W == 2) return c ^ (row & 7);
+  return C::D == 128 ? c ^ (row & 6) : c ^ (row & 2);
+}
+
+struct AttnArgs {
+  const uint16_t *q;
+  const int32_t *q_lens, *seq_lens, *table;
+  uint16_t *out;
+  float *lse;
+  int32_t *tickets;  // [n_seqs][hkv], zero between calls
+  float *parts;      // [grid][2][R][D + 2]
+  int32_t *err;
+  int width, n_seqs, q_len, hq, G, R;
+  float scale_log2;
+};
+
+template <class C>
+__global__ void __launch_bounds__(kPaThreads, C::OCC)
+k_page_attn(const PageView pg, const AttnArgs a) {
+  constexpr int D = C::D, MT = C::MT, WM = C::WM, WT = C::WT, TN = C::TN, NS = C::NS, RB = C::RB;
+  constexpr int KIND = C::KIND, SUB = C::SUB;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ int64_t scan[kPaThreads + 1];
+  __shared__ int sh_seq, sh_flag, sh_last;
+  __shared__ int64_t sh_first;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int wm = warp % WM, wt = warp / WM;      // rows of this warp, token group
+  const int gl = wm * 32 + lane;                 // thread within the group
+  const int qd = lane & 3, ql = lane >> 2;
+  const int hkv = pg.hkv;
+  // (a tile past the last position still fits 32 bits)
+  const int64_t most = min((int64_t)a.width * pg.rows, (int64_t)INT32_MAX - 1024);
+
+  // queries and visible length of a sequence, and its blocks per kv head
+  auto shape = [&](int i, int &nq, int &len) {
+    nq = a.q_lens ? a.q_lens[i] : a.q_len;
+    len = a.seq_lens[i];
+    if (nq < 0 || nq > a.q_len || len < 0 || len > most) {
+      page_error(a.err, DC_ROW_RANGE, DHS_SITE_PAGE_ATTEND);
+      nq = max(0, min(nq, a.q_len));
+      len = (int)max((int64_t)0, min((int64_t)len, most));
+    }
+  };
+  auto blocks = [&](int i) -> int64_t {
+    int nq, len;
+    shape(i, nq, len);
+    return nq > 0 ? ((int64_t)len + C::BLOCK - 1) / C::BLOCK : 0;
+  };
+
+  // block counts of all sequences: thread t adds up its run of them
+  const int per = (a.n_seqs + kPaThreads - 1) / kPaThreads;
+  {
+    int64_t s = 0;
+    for (int i = tid * per; i < min(a.n_seqs, (tid + 1) * per); ++i) s += blocks(i);
+    int64_t x = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) scan[warp] = x;
+    __syncthreads();
+    int64_t before = 0;
+    for (int w = 0; w < warp; ++w) before += scan[w];
+    __syncthreads();
+    scan[tid + 1] = before + x;
+    if (tid == 0) scan[0] = 0;
+    __syncthreads();
   }
-  if (j >= nq) return;
-  const int seen = len - nq + j + 1;
-  float qv[D / 32], o[D / 32], m = -CUDART_INF_F, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e) {
-    qv[e] = __bfloat162float(q[item * D + lane * (D / 32) + e]);
-    o[e] = 0.f;
+  const int64_t total = scan[kPaThreads] * hkv;
+
+  // sequences without a block: their queries see nothing
+  for (int i = blockIdx.x; i < a.n_seqs; i += gridDim.x) {
+    int nq, len;
+    shape(i, nq, len);
+    if (nq == 0 || len > 0) continue;
+    const int64_t base = (int64_t)i * a.q_len * a.hq;
+    for (int e = tid; e < nq * a.hq * (D / 8); e += kPaThreads)
+      *reinterpret_cast<uint4 *>(a.out + (base * D + (int64_t)e * 8)) = make_uint4(0u, 0u, 0u, 0u);
+    if (a.lse)
+      for (int e = tid; e < nq * a.hq; e += kPaThreads) a.lse[base + e] = -CUDART_INF_F;
   }
-  for (int t = 0; t < seen; ++t) {
-    int64_t row = page_row(pg, table + (int64_t)i * width, t, err, DHS_SITE_PAGE_ATTEND);
-    if (row < 0) continue;
-    row += (int64_t)kvh * pg.rows;
-    float x[D / 32], s = 0.f;
-    row_values<D, KIND>(pg.k, pg.ks, row, lane, x);
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) s = fmaf(qv[e], x[e], s);
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-    s *= scale_log2;
-    const float mn = fmaxf(m, s), base = mn == -CUDART_INF_F ? 0.f : mn;
-    const float f = exp2f(m - base), p = exp2f(s - base);
-    m = mn;
-    l = l * f + p;
-    row_values<D, KIND>(pg.v, pg.vs, row, lane, x);
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) o[e] = o[e] * f + p * x[e];
+  const int n_cta = (int)min((int64_t)gridDim.x, total);
+  if ((int)blockIdx.x >= n_cta) return;
+  auto range = [&](int b) -> int64_t { return total * b / n_cta; };
+  const int64_t begin = range(blockIdx.x), end = range(blockIdx.x + 1);
+
+  // the sequence that holds block `begin`
+  if (tid == 0) {
+    const int64_t want = begin / hkv;  // in blocks of one head: only the sequence is looked for
+    int lo = 0, hi = kPaThreads - 1;   // last t with scan[t] <= want
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (scan[mid] <= want) lo = mid;
+      else hi = mid - 1;
+    }
+    int64_t at = scan[lo];
+    int i = lo * per;
+    for (; i < a.n_seqs - 1; ++i) {
+      const int64_t b = blocks(i);
+      if (at + b > want) break;
+      at += b;
+    }
+    sh_seq = i;
+    sh_first = at * hkv;
+    sh_flag = 0;
   }
-  // nothing seen: 0; only scores of -infinity: 0 / 0
-  const float inv = m == -CUDART_INF_F && l == 0.f && seen <= 0 ? 0.f : 1.f / l;
+  __syncthreads();
+  int seq = sh_seq;
+  int64_t seq_at = sh_first;  // global block where the sequence starts
+
+  unsigned char *ring = smem + wt * C::GROUP;
+  int64_t *rowbuf = reinterpret_cast<int64_t *>(smem + C::OFF_ROW) + wt * C::SLOTS * TN;
+  uint32_t *maskbuf = reinterpret_cast<uint32_t *>(smem + C::OFF_MASK) + wt * C::SLOTS * 2;
+  float *ml = reinterpret_cast<float *>(smem + C::OFF_ML);
+  float *osm = reinterpret_cast<float *>(smem);
+  auto group_sync = [&]() {
+    if (WM == 1) __syncwarp();
+    else if (WT == 1) __syncthreads();
+    else named_sync(1 + wt, WM * 32);
+  };
+
+  for (int64_t pos = begin; pos < end && seq < a.n_seqs;) {
+    int nq, len;
+    shape(seq, nq, len);
+    const int64_t nb = nq > 0 ? ((int64_t)len + C::BLOCK - 1) / C::BLOCK : 0;
+    if (pos >= seq_at + nb * hkv) {  // on to the next sequence (empty ones among them)
+      seq_at += nb * hkv;
+      ++seq;
+      continue;
+    }
+    const int kvh = (int)((pos - seq_at) / nb);
+    const int64_t item0 = seq_at + kvh * nb, item1 = item0 + nb;
+    const int64_t stop = min(end, item1);
+    const int b0 = (int)(pos - item0), nblk = (int)(stop - pos);
+    const int32_t *tab = a.table + (int64_t)seq * a.width;
+
+    // ---- row lookups and copies, tile by tile.  Tile t of the group is
+    // positions (b0 + t) * BLOCK + wt * TN ...
+    constexpr int LK = (TN + WM * 32 - 1) / (WM * 32);  // lookups of a thread
+    auto lookup = [&](int t, int64_t (&row)[LK]) {
 #pragma unroll
-  for (int e = 0; e < D / 32; ++e)
-    out[item * D + lane * (D / 32) + e] = __float2bfloat16(seen <= 0 ? 0.f : o[e] * inv);
-  if (lse && lane == 0)
-    lse[item] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994531f;
+      for (int u = 0; u < LK; ++u) {
+        const int x = gl + u * WM * 32;
+        const int64_t p = (int64_t)(b0 + t) * C::BLOCK + wt * TN + x;
+        row[u] = -1;
+        if (t < nblk && x < TN && p < len) {
+          row[u] = page_row(pg, tab, (int)p, a.err, DHS_SITE_PAGE_ATTEND);
+          if (row[u] >= 0) row[u] += (int64_t)kvh * pg.rows;
+        }
+      }
+    };
+    auto keep = [&](int t, const int64_t (&row)[LK]) {
+      int64_t *dst = rowbuf + (t % C::SLOTS) * TN;
+#pragma unroll
+      for (int u = 0; u < LK; ++u) {
+        const int x = gl + u * WM * 32;
+        const uint32_t ok = __ballot_sync(0xffffffffu, row[u] >= 0);
+        if (x < TN) dst[x] = row[u];
+        if (lane == 0 && (x >> 5) < 2) maskbuf[(t % C::SLOTS) * 2 + (x >> 5)] = ok;
+      }
+    };
+    auto copy = [&](int t) {
+      if (t < nblk) {
+        unsigned char *kst = ring + (t % NS) * C::STAGE, *vst = kst + C::KV;
+        const int64_t *src = rowbuf + (t % C::SLOTS) * TN;
+#pragma unroll
+        for (int u = 0; u < TN * C::CH / (WM * 32); ++u) {
+          const int x = (gl + u * WM * 32) / C::CH, c = (gl + u * WM * 32) % C::CH;
+          const int64_t row = src[x];
+          const int64_t off = (row < 0 ? 0 : row) * RB + c * 16;
+          cp_async_16_zfill(kst + x * RB + kchunk<C>(x, c) * 16, pg.k + off, row < 0 ? 0 : 16);
+          cp_async_16_zfill(vst + x * RB + vchunk<C>(x, c) * 16, pg.v + off, row < 0 ? 0 : 16);
+        }
+        if (C::W == 1) {
+          float *sc = reinterpret_cast<float *>(vst + C::KV);
+#pragma unroll
+          for (int u = 0; u < LK; ++u) {
+            const int x = gl + u * WM * 32;
+            if (x < TN) {
+              const int64_t row = src[x];
+              cp_async_4_zfill(sc + x, pg.ks + (row < 0 ? 0 : row), row < 0 ? 0 : 4);
+              cp_async_4_zfill(sc + TN + x, pg.vs + (row < 0 ? 0 : row), row < 0 ? 0 : 4);
+            }
+          }
+        }
+      }
+      cp_async_commit();
+    };
+
+    {
+      int64_t row[NS][LK];
+#pragma unroll
+      for (int t = 0; t < NS; ++t) lookup(t, row[t]);
+#pragma unroll
+      for (int t = 0; t < NS; ++t) keep(t, row[t]);
+    }
+    group_sync();
+#pragma unroll
+    for (int t = 0; t < NS - 1; ++t) copy(t);
+
+    // ---- Q fragments of this warp's rows: for bf16 k-step s holds dims 16 s ..;
+    // for 8 bits k index (s, 2 qd + e) is dim 64 j + 16 qd + 4 s + e and
+    // (s, 2 qd + 8 + e) is 2 further on, s = 0 .. 3 of the 64 dims of block j
+    uint32_t qf[MT][D / 16][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int m = (wm * MT + mt) * 16 + half * 8 + ql, j = m / a.G;
+        const bool on = m < a.R && j < nq;
+        const uint16_t *src =
+            a.q + (((int64_t)seq * a.q_len + j) * a.hq + kvh * a.G + (m - j * a.G)) * D;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+          const int lo = KIND == DHS_PAGE_BF16 ? 16 * s + 2 * qd
+                                               : 64 * (s >> 2) + 16 * qd + 4 * (s & 3);
+          const int hi = lo + (KIND == DHS_PAGE_BF16 ? 8 : 2);
+          qf[mt][s][half] = on ? *reinterpret_cast<const uint32_t *>(src + lo) : 0u;
+          qf[mt][s][2 + half] = on ? *reinterpret_cast<const uint32_t *>(src + hi) : 0u;
+        }
+      }
+    // visible positions of this thread's rows (idle rows: all, never written)
+    int seen[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int j = ((wm * MT + mt) * 16 + half * 8 + ql) / a.G;
+        seen[mt][half] = j < nq ? len - nq + j + 1 : len;
+      }
+    const int common = len - nq + 1;  // positions that every query sees
+
+    float o[MT][D / 8][4], mx[MT][2], l[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][i][e] = 0.f;
+      mx[mt][0] = mx[mt][1] = -CUDART_INF_F;
+      l[mt][0] = l[mt][1] = 0.f;
+    }
+
+    for (int t = 0; t < nblk; ++t) {
+      cp_async_wait_group<NS - 2>();
+      group_sync();
+      int64_t ahead[LK];
+      lookup(t + NS, ahead);
+      copy(t + NS - 1);
+      unsigned char *kst = ring + (t % NS) * C::STAGE, *vst = kst + C::KV;
+      const float *sc = reinterpret_cast<const float *>(vst + C::KV);
+      const int p0 = (int)((int64_t)(b0 + t) * C::BLOCK) + wt * TN;
+      const uint32_t ok0 = maskbuf[(t % C::SLOTS) * 2];
+      const uint32_t ok1 = TN > 32 ? maskbuf[(t % C::SLOTS) * 2 + 1] : 0xffffffffu;
+      const bool full = TN == 16 ? (ok0 & 0xffffu) == 0xffffu : (ok0 & ok1) == 0xffffffffu;
+      const bool masked = !full || p0 + TN > common;
+      if (KIND == DHS_PAGE_BF16 && nq > 1 && p0 + TN > common) {
+        // values that only some queries see: those that are not finite out
+        const int x0 = max(0, common - p0), x1 = min(TN, len - p0);
+        for (int e = x0 * C::CH + lane; e < x1 * C::CH; e += 32) {
+          const int x = e / C::CH, c = e % C::CH;
+          uint4 *at = reinterpret_cast<uint4 *>(vst + x * RB + vchunk<C>(x, c) * 16);
+          uint32_t w[4] = {at->x, at->y, at->z, at->w};
+          bool bad = false;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if ((w[i] & 0x7F80u) == 0x7F80u) { w[i] &= 0xFFFF0000u; bad = true; }
+            if ((w[i] & 0x7F800000u) == 0x7F800000u) { w[i] &= 0x0000FFFFu; bad = true; }
+          }
+          if (bad) {
+            *at = make_uint4(w[0], w[1], w[2], w[3]);
+            sh_flag = 1;
+          }
+        }
+        __syncwarp();
+      }
+#pragma unroll
+      for (int sub = 0; sub < TN / SUB; ++sub) {
+        const int s0 = sub * SUB;
+        // scores
+        float s[MT][SUB / 8][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int i = 0; i < SUB / 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[mt][i][e] = 0.f;
+        if (KIND == DHS_PAGE_BF16) {
+#pragma unroll
+          for (int i = 0; i < SUB / 16; ++i)
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+              // matrices: positions 0-7 and 8-15 of the 16, each with two chunks
+              const int x = s0 + i * 16 + (lane & 7) + ((lane >> 4) << 3);
+              const int c = ks * 2 + ((lane >> 3) & 1);
+              uint32_t b0r, b1r, b2r, b3r;
+              ldmatrix_x4(b0r, b1r, b2r, b3r, kst + x * RB + kchunk<C>(x, c) * 16);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                mma_bf16_16816(s[mt][2 * i], qf[mt][ks], b0r, b1r);
+                mma_bf16_16816(s[mt][2 * i + 1], qf[mt][ks], b2r, b3r);
+              }
+            }
+        } else {
+#pragma unroll
+          for (int i = 0; i < SUB / 8; ++i)
+#pragma unroll
+            for (int jb = 0; jb < D / 64; ++jb) {
+              const int x = s0 + i * 8 + ql;
+              const uint4 w = *reinterpret_cast<const uint4 *>(
+                  kst + x * RB + kchunk<C>(x, jb * 4 + qd) * 16);
+              const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks) {
+                const uint32_t b0r = next_pair<KIND>(ww[ks], 0), b1r = next_pair<KIND>(ww[ks], 2);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                  mma_bf16_16816(s[mt][i], qf[mt][jb * 4 + ks], b0r, b1r);
+              }
+            }
+        }
+        // to log2 units, masks, the rows' maxima
+        float top[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) top[mt][0] = top[mt][1] = -CUDART_INF_F;
+#pragma unroll
+        for (int i = 0; i < SUB / 8; ++i) {
+          float f0 = a.scale_log2, f1 = a.scale_log2;
+          if (C::W == 1) {
+            const float2 ks = *reinterpret_cast<const float2 *>(sc + s0 + i * 8 + 2 * qd);
+            f0 *= ks.x;
+            f1 *= ks.y;
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[mt][i][e] *= (e & 1) ? f1 : f0;
+            if (masked) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int x = s0 + i * 8 + 2 * qd + (e & 1);
+                const bool there = ((x < 32 ? ok0 >> x : ok1 >> (x - 32)) & 1u) != 0u;
+                if (!there || p0 + x >= seen[mt][e >> 1]) s[mt][i][e] = -CUDART_INF_F;
+              }
+            }
+            top[mt][0] = fmaxf(top[mt][0], fmaxf(s[mt][i][0], s[mt][i][1]));
+            top[mt][1] = fmaxf(top[mt][1], fmaxf(s[mt][i][2], s[mt][i][3]));
+          }
+        }
+        bool grow = false;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            top[mt][h] = fmaxf(top[mt][h], __shfl_xor_sync(0xffffffffu, top[mt][h], 1));
+            top[mt][h] = fmaxf(top[mt][h], __shfl_xor_sync(0xffffffffu, top[mt][h], 2));
+            grow |= top[mt][h] > mx[mt][h] + kRescale;
+          }
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float m_new = fmaxf(mx[mt][h], top[mt][h]);
+              // (a row that has seen nothing keeps its zeros)
+              const float f = mx[mt][h] == -CUDART_INF_F ? 0.f : ex2_approx(mx[mt][h] - m_new);
+              mx[mt][h] = m_new;
+              if (f != 1.f) {
+                l[mt][h] *= f;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                  o[mt][i][2 * h] *= f;
+                  o[mt][i][2 * h + 1] *= f;
+                }
+              }
+            }
+        }
+        // weights, rounded to bf16 for the product with V (a rounding of at most
+        // 2^-8 of each weight; the sum l takes them unrounded)
+        uint32_t pf[MT][SUB / 16][4];
+#pragma unroll
+        for (int i = 0; i < SUB / 8; ++i) {
+          float v0 = 1.f, v1 = 1.f;
+          if (C::W == 1) {
+            const float2 vs = *reinterpret_cast<const float2 *>(sc + TN + s0 + i * 8 + 2 * qd);
+            v0 = vs.x;
+            v1 = vs.y;
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            float p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float m = mx[mt][e >> 1];
+              const float x = s[mt][i][e];
+              // -inf - -inf: a row that has seen nothing yet, or a score of -inf
+              p[e] = x == -CUDART_INF_F ? 0.f : ex2_approx(x - m);
+              l[mt][e >> 1] += p[e];
+              // a scale that is not finite may stand at a masked place
+              if (C::W == 1) p[e] = p[e] == 0.f ? 0.f : p[e] * ((e & 1) ? v1 : v0);
+            }
+            pf[mt][i >> 1][(i & 1) * 2] = pack_bf16(p[0], p[1]);
+            pf[mt][i >> 1][(i & 1) * 2 + 1] = pack_bf16(p[2], p[3]);
+          }
+        }
+        // O += P V
+#pragma unroll
+        for (int i = 0; i < SUB / 16; ++i) {
+          if (KIND == DHS_PAGE_BF16) {
+#pragma unroll
+            for (int n = 0; n < D / 16; ++n) {
+              const int x = s0 + i * 16 + (lane & 15);
+              const int c = n * 2 + (lane >> 4);
+              uint32_t b0r, b1r, b2r, b3r;
+              ldmatrix_x4_trans(b0r, b1r, b2r, b3r, vst + x * RB + vchunk<C>(x, c) * 16);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                mma_bf16_16816(o[mt][2 * n], pf[mt][i], b0r, b1r);
+                mma_bf16_16816(o[mt][2 * n + 1], pf[mt][i], b2r, b3r);
+              }
+            }
+          } else {
+            // output column n of tile c is dim n * (D / 8) + c; this thread's
+            // n = ql of positions 2 qd, 2 qd + 1, 2 qd + 8, 2 qd + 9
+            constexpr int NW = D / 32;  // words of a thread per position
+            uint32_t w[4][NW];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int x = s0 + i * 16 + 2 * qd + (e & 1) + (e >> 1) * 8;
+              if (D == 128) {
+                const uint4 y = *reinterpret_cast<const uint4 *>(
+                    vst + x * RB + vchunk<C>(x, ql) * 16);
+                w[e][0] = y.x;
+                w[e][1] = y.y;
+                w[e][NW - 2] = y.z;
+                w[e][NW - 1] = y.w;
+              } else {
+                const uint2 y = *reinterpret_cast<const uint2 *>(
+                    vst + x * RB + vchunk<C>(x, ql >> 1) * 16 + (ql & 1) * 8);
+                w[e][0] = y.x;
+                w[e][1] = y.y;
+              }
+            }
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+              const uint32_t b0r = byte_pair<KIND>(w[0][c >> 2], w[1][c >> 2], c & 3);
+              const uint32_t b1r = byte_pair<KIND>(w[2][c >> 2], w[3][c >> 2], c & 3);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) mma_bf16_16816(o[mt][c], pf[mt][i], b0r, b1r);
+            }
+          }
+        }
+      }
+      keep(t + NS, ahead);
+    }
+
+    // ---- merge the groups: ml [WT][ROWS] and O scaled to the rows' maxima
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        l[mt][h] += __shfl_xor_sync(0xffffffffu, l[mt][h], 1);
+        l[mt][h] += __shfl_xor_sync(0xffffffffu, l[mt][h], 2);
+        const int m = (wm * MT + mt) * 16 + h * 8 + ql;
+        if (qd == 0)
+          *reinterpret_cast<float2 *>(ml + (wt * C::ROWS + m) * 2) = make_float2(mx[mt][h], l[mt][h]);
+      }
+    cp_async_wait_all();
+    __syncthreads();
+    const bool patch = sh_flag != 0;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int m = (wm * MT + mt) * 16 + h * 8 + ql;
+        float top = -CUDART_INF_F;
+#pragma unroll
+        for (int g = 0; g < WT; ++g) top = fmaxf(top, ml[(g * C::ROWS + m) * 2]);
+        const float f = mx[mt][h] == -CUDART_INF_F ? 0.f : ex2_approx(mx[mt][h] - top);
+        // (not zero times a NaN: a row of NaN scores keeps m = -inf and O = NaN)
+        const bool nan = l[mt][h] != l[mt][h];
+        float *dst = osm + (wt * C::ROWS + m) * C::OPAD;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const float x = nan ? CUDART_NAN_F : o[mt][i][2 * h] * f;
+          const float y = nan ? CUDART_NAN_F : o[mt][i][2 * h + 1] * f;
+          if (KIND == DHS_PAGE_BF16) {
+            *reinterpret_cast<float2 *>(dst + 8 * i + 2 * qd) = make_float2(x, y);
+          } else {
+            dst[2 * qd * (D / 8) + i] = x;
+            dst[(2 * qd + 1) * (D / 8) + i] = y;
+          }
+        }
+      }
+    __syncthreads();
+
+    const bool whole = pos == item0 && stop == item1;
+    const int64_t item = (int64_t)seq * hkv + kvh;
+    const int slot = pos > item0 ? 0 : 1;
+    float *part = a.parts + ((int64_t)blockIdx.x * 2 + slot) * a.R * (D + 2);
+    if (tid == 0) sh_flag = 0;  // every thread has read it
+    // one row's 4 dims at a time
+    for (int e = tid; e < a.R * (D / 4); e += kPaThreads) {
+      const int m = e / (D / 4), d4 = (e % (D / 4)) * 4, j = m / a.G;
+      if (j >= nq) continue;
+      float top = -CUDART_INF_F, den = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int g = 0; g < WT; ++g) top = fmaxf(top, ml[(g * C::ROWS + m) * 2]);
+#pragma unroll
+      for (int g = 0; g < WT; ++g) {
+        const float2 x = *reinterpret_cast<const float2 *>(ml + (g * C::ROWS + m) * 2);
+        const float f = x.x == -CUDART_INF_F ? (x.y != x.y ? 1.f : 0.f) : ex2_approx(x.x - top);
+        den += x.y * f;
+        const float4 y = *reinterpret_cast<const float4 *>(osm + (g * C::ROWS + m) * C::OPAD + d4);
+        acc.x += y.x;
+        acc.y += y.y;
+        acc.z += y.z;
+        acc.w += y.w;
+      }
+      const int sees = len - nq + j + 1;
+      if (KIND == DHS_PAGE_BF16 && patch) {
+        // the values taken out above, for the queries that see them
+        const int64_t lo = max((int64_t)max(0, common), (int64_t)b0 * C::BLOCK);
+        const int64_t hi = min((int64_t)sees, (int64_t)(b0 + nblk) * C::BLOCK);
+        for (int64_t p = lo; p < hi; ++p) {
+          int64_t row = page_row(pg, tab, (int)p, a.err, DHS_SITE_PAGE_ATTEND);
+          if (row < 0) continue;
+          row += (int64_t)kvh * pg.rows;
+          const uint2 w = *reinterpret_cast<const uint2 *>(pg.v + row * RB + d4 * 2);
+          const uint32_t b[4] = {w.x << 16, w.x & 0xFFFF0000u, w.y << 16, w.y & 0xFFFF0000u};
+          float *c4[4] = {&acc.x, &acc.y, &acc.z, &acc.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if ((b[i] & 0x7F800000u) == 0x7F800000u) *c4[i] += __uint_as_float(b[i]);
+        }
+      }
+      if (whole) {
+        const float inv = sees <= 0 ? 0.f : 1.f / den;  // only -inf scores: 0 / 0
+        const int64_t row = ((int64_t)seq * a.q_len + j) * a.hq + kvh * a.G + (m - j * a.G);
+        *reinterpret_cast<uint2 *>(a.out + row * D + d4) =
+            sees <= 0 ? make_uint2(0u, 0u)
+                      : make_uint2(pack_bf16(acc.x * inv, acc.y * inv),
+                                   pack_bf16(acc.z * inv, acc.w * inv));
+        if (a.lse && d4 == 0)
+          a.lse[row] = top == CUDART_INF_F ? top
+                       : den == 0.f        ? -CUDART_INF_F
+                                           : (top + log2f(den)) * 0.69314718055994531f;
+      } else {
+        *reinterpret_cast<float2 *>(part + m * (D + 2) + d4) = make_float2(acc.x, acc.y);
+        *reinterpret_cast<float2 *>(part + m * (D + 2) + d4 + 2) = make_float2(acc.z, acc.w);
+        if (d4 == 0) *reinterpret_cast<float2 *>(part + m * (D + 2) + D) = make_float2(top, den);
+      }
+    }
+    if (!whole) {
+      // the CTAs that share the item, and whether this is the last of them
+      auto owner = [&](int64_t blk) {  // largest b with range(b) <= blk
+        int b = (int)min((int64_t)n_cta - 1, ((blk + 1) * n_cta - 1) / total);
+        while (b > 0 && range(b) > blk) --b;
+        while (b + 1 < n_cta && range(b + 1) <= blk) ++b;
+        return b;
+      };
+      const int c0 = owner(item0), c1 = owner(item1 - 1);
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) sh_last = atomicAdd(a.tickets + item, 1) == c1 - c0;
+      __syncthreads();
+      if (sh_last) {
+        __threadfence();
+        if (tid == 0) a.tickets[item] = 0;
+        for (int e = tid; e < a.R * (D / 2); e += kPaThreads) {
+          const int m = e / (D / 2), d2 = (e % (D / 2)) * 2, j = m / a.G;
+          if (j >= nq) continue;
+          auto at = [&](int c) {
+            return a.parts + (((int64_t)c * 2 + (c == c0 ? 1 : 0)) * a.R + m) * (D + 2);
+          };
+          float top = -CUDART_INF_F, den = 0.f;
+          float2 acc = make_float2(0.f, 0.f);
+#pragma unroll 4
+          for (int c = c0; c <= c1; ++c)
+            top = fmaxf(top, __ldcg(at(c) + D));
+#pragma unroll 4
+          for (int c = c0; c <= c1; ++c) {
+            const float2 x = __ldcg(reinterpret_cast<const float2 *>(at(c) + D));
+            const float2 y = __ldcg(reinterpret_cast<const float2 *>(at(c) + d2));
+            const float f = x.x == -CUDART_INF_F ? (x.y != x.y ? 1.f : 0.f) : ex2_approx(x.x - top);
+            den += x.y * f;
+            // (a part whose weight is nothing adds nothing, unless it is not finite)
+            acc.x += y.x * f;
+            acc.y += y.y * f;
+          }
+          const int sees = len - nq + j + 1;
+          const float inv = 1.f / den;
+          const int64_t row = ((int64_t)seq * a.q_len + j) * a.hq + kvh * a.G + (m - j * a.G);
+          *reinterpret_cast<uint32_t *>(a.out + row * D + d2) =
+              sees <= 0 ? 0u : pack_bf16(acc.x * inv, acc.y * inv);
+          if (a.lse && d2 == 0)
+            a.lse[row] = top == CUDART_INF_F ? top
+                         : den == 0.f        ? -CUDART_INF_F
+                                             : (top + log2f(den)) * 0.69314718055994531f;
+        }
+      }
+    }
+    __syncthreads();  // shared memory goes to the next item
+    pos = stop;
+  }
 }
 
 bool attend_args(const dhs_pages *pages, int32_t n_seqs, int32_t q_len, int32_t q_heads,
@@ -90,13 +740,65 @@ bool attend_args(const dhs_pages *pages, int32_t n_seqs, int32_t q_len, int32_t 
          q_heads % pg->hkv == 0 && (int64_t)q_len * (q_heads / pg->hkv) <= 128;
 }
 
+int64_t ticket_bytes(int32_t n_seqs, int hkv) {
+  return ((int64_t)n_seqs * hkv * 4 + 255) / 256 * 256;
+}
+
+// Calls f with the configuration for R rows.  16 rows fit one warp and four
+// token groups stream at once; more rows take more warps of the same tile, and
+// above 64 two row tiles a warp.
+template <int D, int KIND, class F>
+auto pick_rows(int R, F f) {
+  if (R <= 16) return f(Cfg<D, KIND, 1, 1>());
+  if (R <= 32) return f(Cfg<D, KIND, 2, 1>());
+  if (R <= 64) return f(Cfg<D, KIND, 4, 1>());
+  return f(Cfg<D, KIND, 4, 2>());
+}
+template <class F>
+auto pick(const PageView &pg, int R, F f) {
+  switch ((pg.d == 128 ? 4 : 0) + pg.kind) {
+    case 0: return pick_rows<64, DHS_PAGE_BF16>(R, f);
+    case 1: return pick_rows<64, DHS_PAGE_INT8>(R, f);
+    case 2: return pick_rows<64, DHS_PAGE_E4M3>(R, f);
+    case 4: return pick_rows<128, DHS_PAGE_BF16>(R, f);
+    case 5: return pick_rows<128, DHS_PAGE_INT8>(R, f);
+    default: return pick_rows<128, DHS_PAGE_E4M3>(R, f);
+  }
+}
+
 }  // namespace
+
+int device_sms(int dev) {
+  static std::atomic<int> known[kMaxDevices];
+  if (dev < 0 || dev >= kMaxDevices) return 0;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
 }  // namespace dhs
 
 extern "C" int64_t dhs_page_attend_workspace(const dhs_pages *pages, int32_t n_seqs, int32_t q_len,
                                              int32_t q_heads) {
-  dhs::PageView pg;
-  return dhs::attend_args(pages, n_seqs, q_len, q_heads, &pg) ? 0 : -1;
+  using namespace dhs;
+  PageView pg;
+  if (!attend_args(pages, n_seqs, q_len, q_heads, &pg)) return -1;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return -1;
+  }
+  const int R = q_len * (q_heads / pg.hkv), sms = device_sms(dev);
+  if (sms < 1) return -1;
+  return pick(pg, R, [&](auto c) -> int64_t {
+    return ticket_bytes(n_seqs, pg.hkv) + (int64_t)sms * decltype(c)::OCC * 2 * R * (pg.d + 2) * 4;
+  });
 }
 
 extern "C" int dhs_page_attend(const dhs_pages *pages, const void *q, const int32_t *q_lens,
@@ -111,31 +813,47 @@ extern "C" int dhs_page_attend(const dhs_pages *pages, const void *q, const int3
       scale > 3e38f || workspace_bytes < 0)
     return DHS_ERR_INVALID;
   if (n_seqs == 0) return DHS_OK;
-  if (!q || !seq_lens || !page_table || !out || ((uintptr_t)q & 15u) || ((uintptr_t)out & 15u) ||
-      ((uintptr_t)workspace & 15u))
+  if (!q || !seq_lens || !page_table || !out || !workspace || ((uintptr_t)q & 15u) ||
+      ((uintptr_t)out & 15u) || ((uintptr_t)workspace & 15u))
     return DHS_ERR_INVALID;
-  (void)workspace;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const float sl2 = (scale == 0.f ? 1.f / sqrtf((float)pg.d) : scale) * 1.4426950408889634f;
-  const int64_t items = (int64_t)n_seqs * q_len * q_heads;
-  auto go = [&](auto kern) {
-    return launch_prio(kern, dim3((unsigned)((items + kPaWarps - 1) / kPaWarps)),
-                       dim3(kPaWarps * 32), 0, s, pg, static_cast<const __nv_bfloat16 *>(q),
-                       q_lens, seq_lens, page_table, table_width, n_seqs, q_len, q_heads, sl2,
-                       static_cast<__nv_bfloat16 *>(out), lse, err);
-  };
-  cudaError_t e;
-  switch ((pg.d == 128 ? 4 : 0) + pg.kind) {
-    case 0: e = go(k_page_attn<64, DHS_PAGE_BF16>); break;
-    case 1: e = go(k_page_attn<64, DHS_PAGE_INT8>); break;
-    case 2: e = go(k_page_attn<64, DHS_PAGE_E4M3>); break;
-    case 4: e = go(k_page_attn<128, DHS_PAGE_BF16>); break;
-    case 5: e = go(k_page_attn<128, DHS_PAGE_INT8>); break;
-    default: e = go(k_page_attn<128, DHS_PAGE_E4M3>); break;
-  }
-  if (e != cudaSuccess) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();
     return DHS_ERR_CUDA;
   }
-  return DHS_OK;
+  const int sms = device_sms(dev);
+  if (sms < 1) return DHS_ERR_CUDA;
+  AttnArgs a;
+  a.q = static_cast<const uint16_t *>(q);
+  a.q_lens = q_lens;
+  a.seq_lens = seq_lens;
+  a.table = page_table;
+  a.out = static_cast<uint16_t *>(out);
+  a.lse = lse;
+  a.tickets = static_cast<int32_t *>(workspace);
+  a.parts = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) +
+                                      ticket_bytes(n_seqs, pg.hkv));
+  a.err = err;
+  a.width = table_width;
+  a.n_seqs = n_seqs;
+  a.q_len = q_len;
+  a.hq = q_heads;
+  a.G = q_heads / pg.hkv;
+  a.R = q_len * a.G;
+  a.scale_log2 = (scale == 0.f ? 1.f / sqrtf((float)pg.d) : scale) * 1.4426950408889634f;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return pick(pg, a.R, [&](auto c) -> int {
+    using C = decltype(c);
+    const int grid = sms * C::OCC;
+    if (workspace_bytes < ticket_bytes(n_seqs, pg.hkv) + (int64_t)grid * 2 * a.R * (C::D + 2) * 4)
+      return DHS_ERR_INVALID;
+    static DeviceSmem granted;
+    if (granted.ensure(k_page_attn<C>, C::SMEM, dev) != cudaSuccess ||
+        launch_prio(k_page_attn<C>, dim3(grid), dim3(kPaThreads), C::SMEM, s, pg, a) !=
+            cudaSuccess) {
+      cudaGetLastError();
+      return DHS_ERR_CUDA;
+    }
+    return DHS_OK;
+  });
 }

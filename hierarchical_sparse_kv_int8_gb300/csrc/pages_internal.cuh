@@ -4,9 +4,30 @@
 #include "dhs_internal.cuh"
 #include "ptx_util.cuh"
 
+#include <atomic>
+
 namespace dhs {
 
 constexpr int kPageMaxHeads = 1024;
+constexpr int kMaxDevices = 64;
+
+// Streaming multiprocessors of a device (asked once), 0 on failure.
+int device_sms(int dev);
+
+// A kernel's dynamic shared-memory limit, raised once on each device.
+struct DeviceSmem {
+  std::atomic<int> done[kMaxDevices] = {};
+  template <typename F>
+  cudaError_t ensure(F *func, int bytes, int dev) {
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    cudaError_t e = same_carveout(func);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done[dev].store(1, std::memory_order_release);
+    return e;
+  }
+};
 
 // The cache, by value.  A "row" is one (page, kv head, page row): head_dim
 // elements at row * head_dim and one scale at `row` of the scale arrays.

@@ -69,11 +69,11 @@ def test_attend_refusals(dhs):
     for b in BAD_PAGES:
         assert _attend(lib, _pages(**b)) == INVALID, b
     for b in [dict(q=None), dict(lens=None), dict(table=None), dict(out=None), dict(q=A + 8), dict(out=A + 2),
-              dict(ws=A + 4), dict(width=-1), dict(seqs=-1), dict(q_len=0), dict(q_len=9), dict(hq=0),
+              dict(ws=A + 4), dict(ws=None), dict(width=-1), dict(seqs=-1), dict(q_len=0), dict(q_len=9), dict(hq=0),
               dict(hq=7), dict(hq=512), dict(q_len=8, hq=34), dict(scale=-1.0), dict(scale=float("nan")),
               dict(scale=float("inf")), dict(nbytes=-1)]:
         assert _attend(lib, **b) == INVALID, b
-    assert _attend(lib, seqs=0, q=None) == 0
+    assert _attend(lib, seqs=0, q=None, ws=None) == 0
 
 
 def test_attend_workspace_arguments(dhs):
