@@ -15,9 +15,9 @@
 // [b T / n, (b + 1) T / n) of the T.  Every CTA so reads the same number of rows
 // whatever the lengths are, and an item lies in as many CTAs as its length asks
 // for.  An item inside one CTA is finished there; otherwise each CTA leaves (m,
-// l, O) of its part in the workspace, and the last one to arrive (a counter per
-// item, which it sets back) joins the parts in CTA order, so bits repeat.  The
-// lengths are read on the device: every CTA adds up the block counts itself.
+// l, O) of its part in the workspace and a second launch joins the parts in CTA
+// order, so bits repeat.  The lengths are read on the device: every CTA adds up
+// the block counts itself.
 //
 // Inside a CTA four warps form WT token groups of WM warps.  A group streams
 // tiles of TN positions through a ring of NS stages of shared memory with
@@ -26,8 +26,15 @@
 // with its own 16 MT rows of Q and O in registers.  Groups need no barrier but
 // their own until the item's end, where they are merged through shared memory.
 //
-// 8-bit rows: the codes are turned into bf16 in registers (exactly), a key's
-// scale multiplies its column of scores, a value's scale its column of weights.
+// 8-bit rows: the codes become f16 in registers, exactly.  A row of Q is scaled
+// by a power of two to fit f16 (exact down to 2^-32 of its largest element, and
+// off by 2^-40 of it below), a key's scale multiplies its column of scores.  A
+// value's scale goes into the weight's exponent: with y = x + log2(scale), the
+// weights of the product are 2^(y - m' + 7), m' the running maximum of y, so that
+// they fit f16 whatever the scales are, and l is summed from 2^(x - m) beside
+// them; O is brought from m' to m once, at the end.  (Codes to bf16 instead, with
+// scaled bf16 weights, took 4 instructions a pair on the half-rate integer pipe
+// instead of 1.5 to 2, and bound the kernel.)
 // The fragments are read so that no transposition is needed: a thread's 16
 // bytes of a key are 16 consecutive dims, which Q's fragments are loaded to
 // match, and of a value 16 (8) consecutive output columns of two positions,
@@ -51,34 +58,49 @@ namespace {
 constexpr int kPaWarps = 4;
 constexpr int kPaThreads = kPaWarps * 32;
 constexpr float kRescale = 8.f;
+constexpr float kF16Up = 7.f;  // f16 weights are 2^kF16Up times larger: up to 2^15
 
-// ------------------------------------------------------------ 8-bit to bf16 pairs
-// int8 x in the low byte of each half (other bytes ignored): 128 + (x & 127) and
-// 128 + (x & 128) are bf16 numbers of the same exponent pattern, and their
-// difference is x, exactly.
-__device__ __forceinline__ uint32_t int8_pair(uint32_t t) {
-  uint32_t a = (t & 0x007F007Fu) | 0x43004300u, b = (t & 0x00800080u) | 0x43004300u, r;
-  asm("sub.rn.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+// ------------------------------------------------------------ 8-bit to f16 pairs
+// int8: with its sign bit flipped x is u = x + 128, and 0x6400 | u is 1024 + u in
+// f16; 1152 less is x, exactly.  e4m3: the conversion instruction, exact too.
+__device__ __forceinline__ uint32_t sub_1152(uint32_t t) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(t), "r"(0x64806480u));
   return r;
 }
-// e4m3 x in the high byte of each half: its seven lower bits at bf16's exponent
-// and mantissa are x times 2^-120 (subnormals too); the product is exact.
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t t) {
-  uint32_t a = ((t >> 4) & 0x07F007F0u) | (t & 0x80008000u), r;
-  asm("mul.rn.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(0x7B807B80u));
+__device__ __forceinline__ uint32_t e4m3_f16(uint32_t two) {
+  uint32_t r;
+  asm("{\n .reg .b16 h;\n cvt.u16.u32 h, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}\n" : "=r"(r) : "r"(two));
   return r;
 }
-// bytes `i` of a and of b, as a pair of bf16
+// the four codes of w as two pairs
 template <int KIND>
-__device__ __forceinline__ uint32_t byte_pair(uint32_t a, uint32_t b, int i) {
-  if (KIND == DHS_PAGE_INT8) return int8_pair(__byte_perm(a, b, 0x0400u + 0x0101u * i));
-  return e4m3_pair(__byte_perm(a, b, 0x4000u + 0x1010u * i));
+__device__ __forceinline__ void f16_pairs(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  if (KIND == DHS_PAGE_INT8) {
+    w ^= 0x80808080u;
+    lo = sub_1152(__byte_perm(w, 0x64646464u, 0x4140));
+    hi = sub_1152(__byte_perm(w, 0x64646464u, 0x4342));
+  } else {
+    lo = e4m3_f16(w & 0xFFFFu);
+    hi = e4m3_f16(w >> 16);
+  }
 }
-// bytes `i` and i + 1 of a
+
+__device__ __forceinline__ float lg2_approx(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 template <int KIND>
-__device__ __forceinline__ uint32_t next_pair(uint32_t a, int i) {
-  if (KIND == DHS_PAGE_INT8) return int8_pair(__byte_perm(a, 0u, 0x0100u + 0x0101u * i));
-  return e4m3_pair(__byte_perm(a, 0u, 0x1000u + 0x1010u * i));
+__device__ __forceinline__ void mma_kind(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  if (KIND == DHS_PAGE_BF16) mma_bf16_16816(d, a, b0, b1);
+  else mma_f16_16816(d, a[0], a[1], a[2], a[3], b0, b1);
 }
 
 __device__ __forceinline__ void cp_async_4_zfill(void *dst, const void *src, int bytes) {
@@ -134,8 +156,8 @@ struct AttnArgs {
   const int32_t *q_lens, *seq_lens, *table;
   uint16_t *out;
   float *lse;
-  int32_t *tickets;  // [n_seqs][hkv], zero between calls
-  float *parts;      // [grid][2][R][D + 2]
+  int2 *plan;        // [n_seqs][hkv]: first and last CTA of an item in parts, or (-1, -1)
+  float *parts;      // [grid][2][R][D + 2]: O, m, l
   int32_t *err;
   int width, n_seqs, q_len, hq, G, R;
   float scale_log2;
@@ -148,7 +170,7 @@ k_page_attn(const PageView pg, const AttnArgs a) {
   constexpr int KIND = C::KIND, SUB = C::SUB;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int64_t scan[kPaThreads + 1];
-  __shared__ int sh_seq, sh_flag, sh_last;
+  __shared__ int sh_seq, sh_flag, sh_items;
   __shared__ int64_t sh_first;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int wm = warp % WM, wt = warp / WM;      // rows of this warp, token group
@@ -177,9 +199,17 @@ k_page_attn(const PageView pg, const AttnArgs a) {
   // block counts of all sequences: thread t adds up its run of them
   const int per = (a.n_seqs + kPaThreads - 1) / kPaThreads;
   {
-    int64_t s = 0;
-    for (int i = tid * per; i < min(a.n_seqs, (tid + 1) * per); ++i) s += blocks(i);
-    int64_t x = s;
+    int64_t x = 0;
+    int some = 0;
+    for (int i = tid * per; i < min(a.n_seqs, (tid + 1) * per); ++i) {
+      const int64_t b = blocks(i);
+      x += b;
+      some += b > 0 ? 1 : 0;
+    }
+    if (tid == 0) sh_items = 0;
+    __syncthreads();
+    some = __reduce_add_sync(0xffffffffu, some);
+    if (lane == 0) atomicAdd(&sh_items, some);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
@@ -200,14 +230,25 @@ k_page_attn(const PageView pg, const AttnArgs a) {
   for (int i = blockIdx.x; i < a.n_seqs; i += gridDim.x) {
     int nq, len;
     shape(i, nq, len);
-    if (nq == 0 || len > 0) continue;
+    if (nq > 0 && len > 0) continue;
+    for (int h = tid; h < hkv; h += kPaThreads) a.plan[(int64_t)i * hkv + h] = make_int2(-1, -1);
+    if (nq == 0) continue;
     const int64_t base = (int64_t)i * a.q_len * a.hq;
     for (int e = tid; e < nq * a.hq * (D / 8); e += kPaThreads)
       *reinterpret_cast<uint4 *>(a.out + (base * D + (int64_t)e * 8)) = make_uint4(0u, 0u, 0u, 0u);
     if (a.lse)
       for (int e = tid; e < nq * a.hq; e += kPaThreads) a.lse[base + e] = -CUDART_INF_F;
   }
-  const int n_cta = (int)min((int64_t)gridDim.x, total);
+  // CTAs that take part.  An item of b blocks in P parts costs b / P blocks of
+  // streaming and P parts of (R, D) in the join, least at P = sqrt(b x block
+  // bytes / part bytes); more CTAs than that lengthen a short call.
+  const int64_t items = (int64_t)sh_items * hkv;
+  const float parts =
+      items > 0 ? ceilf(sqrtf((float)total / (float)items * ((float)C::BLOCK * 2 * RB) /
+                              (float)(a.R * D * 4)))
+                : 0.f;
+  const int n_cta = (int)min(min((int64_t)gridDim.x, total), (int64_t)((float)items * parts));
+  pdl_trigger();  // the join may be placed; it waits for this grid's end
   if ((int)blockIdx.x >= n_cta) return;
   auto range = [&](int b) -> int64_t { return total * b / n_cta; };
   const int64_t begin = range(blockIdx.x), end = range(blockIdx.x + 1);
@@ -283,7 +324,7 @@ k_page_attn(const PageView pg, const AttnArgs a) {
       for (int u = 0; u < LK; ++u) {
         const int x = gl + u * WM * 32;
         const uint32_t ok = __ballot_sync(0xffffffffu, row[u] >= 0);
-        if (x < TN) dst[x] = row[u];
+        if (x < TN) dst[x] = row[u];  // (-1: nothing there)
         if (lane == 0 && (x >> 5) < 2) maskbuf[(t % C::SLOTS) * 2 + (x >> 5)] = ok;
       }
     };
@@ -291,13 +332,19 @@ k_page_attn(const PageView pg, const AttnArgs a) {
       if (t < nblk) {
         unsigned char *kst = ring + (t % NS) * C::STAGE, *vst = kst + C::KV;
         const int64_t *src = rowbuf + (t % C::SLOTS) * TN;
+        // a thread copies one chunk column of every STEP-th row; STEP is a multiple
+        // of 8 or the swizzle's row bits are spelled out by the unrolled index
+        constexpr int STEP = WM * 32 / C::CH;
+        const int xr = gl / C::CH, c = gl % C::CH;
+        const unsigned char *gk = pg.k + c * 16, *gv = pg.v + c * 16;
 #pragma unroll
-        for (int u = 0; u < TN * C::CH / (WM * 32); ++u) {
-          const int x = (gl + u * WM * 32) / C::CH, c = (gl + u * WM * 32) % C::CH;
+        for (int u = 0; u < TN / STEP; ++u) {
+          const int x = xr + u * STEP;
           const int64_t row = src[x];
-          const int64_t off = (row < 0 ? 0 : row) * RB + c * 16;
-          cp_async_16_zfill(kst + x * RB + kchunk<C>(x, c) * 16, pg.k + off, row < 0 ? 0 : 16);
-          cp_async_16_zfill(vst + x * RB + vchunk<C>(x, c) * 16, pg.v + off, row < 0 ? 0 : 16);
+          const int n = row < 0 ? 0 : 16;
+          const int64_t off = row < 0 ? 0 : row * RB;
+          cp_async_16_zfill(kst + x * RB + kchunk<C>(x, c) * 16, gk + off, n);
+          cp_async_16_zfill(vst + x * RB + vchunk<C>(x, c) * 16, gv + off, n);
         }
         if (C::W == 1) {
           float *sc = reinterpret_cast<float *>(vst + C::KV);
@@ -330,6 +377,7 @@ k_page_attn(const PageView pg, const AttnArgs a) {
     // for 8 bits k index (s, 2 qd + e) is dim 64 j + 16 qd + 4 s + e and
     // (s, 2 qd + 8 + e) is 2 further on, s = 0 .. 3 of the 64 dims of block j
     uint32_t qf[MT][D / 16][4];
+    float fr[MT][2];  // a score's factor by row: softmax scale in log2 units, f16 scaling
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -338,13 +386,35 @@ k_page_attn(const PageView pg, const AttnArgs a) {
         const bool on = m < a.R && j < nq;
         const uint16_t *src =
             a.q + (((int64_t)seq * a.q_len + j) * a.hq + kvh * a.G + (m - j * a.G)) * D;
+        uint32_t top = 0u;
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
           const int lo = KIND == DHS_PAGE_BF16 ? 16 * s + 2 * qd
                                                : 64 * (s >> 2) + 16 * qd + 4 * (s & 3);
           const int hi = lo + (KIND == DHS_PAGE_BF16 ? 8 : 2);
-          qf[mt][s][half] = on ? *reinterpret_cast<const uint32_t *>(src + lo) : 0u;
-          qf[mt][s][2 + half] = on ? *reinterpret_cast<const uint32_t *>(src + hi) : 0u;
+          const uint32_t x = on ? *reinterpret_cast<const uint32_t *>(src + lo) : 0u;
+          const uint32_t y = on ? *reinterpret_cast<const uint32_t *>(src + hi) : 0u;
+          qf[mt][s][half] = x;
+          qf[mt][s][2 + half] = y;
+          top = max(top, max(max(x & 0x7FFFu, (x >> 16) & 0x7FFFu),
+                             max(y & 0x7FFFu, (y >> 16) & 0x7FFFu)));
+        }
+        fr[mt][half] = a.scale_log2;
+        if (C::W == 1) {
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          // the largest element goes to [2^14, 2^15) (infinities and NaN stay)
+          const int e = top >= 0x7F80u ? 0 : max((int)(top >> 7) - 127 - 14, -110);
+          const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+          fr[mt][half] *= __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t x = qf[mt][s][2 * k + half];
+              qf[mt][s][2 * k + half] = pack_f16(__uint_as_float(x << 16) * down,
+                                                 __uint_as_float(x & 0xFFFF0000u) * down);
+            }
         }
       }
     // visible positions of this thread's rows (idle rows: all, never written)
@@ -358,14 +428,15 @@ k_page_attn(const PageView pg, const AttnArgs a) {
       }
     const int common = len - nq + 1;  // positions that every query sees
 
-    float o[MT][D / 8][4], mx[MT][2], l[MT][2];
+    // mx: running maximum of x, my: of y (8-bit kinds; else the same as mx)
+    float o[MT][D / 8][4], mx[MT][2], my[MT][2], l[MT][2];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
       for (int i = 0; i < D / 8; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[mt][i][e] = 0.f;
-      mx[mt][0] = mx[mt][1] = -CUDART_INF_F;
+      mx[mt][0] = mx[mt][1] = my[mt][0] = my[mt][1] = -CUDART_INF_F;
       l[mt][0] = l[mt][1] = 0.f;
     }
 
@@ -440,39 +511,59 @@ k_page_attn(const PageView pg, const AttnArgs a) {
               const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks) {
-                const uint32_t b0r = next_pair<KIND>(ww[ks], 0), b1r = next_pair<KIND>(ww[ks], 2);
+                uint32_t b0r, b1r;
+                f16_pairs<KIND>(ww[ks], b0r, b1r);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
-                  mma_bf16_16816(s[mt][i], qf[mt][jb * 4 + ks], b0r, b1r);
+                  mma_kind<KIND>(s[mt][i], qf[mt][jb * 4 + ks], b0r, b1r);
               }
             }
         }
-        // to log2 units, masks, the rows' maxima
-        float top[MT][2];
+        // to log2 units, masks, the rows' maxima of x and (8-bit) of y
+        float y[MT][C::W == 1 ? SUB / 8 : 1][4];
+        float top[MT][2], tpy[MT][2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) top[mt][0] = top[mt][1] = -CUDART_INF_F;
+        for (int mt = 0; mt < MT; ++mt)
+          top[mt][0] = top[mt][1] = tpy[mt][0] = tpy[mt][1] = -CUDART_INF_F;
 #pragma unroll
         for (int i = 0; i < SUB / 8; ++i) {
-          float f0 = a.scale_log2, f1 = a.scale_log2;
+          float k0 = 1.f, k1 = 1.f, v0 = 0.f, v1 = 0.f;
           if (C::W == 1) {
             const float2 ks = *reinterpret_cast<const float2 *>(sc + s0 + i * 8 + 2 * qd);
-            f0 *= ks.x;
-            f1 *= ks.y;
+            const float2 vs = *reinterpret_cast<const float2 *>(sc + TN + s0 + i * 8 + 2 * qd);
+            k0 = ks.x;
+            k1 = ks.y;
+            v0 = lg2_approx(vs.x);
+            v1 = lg2_approx(vs.y);
           }
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[mt][i][e] *= (e & 1) ? f1 : f0;
+            for (int e = 0; e < 4; ++e) {
+              float x = s[mt][i][e];
+              if (C::W == 1) {
+                x *= (e & 1) ? k1 : k0;
+                y[mt][i][e] = fmaf(x, fr[mt][e >> 1], (e & 1) ? v1 : v0);
+              }
+              s[mt][i][e] = x * fr[mt][e >> 1];
+            }
             if (masked) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const int x = s0 + i * 8 + 2 * qd + (e & 1);
                 const bool there = ((x < 32 ? ok0 >> x : ok1 >> (x - 32)) & 1u) != 0u;
-                if (!there || p0 + x >= seen[mt][e >> 1]) s[mt][i][e] = -CUDART_INF_F;
+                if (!there || p0 + x >= seen[mt][e >> 1]) {
+                  s[mt][i][e] = -CUDART_INF_F;
+                  if (C::W == 1) y[mt][i][e] = -CUDART_INF_F;
+                }
               }
             }
-            top[mt][0] = fmaxf(top[mt][0], fmaxf(s[mt][i][0], s[mt][i][1]));
-            top[mt][1] = fmaxf(top[mt][1], fmaxf(s[mt][i][2], s[mt][i][3]));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              top[mt][h] = fmaxf(top[mt][h], fmaxf(s[mt][i][2 * h], s[mt][i][2 * h + 1]));
+              if (C::W == 1)
+                tpy[mt][h] = fmaxf(tpy[mt][h], fmaxf(y[mt][i][2 * h], y[mt][i][2 * h + 1]));
+            }
           }
         }
         bool grow = false;
@@ -483,54 +574,59 @@ k_page_attn(const PageView pg, const AttnArgs a) {
             top[mt][h] = fmaxf(top[mt][h], __shfl_xor_sync(0xffffffffu, top[mt][h], 1));
             top[mt][h] = fmaxf(top[mt][h], __shfl_xor_sync(0xffffffffu, top[mt][h], 2));
             grow |= top[mt][h] > mx[mt][h] + kRescale;
+            if (C::W == 1) {
+              tpy[mt][h] = fmaxf(tpy[mt][h], __shfl_xor_sync(0xffffffffu, tpy[mt][h], 1));
+              tpy[mt][h] = fmaxf(tpy[mt][h], __shfl_xor_sync(0xffffffffu, tpy[mt][h], 2));
+              grow |= tpy[mt][h] > my[mt][h] + kRescale;
+            }
           }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const float m_new = fmaxf(mx[mt][h], top[mt][h]);
               // (a row that has seen nothing keeps its zeros)
-              const float f = mx[mt][h] == -CUDART_INF_F ? 0.f : ex2_approx(mx[mt][h] - m_new);
+              const float m_new = fmaxf(mx[mt][h], top[mt][h]);
+              float f = mx[mt][h] == -CUDART_INF_F ? 0.f : ex2_approx(mx[mt][h] - m_new);
               mx[mt][h] = m_new;
-              if (f != 1.f) {
-                l[mt][h] *= f;
+              l[mt][h] *= f;
+              if (C::W == 1) {
+                const float n_new = fmaxf(my[mt][h], tpy[mt][h]);
+                f = my[mt][h] == -CUDART_INF_F ? 0.f : ex2_approx(my[mt][h] - n_new);
+                my[mt][h] = n_new;
+              }
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                  o[mt][i][2 * h] *= f;
-                  o[mt][i][2 * h + 1] *= f;
-                }
+              for (int i = 0; i < D / 8; ++i) {
+                o[mt][i][2 * h] *= f;
+                o[mt][i][2 * h + 1] *= f;
               }
             }
         }
-        // weights, rounded to bf16 for the product with V (a rounding of at most
-        // 2^-8 of each weight; the sum l takes them unrounded)
+        // weights, rounded for the product with V: to bf16 (at most 2^-8 of each) or
+        // f16 (2^-11, or 2^-32 of the largest for those below 2^-21 of it); l takes
+        // them unrounded.
+        // -inf - -inf must not arise in a row that has seen nothing yet
         uint32_t pf[MT][SUB / 16][4];
 #pragma unroll
-        for (int i = 0; i < SUB / 8; ++i) {
-          float v0 = 1.f, v1 = 1.f;
-          if (C::W == 1) {
-            const float2 vs = *reinterpret_cast<const float2 *>(sc + TN + s0 + i * 8 + 2 * qd);
-            v0 = vs.x;
-            v1 = vs.y;
-          }
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            float p[4];
+          for (int h = 0; h < 2; ++h) {
+            const float bx = mx[mt][h] == -CUDART_INF_F ? 0.f : mx[mt][h];
+            const float by = my[mt][h] == -CUDART_INF_F ? 0.f : my[mt][h] - kF16Up;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float m = mx[mt][e >> 1];
-              const float x = s[mt][i][e];
-              // -inf - -inf: a row that has seen nothing yet, or a score of -inf
-              p[e] = x == -CUDART_INF_F ? 0.f : ex2_approx(x - m);
-              l[mt][e >> 1] += p[e];
-              // a scale that is not finite may stand at a masked place
-              if (C::W == 1) p[e] = p[e] == 0.f ? 0.f : p[e] * ((e & 1) ? v1 : v0);
+            for (int i = 0; i < SUB / 8; ++i) {
+              float p0w = ex2_approx(s[mt][i][2 * h] - bx);
+              float p1w = ex2_approx(s[mt][i][2 * h + 1] - bx);
+              l[mt][h] += p0w + p1w;
+              if (C::W == 1) {
+                p0w = ex2_approx(y[mt][i][2 * h] - by);
+                p1w = ex2_approx(y[mt][i][2 * h + 1] - by);
+                pf[mt][i >> 1][(i & 1) * 2 + h] = pack_f16(p0w, p1w);
+              } else {
+                pf[mt][i >> 1][(i & 1) * 2 + h] = pack_bf16(p0w, p1w);
+              }
             }
-            pf[mt][i >> 1][(i & 1) * 2] = pack_bf16(p[0], p[1]);
-            pf[mt][i >> 1][(i & 1) * 2 + 1] = pack_bf16(p[2], p[3]);
           }
-        }
         // O += P V
 #pragma unroll
         for (int i = 0; i < SUB / 16; ++i) {
@@ -570,11 +666,18 @@ k_page_attn(const PageView pg, const AttnArgs a) {
               }
             }
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-              const uint32_t b0r = byte_pair<KIND>(w[0][c >> 2], w[1][c >> 2], c & 3);
-              const uint32_t b1r = byte_pair<KIND>(w[2][c >> 2], w[3][c >> 2], c & 3);
+            for (int c4 = 0; c4 < NW; ++c4) {
+              // the two positions' bytes side by side, then four pairs of each half
+              uint32_t b0r[4], b1r[4];
+              f16_pairs<KIND>(__byte_perm(w[0][c4], w[1][c4], 0x5140), b0r[0], b0r[1]);
+              f16_pairs<KIND>(__byte_perm(w[0][c4], w[1][c4], 0x7362), b0r[2], b0r[3]);
+              f16_pairs<KIND>(__byte_perm(w[2][c4], w[3][c4], 0x5140), b1r[0], b1r[1]);
+              f16_pairs<KIND>(__byte_perm(w[2][c4], w[3][c4], 0x7362), b1r[2], b1r[3]);
 #pragma unroll
-              for (int mt = 0; mt < MT; ++mt) mma_bf16_16816(o[mt][c], pf[mt][i], b0r, b1r);
+              for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                  mma_kind<KIND>(o[mt][c4 * 4 + c], pf[mt][i], b0r[c], b1r[c]);
             }
           }
         }
@@ -604,7 +707,9 @@ k_page_attn(const PageView pg, const AttnArgs a) {
         float top = -CUDART_INF_F;
 #pragma unroll
         for (int g = 0; g < WT; ++g) top = fmaxf(top, ml[(g * C::ROWS + m) * 2]);
-        const float f = mx[mt][h] == -CUDART_INF_F ? 0.f : ex2_approx(mx[mt][h] - top);
+        // O from its reference (my for 8 bits) to the item's maximum of x so far
+        const float ref = C::W == 1 ? my[mt][h] - kF16Up : mx[mt][h];
+        const float f = ref == -CUDART_INF_F ? 0.f : ex2_approx(ref - top);
         // (not zero times a NaN: a row of NaN scores keeps m = -inf and O = NaN)
         const bool nan = l[mt][h] != l[mt][h];
         float *dst = osm + (wt * C::ROWS + m) * C::OPAD;
@@ -623,7 +728,6 @@ k_page_attn(const PageView pg, const AttnArgs a) {
     __syncthreads();
 
     const bool whole = pos == item0 && stop == item1;
-    const int64_t item = (int64_t)seq * hkv + kvh;
     const int slot = pos > item0 ? 0 : 1;
     float *part = a.parts + ((int64_t)blockIdx.x * 2 + slot) * a.R * (D + 2);
     if (tid == 0) sh_flag = 0;  // every thread has read it
@@ -680,58 +784,91 @@ k_page_attn(const PageView pg, const AttnArgs a) {
         if (d4 == 0) *reinterpret_cast<float2 *>(part + m * (D + 2) + D) = make_float2(top, den);
       }
     }
-    if (!whole) {
-      // the CTAs that share the item, and whether this is the last of them
+    if (pos == item0 && tid == 0) {
+      // for the join: the CTAs that share the item
       auto owner = [&](int64_t blk) {  // largest b with range(b) <= blk
         int b = (int)min((int64_t)n_cta - 1, ((blk + 1) * n_cta - 1) / total);
         while (b > 0 && range(b) > blk) --b;
         while (b + 1 < n_cta && range(b + 1) <= blk) ++b;
         return b;
       };
-      const int c0 = owner(item0), c1 = owner(item1 - 1);
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) sh_last = atomicAdd(a.tickets + item, 1) == c1 - c0;
-      __syncthreads();
-      if (sh_last) {
-        __threadfence();
-        if (tid == 0) a.tickets[item] = 0;
-        for (int e = tid; e < a.R * (D / 2); e += kPaThreads) {
-          const int m = e / (D / 2), d2 = (e % (D / 2)) * 2, j = m / a.G;
-          if (j >= nq) continue;
-          auto at = [&](int c) {
-            return a.parts + (((int64_t)c * 2 + (c == c0 ? 1 : 0)) * a.R + m) * (D + 2);
-          };
-          float top = -CUDART_INF_F, den = 0.f;
-          float2 acc = make_float2(0.f, 0.f);
-#pragma unroll 4
-          for (int c = c0; c <= c1; ++c)
-            top = fmaxf(top, __ldcg(at(c) + D));
-#pragma unroll 4
-          for (int c = c0; c <= c1; ++c) {
-            const float2 x = __ldcg(reinterpret_cast<const float2 *>(at(c) + D));
-            const float2 y = __ldcg(reinterpret_cast<const float2 *>(at(c) + d2));
-            const float f = x.x == -CUDART_INF_F ? (x.y != x.y ? 1.f : 0.f) : ex2_approx(x.x - top);
-            den += x.y * f;
-            // (a part whose weight is nothing adds nothing, unless it is not finite)
-            acc.x += y.x * f;
-            acc.y += y.y * f;
-          }
-          const int sees = len - nq + j + 1;
-          const float inv = 1.f / den;
-          const int64_t row = ((int64_t)seq * a.q_len + j) * a.hq + kvh * a.G + (m - j * a.G);
-          *reinterpret_cast<uint32_t *>(a.out + row * D + d2) =
-              sees <= 0 ? 0u : pack_bf16(acc.x * inv, acc.y * inv);
-          if (a.lse && d2 == 0)
-            a.lse[row] = top == CUDART_INF_F ? top
-                         : den == 0.f        ? -CUDART_INF_F
-                                             : (top + log2f(den)) * 0.69314718055994531f;
-        }
-      }
+      a.plan[(int64_t)seq * hkv + kvh] =
+          whole ? make_int2(-1, -1) : make_int2(blockIdx.x, owner(item1 - 1));
     }
     __syncthreads();  // shared memory goes to the next item
     pos = stop;
   }
+}
+
+// Joins an item's parts: out = sum_p w_p O_p / sum_p w_p l_p, w_p = 2^(m_p - max m).
+// One row is shared by SPLIT warps, each with every SPLIT-th part.
+template <int D, int SPLIT>
+__global__ void __launch_bounds__(128)
+k_page_join(const AttnArgs a, int hkv, int width_rows) {
+  constexpr int V = D / 32;  // dims of a lane
+  __shared__ float red[4][D + 2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, part0 = warp % SPLIT;
+  const int64_t e = (int64_t)blockIdx.x * (4 / SPLIT) + warp / SPLIT;
+  pdl_wait();
+  const bool on = e < (int64_t)a.n_seqs * hkv * a.R;
+  const int m = on ? (int)(e % a.R) : 0;
+  const int64_t item = on ? e / a.R : 0;
+  const int2 pl = on ? a.plan[item] : make_int2(-1, -1);
+  const int seq = (int)(item / hkv), kvh = (int)(item % hkv), j = m / a.G;
+  int nq = a.q_lens ? a.q_lens[seq] : a.q_len;
+  nq = max(0, min(nq, a.q_len));
+  const bool live = pl.x >= 0 && j < nq;
+  auto at = [&](int c) {
+    return a.parts + (((int64_t)c * 2 + (c == pl.x ? 1 : 0)) * a.R + m) * (D + 2);
+  };
+  float top = -CUDART_INF_F, den = 0.f, acc[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.f;
+  if (live) {
+    for (int c = pl.x + lane; c <= pl.y; c += 32) top = fmaxf(top, at(c)[D]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll 8
+    for (int c = pl.x + part0; c <= pl.y; c += SPLIT) {
+      const float *src = at(c);
+      const float2 x = *reinterpret_cast<const float2 *>(src + D);
+      // (a part that saw nothing weighs nothing; one of NaN scores has m = -inf too)
+      const float f = x.x == -CUDART_INF_F ? (x.y != x.y ? 1.f : 0.f) : ex2_approx(x.x - top);
+      den += x.y * f;
+#pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        const float2 y = *reinterpret_cast<const float2 *>(src + lane * V + i);
+        acc[i] += y.x * f;
+        acc[i + 1] += y.y * f;
+      }
+    }
+  }
+  if (SPLIT > 1) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) red[warp][lane * V + i] = acc[i];
+    if (lane == 0) red[warp][D] = den;
+    __syncthreads();
+    if (part0 != 0) return;
+#pragma unroll
+    for (int w = 1; w < SPLIT; ++w) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] += red[warp + w][lane * V + i];
+      den += red[warp + w][D];
+    }
+  }
+  if (!live) return;
+  const int len = max(0, min(a.seq_lens[seq], width_rows));
+  const int sees = len - nq + j + 1;
+  const float inv = 1.f / den;
+  const int64_t row = ((int64_t)seq * a.q_len + j) * a.hq + kvh * a.G + (m - j * a.G);
+#pragma unroll
+  for (int i = 0; i < V; i += 2)
+    *reinterpret_cast<uint32_t *>(a.out + row * D + lane * V + i) =
+        sees <= 0 ? 0u : pack_bf16(acc[i] * inv, acc[i + 1] * inv);
+  if (a.lse && lane == 0)
+    a.lse[row] = top == CUDART_INF_F ? top
+                 : den == 0.f        ? -CUDART_INF_F
+                                     : (top + log2f(den)) * 0.69314718055994531f;
 }
 
 bool attend_args(const dhs_pages *pages, int32_t n_seqs, int32_t q_len, int32_t q_heads,
@@ -740,8 +877,8 @@ bool attend_args(const dhs_pages *pages, int32_t n_seqs, int32_t q_len, int32_t 
          q_heads % pg->hkv == 0 && (int64_t)q_len * (q_heads / pg->hkv) <= 128;
 }
 
-int64_t ticket_bytes(int32_t n_seqs, int hkv) {
-  return ((int64_t)n_seqs * hkv * 4 + 255) / 256 * 256;
+int64_t plan_bytes(int32_t n_seqs, int hkv) {
+  return ((int64_t)n_seqs * hkv * 8 + 255) / 256 * 256;
 }
 
 // Calls f with the configuration for R rows.  16 rows fit one warp and four
@@ -797,7 +934,7 @@ extern "C" int64_t dhs_page_attend_workspace(const dhs_pages *pages, int32_t n_s
   const int R = q_len * (q_heads / pg.hkv), sms = device_sms(dev);
   if (sms < 1) return -1;
   return pick(pg, R, [&](auto c) -> int64_t {
-    return ticket_bytes(n_seqs, pg.hkv) + (int64_t)sms * decltype(c)::OCC * 2 * R * (pg.d + 2) * 4;
+    return plan_bytes(n_seqs, pg.hkv) + (int64_t)sms * decltype(c)::OCC * 2 * R * (pg.d + 2) * 4;
   });
 }
 
@@ -830,9 +967,9 @@ extern "C" int dhs_page_attend(const dhs_pages *pages, const void *q, const int3
   a.table = page_table;
   a.out = static_cast<uint16_t *>(out);
   a.lse = lse;
-  a.tickets = static_cast<int32_t *>(workspace);
+  a.plan = static_cast<int2 *>(workspace);
   a.parts = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) +
-                                      ticket_bytes(n_seqs, pg.hkv));
+                                      plan_bytes(n_seqs, pg.hkv));
   a.err = err;
   a.width = table_width;
   a.n_seqs = n_seqs;
@@ -845,12 +982,20 @@ extern "C" int dhs_page_attend(const dhs_pages *pages, const void *q, const int3
   return pick(pg, a.R, [&](auto c) -> int {
     using C = decltype(c);
     const int grid = sms * C::OCC;
-    if (workspace_bytes < ticket_bytes(n_seqs, pg.hkv) + (int64_t)grid * 2 * a.R * (C::D + 2) * 4)
+    if (workspace_bytes < plan_bytes(n_seqs, pg.hkv) + (int64_t)grid * 2 * a.R * (C::D + 2) * 4)
       return DHS_ERR_INVALID;
     static DeviceSmem granted;
+    const int64_t rows = (int64_t)n_seqs * pg.hkv * a.R;
+    const int width_rows =
+        (int)std::min<int64_t>((int64_t)table_width * pg.rows, (int64_t)INT32_MAX - 1024);
+    // few rows: four warps a row
+    const bool few = rows <= 4 * sms;
+    const unsigned jgrid = (unsigned)(few ? rows : (rows + 3) / 4);
     if (granted.ensure(k_page_attn<C>, C::SMEM, dev) != cudaSuccess ||
         launch_prio(k_page_attn<C>, dim3(grid), dim3(kPaThreads), C::SMEM, s, pg, a) !=
-            cudaSuccess) {
+            cudaSuccess ||
+        launch_pdl(few ? k_page_join<C::D, 4> : k_page_join<C::D, 1>, dim3(jgrid), dim3(128), 0, s,
+                   a, pg.hkv, width_rows) != cudaSuccess) {
       cudaGetLastError();
       return DHS_ERR_CUDA;
     }
