@@ -7,8 +7,8 @@
 // head against 22 cycles of HBM for its 512 bytes in bf16, 11 in 8 bits).
 // The softmax is online in log2 units: with the running maximum m of a row,
 //   l = sum 2^(x - m),  O = sum 2^(x - m) v,
-// and O and l are rescaled only when m grows by more than kRescale, so weights
-// stay below 2^kRescale.
+// and O and l are rescaled only when m grows by more than 4 (8 bits) or 8 (bf16),
+// so weights stay below 2^4 or 2^8.
 //
 // Work split: the positions of every (sequence, kv head) item are cut into
 // blocks, all items' blocks are laid end to end, and CTA b of n takes blocks
@@ -29,12 +29,11 @@
 // 8-bit rows: the codes become f16 in registers, exactly.  A row of Q is scaled
 // by a power of two to fit f16 (exact down to 2^-32 of its largest element, and
 // off by 2^-40 of it below), a key's scale multiplies its column of scores.  A
-// value's scale goes into the weight's exponent: with y = x + log2(scale), the
-// weights of the product are 2^(y - m' + 7), m' the running maximum of y, so that
-// they fit f16 whatever the scales are, and l is summed from 2^(x - m) beside
-// them; O is brought from m' to m once, at the end.  (Codes to bf16 instead, with
-// scaled bf16 weights, took 4 instructions a pair on the half-rate integer pipe
-// instead of 1.5 to 2, and bound the kernel.)
+// value's scale multiplies its column of weights over a common power of two, which
+// follows the largest scale read so far: f16 then holds a weight times scale to 2^-11,
+// or to 2^-31 of the largest weight times the largest scale.  (Codes to bf16 instead,
+// with scaled bf16 weights, took 4 instructions a pair on the half-rate integer
+// pipe instead of 1.5 to 2, and bound the kernel.)
 // The fragments are read so that no transposition is needed: a thread's 16
 // bytes of a key are 16 consecutive dims, which Q's fragments are loaded to
 // match, and of a value 16 (8) consecutive output columns of two positions,
@@ -56,9 +55,12 @@ namespace dhs {
 namespace {
 
 constexpr int kPaWarps = 4;
+constexpr int TILE8 = 8192, NS8 = 3, OCC8 = 2, SUB8 = 32;
 constexpr int kPaThreads = kPaWarps * 32;
-constexpr float kRescale = 8.f;
-constexpr float kF16Up = 7.f;  // f16 weights are 2^kF16Up times larger: up to 2^15
+constexpr float kRescale8 = 4.f, kRescale16 = 8.f;  // 8-bit caches, bf16
+// f16 weights: value scales over 2^vref are in [2^6, 2^7) when vref is set and may
+// grow to 2^11 before it is set anew, so that a weight is at most 2^15
+constexpr int kVrefUp = 6, kVrefMax = 11;
 
 // ------------------------------------------------------------ 8-bit to f16 pairs
 // int8: with its sign bit flipped x is u = x + 128, and 0x6400 | u is 1024 + u in
@@ -86,11 +88,6 @@ __device__ __forceinline__ void f16_pairs(uint32_t w, uint32_t &lo, uint32_t &hi
   }
 }
 
-__device__ __forceinline__ float lg2_approx(float x) {
-  float y;
-  asm("lg2.approx.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
@@ -116,12 +113,12 @@ struct Cfg {
   static constexpr int RB = D * W;                       // bytes of a row
   static constexpr int CH = RB / 16;                     // 16-byte chunks of a row
   // positions of a group's tile: 8 KB of keys and values per warp of the group
-  static constexpr int TN0 = 8192 * WM / (2 * RB);
+  static constexpr int TN0 = (W == 1 ? TILE8 : 8192) * WM / (2 * RB);
   static constexpr int TN = TN0 > 64 ? 64 : TN0;
-  static constexpr int SUB = MT == 1 && TN >= 32 ? 32 : 16;  // positions scored at a time
+  static constexpr int SUB = MT == 1 && TN >= 32 && (W == 2 || SUB8 == 32) ? 32 : 16;  // positions scored at a time
   static constexpr int KV = TN * RB;
   static constexpr int STAGE = 2 * KV + (W == 1 ? 2 * TN * 4 : 0);  // keys, values, scales
-  static constexpr int NS = 3;
+  static constexpr int NS = W == 1 ? NS8 : 3;
   static constexpr int GROUP = NS * STAGE;
   static constexpr int ROWS = WM * MT * 16;              // rows of Q that fit
   static constexpr int OPAD = D + 4;
@@ -132,7 +129,7 @@ struct Cfg {
   static constexpr int OFF_MASK = OFF_ROW + WT * SLOTS * TN * 8; // uint32 [WT][SLOTS][2]
   static constexpr int OFF_ML = OFF_MASK + WT * SLOTS * 8;       // float [WT][ROWS][2]
   static constexpr int SMEM = OFF_ML + WT * ROWS * 8;
-  static constexpr int OCC = SMEM * 2 <= 226 * 1024 ? 2 : 1;
+  static constexpr int OCC = W == 1 && MT == 1 ? OCC8 : SMEM * 2 <= 226 * 1024 ? 2 : 1;
   static constexpr int BLOCK = WT * TN;                  // positions of a block
 };
 
@@ -247,7 +244,9 @@ k_page_attn(const PageView pg, const AttnArgs a) {
       items > 0 ? ceilf(sqrtf((float)total / (float)items * ((float)C::BLOCK * 2 * RB) /
                               (float)(a.R * D * 4)))
                 : 0.f;
-  const int n_cta = (int)min(min((int64_t)gridDim.x, total), (int64_t)((float)items * parts));
+  int64_t n_parts = (int64_t)((float)items * parts);
+  if (n_parts > gridDim.x / C::OCC) n_parts = gridDim.x;
+  const int n_cta = (int)min(min((int64_t)gridDim.x, total), n_parts);
   pdl_trigger();  // the join may be placed; it waits for this grid's end
   if ((int)blockIdx.x >= n_cta) return;
   auto range = [&](int b) -> int64_t { return total * b / n_cta; };
@@ -328,37 +327,67 @@ k_page_attn(const PageView pg, const AttnArgs a) {
         if (lane == 0 && (x >> 5) < 2) maskbuf[(t % C::SLOTS) * 2 + (x >> 5)] = ok;
       }
     };
+    // In-page offset of the tile that is copied next: a tile inside one page and
+    // below the length is one run of memory, copied from one address with constant
+    // offsets; others row by row.
+    int in_page = (int)(((int64_t)b0 * C::BLOCK + wt * TN) % pg.rows);
+    const int in_step = C::BLOCK % pg.rows;
     auto copy = [&](int t) {
+      // a thread copies one chunk column of every STEP-th row
+      constexpr int STEP = WM * 32 / C::CH;
+      constexpr int XM = STEP >= 8 ? 7 : STEP - 1;  // x & 7 = (xr & XM) + (u * STEP & 7)
+      const int xr = gl / C::CH, c = gl % C::CH;
       if (t < nblk) {
         unsigned char *kst = ring + (t % NS) * C::STAGE, *vst = kst + C::KV;
+        float *sc = reinterpret_cast<float *>(vst + C::KV);
         const int64_t *src = rowbuf + (t % C::SLOTS) * TN;
-        // a thread copies one chunk column of every STEP-th row; STEP is a multiple
-        // of 8 or the swizzle's row bits are spelled out by the unrolled index
-        constexpr int STEP = WM * 32 / C::CH;
-        const int xr = gl / C::CH, c = gl % C::CH;
-        const unsigned char *gk = pg.k + c * 16, *gv = pg.v + c * 16;
+        const int64_t row0 = src[0];
+        const bool run = in_page + TN <= pg.rows && row0 >= 0 &&
+                         (int64_t)(b0 + t) * C::BLOCK + wt * TN + TN <= len;
+        if (run) {
+          const unsigned char *gk = pg.k + (row0 + xr) * RB + c * 16;
+          const unsigned char *gv = pg.v + (row0 + xr) * RB + c * 16;
 #pragma unroll
-        for (int u = 0; u < TN / STEP; ++u) {
-          const int x = xr + u * STEP;
-          const int64_t row = src[x];
-          const int n = row < 0 ? 0 : 16;
-          const int64_t off = row < 0 ? 0 : row * RB;
-          cp_async_16_zfill(kst + x * RB + kchunk<C>(x, c) * 16, gk + off, n);
-          cp_async_16_zfill(vst + x * RB + vchunk<C>(x, c) * 16, gv + off, n);
-        }
-        if (C::W == 1) {
-          float *sc = reinterpret_cast<float *>(vst + C::KV);
+          for (int u = 0; u < TN / STEP; ++u) {
+            const int low = (xr & XM) + (u * STEP & 7);
+            cp_async_16(kst + (xr + u * STEP) * RB + kchunk<C>(low, c) * 16, gk + u * STEP * RB);
+            cp_async_16(vst + (xr + u * STEP) * RB + vchunk<C>(low, c) * 16, gv + u * STEP * RB);
+          }
+          if (C::W == 1) {
 #pragma unroll
-          for (int u = 0; u < LK; ++u) {
-            const int x = gl + u * WM * 32;
-            if (x < TN) {
-              const int64_t row = src[x];
-              cp_async_4_zfill(sc + x, pg.ks + (row < 0 ? 0 : row), row < 0 ? 0 : 4);
-              cp_async_4_zfill(sc + TN + x, pg.vs + (row < 0 ? 0 : row), row < 0 ? 0 : 4);
+            for (int u = 0; u < LK; ++u) {
+              const int x = gl + u * WM * 32;
+              if (x < TN) {
+                cp_async_4(sc + x, pg.ks + row0 + x);
+                cp_async_4(sc + TN + x, pg.vs + row0 + x);
+              }
+            }
+          }
+        } else {
+#pragma unroll 4
+          for (int u = 0; u < TN / STEP; ++u) {
+            const int x = xr + u * STEP;
+            const int64_t row = src[x];
+            const int n = row < 0 ? 0 : 16;
+            const int64_t off = (row < 0 ? 0 : row * RB) + c * 16;
+            cp_async_16_zfill(kst + x * RB + kchunk<C>(x, c) * 16, pg.k + off, n);
+            cp_async_16_zfill(vst + x * RB + vchunk<C>(x, c) * 16, pg.v + off, n);
+          }
+          if (C::W == 1) {
+#pragma unroll
+            for (int u = 0; u < LK; ++u) {
+              const int x = gl + u * WM * 32;
+              if (x < TN) {
+                const int64_t row = src[x];
+                cp_async_4_zfill(sc + x, pg.ks + (row < 0 ? 0 : row), row < 0 ? 0 : 4);
+                cp_async_4_zfill(sc + TN + x, pg.vs + (row < 0 ? 0 : row), row < 0 ? 0 : 4);
+              }
             }
           }
         }
       }
+      in_page += in_step;
+      if (in_page >= pg.rows) in_page -= pg.rows;
       cp_async_commit();
     };
 
@@ -406,7 +435,8 @@ k_page_attn(const PageView pg, const AttnArgs a) {
           // the largest element goes to [2^14, 2^15) (infinities and NaN stay)
           const int e = top >= 0x7F80u ? 0 : max((int)(top >> 7) - 127 - 14, -110);
           const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-          fr[mt][half] *= __uint_as_float((uint32_t)(127 + e) << 23);
+          // (above zero, as it multiplies -infinity)
+          fr[mt][half] = fmaxf(fr[mt][half] * __uint_as_float((uint32_t)(127 + e) << 23), 1e-37f);
 #pragma unroll
           for (int s = 0; s < D / 16; ++s)
 #pragma unroll
@@ -428,15 +458,16 @@ k_page_attn(const PageView pg, const AttnArgs a) {
       }
     const int common = len - nq + 1;  // positions that every query sees
 
-    // mx: running maximum of x, my: of y (8-bit kinds; else the same as mx)
-    float o[MT][D / 8][4], mx[MT][2], my[MT][2], l[MT][2];
+    float o[MT][D / 8][4], mx[MT][2];
+    float l[MT][2];
+    int vref = -200;   // 8 bits: weights times scales are over 2^vref
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
       for (int i = 0; i < D / 8; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[mt][i][e] = 0.f;
-      mx[mt][0] = mx[mt][1] = my[mt][0] = my[mt][1] = -CUDART_INF_F;
+      mx[mt][0] = mx[mt][1] = -CUDART_INF_F;
       l[mt][0] = l[mt][1] = 0.f;
     }
 
@@ -473,6 +504,29 @@ k_page_attn(const PageView pg, const AttnArgs a) {
         }
         __syncwarp();
       }
+      if (C::W == 1) {
+        // the tile's largest value scale (as bits; not one that is not finite)
+        uint32_t top = 0u;
+#pragma unroll
+        for (int u = 0; u < (TN + 31) / 32; ++u) {
+          const int x = lane + u * 32;
+          const uint32_t b = x < TN ? __float_as_uint(sc[TN + x]) : 0u;
+          top = max(top, b < 0x7F800000u ? b : 0u);
+        }
+        const int e = (int)(__reduce_max_sync(0xffffffffu, top) >> 23) - 127;
+        if (e >= vref + kVrefMax) {
+          const int to = max(e - kVrefUp, -100);
+          const float f = vref < -100 ? 0.f : ex2_approx((float)(vref - to));
+          vref = to;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) o[mt][i][x] *= f;
+        }
+      }
+      const float vdown = C::W == 1 ? __uint_as_float((uint32_t)(127 - max(vref, -100)) << 23) : 1.f;
 #pragma unroll
       for (int sub = 0; sub < TN / SUB; ++sub) {
         const int s0 = sub * SUB;
@@ -519,52 +573,30 @@ k_page_attn(const PageView pg, const AttnArgs a) {
               }
             }
         }
-        // to log2 units, masks, the rows' maxima of x and (8-bit) of y
-        float y[MT][C::W == 1 ? SUB / 8 : 1][4];
-        float top[MT][2], tpy[MT][2];
+        // key scales, masks, the rows' maxima (a row's factor fr comes later)
+        float top[MT][2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-          top[mt][0] = top[mt][1] = tpy[mt][0] = tpy[mt][1] = -CUDART_INF_F;
+        for (int mt = 0; mt < MT; ++mt) top[mt][0] = top[mt][1] = -CUDART_INF_F;
 #pragma unroll
         for (int i = 0; i < SUB / 8; ++i) {
-          float k0 = 1.f, k1 = 1.f, v0 = 0.f, v1 = 0.f;
-          if (C::W == 1) {
-            const float2 ks = *reinterpret_cast<const float2 *>(sc + s0 + i * 8 + 2 * qd);
-            const float2 vs = *reinterpret_cast<const float2 *>(sc + TN + s0 + i * 8 + 2 * qd);
-            k0 = ks.x;
-            k1 = ks.y;
-            v0 = lg2_approx(vs.x);
-            v1 = lg2_approx(vs.y);
-          }
+          float2 ks = make_float2(1.f, 1.f);
+          if (C::W == 1) ks = *reinterpret_cast<const float2 *>(sc + s0 + i * 8 + 2 * qd);
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float x = s[mt][i][e];
-              if (C::W == 1) {
-                x *= (e & 1) ? k1 : k0;
-                y[mt][i][e] = fmaf(x, fr[mt][e >> 1], (e & 1) ? v1 : v0);
-              }
-              s[mt][i][e] = x * fr[mt][e >> 1];
-            }
-            if (masked) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int x = s0 + i * 8 + 2 * qd + (e & 1);
-                const bool there = ((x < 32 ? ok0 >> x : ok1 >> (x - 32)) & 1u) != 0u;
-                if (!there || p0 + x >= seen[mt][e >> 1]) {
-                  s[mt][i][e] = -CUDART_INF_F;
-                  if (C::W == 1) y[mt][i][e] = -CUDART_INF_F;
-                }
-              }
-            }
+          for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              top[mt][h] = fmaxf(top[mt][h], fmaxf(s[mt][i][2 * h], s[mt][i][2 * h + 1]));
-              if (C::W == 1)
-                tpy[mt][h] = fmaxf(tpy[mt][h], fmaxf(y[mt][i][2 * h], y[mt][i][2 * h + 1]));
+              float2 x = make_float2(s[mt][i][2 * h], s[mt][i][2 * h + 1]);
+              if (C::W == 1) x = make_float2(x.x * ks.x, x.y * ks.y);
+              if (masked) {
+                const int c = s0 + i * 8 + 2 * qd;
+                const uint32_t there = c < 32 ? ok0 >> c : ok1 >> (c - 32);
+                if (!(there & 1u) || p0 + c >= seen[mt][h]) x.x = -CUDART_INF_F;
+                if (!(there & 2u) || p0 + c + 1 >= seen[mt][h]) x.y = -CUDART_INF_F;
+              }
+              s[mt][i][2 * h] = x.x;
+              s[mt][i][2 * h + 1] = x.y;
+              top[mt][h] = fmaxf(top[mt][h], fmaxf(x.x, x.y));
             }
-          }
         }
         bool grow = false;
 #pragma unroll
@@ -573,12 +605,8 @@ k_page_attn(const PageView pg, const AttnArgs a) {
           for (int h = 0; h < 2; ++h) {
             top[mt][h] = fmaxf(top[mt][h], __shfl_xor_sync(0xffffffffu, top[mt][h], 1));
             top[mt][h] = fmaxf(top[mt][h], __shfl_xor_sync(0xffffffffu, top[mt][h], 2));
-            grow |= top[mt][h] > mx[mt][h] + kRescale;
-            if (C::W == 1) {
-              tpy[mt][h] = fmaxf(tpy[mt][h], __shfl_xor_sync(0xffffffffu, tpy[mt][h], 1));
-              tpy[mt][h] = fmaxf(tpy[mt][h], __shfl_xor_sync(0xffffffffu, tpy[mt][h], 2));
-              grow |= tpy[mt][h] > my[mt][h] + kRescale;
-            }
+            top[mt][h] *= fr[mt][h];
+            grow |= top[mt][h] > mx[mt][h] + (C::W == 1 ? kRescale8 : kRescale16);
           }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -587,14 +615,9 @@ k_page_attn(const PageView pg, const AttnArgs a) {
             for (int h = 0; h < 2; ++h) {
               // (a row that has seen nothing keeps its zeros)
               const float m_new = fmaxf(mx[mt][h], top[mt][h]);
-              float f = mx[mt][h] == -CUDART_INF_F ? 0.f : ex2_approx(mx[mt][h] - m_new);
+              const float f = mx[mt][h] == -CUDART_INF_F ? 0.f : ex2_approx(mx[mt][h] - m_new);
               mx[mt][h] = m_new;
               l[mt][h] *= f;
-              if (C::W == 1) {
-                const float n_new = fmaxf(my[mt][h], tpy[mt][h]);
-                f = my[mt][h] == -CUDART_INF_F ? 0.f : ex2_approx(my[mt][h] - n_new);
-                my[mt][h] = n_new;
-              }
 #pragma unroll
               for (int i = 0; i < D / 8; ++i) {
                 o[mt][i][2 * h] *= f;
@@ -602,31 +625,41 @@ k_page_attn(const PageView pg, const AttnArgs a) {
               }
             }
         }
-        // weights, rounded for the product with V: to bf16 (at most 2^-8 of each) or
-        // f16 (2^-11, or 2^-32 of the largest for those below 2^-21 of it); l takes
-        // them unrounded.
-        // -inf - -inf must not arise in a row that has seen nothing yet
+        // weights, rounded for the product with V: to bf16 (at most 2^-8 of each) or,
+        // times the value's scale, to f16 (2^-11, or 2^-31 of the largest weight times
+        // the largest scale); l takes the weights unrounded.  -inf - -inf must not
+        // arise in a row that has seen nothing yet
         uint32_t pf[MT][SUB / 16][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int i = 0; i < SUB / 8; ++i) {
+          float2 vs = make_float2(1.f, 1.f);
+          if (C::W == 1)
+            vs = *reinterpret_cast<const float2 *>(sc + TN + s0 + i * 8 + 2 * qd);
+          vs.x *= vdown;
+          vs.y *= vdown;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float bx = mx[mt][h] == -CUDART_INF_F ? 0.f : mx[mt][h];
-            const float by = my[mt][h] == -CUDART_INF_F ? 0.f : my[mt][h] - kF16Up;
+          for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int i = 0; i < SUB / 8; ++i) {
-              float p0w = ex2_approx(s[mt][i][2 * h] - bx);
-              float p1w = ex2_approx(s[mt][i][2 * h + 1] - bx);
-              l[mt][h] += p0w + p1w;
+            for (int h = 0; h < 2; ++h) {
+              const float b = mx[mt][h] == -CUDART_INF_F ? 0.f : -mx[mt][h];
+              float2 p = make_float2(ex2_approx(fmaf(s[mt][i][2 * h], fr[mt][h], b)),
+                                     ex2_approx(fmaf(s[mt][i][2 * h + 1], fr[mt][h], b)));
+              l[mt][h] += p.x + p.y;
               if (C::W == 1) {
-                p0w = ex2_approx(y[mt][i][2 * h] - by);
-                p1w = ex2_approx(y[mt][i][2 * h + 1] - by);
-                pf[mt][i >> 1][(i & 1) * 2 + h] = pack_f16(p0w, p1w);
+                p.x *= vs.x;
+                p.y *= vs.y;
+                if (masked) {  // (a scale that is not finite at a masked place)
+                  const int c = s0 + i * 8 + 2 * qd;
+                  const uint32_t there = c < 32 ? ok0 >> c : ok1 >> (c - 32);
+                  if (!(there & 1u) || p0 + c >= seen[mt][h]) p.x = 0.f;
+                  if (!(there & 2u) || p0 + c + 1 >= seen[mt][h]) p.y = 0.f;
+                }
+                pf[mt][i >> 1][(i & 1) * 2 + h] = pack_f16(p.x, p.y);
               } else {
-                pf[mt][i >> 1][(i & 1) * 2 + h] = pack_bf16(p0w, p1w);
+                pf[mt][i >> 1][(i & 1) * 2 + h] = pack_bf16(p.x, p.y);
               }
             }
-          }
+        }
         // O += P V
 #pragma unroll
         for (int i = 0; i < SUB / 16; ++i) {
@@ -707,9 +740,9 @@ k_page_attn(const PageView pg, const AttnArgs a) {
         float top = -CUDART_INF_F;
 #pragma unroll
         for (int g = 0; g < WT; ++g) top = fmaxf(top, ml[(g * C::ROWS + m) * 2]);
-        // O from its reference (my for 8 bits) to the item's maximum of x so far
-        const float ref = C::W == 1 ? my[mt][h] - kF16Up : mx[mt][h];
-        const float f = ref == -CUDART_INF_F ? 0.f : ex2_approx(ref - top);
+        // O to the item's maximum so far, and from its power of two
+        const float up = C::W == 1 ? (float)max(vref, -100) : 0.f;
+        const float f = mx[mt][h] == -CUDART_INF_F ? 0.f : ex2_approx(mx[mt][h] - top + up);
         // (not zero times a NaN: a row of NaN scores keeps m = -inf and O = NaN)
         const bool nan = l[mt][h] != l[mt][h];
         float *dst = osm + (wt * C::ROWS + m) * C::OPAD;

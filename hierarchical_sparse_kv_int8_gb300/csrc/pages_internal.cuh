@@ -36,6 +36,8 @@ struct PageView {
   float *ks, *vs;
   int64_t n_pages;
   int rows, hkv, d, kind;
+  uint32_t div_mul;  // pos / rows = pos * div_mul >> div_shift for 0 <= pos < 2^31
+  int div_shift;
 };
 
 inline bool page_view(const dhs_pages *p, PageView *out) {
@@ -54,6 +56,12 @@ inline bool page_view(const dhs_pages *p, PageView *out) {
   out->hkv = p->kv_heads;
   out->d = p->head_dim;
   out->kind = p->kind;
+  // with 2^s >= rows, ceil(2^(31 + s) / rows) is off by less than 2^-31 of a
+  // quotient's unit for every pos < 2^31, and fits 32 bits
+  int s = 0;
+  while (((int64_t)1 << s) < p->page_rows) ++s;
+  out->div_mul = (uint32_t)((((uint64_t)1 << (31 + s)) + p->page_rows - 1) / p->page_rows);
+  out->div_shift = 31 + s;
   return true;
 }
 
@@ -66,7 +74,8 @@ __device__ __forceinline__ void page_error(int32_t *err, int code, int site) {
 // row is h * rows further on.  The caller has checked 0 <= pos < width * rows.
 __device__ __forceinline__ int64_t page_row(const PageView &p, const int32_t *tab, int pos,
                                             int32_t *err, int site) {
-  const int pg = pos / p.rows, in = pos - pg * p.rows;
+  const int pg = (int)((uint64_t)(uint32_t)pos * p.div_mul >> p.div_shift);
+  const int in = pos - pg * p.rows;
   const int32_t page = tab[pg];
   if (page < 0 || page >= p.n_pages) {
     page_error(err, DC_LOC_RANGE, site);

@@ -6,7 +6,13 @@ of sum p|v|), and what the 32-bit scores and sums are off by: a score of
 magnitude at most `reach` is a sum of d products (d + 16 half-steps of 2^-24, the
 scaling and the base-2 exponential's argument among them), the exponential
 itself 2^-21, the sums one half-step per term.  Log-sum-exp: the same without the
-two roundings to bf16.
+two roundings to bf16.  From an 8-bit cache the weights, times their value's scale,
+are rounded to f16 instead (2^-11, well inside the bf16 term): as multiples of 2^-6
+of the largest scale at most, so that f16's smallest step near zero leaves an error
+of up to 2^-25 2^-6 = 2^-31 of the largest weight times the largest scale in each,
+and in all of nk positions nk 2^-31 max|v| (the largest weight over the sum is at
+most 1; max|v| is taken twice for the largest scale standing on a row without its
+largest code).
 """
 import math
 
@@ -37,7 +43,7 @@ def _close(out, lse, want, d, nk, vmax=0.0):
     o, l, wt, reach = want
     e = reach * (d + 16) * 2.0 ** -24 + 2.0 ** -21
     tol = 2.0 ** -8 * np.abs(o) + wt * (2.0 ** -8 + 2 * e[..., None] + nk * 2.0 ** -24) + 1e-37 \
-        + nk * 2.0 ** -32 * 2 * vmax
+        + nk * 2.0 ** -31 * 2 * vmax
     fine = np.isfinite(o)
     assert np.array_equal(np.isnan(out), np.isnan(o))
     bad = fine & ~(np.abs(np.where(fine, out - o, 0)) <= np.where(fine, tol, 0))
