@@ -1,67 +1,528 @@
-// Causal attention of packed sequences.
+// Causal attention of packed sequences on the fifth-generation tensor cores.
 //
-// One warp per (query token, head): an online softmax over the keys the query
-// sees, one key at a time.
+// For kv head g the rows of the score matrix are (token, head) pairs, the G =
+// q_heads / kv_heads heads of a token next to one another: 128 rows are tpt =
+// 128 / G tokens (the rest of the 128 idle when G does not divide it), so that
+// grouped heads share every key and value tile and the causal edge of a tile is
+// tpt positions wide.  A CTA owns two such row tiles (2 tpt consecutive tokens of
+// one sequence) and walks the keys they see in tiles of 128:
+//   S_i = Q_i K^T (M 128, N 128, K D), P_i = 2^(c S_i - m_i), O_i += P_i V.
+// Warps 0-3 and 4-7 are the softmax threads of row tile 0 and 1, one row each:
+// they read S from tensor memory, keep the row's maximum m (O is rescaled only
+// when it grows by more than kRescale) and its sum l in 32 bits, and write P in
+// bf16 over S in tensor memory, from where the second product reads it.  One thread of
+// warp 8 issues all MMAs in the order  P0 V(t), Q0 K(t+1), P1 V(t), Q1 K(t+1):
+// while one row tile's softmax runs, the tensor cores work for the other.  S_i(t +
+// 1) overwrites P_i(t), which the MMA issued just before it has read: MMAs of a
+// thread run in order.  One thread of warp 9 fetches Q and the ring of K and V
+// tiles with tiled TMA copies in the 128-byte-swizzled layout.
+//
+// A weight is 0 where a row does not see a key, but 0 times an infinity or a NaN is
+// not 0: warps 10-11 go over the value tiles at the causal edge and the sequence's
+// end before they are used, set what is not finite there to 0, and remember it; the
+// rows that do see such a value get it added at the end, value by value.
+//
+// With few row tiles the keys are split over nsplit CTAs, which leave (O, m, l) in
+// the workspace for a join.
+//
+// Waits are bounded; one that runs out records an error and lets the CTA finish:
+// the loader then waits for its copies and the MMA thread for its products before
+// tensor memory is freed.
 #include "pages_internal.cuh"
+#include "tc_util.cuh"
 
+#include <cuda.h>
 #include <math_constants.h>
+
+#include <algorithm>
 
 namespace dhs {
 namespace {
 
-constexpr int kPrWarps = 4;
+constexpr int kPrThreads = 384;
+constexpr int kPrM = 128, kPrN = 128;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kCleanWarp = 10;
+constexpr int kPrSpin = 1 << 20;
+constexpr float kPrRescale = 8.f;
+constexpr uint32_t kPrCols = 512;  // S0, S1 (P over them), O0, O1
 
-struct PromptStrides {
-  int64_t qt, qh, kt, kh, vt, vh;
+struct PromptArgs {
+  const uint16_t *v;
+  int64_t vt, vh;            // strides of v, for values that are not finite
+  const int32_t *cu_q, *cu_k;
+  uint16_t *out;
+  float *lse, *parts;
+  int32_t *err;
+  int64_t n_q, n_k;
+  int n_seqs, hq, hkv, G, tpt, nsplit;
+  float scale_log2;
 };
 
 template <int D>
-__global__ void __launch_bounds__(kPrWarps * 32)
-k_prompt(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ k,
-         const __nv_bfloat16 *__restrict__ v, const PromptStrides st, int64_t n_q, int64_t n_k,
-         const int32_t *__restrict__ cu_q, const int32_t *__restrict__ cu_k, int n_seqs, int hq,
-         int hkv, float scale_log2, __nv_bfloat16 *__restrict__ out, float *__restrict__ lse,
-         int32_t *err) {
-  const int64_t item = (int64_t)blockIdx.x * kPrWarps + threadIdx.x / 32;
+struct PrCfg {
+  static constexpr int HALVES = D / 64;
+  static constexpr int TILE = 128 * D * 2;          // a Q, K or V tile
+  static constexpr int HALF = 128 * 128;            // 64 dims of its 128 rows
+  static constexpr int SLOTS = D == 128 ? 5 : 8;    // K and V tiles in flight
+  static constexpr int OFF_KV = 2 * TILE;
+  static constexpr int OFF_BAR = OFF_KV + SLOTS * TILE;
+  static constexpr int CLEAN = 4;                   // value tiles gone over and not yet used, at most
+  static constexpr int BARS = 2 + 2 * SLOTS + CLEAN + 6;
+  static constexpr int OFF_TMEM = OFF_BAR + BARS * 8;
+  static constexpr int SMEM = OFF_TMEM + 16 + 1024;  // (+ alignment to 1024)
+};
+static_assert(PrCfg<128>::SMEM <= (int)kMaxDynSmem, "shared memory of the prompt kernel");
+
+// D[tmem] (+)= A[tmem] * B[smem]: A's 128 rows are lanes, two elements a column.
+__device__ __forceinline__ void tc_mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                          uint32_t idesc, int accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z,
+                                            void *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3, %4}], [%5];\n" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// A sequence's queries and keys; false (recorded) for offsets out of range.
+__device__ __forceinline__ bool prompt_seq(const PromptArgs &a, int i, int &q0, int &nq, int &k0,
+                                           int &nk) {
+  q0 = a.cu_q[i];
+  k0 = a.cu_k[i];
+  const int64_t q1 = a.cu_q[i + 1], k1 = a.cu_k[i + 1];
+  if (q0 < 0 || q1 < q0 || q1 > a.n_q || k0 < 0 || k1 < k0 || k1 > a.n_k) {
+    page_error(a.err, DC_ROW_RANGE, DHS_SITE_PROMPT_ATTEND);
+    nq = nk = 0;
+    return false;
+  }
+  nq = (int)(q1 - q0);
+  nk = (int)(k1 - k0);
+  return true;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPrThreads, 1)
+k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+         const __grid_constant__ CUtensorMap mv, const PromptArgs a) {
+  using C = PrCfg<D>;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  __shared__ int abort_flag, bad_values, sh_seq, sh_tile, sh_scan[kPrThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  // ---- which sequence and tile: row tiles of all sequences laid end to end, the
+  // last (longest) first, the kv heads of a tile next to one another
+  const int kvh = blockIdx.x % a.hkv;
+  const int span = 2 * a.tpt;  // tokens of a CTA
+  if (tid == 0) sh_seq = -1;
+  {
+    const int per = (a.n_seqs + kPrThreads - 1) / kPrThreads;
+    auto tiles = [&](int i) {
+      int q0, nq, k0, nk;
+      prompt_seq(a, i, q0, nq, k0, nk);
+      return (nq + span - 1) / span;
+    };
+    int s = 0;
+    for (int i = tid * per; i < min(a.n_seqs, (tid + 1) * per); ++i) s += tiles(i);
+    int x = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) sh_scan[warp] = x;
+    __syncthreads();
+    int total = 0, before = 0;
+    for (int w = 0; w < kPrThreads / 32; ++w) {
+      if (w < warp) before += sh_scan[w];
+      total += sh_scan[w];
+    }
+    const int want = total - 1 - (int)(blockIdx.x / a.hkv);
+    int at = before + x - s;  // tiles before this thread's sequences
+    if (want >= at && want < at + s) {
+      for (int i = tid * per; i < min(a.n_seqs, (tid + 1) * per); ++i) {
+        const int n = tiles(i);
+        if (want < at + n) {
+          sh_seq = i;
+          sh_tile = want - at;
+          break;
+        }
+        at += n;
+      }
+    }
+    __syncthreads();
+  }
+  if (sh_seq < 0) return;  // the grid covers the largest number of tiles there can be
+  int q0, nq, k0, nk;
+  prompt_seq(a, sh_seq, q0, nq, k0, nk);
+  const int tok0 = sh_tile * span;              // of the sequence
+  const int off = nk - nq + 1;                  // query u sees keys 0 .. off + u - 1
+  const int tok1 = tok0 + a.tpt;                // row tile 1's first token
+  const int last0 = min(tok1, nq) - 1, last1 = min(tok1 + a.tpt, nq) - 1;
+  const int all = max(0, off + max(last0, last1));           // keys any row sees
+  const int T = (all + kPrN - 1) / kPrN;
+  // this CTA's key tiles, and those of either row tile
+  const int t0 = (int)((int64_t)T * blockIdx.y / a.nsplit);
+  const int t1 = (int)((int64_t)T * (blockIdx.y + 1) / a.nsplit);
+  const int e0 = min(t1, (max(0, off + last0) + kPrN - 1) / kPrN);
+  const int e1 = last1 >= tok1 ? min(t1, (max(0, off + last1) + kPrN - 1) / kPrN) : t0;
+  const int n0 = max(0, e0 - t0), n1 = max(0, e1 - t0), nt = max(n0, n1);
+
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
+  uint64_t *q_full = bars, *full = bars + 1, *empty = full + C::SLOTS, *clean = empty + C::SLOTS;
+  uint64_t *s_full = clean + C::CLEAN, *p_full = s_full + 2, *pv_done = s_full + 4;
+  uint64_t *mma_done = s_full + 6;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_TMEM);
+  volatile int *abort_v = &abort_flag;
+  if (tid == 0) {
+    mbar_init(q_full, 1);
+    for (int i = 0; i < C::SLOTS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < C::CLEAN; ++i) mbar_init(&clean[i], 2);
+    mbar_init(mma_done, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 128);
+      mbar_init(&pv_done[i], 1);
+    }
+    abort_flag = 0;
+    bad_values = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    fence_proxy_async_smem();
+  }
+  if (warp == kMmaWarp) tmem_alloc(tmem_slot, kPrCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  auto wait = [&](uint64_t *bar, uint32_t parity, bool force = false) {
+    int spins = 0;
+    while (!mbar_try_wait(bar, parity)) {
+      if (!force && *abort_v) return;
+      if (++spins > kPrSpin) {
+        page_error(a.err, DC_TIMEOUT, DHS_SITE_PROMPT_ATTEND);
+        *abort_v = 1;
+        return;
+      }
+    }
+  };
+  // K of the n-th tile is copy 2 n of the ring, V copy 2 n + 1
+  auto slot = [&](int c) { return c % C::SLOTS; };
+  auto phase = [&](int c) { return (uint32_t)((c / C::SLOTS) & 1); };
+
+  if (warp >= kMmaWarp) {
+    if (warp == kLoadWarp) {
+      // ------------------------------------------------------------- copies
+      if (lane == 0 && nt > 0) {
+        const int ntile = n1 > 0 ? 2 : 1;
+        mbar_arrive_expect_tx(q_full, (uint32_t)(ntile * C::HALVES * a.G * a.tpt * 128));
+        for (int i = 0; i < ntile; ++i)
+          for (int h = 0; h < C::HALVES; ++h)
+            tma_load_3d(smem + i * C::TILE + h * C::HALF, &mq, h * 64, kvh * a.G,
+                        q0 + (i ? tok1 : tok0), q_full);
+        int c = 0;
+        for (; c < 2 * nt; ++c) {
+          if (c >= C::SLOTS) wait(&empty[slot(c)], phase(c) ^ 1u);
+          if (*abort_v) break;
+          mbar_arrive_expect_tx(&full[slot(c)], (uint32_t)C::TILE);
+          for (int h = 0; h < C::HALVES; ++h)
+            tma_load_3d(smem + C::OFF_KV + slot(c) * C::TILE + h * C::HALF, (c & 1) ? &mv : &mk,
+                        h * 64, kvh, k0 + (t0 + (c >> 1)) * kPrN, &full[slot(c)]);
+        }
+        // every copy has landed before the CTA ends
+        wait(q_full, 0u, true);
+        for (int i = max(0, c - C::SLOTS); i < c; ++i) wait(&full[slot(i)], phase(i), true);
+      }
+    } else if (warp == kMmaWarp) {
+      // ------------------------------------------------------------- products
+      if (lane == 0 && nt > 0) {
+        constexpr uint32_t kIdescQK = tc_idesc_bf16(kPrM, kPrN, 0, 0);
+        constexpr uint32_t kIdescPV = tc_idesc_bf16(kPrM, D, 0, 1);
+        const uint32_t sQ = smem_u32(smem), sKV = smem_u32(smem + C::OFF_KV);
+        auto qk = [&](int i, int n) {
+          const uint32_t q = sQ + i * C::TILE, k = sKV + slot(2 * n) * C::TILE;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t o = (kk >> 2) * C::HALF + (kk & 3) * 32;
+            tc_mma(tmem + i * kPrN, tc_desc_sw128(q + o, 16, 1024), tc_desc_sw128(k + o, 16, 1024),
+                   kIdescQK, kk > 0 ? 1 : 0);
+          }
+          tc_commit(&s_full[i]);
+        };
+        auto pv = [&](int i, int n) {
+          const uint32_t v = sKV + slot(2 * n + 1) * C::TILE;
+#pragma unroll
+          for (int kk = 0; kk < kPrN / 16; ++kk)
+            tc_mma_ta(tmem + 2 * kPrN + i * D, tmem + i * kPrN + kk * 8,
+                      tc_desc_sw128(v + kk * 2048, C::HALF, 1024), kIdescPV,
+                      (n > 0 || kk > 0) ? 1 : 0);
+          tc_commit(&pv_done[i]);
+        };
+        wait(q_full, 0u);
+        wait(&full[slot(0)], phase(0));
+        tc_fence_after();
+        if (n0 > 0) qk(0, 0);
+        if (n1 > 0) qk(1, 0);
+        tc_commit(&empty[slot(0)]);
+        for (int n = 0; n < nt && !*abort_v; ++n) {
+          wait(&clean[n % C::CLEAN], (uint32_t)((n / C::CLEAN) & 1));
+          for (int i = 0; i < 2; ++i) {
+            const int ni = i ? n1 : n0;
+            if (n < ni) {
+              wait(&p_full[i], (uint32_t)(n & 1));
+              tc_fence_after();
+              pv(i, n);
+            }
+            if (i == 0 && n + 1 < nt) {
+              wait(&full[slot(2 * n + 2)], phase(2 * n + 2));
+              tc_fence_after();
+            }
+            if (n + 1 < ni) qk(i, n + 1);
+          }
+          tc_commit(&empty[slot(2 * n + 1)]);
+          if (n + 1 < nt) tc_commit(&empty[slot(2 * n + 2)]);
+        }
+        tc_commit(mma_done);
+        wait(mma_done, 0u, true);
+      }
+    } else {
+      // ------------------------------------------------------------- values
+      const int common = off + tok0;  // keys that every row of the CTA sees
+      for (int n = 0; n < nt; ++n) {
+        const int c = 2 * n + 1;
+        wait(&full[slot(c)], phase(c));
+        if (__any_sync(0xffffffffu, *abort_v)) break;
+        const int r0 = max(0, common - (t0 + n) * kPrN);
+        if (r0 < kPrN) {
+          unsigned char *v = smem + C::OFF_KV + slot(c) * C::TILE;
+          const int inside = nk - (t0 + n) * kPrN;  // rows of this sequence
+          // row r's 64 dims of half h are the 128 bytes at h * HALF + r * 128
+          bool found = false;
+          for (int e = r0 * 8 + (warp - kCleanWarp) * 32 + lane; e < kPrN * 8; e += 64) {
+#pragma unroll
+            for (int h = 0; h < C::HALVES; ++h) {
+              uint4 *at = reinterpret_cast<uint4 *>(v + h * C::HALF + e * 16);
+              uint32_t w[4] = {at->x, at->y, at->z, at->w};
+              bool bad = false;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if ((w[i] & 0x7F80u) == 0x7F80u) { w[i] &= 0xFFFF0000u; bad = true; }
+                if ((w[i] & 0x7F800000u) == 0x7F800000u) { w[i] &= 0x0000FFFFu; bad = true; }
+              }
+              if (bad) {
+                *at = make_uint4(w[0], w[1], w[2], w[3]);
+                found |= (e >> 3) < inside;
+              }
+            }
+          }
+          if (found) bad_values = 1;
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&clean[n % C::CLEAN]);
+      }
+    }
+    __syncwarp();
+  } else {
+    // --------------------------------------------------------------- softmax
+    const int i = warp >> 2, m = tid & 127;
+    const int tloc = m / a.G, h = m - tloc * a.G;
+    const int tok = (i ? tok1 : tok0) + tloc;
+    const bool valid = tloc < a.tpt && tok < nq;
+    const int seen = valid ? off + tok : 0;             // may be negative
+    const int least = off + (i ? tok1 : tok0);          // of this row tile's rows
+    const int ni = i ? n1 : n0;
+    const uint32_t lrow = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lrow + i * kPrN, tO = tmem + lrow + 2 * kPrN + i * D;
+    const float sl2 = a.scale_log2;
+    float m_run = -CUDART_INF_F, l = 0.f;
+    for (int n = 0; n < ni; ++n) {
+      wait(&s_full[i], (uint32_t)(n & 1));
+      if (__any_sync(0xffffffffu, *abort_v)) break;
+      tc_fence_after();
+      uint32_t s[kPrN];
+#pragma unroll
+      for (int c = 0; c < kPrN; c += 32)
+        tmem_ld32(tS + c, *reinterpret_cast<uint32_t(*)[32]>(&s[c]));
+      tmem_wait_ld();
+      const int first = (t0 + n) * kPrN;
+      if (first + kPrN > least) {
+        const int lim = seen - first;  // columns this row sees
+#pragma unroll
+        for (int c = 0; c < kPrN; ++c)
+          if (c >= lim) s[c] = 0xFF800000u;
+      }
+      float mx0 = -CUDART_INF_F, mx1 = mx0, mx2 = mx0, mx3 = mx0;
+#pragma unroll
+      for (int c = 0; c < kPrN; c += 4) {
+        mx0 = fmaxf(mx0, __uint_as_float(s[c]));
+        mx1 = fmaxf(mx1, __uint_as_float(s[c + 1]));
+        mx2 = fmaxf(mx2, __uint_as_float(s[c + 2]));
+        mx3 = fmaxf(mx3, __uint_as_float(s[c + 3]));
+      }
+      const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * sl2;
+      const bool need = mx > m_run + kPrRescale;
+      if (__any_sync(0xffffffffu, need)) {
+        const float m_new = fmaxf(m_run, mx);
+        const float f = m_run == -CUDART_INF_F ? 0.f : ex2_approx(m_run - m_new);
+        m_run = m_new;
+        l *= f;
+        if (n > 0) {
+          wait(&pv_done[i], (uint32_t)((n - 1) & 1));
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(tO + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+            tmem_st32(tO + c, o);
+          }
+        }
+      }
+      // -inf - -inf must not arise in a row that has seen nothing
+      const float b = m_run == -CUDART_INF_F ? 0.f : -m_run;
+      float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+      for (int c = 0; c < kPrN; c += 64) {
+        uint32_t p[32];
+#pragma unroll
+        for (int x = 0; x < 32; ++x) {
+          const float u = ex2_approx(fmaf(__uint_as_float(s[c + 2 * x]), sl2, b));
+          const float w = ex2_approx(fmaf(__uint_as_float(s[c + 2 * x + 1]), sl2, b));
+          l0 += u;
+          l1 += w;
+          // rounded to bf16 for the product (at most 2^-8 of a weight); l is not
+          p[x] = pack_bf16(u, w);
+        }
+        tmem_st32(tS + c / 2, p);
+      }
+      l += l0 + l1;
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&p_full[i]);
+    }
+    if (ni > 0) {
+      wait(&pv_done[i], (uint32_t)((ni - 1) & 1));
+      tc_fence_after();
+    }
+    // every thread of the row tile's warps reads tensor memory; valid rows write
+    const int64_t row = (int64_t)(q0 + tok) * a.hq + kvh * a.G + h;
+    const bool patch = *(volatile int *)&bad_values != 0;
+    const int common = off + tok0;
+    const float inv = 1.f / l;  // only scores of -inf: 0 / 0
+    float *part = a.parts + ((int64_t)blockIdx.y * a.n_q * a.hq + row) * (D + 2);
+#pragma unroll
+    for (int c = 0; c < D; c += 32) {
+      uint32_t o[32];
+      if (ni > 0) {
+        tmem_ld32(tO + c, o);
+        tmem_wait_ld();
+      } else {
+#pragma unroll
+        for (int x = 0; x < 32; ++x) o[x] = 0u;
+      }
+      if (patch && valid) {
+        // values that were taken out, for the keys that this row sees in this CTA's tiles
+        const int lo = max(max(common, 0), t0 * kPrN), hi = min(seen, (t0 + ni) * kPrN);
+        for (int p = lo; p < hi; ++p) {
+          const uint16_t *src = a.v + (int64_t)(k0 + p) * a.vt + (int64_t)kvh * a.vh + c;
+#pragma unroll
+          for (int x = 0; x < 32; ++x) {
+            const uint32_t u = (uint32_t)src[x] << 16;
+            if ((u & 0x7F800000u) == 0x7F800000u)
+              o[x] = __float_as_uint(__uint_as_float(o[x]) + __uint_as_float(u));
+          }
+        }
+      }
+      if (!valid) continue;
+      if (a.nsplit > 1) {
+#pragma unroll
+        for (int x = 0; x < 32; x += 2)
+          *reinterpret_cast<float2 *>(part + c + x) =
+              make_float2(__uint_as_float(o[x]), __uint_as_float(o[x + 1]));
+      } else {
+#pragma unroll
+        for (int x = 0; x < 32; x += 8) {
+          uint4 w = make_uint4(0u, 0u, 0u, 0u);
+          if (seen > 0) {
+            w.x = pack_bf16(__uint_as_float(o[x]) * inv, __uint_as_float(o[x + 1]) * inv);
+            w.y = pack_bf16(__uint_as_float(o[x + 2]) * inv, __uint_as_float(o[x + 3]) * inv);
+            w.z = pack_bf16(__uint_as_float(o[x + 4]) * inv, __uint_as_float(o[x + 5]) * inv);
+            w.w = pack_bf16(__uint_as_float(o[x + 6]) * inv, __uint_as_float(o[x + 7]) * inv);
+          }
+          *reinterpret_cast<uint4 *>(a.out + row * D + c + x) = w;
+        }
+      }
+    }
+    if (valid) {
+      if (a.nsplit > 1)
+        *reinterpret_cast<float2 *>(part + D) = make_float2(m_run, l);
+      else if (a.lse)
+        a.lse[row] = m_run == CUDART_INF_F ? m_run
+                     : l == 0.f            ? -CUDART_INF_F
+                                           : (m_run + log2f(l)) * 0.69314718055994531f;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, kPrCols);
+}
+
+// Joins the parts of a row: sum_s w_s O_s / sum_s w_s l_s, w_s = 2^(m_s - max m).
+template <int D>
+__global__ void __launch_bounds__(128)
+k_prompt_join(const PromptArgs a) {
+  constexpr int V = D / 32;
   const int lane = threadIdx.x & 31;
-  if (item >= n_q * hq) return;
-  const int64_t tok = item / hq;
-  const int h = (int)(item - tok * hq), kvh = h / (hq / hkv);
-  const int i = seq_of(cu_q, n_seqs, tok);
+  const int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / 32, rows = a.n_q * a.hq;
+  pdl_wait();
+  if (row >= rows) return;
+  const int64_t tok = row / a.hq;
+  const int i = seq_of(a.cu_q, a.n_seqs, tok);
   if (i < 0) return;
-  const int64_t k0 = cu_k[i], k1 = cu_k[i + 1];
-  if (k0 < 0 || k1 < k0 || k1 > n_k || cu_q[i + 1] > n_q || cu_q[i] < 0) {
-    page_error(err, DC_ROW_RANGE, DHS_SITE_PROMPT_ATTEND);
-    return;
+  int q0, nq, k0, nk;
+  if (!prompt_seq(a, i, q0, nq, k0, nk) || tok < q0 || tok >= q0 + nq) return;
+  const bool some = nk - nq + (int)(tok - q0) + 1 > 0;
+  const float *p = a.parts + row * (D + 2);
+  const int64_t step = rows * (D + 2);
+  float top = -CUDART_INF_F, den = 0.f, acc[V];
+#pragma unroll
+  for (int x = 0; x < V; ++x) acc[x] = 0.f;
+  for (int s = 0; s < a.nsplit; ++s) top = fmaxf(top, p[s * step + D]);
+#pragma unroll 4
+  for (int s = 0; s < a.nsplit; ++s) {
+    const float2 ml = *reinterpret_cast<const float2 *>(p + s * step + D);
+    const float f = ml.x == -CUDART_INF_F ? (ml.y != ml.y ? 1.f : 0.f) : ex2_approx(ml.x - top);
+    den += ml.y * f;
+#pragma unroll
+    for (int x = 0; x < V; x += 2) {
+      const float2 o = *reinterpret_cast<const float2 *>(p + s * step + lane * V + x);
+      acc[x] += o.x * f;
+      acc[x + 1] += o.y * f;
+    }
   }
-  const int64_t seen = (k1 - k0) - (cu_q[i + 1] - tok) + 1;
-  float qv[D / 32], o[D / 32], m = -CUDART_INF_F, l = 0.f;
+  const float inv = 1.f / den;
 #pragma unroll
-  for (int e = 0; e < D / 32; ++e) {
-    qv[e] = __bfloat162float(q[tok * st.qt + h * st.qh + lane * (D / 32) + e]);
-    o[e] = 0.f;
-  }
-  for (int64_t t = k0; t < k0 + seen; ++t) {
-    const __nv_bfloat16 *kr = k + t * st.kt + kvh * st.kh + lane * (D / 32);
-    const __nv_bfloat16 *vr = v + t * st.vt + kvh * st.vh + lane * (D / 32);
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) s = fmaf(qv[e], __bfloat162float(kr[e]), s);
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-    s *= scale_log2;
-    const float mn = fmaxf(m, s), base = mn == -CUDART_INF_F ? 0.f : mn;
-    const float f = exp2f(m - base), p = exp2f(s - base);
-    m = mn;
-    l = l * f + p;
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) o[e] = o[e] * f + p * __bfloat162float(vr[e]);
-  }
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e)
-    out[item * D + lane * (D / 32) + e] = __float2bfloat16(seen <= 0 ? 0.f : o[e] / l);
-  if (lse && lane == 0)
-    lse[item] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994531f;
+  for (int x = 0; x < V; x += 2)
+    *reinterpret_cast<uint32_t *>(a.out + row * D + lane * V + x) =
+        some ? pack_bf16(acc[x] * inv, acc[x + 1] * inv) : 0u;
+  if (a.lse && lane == 0)
+    a.lse[row] = top == CUDART_INF_F ? top
+                 : den == 0.f        ? -CUDART_INF_F
+                                     : (top + log2f(den)) * 0.69314718055994531f;
 }
 
 bool prompt_args(int64_t n_q, int64_t n_k, int32_t n_seqs, int32_t hq, int32_t hkv, int32_t d) {
@@ -70,13 +531,74 @@ bool prompt_args(int64_t n_q, int64_t n_k, int32_t n_seqs, int32_t hq, int32_t h
          (d == 64 || d == 128);
 }
 
+// Most row-tile pairs n_q tokens of n_seqs sequences can make.
+int64_t prompt_tiles(int64_t n_q, int32_t n_seqs, int G) {
+  const int64_t span = 2 * (128 / G);
+  return n_q / span + std::min<int64_t>(n_seqs, n_q);
+}
+
+// Key splits: when the row tiles leave SMs idle, as many as fill them, as long as a
+// split keeps four key tiles of an average sequence (a split costs the write and
+// read of its part, 4 D bytes a row).
+int prompt_splits(int64_t n_q, int64_t n_k, int32_t n_seqs, int hq, int hkv, int sms) {
+  if (n_q == 0 || n_seqs == 0) return 1;
+  const int64_t ctas = prompt_tiles(n_q, n_seqs, hq / hkv) * hkv;
+  const int64_t fill = sms / std::max<int64_t>(1, ctas);
+  const int64_t room = n_k / n_seqs / (4 * kPrN);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(fill, room), 64));
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                 const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                 const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor-map encoder (looked up once), or nullptr.
+EncodeTiled encoder() {
+  static std::atomic<void *> known{nullptr};
+  void *f = known.load(std::memory_order_acquire);
+  if (!f) {
+    cudaDriverEntryPointQueryResult res;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &res) != cudaSuccess ||
+        res != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      return nullptr;
+    }
+    known.store(f, std::memory_order_release);
+  }
+  return reinterpret_cast<EncodeTiled>(f);
+}
+
+// [tokens][heads][d] of bf16, boxes of 64 dims x box_heads x box_tokens.
+bool encode(EncodeTiled f, CUtensorMap *m, const void *p, int64_t tokens, int heads, int d,
+            int64_t st, int64_t sh, int box_heads, int box_tokens) {
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)sh * 2, (cuuint64_t)st * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+  const cuuint32_t one[3] = {1, 1, 1};
+  return f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims, strides, box, one,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 }  // namespace dhs
 
 extern "C" int64_t dhs_prompt_attend_workspace(int64_t n_q, int64_t n_k, int32_t n_seqs,
                                                int32_t q_heads, int32_t kv_heads,
                                                int32_t head_dim) {
-  return dhs::prompt_args(n_q, n_k, n_seqs, q_heads, kv_heads, head_dim) ? 0 : -1;
+  using namespace dhs;
+  if (!prompt_args(n_q, n_k, n_seqs, q_heads, kv_heads, head_dim)) return -1;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return -1;
+  }
+  const int sms = device_sms(dev);
+  if (sms < 1) return -1;
+  const int n = prompt_splits(n_q, n_k, n_seqs, q_heads, kv_heads, sms);
+  return n > 1 ? (int64_t)n * n_q * q_heads * (head_dim + 2) * 4 : 0;
 }
 
 extern "C" int dhs_prompt_attend(const void *q, const void *k, const void *v,
@@ -95,24 +617,67 @@ extern "C" int dhs_prompt_attend(const void *q, const void *k, const void *v,
       ((uintptr_t)workspace & 15u))
     return DHS_ERR_INVALID;
   const int64_t d = head_dim;
-  PromptStrides st = {q_heads * d, d, kv_heads * d, d, kv_heads * d, d};
-  if (strides) {
-    for (int i = 0; i < 6; ++i)
-      if (strides[i] < 0 || strides[i] % 8 || strides[i] > ((int64_t)1 << 38)) return DHS_ERR_INVALID;
-    st = {strides[0], strides[1], strides[2], strides[3], strides[4], strides[5]};
+  int64_t st[6] = {q_heads * d, d, kv_heads * d, d, kv_heads * d, d};
+  if (strides)
+    for (int i = 0; i < 6; ++i) {
+      const bool used = (i & 1) ? (i == 1 ? q_heads : kv_heads) > 1 : (i == 0 ? n_q : n_k) > 1;
+      if (strides[i] < 0 || strides[i] % 8 || strides[i] >= ((int64_t)1 << 38) ||
+          (used && strides[i] < d))
+        return DHS_ERR_INVALID;
+      if (used) st[i] = strides[i];
+    }
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return DHS_ERR_CUDA;
   }
-  (void)workspace;
+  const int sms = device_sms(dev);
+  EncodeTiled enc = encoder();
+  if (sms < 1 || !enc) return DHS_ERR_CUDA;
+  PromptArgs a;
+  a.v = static_cast<const uint16_t *>(v);
+  a.vt = st[4];
+  a.vh = st[5];
+  a.cu_q = cu_q;
+  a.cu_k = cu_k;
+  a.out = static_cast<uint16_t *>(out);
+  a.lse = lse;
+  a.parts = static_cast<float *>(workspace);
+  a.err = err;
+  a.n_q = n_q;
+  a.n_k = n_k;
+  a.n_seqs = n_seqs;
+  a.hq = q_heads;
+  a.hkv = kv_heads;
+  a.G = q_heads / kv_heads;
+  a.tpt = kPrM / a.G;
+  a.nsplit = prompt_splits(n_q, n_k, n_seqs, q_heads, kv_heads, sms);
+  a.scale_log2 = (scale == 0.f ? 1.f / sqrtf((float)d) : scale) * 1.4426950408889634f;
+  if (a.nsplit > 1 &&
+      (!workspace || workspace_bytes < (int64_t)a.nsplit * n_q * q_heads * (d + 2) * 4))
+    return DHS_ERR_INVALID;
+  const int64_t ctas = prompt_tiles(n_q, n_seqs, a.G) * kv_heads;
+  if (ctas > INT32_MAX) return DHS_ERR_CAPACITY;
+  CUtensorMap mq = {}, mk = {}, mv = {};
+  if (!encode(enc, &mq, q, n_q, q_heads, (int)d, st[0], st[1], a.G, a.tpt)) return DHS_ERR_INVALID;
+  if (n_k > 0 && (!encode(enc, &mk, k, n_k, kv_heads, (int)d, st[2], st[3], 1, kPrN) ||
+                  !encode(enc, &mv, v, n_k, kv_heads, (int)d, st[4], st[5], 1, kPrN)))
+    return DHS_ERR_INVALID;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const float sl2 = (scale == 0.f ? 1.f / sqrtf((float)d) : scale) * 1.4426950408889634f;
-  const int64_t items = n_q * q_heads;
-  auto go = [&](auto kern) {
-    return launch_prio(kern, dim3((unsigned)((items + kPrWarps - 1) / kPrWarps)),
-                       dim3(kPrWarps * 32), 0, s, static_cast<const __nv_bfloat16 *>(q),
-                       static_cast<const __nv_bfloat16 *>(k),
-                       static_cast<const __nv_bfloat16 *>(v), st, n_q, n_k, cu_q, cu_k, n_seqs,
-                       q_heads, kv_heads, sl2, static_cast<__nv_bfloat16 *>(out), lse, err);
+  auto go = [&](auto dim) -> cudaError_t {
+    constexpr int D = decltype(dim)::value;
+    static DeviceSmem granted;
+    cudaError_t e = granted.ensure(k_prompt<D>, PrCfg<D>::SMEM, dev);
+    if (e == cudaSuccess)
+      e = launch_prio(k_prompt<D>, dim3((unsigned)ctas, (unsigned)a.nsplit), dim3(kPrThreads),
+                      (size_t)PrCfg<D>::SMEM, s, mq, mk, mv, a);
+    if (e == cudaSuccess && a.nsplit > 1)
+      e = launch_pdl(k_prompt_join<D>, dim3((unsigned)((n_q * q_heads + 3) / 4)), dim3(128), 0, s,
+                     a);
+    return e;
   };
-  const cudaError_t e = d == 128 ? go(k_prompt<128>) : go(k_prompt<64>);
+  const cudaError_t e = d == 128 ? go(std::integral_constant<int, 128>())
+                                 : go(std::integral_constant<int, 64>());
   if (e != cudaSuccess) {
     cudaGetLastError();
     return DHS_ERR_CUDA;
