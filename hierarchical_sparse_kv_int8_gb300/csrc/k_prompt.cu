@@ -7,18 +7,20 @@
 // tpt positions wide.  A CTA owns two such row tiles (2 tpt consecutive tokens of
 // one sequence) and walks the keys they see in tiles of 128:
 //   S_i = Q_i K^T (M 128, N 128, K D), P_i = 2^(c S_i - m_i), O_i += P_i V.
-// Warps 0-3 and 4-7 are the softmax threads of row tile 0 and 1, one row each:
-// they read S from tensor memory, keep the row's maximum m (O is rescaled only
-// when it grows by more than kRescale) and its sum l in 32 bits, and write P in
-// bf16 over S in tensor memory, from where the second product reads it.  One thread of
-// warp 8 issues all MMAs in the order  P0 V(t), Q0 K(t+1), P1 V(t), Q1 K(t+1):
-// while one row tile's softmax runs, the tensor cores work for the other.  S_i(t +
-// 1) overwrites P_i(t), which the MMA issued just before it has read: MMAs of a
-// thread run in order.  One thread of warp 9 fetches Q and the ring of K and V
+// Warps 0-7 and 8-15 are the softmax threads of row tile 0 and 1, two threads a
+// row, each with half of a tile's columns: they read S from tensor memory, keep the
+// row's maximum m (O is rescaled only when it grows by more than kPrRescale) and its
+// sum l in 32 bits, and write P in bf16 over S in tensor memory, from where the second
+// product reads it.  One thread of warp 16 issues all MMAs in the order  P0 V(t), Q0
+// K(t+1), P1 V(t), Q1 K(t+1): while one row tile's softmax runs, the tensor cores
+// work for the other.  S_i(t + 1) overwrites P_i(t), which the MMA issued just before
+// it has read: MMAs of a thread run in order.  (With one thread a row the softmax of
+// a tile took 2500 cycles against 1300 of the other tile's products, and bound the
+// kernel: 1.02 ms for 16384 tokens of 16 heads.)  One thread of warp 17 fetches Q and the ring of K and V
 // tiles with tiled TMA copies in the 128-byte-swizzled layout.
 //
 // A weight is 0 where a row does not see a key, but 0 times an infinity or a NaN is
-// not 0: warps 10-11 go over the value tiles at the causal edge and the sequence's
+// not 0: warps 18-19 go over the value tiles at the causal edge and the sequence's
 // end before they are used, set what is not finite there to 0, and remember it; the
 // rows that do see such a value get it added at the end, value by value.
 //
@@ -39,9 +41,10 @@
 namespace dhs {
 namespace {
 
-constexpr int kPrThreads = 384;
-constexpr int kPrM = 128, kPrN = 128;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kCleanWarp = 10;
+constexpr int kPrSoftmax = 512;  // two row tiles, two warpgroups each
+constexpr int kPrThreads = kPrSoftmax + 128;
+constexpr int kPrM = 128, kPrN = 128, kPrH = kPrN / 2;
+constexpr int kMmaWarp = 16, kLoadWarp = 17, kCleanWarp = 18;
 constexpr int kPrSpin = 1 << 20;
 constexpr float kPrRescale = 8.f;
 constexpr uint32_t kPrCols = 512;  // S0, S1 (P over them), O0, O1
@@ -65,21 +68,43 @@ struct PrCfg {
   static constexpr int HALF = 128 * 128;            // 64 dims of its 128 rows
   static constexpr int SLOTS = D == 128 ? 5 : 8;    // K and V tiles in flight
   static constexpr int OFF_KV = 2 * TILE;
-  static constexpr int OFF_BAR = OFF_KV + SLOTS * TILE;
+  static constexpr int OFF_RED = OFF_KV + SLOTS * TILE;  // float [2 tiles][2 halves][128]
+  static constexpr int OFF_BAR = OFF_RED + 2 * 2 * 128 * 4;
   static constexpr int CLEAN = 4;                   // value tiles gone over and not yet used, at most
   static constexpr int BARS = 2 + 2 * SLOTS + CLEAN + 6;
   static constexpr int OFF_TMEM = OFF_BAR + BARS * 8;
-  static constexpr int SMEM = OFF_TMEM + 16 + 1024;  // (+ alignment to 1024)
+  static constexpr int OFF_MISC = OFF_TMEM + 16;    // int [4 + warps]
+  static constexpr int SMEM = OFF_MISC + (4 + kPrThreads / 32) * 4;
 };
-static_assert(PrCfg<128>::SMEM <= (int)kMaxDynSmem, "shared memory of the prompt kernel");
+static_assert(PrCfg<128>::SMEM <= 227 * 1024, "shared memory of the prompt kernel");
 
-// D[tmem] (+)= A[tmem] * B[smem]: A's 128 rows are lanes, two elements a column.
-__device__ __forceinline__ void tc_mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                          uint32_t idesc, int accumulate) {
+// The MMAs of this file are issued by a whole warp whose elected lane carries
+// them out: the operands are then warp-uniform values that the compiler keeps
+// where the instruction reads them.  (Issued from a branch of one lane, each MMA
+// took over 70 cycles of moves, more than the 64 it runs for.)
+// D[tmem] (+)= A[smem] * B[smem]
+__device__ __forceinline__ void warp_mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                         uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "{\n .reg .pred e, p;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem]: A's 128 rows are lanes, two elements a column.
+__device__ __forceinline__ void warp_mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred e, p;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void warp_commit(void *bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+          smem_u32(bar))
       : "memory");
 }
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z,
@@ -89,6 +114,19 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, i
       "[%1, {%2, %3, %4}], [%5];\n" ::"r"(smem_u32(dst)),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
+}
+
+// Barrier `id` over `count` threads that also says whether any of them had `on`.
+__device__ __forceinline__ bool named_or(int id, int count, bool on) {
+  uint32_t r;
+  __syncwarp();
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 q, %3, 0;\n barrier.red.or.pred p, %1, %2, q;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(r)
+      : "r"(id), "r"(count), "r"((uint32_t)on)
+      : "memory");
+  return r != 0;
 }
 
 // A sequence's queries and keys; false (recorded) for offsets out of range.
@@ -112,9 +150,15 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
          const __grid_constant__ CUtensorMap mv, const PromptArgs a) {
   using C = PrCfg<D>;
-  extern __shared__ __align__(1024) unsigned char smem_raw[];
-  unsigned char *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  __shared__ int abort_flag, bad_values, sh_seq, sh_tile, sh_scan[kPrThreads / 32];
+  // no static shared memory: the dynamic part starts on the boundary it asks for
+  extern __shared__ __align__(1024) unsigned char smem[];
+  int *misc = reinterpret_cast<int *>(smem + C::OFF_MISC);
+  int &abort_flag = misc[0], &bad_values = misc[1], &sh_seq = misc[2], &sh_tile = misc[3];
+  int *sh_scan = misc + 4;
+  if ((smem_u32(smem) & 1023u) != 0u) {  // (the swizzle pattern follows address bits)
+    page_error(a.err, DC_CAPACITY, DHS_SITE_PROMPT_ATTEND);
+    return;
+  }
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   // ---- which sequence and tile: row tiles of all sequences laid end to end, the
@@ -191,7 +235,7 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
     mbar_init(mma_done, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
+      mbar_init(&p_full[i], kPrSoftmax / 64);  // one arrival per warp
       mbar_init(&pv_done[i], 1);
     }
     abort_flag = 0;
@@ -203,7 +247,9 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  // All 512 columns are this CTA's, so they start at column 0 (lane 0), and the
+  // addresses below are constants.
+  constexpr uint32_t tmem = 0u;
 
   auto wait = [&](uint64_t *bar, uint32_t parity, bool force = false) {
     int spins = 0;
@@ -245,54 +291,57 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
       }
     } else if (warp == kMmaWarp) {
       // ------------------------------------------------------------- products
-      if (lane == 0 && nt > 0) {
+      if (nt > 0) {
         constexpr uint32_t kIdescQK = tc_idesc_bf16(kPrM, kPrN, 0, 0);
         constexpr uint32_t kIdescPV = tc_idesc_bf16(kPrM, D, 0, 1);
         const uint32_t sQ = smem_u32(smem), sKV = smem_u32(smem + C::OFF_KV);
         auto qk = [&](int i, int n) {
-          const uint32_t q = sQ + i * C::TILE, k = sKV + slot(2 * n) * C::TILE;
+          const uint64_t q = tc_desc_sw128(sQ + i * C::TILE, 16, 1024);
+          const uint64_t k = tc_desc_sw128(sKV + slot(2 * n) * C::TILE, 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t o = (kk >> 2) * C::HALF + (kk & 3) * 32;
-            tc_mma(tmem + i * kPrN, tc_desc_sw128(q + o, 16, 1024), tc_desc_sw128(k + o, 16, 1024),
-                   kIdescQK, kk > 0 ? 1 : 0);
+            const uint32_t o = ((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4;
+            warp_mma(i * kPrN, q + o, k + o, kIdescQK, kk);
           }
-          tc_commit(&s_full[i]);
+          warp_commit(&s_full[i]);
         };
         auto pv = [&](int i, int n) {
-          const uint32_t v = sKV + slot(2 * n + 1) * C::TILE;
+          const uint64_t v = tc_desc_sw128(sKV + slot(2 * n + 1) * C::TILE, C::HALF, 1024);
 #pragma unroll
           for (int kk = 0; kk < kPrN / 16; ++kk)
-            tc_mma_ta(tmem + 2 * kPrN + i * D, tmem + i * kPrN + kk * 8,
-                      tc_desc_sw128(v + kk * 2048, C::HALF, 1024), kIdescPV,
-                      (n > 0 || kk > 0) ? 1 : 0);
-          tc_commit(&pv_done[i]);
+            warp_mma_ta(2 * kPrN + i * D, i * kPrN + kk * 8, v + kk * 128, kIdescPV, n | kk);
+          warp_commit(&pv_done[i]);
         };
         wait(q_full, 0u);
         wait(&full[slot(0)], phase(0));
+        __syncwarp();
         tc_fence_after();
         if (n0 > 0) qk(0, 0);
         if (n1 > 0) qk(1, 0);
-        tc_commit(&empty[slot(0)]);
-        for (int n = 0; n < nt && !*abort_v; ++n) {
+        warp_commit(&empty[slot(0)]);
+        for (int n = 0; n < nt && !__any_sync(0xffffffffu, *abort_v); ++n) {
           wait(&clean[n % C::CLEAN], (uint32_t)((n / C::CLEAN) & 1));
+          __syncwarp();
+#pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int ni = i ? n1 : n0;
             if (n < ni) {
               wait(&p_full[i], (uint32_t)(n & 1));
+              __syncwarp();
               tc_fence_after();
               pv(i, n);
             }
-            if (i == 0 && n + 1 < nt) {
+            if (n + 1 < ni) {
               wait(&full[slot(2 * n + 2)], phase(2 * n + 2));
+              __syncwarp();
               tc_fence_after();
+              qk(i, n + 1);
             }
-            if (n + 1 < ni) qk(i, n + 1);
           }
-          tc_commit(&empty[slot(2 * n + 1)]);
-          if (n + 1 < nt) tc_commit(&empty[slot(2 * n + 2)]);
+          warp_commit(&empty[slot(2 * n + 1)]);
+          if (n + 1 < nt) warp_commit(&empty[slot(2 * n + 2)]);
         }
-        tc_commit(mma_done);
+        warp_commit(mma_done);
         wait(mma_done, 0u, true);
       }
     } else {
@@ -335,7 +384,7 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
     __syncwarp();
   } else {
     // --------------------------------------------------------------- softmax
-    const int i = warp >> 2, m = tid & 127;
+    const int i = warp >> 3, hg = (warp >> 2) & 1, m = tid & 127;
     const int tloc = m / a.G, h = m - tloc * a.G;
     const int tok = (i ? tok1 : tok0) + tloc;
     const bool valid = tloc < a.tpt && tok < nq;
@@ -343,78 +392,95 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
     const int least = off + (i ? tok1 : tok0);          // of this row tile's rows
     const int ni = i ? n1 : n0;
     const uint32_t lrow = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lrow + i * kPrN, tO = tmem + lrow + 2 * kPrN + i * D;
+    // this thread's half of the row's scores, and of its output columns
+    const uint32_t tS = tmem + lrow + i * kPrN, tO = tmem + lrow + 2 * kPrN + i * D + hg * (D / 2);
+    float *red = reinterpret_cast<float *>(smem + C::OFF_RED) + i * 256;
     const float sl2 = a.scale_log2;
     float m_run = -CUDART_INF_F, l = 0.f;
+    // (no early exit: every thread of a row tile meets the others' barriers, also
+    // after a wait has run out)
     for (int n = 0; n < ni; ++n) {
       wait(&s_full[i], (uint32_t)(n & 1));
-      if (__any_sync(0xffffffffu, *abort_v)) break;
+      __syncwarp();
       tc_fence_after();
-      uint32_t s[kPrN];
-#pragma unroll
-      for (int c = 0; c < kPrN; c += 32)
-        tmem_ld32(tS + c, *reinterpret_cast<uint32_t(*)[32]>(&s[c]));
+      uint32_t s0[32], s1[32];
+      tmem_ld32(tS + hg * kPrH, s0);
+      tmem_ld32(tS + hg * kPrH + 32, s1);
       tmem_wait_ld();
       const int first = (t0 + n) * kPrN;
       if (first + kPrN > least) {
-        const int lim = seen - first;  // columns this row sees
+        const int lim = seen - first - hg * kPrH;  // columns this row sees
 #pragma unroll
-        for (int c = 0; c < kPrN; ++c)
-          if (c >= lim) s[c] = 0xFF800000u;
+        for (int c = 0; c < 32; ++c) {
+          if (c >= lim) s0[c] = 0xFF800000u;
+          if (c + 32 >= lim) s1[c] = 0xFF800000u;
+        }
       }
-      float mx0 = -CUDART_INF_F, mx1 = mx0, mx2 = mx0, mx3 = mx0;
+      float mx0 = -CUDART_INF_F, mx1 = mx0;
 #pragma unroll
-      for (int c = 0; c < kPrN; c += 4) {
-        mx0 = fmaxf(mx0, __uint_as_float(s[c]));
-        mx1 = fmaxf(mx1, __uint_as_float(s[c + 1]));
-        mx2 = fmaxf(mx2, __uint_as_float(s[c + 2]));
-        mx3 = fmaxf(mx3, __uint_as_float(s[c + 3]));
+      for (int c = 0; c < 32; c += 2) {  // (three-operand maxima)
+        mx0 = fmaxf(mx0, fmaxf(__uint_as_float(s0[c]), __uint_as_float(s0[c + 1])));
+        mx1 = fmaxf(mx1, fmaxf(__uint_as_float(s1[c]), __uint_as_float(s1[c + 1])));
       }
-      const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * sl2;
-      const bool need = mx > m_run + kPrRescale;
-      if (__any_sync(0xffffffffu, need)) {
-        const float m_new = fmaxf(m_run, mx);
-        const float f = m_run == -CUDART_INF_F ? 0.f : ex2_approx(m_run - m_new);
-        m_run = m_new;
-        l *= f;
-        if (n > 0) {
-          wait(&pv_done[i], (uint32_t)((n - 1) & 1));
-          tc_fence_after();
+      float mx = fmaxf(mx0, mx1) * sl2;
+      // The barrier also separates the halves' reads of S from their writes of P.
+      // Rows whose maximum grew much are rare: only then do the halves of every row
+      // exchange their maxima.
+      if (named_or(1 + i, 256, mx > m_run + kPrRescale)) {
+        red[hg * 128 + m] = mx;
+        named_sync(1 + i, 256);
+        mx = fmaxf(mx, red[(hg ^ 1) * 128 + m]);
+        named_sync(1 + i, 256);
+        if (__any_sync(0xffffffffu, mx > m_run + kPrRescale)) {
+          const float m_new = fmaxf(m_run, mx);
+          const float f = m_run == -CUDART_INF_F ? 0.f : ex2_approx(m_run - m_new);
+          m_run = m_new;
+          l *= f;
+          if (n > 0) {  // (the product of tile n - 1 was complete before S of tile n)
+#pragma unroll 1
+            for (int c = 0; c < D / 2; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(tO + c, o);
+              tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(tO + c, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-            tmem_st32(tO + c, o);
+              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+              tmem_st16(tO + c, o);
+            }
           }
         }
       }
       // -inf - -inf must not arise in a row that has seen nothing
       const float b = m_run == -CUDART_INF_F ? 0.f : -m_run;
       float l0 = 0.f, l1 = 0.f;
+      uint32_t p[16];
+      // weights are rounded to bf16 for the product (at most 2^-8 of each); l is not
+      auto weights = [&](const uint32_t(&s)[32]) {
 #pragma unroll
-      for (int c = 0; c < kPrN; c += 64) {
-        uint32_t p[32];
-#pragma unroll
-        for (int x = 0; x < 32; ++x) {
-          const float u = ex2_approx(fmaf(__uint_as_float(s[c + 2 * x]), sl2, b));
-          const float w = ex2_approx(fmaf(__uint_as_float(s[c + 2 * x + 1]), sl2, b));
+        for (int x = 0; x < 16; ++x) {
+          const float u = ex2_approx(fmaf(__uint_as_float(s[2 * x]), sl2, b));
+          const float w = ex2_approx(fmaf(__uint_as_float(s[2 * x + 1]), sl2, b));
           l0 += u;
           l1 += w;
-          // rounded to bf16 for the product (at most 2^-8 of a weight); l is not
           p[x] = pack_bf16(u, w);
         }
-        tmem_st32(tS + c / 2, p);
-      }
+      };
+      weights(s0);
+      tmem_st16(tS + hg * (kPrH / 2), p);
+      weights(s1);
+      tmem_st16(tS + hg * (kPrH / 2) + 16, p);
       l += l0 + l1;
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(&p_full[i]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[i]);
     }
+    // the row's sum over both halves
+    red[hg * 128 + m] = l;
+    named_sync(1 + i, 256);
+    l += red[(hg ^ 1) * 128 + m];
     if (ni > 0) {
       wait(&pv_done[i], (uint32_t)((ni - 1) & 1));
+      __syncwarp();
       tc_fence_after();
     }
     // every thread of the row tile's warps reads tensor memory; valid rows write
@@ -423,23 +489,24 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
     const int common = off + tok0;
     const float inv = 1.f / l;  // only scores of -inf: 0 / 0
     float *part = a.parts + ((int64_t)blockIdx.y * a.n_q * a.hq + row) * (D + 2);
-#pragma unroll
-    for (int c = 0; c < D; c += 32) {
-      uint32_t o[32];
+#pragma unroll 1
+    for (int c = 0; c < D / 2; c += 16) {
+      const int col = hg * (D / 2) + c;
+      uint32_t o[16];
       if (ni > 0) {
-        tmem_ld32(tO + c, o);
+        tmem_ld16(tO + c, o);
         tmem_wait_ld();
       } else {
 #pragma unroll
-        for (int x = 0; x < 32; ++x) o[x] = 0u;
+        for (int x = 0; x < 16; ++x) o[x] = 0u;
       }
       if (patch && valid) {
         // values that were taken out, for the keys that this row sees in this CTA's tiles
         const int lo = max(max(common, 0), t0 * kPrN), hi = min(seen, (t0 + ni) * kPrN);
         for (int p = lo; p < hi; ++p) {
-          const uint16_t *src = a.v + (int64_t)(k0 + p) * a.vt + (int64_t)kvh * a.vh + c;
+          const uint16_t *src = a.v + (int64_t)(k0 + p) * a.vt + (int64_t)kvh * a.vh + col;
 #pragma unroll
-          for (int x = 0; x < 32; ++x) {
+          for (int x = 0; x < 16; ++x) {
             const uint32_t u = (uint32_t)src[x] << 16;
             if ((u & 0x7F800000u) == 0x7F800000u)
               o[x] = __float_as_uint(__uint_as_float(o[x]) + __uint_as_float(u));
@@ -449,12 +516,12 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
       if (!valid) continue;
       if (a.nsplit > 1) {
 #pragma unroll
-        for (int x = 0; x < 32; x += 2)
-          *reinterpret_cast<float2 *>(part + c + x) =
+        for (int x = 0; x < 16; x += 2)
+          *reinterpret_cast<float2 *>(part + col + x) =
               make_float2(__uint_as_float(o[x]), __uint_as_float(o[x + 1]));
       } else {
 #pragma unroll
-        for (int x = 0; x < 32; x += 8) {
+        for (int x = 0; x < 16; x += 8) {
           uint4 w = make_uint4(0u, 0u, 0u, 0u);
           if (seen > 0) {
             w.x = pack_bf16(__uint_as_float(o[x]) * inv, __uint_as_float(o[x + 1]) * inv);
@@ -462,11 +529,11 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
             w.z = pack_bf16(__uint_as_float(o[x + 4]) * inv, __uint_as_float(o[x + 5]) * inv);
             w.w = pack_bf16(__uint_as_float(o[x + 6]) * inv, __uint_as_float(o[x + 7]) * inv);
           }
-          *reinterpret_cast<uint4 *>(a.out + row * D + c + x) = w;
+          *reinterpret_cast<uint4 *>(a.out + row * D + col + x) = w;
         }
       }
     }
-    if (valid) {
+    if (valid && hg == 0) {
       if (a.nsplit > 1)
         *reinterpret_cast<float2 *>(part + D) = make_float2(m_run, l);
       else if (a.lse)
@@ -478,7 +545,7 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, kPrCols);
+  if (warp == kMmaWarp) tmem_dealloc(*tmem_slot, kPrCols);
 }
 
 // Joins the parts of a row: sum_s w_s O_s / sum_s w_s l_s, w_s = 2^(m_s - max m).
