@@ -73,8 +73,8 @@ struct PrCfg {
   static constexpr int CLEAN = 4;                   // value tiles gone over and not yet used, at most
   static constexpr int BARS = 2 + 2 * SLOTS + CLEAN + 6;
   static constexpr int OFF_TMEM = OFF_BAR + BARS * 8;
-  static constexpr int OFF_MISC = OFF_TMEM + 16;    // int [4 + warps]
-  static constexpr int SMEM = OFF_MISC + (4 + kPrThreads / 32) * 4;
+  static constexpr int OFF_MISC = OFF_TMEM + 16;    // int [2]
+  static constexpr int SMEM = OFF_MISC + 16;
 };
 static_assert(PrCfg<128>::SMEM <= 227 * 1024, "shared memory of the prompt kernel");
 
@@ -116,6 +116,10 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, i
       : "memory");
 }
 
+__device__ __forceinline__ void tma_prefetch(const CUtensorMap *map) {
+  asm volatile("prefetch.tensormap [%0];\n" ::"l"(map) : "memory");
+}
+
 // Barrier `id` over `count` threads that also says whether any of them had `on`.
 __device__ __forceinline__ bool named_or(int id, int count, bool on) {
   uint32_t r;
@@ -153,71 +157,12 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
   // no static shared memory: the dynamic part starts on the boundary it asks for
   extern __shared__ __align__(1024) unsigned char smem[];
   int *misc = reinterpret_cast<int *>(smem + C::OFF_MISC);
-  int &abort_flag = misc[0], &bad_values = misc[1], &sh_seq = misc[2], &sh_tile = misc[3];
-  int *sh_scan = misc + 4;
+  int &abort_flag = misc[0], &bad_values = misc[1];
   if ((smem_u32(smem) & 1023u) != 0u) {  // (the swizzle pattern follows address bits)
     page_error(a.err, DC_CAPACITY, DHS_SITE_PROMPT_ATTEND);
     return;
   }
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-
-  // ---- which sequence and tile: row tiles of all sequences laid end to end, the
-  // last (longest) first, the kv heads of a tile next to one another
-  const int kvh = blockIdx.x % a.hkv;
-  const int span = 2 * a.tpt;  // tokens of a CTA
-  if (tid == 0) sh_seq = -1;
-  {
-    const int per = (a.n_seqs + kPrThreads - 1) / kPrThreads;
-    auto tiles = [&](int i) {
-      int q0, nq, k0, nk;
-      prompt_seq(a, i, q0, nq, k0, nk);
-      return (nq + span - 1) / span;
-    };
-    int s = 0;
-    for (int i = tid * per; i < min(a.n_seqs, (tid + 1) * per); ++i) s += tiles(i);
-    int x = s;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) sh_scan[warp] = x;
-    __syncthreads();
-    int total = 0, before = 0;
-    for (int w = 0; w < kPrThreads / 32; ++w) {
-      if (w < warp) before += sh_scan[w];
-      total += sh_scan[w];
-    }
-    const int want = total - 1 - (int)(blockIdx.x / a.hkv);
-    int at = before + x - s;  // tiles before this thread's sequences
-    if (want >= at && want < at + s) {
-      for (int i = tid * per; i < min(a.n_seqs, (tid + 1) * per); ++i) {
-        const int n = tiles(i);
-        if (want < at + n) {
-          sh_seq = i;
-          sh_tile = want - at;
-          break;
-        }
-        at += n;
-      }
-    }
-    __syncthreads();
-  }
-  if (sh_seq < 0) return;  // the grid covers the largest number of tiles there can be
-  int q0, nq, k0, nk;
-  prompt_seq(a, sh_seq, q0, nq, k0, nk);
-  const int tok0 = sh_tile * span;              // of the sequence
-  const int off = nk - nq + 1;                  // query u sees keys 0 .. off + u - 1
-  const int tok1 = tok0 + a.tpt;                // row tile 1's first token
-  const int last0 = min(tok1, nq) - 1, last1 = min(tok1 + a.tpt, nq) - 1;
-  const int all = max(0, off + max(last0, last1));           // keys any row sees
-  const int T = (all + kPrN - 1) / kPrN;
-  // this CTA's key tiles, and those of either row tile
-  const int t0 = (int)((int64_t)T * blockIdx.y / a.nsplit);
-  const int t1 = (int)((int64_t)T * (blockIdx.y + 1) / a.nsplit);
-  const int e0 = min(t1, (max(0, off + last0) + kPrN - 1) / kPrN);
-  const int e1 = last1 >= tok1 ? min(t1, (max(0, off + last1) + kPrN - 1) / kPrN) : t0;
-  const int n0 = max(0, e0 - t0), n1 = max(0, e1 - t0), nt = max(n0, n1);
 
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
   uint64_t *q_full = bars, *full = bars + 1, *empty = full + C::SLOTS, *clean = empty + C::SLOTS;
@@ -225,7 +170,8 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
   uint64_t *mma_done = s_full + 6;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_TMEM);
   volatile int *abort_v = &abort_flag;
-  if (tid == 0) {
+  // set up while the offsets are on their way
+  if (tid == kLoadWarp * 32) {
     mbar_init(q_full, 1);
     for (int i = 0; i < C::SLOTS; ++i) {
       mbar_init(&full[i], 1);
@@ -244,9 +190,71 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
     fence_proxy_async_smem();
   }
   if (warp == kMmaWarp) tmem_alloc(tmem_slot, kPrCols);
+  if (tid == kLoadWarp * 32 + 1) {
+    tma_prefetch(&mq);
+    tma_prefetch(&mk);
+    tma_prefetch(&mv);
+  }
+  // ---- which sequence and tile: row tiles of all sequences laid end to end, the
+  // last (longest) first, the kv heads of a tile next to one another.  Every warp
+  // looks for itself, 32 sequences at a time: first their number of tiles, then the
+  // sequence (32 sequences or fewer are read once).
+  const int kvh = blockIdx.x % a.hkv;
+  const int span = 2 * a.tpt;  // tokens of a CTA
+  int q0 = 0, nq = 0, k0 = 0, nk = 0, tile = -1;
+  {
+    auto tiles = [&](int i) {
+      q0 = nq = k0 = nk = 0;
+      if (i < a.n_seqs) prompt_seq(a, i, q0, nq, k0, nk);
+      return (nq + span - 1) / span;
+    };
+    int total = 0, n = 0;
+    for (int i = 0; i < a.n_seqs; i += 32) {
+      n = tiles(i + lane);
+      total += __reduce_add_sync(0xffffffffu, n);
+    }
+    const int want = total - 1 - (int)(blockIdx.x / a.hkv);
+    for (int i = 0, at = 0; i < a.n_seqs && want >= 0; i += 32) {
+      if (a.n_seqs > 32) n = tiles(i + lane);
+      int x = n;  // inclusive sums
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      const uint32_t here = __ballot_sync(0xffffffffu, want < at + x);
+      if (here) {
+        const int src = __ffs(here) - 1;
+        tile = want - at - __shfl_sync(0xffffffffu, x - n, src);
+        q0 = __shfl_sync(0xffffffffu, q0, src);
+        nq = __shfl_sync(0xffffffffu, nq, src);
+        k0 = __shfl_sync(0xffffffffu, k0, src);
+        nk = __shfl_sync(0xffffffffu, nk, src);
+        break;
+      }
+      at += __shfl_sync(0xffffffffu, x, 31);
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (tile < 0) {  // the grid covers the largest number of tiles there can be
+    if (warp == kMmaWarp) tmem_dealloc(*tmem_slot, kPrCols);
+    return;
+  }
+  const int tok0 = tile * span;              // of the sequence
+  const int off = nk - nq + 1;                  // query u sees keys 0 .. off + u - 1
+  const int tok1 = tok0 + a.tpt;                // row tile 1's first token
+  const int last0 = min(tok1, nq) - 1, last1 = min(tok1 + a.tpt, nq) - 1;
+  const int all = max(0, off + max(last0, last1));           // keys any row sees
+  const int T = (all + kPrN - 1) / kPrN;
+  // this CTA's key tiles, and those of either row tile
+  const int t0 = (int)((int64_t)T * blockIdx.y / a.nsplit);
+  const int t1 = (int)((int64_t)T * (blockIdx.y + 1) / a.nsplit);
+  const int e0 = min(t1, (max(0, off + last0) + kPrN - 1) / kPrN);
+  const int e1 = last1 >= tok1 ? min(t1, (max(0, off + last1) + kPrN - 1) / kPrN) : t0;
+  const int n0 = max(0, e0 - t0), n1 = max(0, e1 - t0), nt = max(n0, n1);
+
   // All 512 columns are this CTA's, so they start at column 0 (lane 0), and the
   // addresses below are constants.
   constexpr uint32_t tmem = 0u;
@@ -395,10 +403,11 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
     // this thread's half of the row's scores, and of its output columns
     const uint32_t tS = tmem + lrow + i * kPrN, tO = tmem + lrow + 2 * kPrN + i * D + hg * (D / 2);
     float *red = reinterpret_cast<float *>(smem + C::OFF_RED) + i * 256;
+    const int pair = 1 + i * 4 + (warp & 3);            // barrier of the warps of these rows
     const float sl2 = a.scale_log2;
     float m_run = -CUDART_INF_F, l = 0.f;
-    // (no early exit: every thread of a row tile meets the others' barriers, also
-    // after a wait has run out)
+    // (no early exit: the warps of a pair meet at their barriers, also after a wait has
+    // run out)
     for (int n = 0; n < ni; ++n) {
       wait(&s_full[i], (uint32_t)(n & 1));
       __syncwarp();
@@ -423,14 +432,14 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
         mx1 = fmaxf(mx1, fmaxf(__uint_as_float(s1[c]), __uint_as_float(s1[c + 1])));
       }
       float mx = fmaxf(mx0, mx1) * sl2;
-      // The barrier also separates the halves' reads of S from their writes of P.
-      // Rows whose maximum grew much are rare: only then do the halves of every row
-      // exchange their maxima.
-      if (named_or(1 + i, 256, mx > m_run + kPrRescale)) {
+      // The two warps that share 32 rows meet here, which also separates the halves'
+      // reads of S from their writes of P.  Rows whose maximum grew much are rare:
+      // only then do the halves exchange their maxima.
+      if (named_or(pair, 64, mx > m_run + kPrRescale)) {
         red[hg * 128 + m] = mx;
-        named_sync(1 + i, 256);
+        named_sync(pair, 64);
         mx = fmaxf(mx, red[(hg ^ 1) * 128 + m]);
-        named_sync(1 + i, 256);
+        named_sync(pair, 64);
         if (__any_sync(0xffffffffu, mx > m_run + kPrRescale)) {
           const float m_new = fmaxf(m_run, mx);
           const float f = m_run == -CUDART_INF_F ? 0.f : ex2_approx(m_run - m_new);
@@ -457,10 +466,11 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
       auto weights = [&](const uint32_t(&s)[32]) {
 #pragma unroll
         for (int x = 0; x < 16; ++x) {
-          const float u = ex2_approx(fmaf(__uint_as_float(s[2 * x]), sl2, b));
-          const float w = ex2_approx(fmaf(__uint_as_float(s[2 * x + 1]), sl2, b));
-          l0 += u;
-          l1 += w;
+          float u, w;
+          fma_f32x2(u, w, __uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1]), sl2, sl2, b, b);
+          u = ex2_approx(u);
+          w = ex2_approx(w);
+          add_f32x2(l0, l1, u, w);
           p[x] = pack_bf16(u, w);
         }
       };
@@ -469,14 +479,14 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
       weights(s1);
       tmem_st16(tS + hg * (kPrH / 2) + 16, p);
       l += l0 + l1;
-      tmem_wait_st();
+      tmem_wait_st();  // (of the rescaled O, too)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[i]);
     }
     // the row's sum over both halves
     red[hg * 128 + m] = l;
-    named_sync(1 + i, 256);
+    named_sync(pair, 64);
     l += red[(hg ^ 1) * 128 + m];
     if (ni > 0) {
       wait(&pv_done[i], (uint32_t)((ni - 1) & 1));

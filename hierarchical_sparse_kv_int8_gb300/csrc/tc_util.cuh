@@ -143,6 +143,21 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
+// Two fp32 numbers at a time: a * b + c and a + b, each rounded to nearest.
+__device__ __forceinline__ void fma_f32x2(float &x, float &y, float ax, float ay, float bx,
+                                          float by, float cx, float cy) {
+  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mov.b64 c, {%6, %7};\n fma.rn.f32x2 c, a, b, c;\n mov.b64 {%0, %1}, c;\n}\n"
+      : "=f"(x), "=f"(y)
+      : "f"(ax), "f"(ay), "f"(bx), "f"(by), "f"(cx), "f"(cy));
+}
+__device__ __forceinline__ void add_f32x2(float &x, float &y, float ax, float ay) {
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n"
+      " add.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "+f"(x), "+f"(y)
+      : "f"(ax), "f"(ay));
+}
+
 // Plain arrival on an mbarrier (release at CTA scope).
 __device__ __forceinline__ void mbar_arrive(void *bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(bar)) : "memory");
