@@ -4,10 +4,22 @@
 // i and lives in row p mod R of page table[i][p / R].  In the 8-bit kinds each
 // (token, head) row x keeps s = max|x| / Q and the codes round(x / s).
 //
-// Both directions move every byte once and are bound by HBM: a row of 64 or 128
-// values is shared by 8 or 16 lanes of 16 bytes, so that the bf16 side is read
-// or written in whole 128- and 256-byte rows and the 8-bit side in 64- and
-// 128-byte ones; the row's maximum takes three or four shuffles.
+// Both directions move every byte once and are bound by HBM.  A thread takes 8
+// values (bf16) or 16 (8 bits) of a row of keys and of the same row of values: 16-byte
+// accesses on both sides but for the bf16 side of 8-bit rows, where it is two, and
+// 64 bytes in flight a thread.
+//
+// Rounding exactly costs a comparison per row, not per value.  With s = max / Q
+// rounded to 24 bits, x / s is either at least 2^-13 (e4m3) or 2^-16 (int8) of itself
+// away from the middle of two codes, or max / Q and x would meet the middle
+// exactly: x Q = middle max is an equation of small whole numbers.  Which side x / s
+// falls on there follows from s being rounded down or up, the sign of max - Q s.  So x
+// is multiplied by 1 / s times 1 +- 2^-15 (2^-18) by that sign, which moves only those
+// values to their side.  Where s is exact (sign 0) a middle is a true tie: for int8 s is
+// then a power of two and x / s exact; for e4m3 x / s is rounded to 17 bits first, which
+// puts it on the middle again, and the conversion takes the even code.  (With every
+// value's side decided by itself the write of 37,000 tokens took 113 us and 40
+// instructions a value.)
 #include "pages_internal.cuh"
 
 namespace dhs {
@@ -22,62 +34,66 @@ struct TokenRows {
   int64_t kt, kh, vt, vh;        // strides of a token and a head, in elements
 };
 
-// Whether x / s > mid in real numbers, `mid` of at most 8 significant bits:
-// the product's rounding error is recovered by the fused multiply-add, and
-// x - hi is exact because the two are within a factor of two (x / s is next to
-// mid).  Returns -1, 0, 1 for below, equal, above.
-__device__ __forceinline__ int side_of(float x, float s, float mid) {
-  const float hi = mid * s, lo = fmaf(mid, s, -hi);
-  const float d = (x - hi) - lo;
-  return d > 0.f ? 1 : (d < 0.f ? -1 : 0);
+__device__ __forceinline__ uint32_t e4m3_pair_code(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// y rounded to 17 bits (the intrinsics keep the product and differences apart)
+__device__ __forceinline__ float bits17(float y) {
+  const float t = __fmul_rn(y, 129.f);
+  return __fsub_rn(t, __fsub_rn(t, y));
 }
 
-// The code value (a whole number up to 127) of x >= 0: x / s to nearest even.
-// y = x * (1 / s) is off by less than 2^-15, which matters only next to a
-// half; there the side is decided exactly.
-__device__ __forceinline__ float round_int8(float x, float s, float inv) {
-  const float y = x * inv;
-  float c = rintf(y);
-  if (fabsf(fabsf(y - c) - 0.5f) < 1e-3f) {
-    const float f = floorf(y), mid = f + 0.5f;
-    const int side = side_of(x, s, mid);
-    const bool odd = (((int)f) & 1) != 0;
-    c = (side > 0 || (side == 0 && odd)) ? f + 1.f : f;
+// Codes of N bf16 values (two a word) of a row with the largest magnitude `big`
+// and scale s, four codes a word.
+template <int KIND, int N>
+__device__ __forceinline__ void quantise(const uint32_t (&u)[N / 2], float big, float s,
+                                         uint32_t (&code)[N / 4]) {
+  const float off = fmaf(KIND == DHS_PAGE_INT8 ? -127.f : -448.f, s, big);  // (its sign is exact)
+  const float move = KIND == DHS_PAGE_INT8 ? 3.814697265625e-6f : 3.0517578125e-5f;
+  const float by = __frcp_rn(s) * (off > 0.f ? 1.f + move : off < 0.f ? 1.f - move : 1.f);
+#pragma unroll
+  for (int w = 0; w < N / 4; ++w) {
+    float x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t b = u[w * 2 + (i >> 1)];
+      x[i] = __uint_as_float(i & 1 ? b & 0xFFFF0000u : b << 16);
+    }
+    if (KIND == DHS_PAGE_INT8) {
+      // 1.5 * 2^23 more leaves the nearest whole number, ties to even, in the low bits
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = fmaf(x[i], by, 12582912.f);
+      code[w] = __byte_perm(
+          __byte_perm(__float_as_uint(x[0]), __float_as_uint(x[1]), 0x0040),
+          __byte_perm(__float_as_uint(x[2]), __float_as_uint(x[3]), 0x0040), 0x5410);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = bits17(x[i] * by);
+      code[w] = __byte_perm(e4m3_pair_code(x[0], x[1]), e4m3_pair_code(x[2], x[3]), 0x5410);
+    }
   }
-  return fminf(c, 127.f);
 }
-// The same on the e4m3 grid, whose spacing at y is 2^(max(e, -6) - 3), e the
-// exponent of y: y over the spacing is a whole number of at most 16 plus a
-// fraction.
-__device__ __forceinline__ float round_e4m3(float x, float s, float inv) {
-  const float y = x * inv;
-  const int e = max((int)(__float_as_uint(y) >> 23) - 127, -6);
-  const float up = __uint_as_float((uint32_t)(127 + 3 - e) << 23);    // 2^(3 - e)
-  const float step = __uint_as_float((uint32_t)(127 + e - 3) << 23);  // 2^(e - 3)
-  const float z = y * up;
-  float c = rintf(z);
-  if (fabsf(fabsf(z - c) - 0.5f) < 1e-4f) {
-    const float f = floorf(z);
-    const int side = side_of(x, s, (f + 0.5f) * step);
-    const bool odd = (((int)f) & 1) != 0;
-    c = (side > 0 || (side == 0 && odd)) ? f + 1.f : f;
+
+// Four codes times s as bf16, two a word.
+template <int KIND>
+__device__ __forceinline__ void dequantise(uint32_t c, float s, uint32_t &lo, uint32_t &hi) {
+  float x[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t b = (c >> (i * 8)) & 0xFFu;
+    if (KIND == DHS_PAGE_INT8) {
+      x[i] = (float)(int8_t)b * s;
+    } else {
+      // the code's seven lower bits at a float's exponent and mantissa give the
+      // value times 2^-120, subnormals included
+      const float m = __uint_as_float(((b & 0x7Fu) << 20) | ((b & 0x80u) << 24));
+      x[i] = m * 1.329227995784916e36f * s;
+    }
   }
-  return fminf(c * step, 448.f);
-}
-
-// Bits of a finite non-negative value that lies on the e4m3 grid.
-__device__ __forceinline__ uint32_t e4m3_bits(float v) {
-  const uint32_t u = __float_as_uint(v);
-  const int e = (int)(u >> 23) - 127;
-  return e >= -6 ? (uint32_t)((e + 7) << 3) | ((u >> 20) & 7u) : (uint32_t)(v * 512.f);
-}
-
-// e4m3 code to its value (finite codes).
-__device__ __forceinline__ float e4m3_value(uint32_t c) {
-  // the code's seven lower bits at a float's exponent and mantissa give the
-  // value times 2^-120, subnormals included
-  const float m = __uint_as_float((c & 0x7Fu) << 20) * 1.329227995784916e36f;  // 2^120
-  return (c & 0x80u) ? -m : m;
+  lo = pack_bf16(x[0], x[1]);
+  hi = pack_bf16(x[2], x[3]);
 }
 
 // Where the tokens of this CTA live: row of kv head 0, -1 none, -2 padding.
@@ -99,7 +115,8 @@ __global__ void __launch_bounds__(kPgThreads)
 k_page_write(const PageView pg, const TokenRows src, int64_t n_tok, int per_cta,
              const int32_t *__restrict__ cu, const int32_t *__restrict__ lens,
              const int32_t *__restrict__ table, int width, int n_seqs, int32_t *err) {
-  constexpr int L = D / 8;  // lanes of a row
+  constexpr int E = KIND == DHS_PAGE_BF16 ? 8 : 16;  // values of a thread
+  constexpr int L = D / E;                           // lanes of a row
   __shared__ int64_t dst[kPgTok];
   const int64_t t0 = (int64_t)blockIdx.x * per_cta;
   const int nt = (int)min((int64_t)per_cta, n_tok - t0);
@@ -115,51 +132,50 @@ k_page_write(const PageView pg, const TokenRows src, int64_t n_tok, int per_cta,
     const int t = e / pg.hkv, h = e - t * pg.hkv;
     const int64_t base = e < total ? dst[t] : -2;
     const bool on = base >= 0;
+    uint32_t u[2][E / 2];
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
-      uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      if (on)
-        w = *reinterpret_cast<const uint4 *>(
-            (side ? src.v : src.k) +
-            2 * ((t0 + t) * (side ? src.vt : src.kt) + h * (side ? src.vh : src.kh) + sub * 8));
-      const int64_t row = base + (int64_t)h * pg.rows;
+      const uint4 *at = reinterpret_cast<const uint4 *>(
+          (side ? src.v : src.k) +
+          2 * ((t0 + t) * (side ? src.vt : src.kt) + h * (side ? src.vh : src.kh) + sub * E));
+#pragma unroll
+      for (int x = 0; x < E / 8; ++x) {
+        const uint4 w = on ? at[x] : make_uint4(0u, 0u, 0u, 0u);
+        u[side][4 * x] = w.x;
+        u[side][4 * x + 1] = w.y;
+        u[side][4 * x + 2] = w.z;
+        u[side][4 * x + 3] = w.w;
+      }
+    }
+    const int64_t row = base + (int64_t)h * pg.rows;
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
       unsigned char *out = side ? pg.v : pg.k;
       if (KIND == DHS_PAGE_BF16) {
-        if (on) *reinterpret_cast<uint4 *>(out + (row * D + sub * 8) * 2) = w;
+        if (on)
+          *reinterpret_cast<uint4 *>(out + (row * D + sub * E) * 2) =
+              make_uint4(u[side][0], u[side][1], u[side][2], u[side][3]);
         continue;
       }
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-      // the largest magnitude as bits: an infinity or a NaN is the largest
-      uint32_t top = 0u;
+      // the largest magnitude, of both halves of a word at a time: as bits an
+      // infinity or a NaN is the largest
+      uint32_t two = 0u;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        top = max(top, max(u[i] & 0x7FFFu, (u[i] >> 16) & 0x7FFFu));
+      for (int i = 0; i < E / 2; ++i) two = __vmaxu2(two, u[side][i] & 0x7FFF7FFFu);
+      uint32_t top = max(two & 0xFFFFu, two >> 16);
 #pragma unroll
       for (int o = L / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
       const float big = __uint_as_float(top << 16);
       const bool bad = top >= 0x7F80u;
       const float s = (bad || big < kTiny) ? 0.f
                                            : __fdiv_rn(big, KIND == DHS_PAGE_INT8 ? 127.f : 448.f);
-      const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
-      uint32_t code[2] = {0u, 0u};
-      if (s > 0.f) {
+      uint32_t code[E / 4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t b = (u[i >> 1] >> ((i & 1) * 16)) & 0xFFFFu;
-          const float x = __uint_as_float((b & 0x7FFFu) << 16);
-          const bool neg = (b & 0x8000u) != 0u;
-          uint32_t c;
-          if (KIND == DHS_PAGE_INT8) {
-            const int v = (int)round_int8(x, s, inv);
-            c = (uint32_t)(neg ? -v : v) & 0xFFu;
-          } else {
-            c = e4m3_bits(round_e4m3(x, s, inv)) | (neg ? 0x80u : 0u);
-          }
-          code[i >> 2] |= c << ((i & 3) * 8);
-        }
-      }
+      for (int i = 0; i < E / 4; ++i) code[i] = 0u;
+      if (s > 0.f) quantise<KIND, E>(u[side], big, s, code);
       if (on) {
-        *reinterpret_cast<uint2 *>(out + row * D + sub * 8) = make_uint2(code[0], code[1]);
+        *reinterpret_cast<uint4 *>(out + row * D + sub * E) =
+            make_uint4(code[0], code[1], code[E / 4 - 2], code[E / 4 - 1]);
         if (sub == 0) (side ? pg.vs : pg.ks)[row] = bad ? __uint_as_float(0x7FC00000u) : s;
       }
     }
@@ -171,7 +187,8 @@ __global__ void __launch_bounds__(kPgThreads)
 k_page_read(const PageView pg, const TokenRows to, int64_t n_tok, int per_cta,
             const int32_t *__restrict__ cu, const int32_t *__restrict__ lens,
             const int32_t *__restrict__ table, int width, int n_seqs, int32_t *err) {
-  constexpr int L = D / 8;
+  constexpr int E = KIND == DHS_PAGE_BF16 ? 8 : 16;
+  constexpr int L = D / E;
   __shared__ int64_t src[kPgTok];
   const int64_t t0 = (int64_t)blockIdx.x * per_cta;
   const int nt = (int)min((int64_t)per_cta, n_tok - t0);
@@ -180,34 +197,39 @@ k_page_read(const PageView pg, const TokenRows to, int64_t n_tok, int per_cta,
                              DHS_SITE_PAGE_READ);
   __syncthreads();
   const int sub = threadIdx.x % L, total = nt * pg.hkv;
+#pragma unroll 2
   for (int e = threadIdx.x / L; e < total; e += kPgThreads / L) {
     const int t = e / pg.hkv, h = e - t * pg.hkv;
     const int64_t base = src[t];
     if (base == -2) continue;
     const int64_t row = base + (int64_t)h * pg.rows;
+    uint4 w[2];
+    float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
-      uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      const unsigned char *in = side ? pg.v : pg.k;
+      w[side] = make_uint4(0u, 0u, 0u, 0u);
       if (base >= 0) {
-        if (KIND == DHS_PAGE_BF16) {
-          w = *reinterpret_cast<const uint4 *>(in + (row * D + sub * 8) * 2);
-        } else {
-          const uint2 c = *reinterpret_cast<const uint2 *>(in + row * D + sub * 8);
-          const float s = (side ? pg.vs : pg.ks)[row];
-          float x[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t b = ((i < 4 ? c.x : c.y) >> ((i & 3) * 8)) & 0xFFu;
-            x[i] = (KIND == DHS_PAGE_INT8 ? (float)(int8_t)b : e4m3_value(b)) * s;
-          }
-          w = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                         pack_bf16(x[6], x[7]));
-        }
+        w[side] = *reinterpret_cast<const uint4 *>((side ? pg.v : pg.k) +
+                                                   (row * D + sub * E) * (16 / E));
+        if (KIND != DHS_PAGE_BF16) s[side] = (side ? pg.vs : pg.ks)[row];
       }
-      *reinterpret_cast<uint4 *>(
+    }
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      uint4 *at = reinterpret_cast<uint4 *>(
           (side ? to.v : to.k) +
-          2 * ((t0 + t) * (side ? to.vt : to.kt) + h * (side ? to.vh : to.kh) + sub * 8)) = w;
+          2 * ((t0 + t) * (side ? to.vt : to.kt) + h * (side ? to.vh : to.kh) + sub * E));
+      if (KIND == DHS_PAGE_BF16) {
+        *at = w[side];
+      } else {
+        uint4 a, b;
+        dequantise<KIND>(w[side].x, s[side], a.x, a.y);
+        dequantise<KIND>(w[side].y, s[side], a.z, a.w);
+        dequantise<KIND>(w[side].z, s[side], b.x, b.y);
+        dequantise<KIND>(w[side].w, s[side], b.z, b.w);
+        at[0] = a;
+        at[1] = b;
+      }
     }
   }
 }

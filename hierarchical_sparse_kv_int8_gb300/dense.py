@@ -22,11 +22,25 @@ _CHECK = {1: "a length or offset outside its range", 2: "a page outside the cach
 _SITE = {1: "dhs_page_write", 2: "dhs_page_read", 3: "dhs_page_attend", 4: "dhs_prompt_attend"}
 
 
+_Strides4, _Strides6 = ctypes.c_int64 * 4, ctypes.c_int64 * 6
+
+
 class Pages(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
                 ("page_rows", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("kind", ctypes.c_int32)]
+
+
+try:  # the current stream's handle without building a Stream object (a decode step makes
+    # several calls of a few microseconds each)
+    from torch._C import _cuda_getCurrentRawStream as _current_stream
+except ImportError:
+    def _current_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
+
+_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+_HERE = nullcontext()
 
 
 def _lib():
@@ -39,61 +53,65 @@ def _raise(code, what):
     raise DhsError(code, what)
 
 
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
+def _bad(name, t, dtype, shape, index):
+    """The complaint about a tensor that is not a contiguous ``dtype`` of ``shape``
+    (None: any) on CUDA device ``index``."""
+    raise ValueError("%s: contiguous %s%s on cuda:%s expected, not %s %s %s on %s" % (
+        name, dtype, "" if shape is None else " %s" % (tuple(shape),), index,
+        "contiguous" if t.is_contiguous() else "strided", t.dtype, tuple(t.shape), t.device))
 
 
-def _rows(t, name, heads, dim, device):
-    """Token and head stride of a packed bf16 tensor [tokens, heads, dim]."""
-    _need(t.dtype is torch.bfloat16 and t.dim() == 3, "%s: bf16 [tokens, heads, dim] expected" % name)
-    _need(t.device == device, "%s is on %s, not on %s" % (name, t.device, device))
+def _plain(t, name, dtype, shape, index):
+    if not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == index):
+        _bad(name, t, dtype, shape, index)
+    return t.data_ptr()
+
+
+def _table(t, n, index):
+    if not (t.dtype is _I32 and t.dim() == 2 and t.shape[0] == n and t.is_contiguous()
+            and t.get_device() == index):
+        _bad("page_table", t, _I32, (n, "width"), index)
+    return t.data_ptr()
+
+
+def _rows(t, name, index):
+    """Tokens, heads, elements, token and head stride of a packed bf16 tensor."""
+    if not (t.dtype is _BF16 and t.dim() == 3 and t.get_device() == index):
+        raise ValueError("%s: bf16 [tokens, heads, dim] on cuda:%s expected, not %s %s on %s"
+                         % (name, index, t.dtype, tuple(t.shape), t.device))
     n, h, d = t.shape
-    _need((heads is None or h == heads) and (dim is None or d == dim),
-          "%s has %d heads of %d elements" % (name, h, d))
     st, sh, sd = t.stride()
-    _need(sd == 1 or t.numel() == 0, "%s: the elements of a head must be contiguous" % name)
+    if sd != 1 and d > 1 and n and h:
+        raise ValueError("%s: the elements of a head must be contiguous" % name)
     # a stride that no second token or head uses may be anything
-    return (st if n > 1 else h * d), (sh if h > 1 else d)
+    return n, h, d, (st if n > 1 else h * d), (sh if h > 1 else d)
 
 
-def _ints(t, name, shape, device):
-    _need(t.dtype is torch.int32 and t.is_contiguous(), "%s: contiguous int32 expected" % name)
-    _need(t.device == device, "%s is on %s, not on %s" % (name, t.device, device))
-    _need(shape is None or tuple(t.shape) == shape, "%s has shape %s, not %s"
-          % (name, tuple(t.shape), shape))
-    return t.data_ptr()
-
-
-def _plain(t, name, dtype, shape, device):
-    _need(t.dtype is dtype and t.is_contiguous() and tuple(t.shape) == shape,
-          "%s: contiguous %s %s expected" % (name, dtype, shape))
-    _need(t.device == device, "%s is on %s, not on %s" % (name, t.device, device))
-    return t.data_ptr()
-
-
-def _space(t, device):
+def _space(t, index):
     if t is None:
         return None, 0
-    _need(t.is_contiguous() and t.device == device, "workspace: contiguous, on %s expected" % device)
+    if not (t.is_contiguous() and t.get_device() == index):
+        raise ValueError("workspace: contiguous, on cuda:%s expected" % index)
     return t.data_ptr(), t.numel() * t.element_size()
 
 
-def _on(device):
-    _need(device.type == "cuda", "CUDA tensors expected, not %s" % device)
-    return nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+def _on(index):
+    """The context in which a call runs on device ``index``."""
+    if index < 0:
+        raise ValueError("CUDA tensors expected")
+    return _HERE if torch.cuda.current_device() == index else torch.cuda.device(index)
 
 
-def _raw(stream, device):
+def _raw(stream, index):
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return _current_stream(index)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def check_errors(errors, stream=None):
     """Waits for ``stream``, raises DhsError (code 5) if a call recorded a bad
     page, length or offset in ``errors`` (int32[2]), and clears the record."""
-    with _on(errors.device):
+    with _on(errors.get_device()):
         s = torch.cuda.current_stream() if stream is None else stream
         if isinstance(s, int):
             s = torch.cuda.ExternalStream(s)
@@ -115,26 +133,24 @@ class PageCache:
     """
 
     def __init__(self, k, v, k_scale=None, v_scale=None, errors=None):
-        _need(k.dtype in _KIND, "a cache of %s is not supported" % k.dtype)
-        _need(k.dim() == 4 and k.is_contiguous() and v.is_contiguous() and v.shape == k.shape
-              and v.dtype is k.dtype, "k and v: contiguous, of one shape and type expected")
-        self.device = k.device
-        _on(self.device)
-        _need(v.device == self.device, "k and v are on different devices")
+        if k.dtype not in _KIND:
+            raise ValueError("a cache of %s is not supported" % k.dtype)
+        if k.dim() != 4:
+            raise ValueError("k: [n_pages, kv_heads, page_rows, head_dim] expected, not %s"
+                             % (tuple(k.shape),))
+        self.device, self._index = k.device, k.get_device()
+        _on(self._index)
         self.kind = _KIND[k.dtype]
         self.n_pages, self.kv_heads, self.page_rows, self.head_dim = k.shape
-        if self.kind == PAGE_BF16:
-            _need(k_scale is None and v_scale is None, "a bf16 cache has no scales")
-        else:
-            _need(k_scale is not None and v_scale is not None, "an 8-bit cache needs scales")
-            for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-                _plain(t, name, torch.float32, tuple(k.shape[:3]), self.device)
+        if (self.kind == PAGE_BF16) != (k_scale is None and v_scale is None):
+            raise ValueError("an 8-bit cache needs scales, a bf16 cache has none")
+        ptr = [_plain(t, name, k.dtype, k.shape, self._index) for t, name in ((k, "k"), (v, "v"))]
+        ptr += [None if t is None else _plain(t, name, _F32, k.shape[:3], self._index)
+                for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale"))]
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.errors = torch.zeros(2, dtype=torch.int32, device=self.device) if errors is None else errors
-        self._err = _plain(self.errors, "errors", torch.int32, (2,), self.device)
-        ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-        self._desc = Pages(ptr(k), ptr(v), ptr(k_scale), ptr(v_scale), self.n_pages,
-                           self.page_rows, self.kv_heads, self.head_dim, self.kind)
+        self.errors = torch.zeros(2, dtype=_I32, device=self.device) if errors is None else errors
+        self._err = _plain(self.errors, "errors", _I32, (2,), self._index)
+        self._desc = Pages(*ptr, self.n_pages, self.page_rows, self.kv_heads, self.head_dim, self.kind)
         self._ref = ctypes.byref(self._desc)
         self._lib = _lib()
 
@@ -155,17 +171,18 @@ class PageCache:
                    for t in (self.k, self.v, self.k_scale, self.v_scale) if t is not None)
 
     def _copy(self, fn, what, k, v, cu, seq_lens, page_table, stream):
-        dev = self.device
-        strides = (ctypes.c_int64 * 4)(*_rows(k, "k", self.kv_heads, self.head_dim, dev),
-                                       *_rows(v, "v", self.kv_heads, self.head_dim, dev))
-        n, tok = seq_lens.shape[0], k.shape[0]
-        _need(v.shape[0] == tok, "k has %d tokens, v %d" % (tok, v.shape[0]))
-        _need(page_table.dim() == 2 and page_table.shape[0] == n, "page_table: [%d, width] expected" % n)
-        with _on(dev):
-            rc = fn(self._ref, k.data_ptr(), v.data_ptr(), strides, tok,
-                    _ints(cu, "cu", (n + 1,), dev), _ints(seq_lens, "seq_lens", (n,), dev),
-                    _ints(page_table, "page_table", None, dev), page_table.shape[1], n, self._err,
-                    _raw(stream, dev))
+        ix = self._index
+        tok, h, d, kt, kh = _rows(k, "k", ix)
+        tv, hv, dv, vt, vh = _rows(v, "v", ix)
+        if (tv, hv, dv) != (tok, h, d) or h != self.kv_heads or d != self.head_dim:
+            raise ValueError("k and v: [tokens, %d, %d] expected, not %s and %s" % (
+                self.kv_heads, self.head_dim, tuple(k.shape), tuple(v.shape)))
+        n = seq_lens.shape[0]
+        with _on(ix):
+            rc = fn(self._ref, k.data_ptr(), v.data_ptr(), _Strides4(kt, kh, vt, vh), tok,
+                    _plain(cu, "cu", _I32, (n + 1,), ix),
+                    _plain(seq_lens, "seq_lens", _I32, (n,), ix), _table(page_table, n, ix),
+                    page_table.shape[1], n, self._err, _raw(stream, ix))
         if rc:
             _raise(rc, what)
 
@@ -181,30 +198,31 @@ class PageCache:
     def attend_workspace(self, n_seqs: int, q_len: int, q_heads: int):
         """A new workspace for :meth:`attend` calls of these sizes.  Calls that may
         overlap on the GPU (other streams, other graphs) each need their own."""
-        with _on(self.device):
+        with _on(self._index):
             nbytes = self._lib.dhs_page_attend_workspace(self._ref, n_seqs, q_len, q_heads)
-        _need(nbytes >= 0, "attend does not serve n_seqs=%d, q_len=%d, q_heads=%d"
-              % (n_seqs, q_len, q_heads))
+        if nbytes < 0:
+            raise ValueError("attend does not serve n_seqs=%d, q_len=%d, q_heads=%d"
+                             % (n_seqs, q_len, q_heads))
         return torch.zeros(max(16, nbytes), dtype=torch.uint8, device=self.device)
 
     def attend(self, q, seq_lens, page_table, out, workspace, lse=None, q_lens=None,
                scale: float = 0.0, stream=None):
         """Attention of the newest tokens over the cache (dhs_page_attend):
         ``q`` and ``out`` [n_seqs, q_len, q_heads, head_dim]."""
-        dev = self.device
-        n, qn, hq, d = q.shape
-        _need(d == self.head_dim, "q has %d elements a head, the cache %d" % (d, self.head_dim))
-        _need(page_table.dim() == 2 and page_table.shape[0] == n, "page_table: [%d, width] expected" % n)
-        space, nbytes = _space(workspace, dev)
-        with _on(dev):
+        ix, shape = self._index, q.shape
+        if len(shape) != 4 or shape[3] != self.head_dim:
+            raise ValueError("q: [n_seqs, q_len, q_heads, %d] expected, not %s"
+                             % (self.head_dim, tuple(shape)))
+        n, qn, hq, _ = shape
+        space, nbytes = _space(workspace, ix)
+        with _on(ix):
             rc = self._lib.dhs_page_attend(
-                self._ref, _plain(q, "q", torch.bfloat16, (n, qn, hq, d), dev),
-                None if q_lens is None else _ints(q_lens, "q_lens", (n,), dev),
-                _ints(seq_lens, "seq_lens", (n,), dev),
-                _ints(page_table, "page_table", None, dev), page_table.shape[1], n, qn, hq, scale,
-                _plain(out, "out", torch.bfloat16, (n, qn, hq, d), dev),
-                None if lse is None else _plain(lse, "lse", torch.float32, (n, qn, hq), dev),
-                space, nbytes, self._err, _raw(stream, dev))
+                self._ref, _plain(q, "q", _BF16, shape, ix),
+                None if q_lens is None else _plain(q_lens, "q_lens", _I32, (n,), ix),
+                _plain(seq_lens, "seq_lens", _I32, (n,), ix), _table(page_table, n, ix),
+                page_table.shape[1], n, qn, hq, scale, _plain(out, "out", _BF16, shape, ix),
+                None if lse is None else _plain(lse, "lse", _F32, (n, qn, hq), ix), space, nbytes,
+                self._err, _raw(stream, ix))
         if rc:
             _raise(rc, "dhs_page_attend")
 
@@ -216,10 +234,11 @@ class PageCache:
 def prompt_workspace(q, k, n_seqs: int) -> Optional[torch.Tensor]:
     """A new workspace for :func:`prompt_attend` of tensors of these shapes, or
     None where the call needs none."""
-    with _on(q.device):
+    with _on(q.get_device()):
         nbytes = _lib().dhs_prompt_attend_workspace(q.shape[0], k.shape[0], n_seqs, q.shape[1],
                                                     k.shape[1], q.shape[2])
-    _need(nbytes >= 0, "prompt_attend does not serve q %s, k %s" % (tuple(q.shape), tuple(k.shape)))
+    if nbytes < 0:
+        raise ValueError("prompt_attend does not serve q %s, k %s" % (tuple(q.shape), tuple(k.shape)))
     return torch.zeros(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
 
 
@@ -227,23 +246,23 @@ def prompt_attend(q, k, v, cu_q, cu_k, out, lse=None, workspace=None, scale: flo
                   errors=None, stream=None):
     """Causal attention of packed sequences (dhs_prompt_attend): ``q`` [n_q, q_heads,
     head_dim], ``k`` and ``v`` [n_k, kv_heads, head_dim], ``out`` like ``q``."""
-    dev = q.device
-    strides = (ctypes.c_int64 * 6)(*_rows(q, "q", None, None, dev),
-                                   *_rows(k, "k", None, q.shape[2], dev),
-                                   *_rows(v, "v", k.shape[1], q.shape[2], dev))
-    nq, hq, d = q.shape
-    nk, hkv = k.shape[:2]
+    ix = q.get_device()
+    nq, hq, d, qt, qh = _rows(q, "q", ix)
+    nk, hkv, dk, kt, kh = _rows(k, "k", ix)
+    nv, hv, dv, vt, vh = _rows(v, "v", ix)
+    if (nv, hv, dv) != (nk, hkv, dk) or dk != d:
+        raise ValueError("k and v: [tokens, kv_heads, %d] expected, not %s and %s"
+                         % (d, tuple(k.shape), tuple(v.shape)))
     n = cu_q.shape[0] - 1
-    _need(n >= 0, "cu_q: [n_seqs + 1] expected")
-    _need(v.shape[0] == nk, "k has %d tokens, v %d" % (nk, v.shape[0]))
-    space, nbytes = _space(workspace, dev)
-    with _on(dev):
+    if n < 0:
+        raise ValueError("cu_q: [n_seqs + 1] expected")
+    space, nbytes = _space(workspace, ix)
+    with _on(ix):
         rc = _lib().dhs_prompt_attend(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), strides, nq, nk,
-            _ints(cu_q, "cu_q", (n + 1,), dev), _ints(cu_k, "cu_k", (n + 1,), dev), n, hq, hkv, d,
-            scale, _plain(out, "out", torch.bfloat16, (nq, hq, d), dev),
-            None if lse is None else _plain(lse, "lse", torch.float32, (nq, hq), dev), space, nbytes,
-            None if errors is None else _plain(errors, "errors", torch.int32, (2,), dev),
-            _raw(stream, dev))
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), _Strides6(qt, qh, kt, kh, vt, vh), nq, nk,
+            _plain(cu_q, "cu_q", _I32, (n + 1,), ix), _plain(cu_k, "cu_k", _I32, (n + 1,), ix), n, hq,
+            hkv, d, scale, _plain(out, "out", _BF16, q.shape, ix),
+            None if lse is None else _plain(lse, "lse", _F32, (nq, hq), ix), space, nbytes,
+            None if errors is None else _plain(errors, "errors", _I32, (2,), ix), _raw(stream, ix))
     if rc:
         _raise(rc, "dhs_prompt_attend")
