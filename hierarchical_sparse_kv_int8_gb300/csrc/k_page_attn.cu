@@ -55,7 +55,6 @@ namespace dhs {
 namespace {
 
 constexpr int kPaWarps = 4;
-constexpr int TILE8 = 8192, NS8 = 3, OCC8 = 2, SUB8 = 32;
 constexpr int kPaThreads = kPaWarps * 32;
 constexpr float kRescale8 = 4.f, kRescale16 = 8.f;  // 8-bit caches, bf16
 // f16 weights: value scales over 2^vref are in [2^6, 2^7) when vref is set and may
@@ -105,21 +104,27 @@ __device__ __forceinline__ void cp_async_4_zfill(void *dst, const void *src, int
                "r"(bytes));
 }
 
-template <int D_, int KIND_, int WM_, int MT_>
+template <int D_, int KIND_, int WM_, int MT_, int NH_>
 struct Cfg {
   static constexpr int D = D_, KIND = KIND_, WM = WM_, MT = MT_;
+  static constexpr int NH = NH_;                         // 8-row halves of a row tile in use
   static constexpr int WT = kPaWarps / WM;
   static constexpr int W = KIND == DHS_PAGE_BF16 ? 2 : 1;
   static constexpr int RB = D * W;                       // bytes of a row
   static constexpr int CH = RB / 16;                     // 16-byte chunks of a row
+  // 8-bit tiles that four warps read are turned into f16 in shared memory once (32 x
+  // 64K int8, 128 rows: 916 -> 875 us; with two warps 185 -> 225 us, so not there)
+  static constexpr bool CONV = W == 1 && WM > 2;
   // positions of a group's tile: 8 KB of keys and values per warp of the group
-  static constexpr int TN0 = (W == 1 ? TILE8 : 8192) * WM / (2 * RB);
+  static constexpr int TN0 = 8192 * WM / (2 * RB);
   static constexpr int TN = TN0 > 64 ? 64 : TN0;
-  static constexpr int SUB = MT == 1 && TN >= 32 && (W == 2 || SUB8 == 32) ? 32 : 16;  // positions scored at a time
+  static constexpr int SUB = MT == 1 && TN >= 32 ? 32 : 16;  // positions scored at a time
   static constexpr int KV = TN * RB;
   static constexpr int STAGE = 2 * KV + (W == 1 ? 2 * TN * 4 : 0);  // keys, values, scales
-  static constexpr int NS = W == 1 ? NS8 : 3;
-  static constexpr int GROUP = NS * STAGE;
+  static constexpr int NS = 3;
+  static constexpr int RING = NS * STAGE;
+  static constexpr int RC = CONV ? 2 * D : RB;           // bytes of a row as it is read
+  static constexpr int GROUP = RING + (CONV ? 2 * TN * RC : 0);
   static constexpr int ROWS = WM * MT * 16;              // rows of Q that fit
   static constexpr int OPAD = D + 4;
   static constexpr int MERGE = WT * ROWS * OPAD * 4;
@@ -129,7 +134,8 @@ struct Cfg {
   static constexpr int OFF_MASK = OFF_ROW + WT * SLOTS * TN * 8; // uint32 [WT][SLOTS][2]
   static constexpr int OFF_ML = OFF_MASK + WT * SLOTS * 8;       // float [WT][ROWS][2]
   static constexpr int SMEM = OFF_ML + WT * ROWS * 8;
-  static constexpr int OCC = W == 1 && MT == 1 ? OCC8 : SMEM * 2 <= 226 * 1024 ? 2 : 1;
+  static constexpr int OCC = SMEM * 2 <= 226 * 1024 ? 2 : 1;
+  static constexpr bool B16 = W == 2 || CONV;            // the products read 16-bit rows
   static constexpr int BLOCK = WT * TN;                  // positions of a block
 };
 
@@ -140,12 +146,18 @@ struct Cfg {
 template <class C>
 __device__ __forceinline__ int kchunk(int row, int c) {
   if (C::W == 2) return c ^ (row & 7);
-  return C::D == 128 ? c ^ ((row & 1) << 2) : c;
+  return C::D == 128 && !C::CONV ? c ^ ((row & 1) << 2) : c;
 }
 template <class C>
 __device__ __forceinline__ int vchunk(int row, int c) {
   if (C::W == 2) return c ^ (row & 7);
-  return C::D == 128 ? c ^ (row & 6) : c ^ (row & 2);
+  return C::CONV ? c : C::D == 128 ? c ^ (row & 6) : c ^ (row & 2);
+}
+
+// a / b for a >= 0, b > 0, in 32 bits where both fit (a 64-bit division takes some
+// hundred instructions, and every CTA starts with several)
+__device__ __forceinline__ int64_t idiv(int64_t a, int64_t b) {
+  return ((uint64_t)a | (uint64_t)b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
 
 struct AttnArgs {
@@ -164,11 +176,9 @@ template <class C>
 __global__ void __launch_bounds__(kPaThreads, C::OCC)
 k_page_attn(const PageView pg, const AttnArgs a) {
   constexpr int D = C::D, MT = C::MT, WM = C::WM, WT = C::WT, TN = C::TN, NS = C::NS, RB = C::RB;
-  constexpr int KIND = C::KIND, SUB = C::SUB;
+  constexpr int KIND = C::KIND, SUB = C::SUB, NH = C::NH, RC = C::RC;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ int64_t scan[kPaThreads + 1];
-  __shared__ int sh_seq, sh_flag, sh_items;
-  __shared__ int64_t sh_first;
+  __shared__ int sh_flag;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int wm = warp % WM, wt = warp / WM;      // rows of this warp, token group
   const int gl = wm * 32 + lane;                 // thread within the group
@@ -193,35 +203,18 @@ k_page_attn(const PageView pg, const AttnArgs a) {
     return nq > 0 ? ((int64_t)len + C::BLOCK - 1) / C::BLOCK : 0;
   };
 
-  // block counts of all sequences: thread t adds up its run of them
-  const int per = (a.n_seqs + kPaThreads - 1) / kPaThreads;
-  {
-    int64_t x = 0;
-    int some = 0;
-    for (int i = tid * per; i < min(a.n_seqs, (tid + 1) * per); ++i) {
-      const int64_t b = blocks(i);
-      x += b;
-      some += b > 0 ? 1 : 0;
-    }
-    if (tid == 0) sh_items = 0;
-    __syncthreads();
-    some = __reduce_add_sync(0xffffffffu, some);
-    if (lane == 0) atomicAdd(&sh_items, some);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) scan[warp] = x;
-    __syncthreads();
-    int64_t before = 0;
-    for (int w = 0; w < warp; ++w) before += scan[w];
-    __syncthreads();
-    scan[tid + 1] = before + x;
-    if (tid == 0) scan[0] = 0;
-    __syncthreads();
+  // Blocks (of one kv head) and sequences with any: every warp adds up all of them,
+  // 32 at a time.
+  int64_t sum = 0;
+  int some = 0;
+  for (int i = 0; i < a.n_seqs; i += 32) {
+    const int n = i + lane < a.n_seqs ? (int)blocks(i + lane) : 0;
+    some += __popc(__ballot_sync(0xffffffffu, n > 0));
+    sum += n;  // (this lane's)
   }
-  const int64_t total = scan[kPaThreads] * hkv;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const int64_t total = sum * hkv;
 
   // sequences without a block: their queries see nothing
   for (int i = blockIdx.x; i < a.n_seqs; i += gridDim.x) {
@@ -239,42 +232,64 @@ k_page_attn(const PageView pg, const AttnArgs a) {
   // CTAs that take part.  An item of b blocks in P parts costs b / P blocks of
   // streaming and P parts of (R, D) in the join, least at P = sqrt(b x block
   // bytes / part bytes); more CTAs than that lengthen a short call.
-  const int64_t items = (int64_t)sh_items * hkv;
+  const int64_t items = (int64_t)some * hkv;
   const float parts =
       items > 0 ? ceilf(sqrtf((float)total / (float)items * ((float)C::BLOCK * 2 * RB) /
                               (float)(a.R * D * 4)))
                 : 0.f;
   int64_t n_parts = (int64_t)((float)items * parts);
   if (n_parts > gridDim.x / C::OCC) n_parts = gridDim.x;
-  const int n_cta = (int)min(min((int64_t)gridDim.x, total), n_parts);
+  int n_cta = (int)min(min((int64_t)gridDim.x, total), n_parts);
+  // Few long items: a CTA whose blocks belong to two items fills and drains its ring
+  // twice (some 4 us), and the others wait for it.  Then each CTA takes one chunk of
+  // at most `most_blocks` blocks of one item, of which there are at most n_cta: 8
+  // items of 22,000 positions on 304 CTAs take 30.0 us instead of 31.2.  Chunks are up
+  // to items / n_cta longer than even shares (3% there); 32 items lose 6% by them.
+  const bool chunked = items > 1 && items * 32 <= n_cta;
+  const int64_t most_blocks =
+      chunked ? idiv(total + n_cta - items - 1, max((int64_t)1, n_cta - items)) : 1;
+  auto units = [&](int64_t n) { return chunked ? idiv(n + most_blocks - 1, most_blocks) : n; };
+  int64_t total_units = total;
+  if (chunked) {
+    int64_t x = 0;
+    for (int i = lane; i < a.n_seqs; i += 32) x += units(blocks(i));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    total_units = x * hkv;
+    n_cta = (int)total_units;
+  }
   pdl_trigger();  // the join may be placed; it waits for this grid's end
   if ((int)blockIdx.x >= n_cta) return;
-  auto range = [&](int b) -> int64_t { return total * b / n_cta; };
+  // from here on places are in units: chunks, or blocks
+  auto range = [&](int b) -> int64_t { return chunked ? b : idiv(total_units * b, n_cta); };
   const int64_t begin = range(blockIdx.x), end = range(blockIdx.x + 1);
 
-  // the sequence that holds block `begin`
-  if (tid == 0) {
-    const int64_t want = begin / hkv;  // in blocks of one head: only the sequence is looked for
-    int lo = 0, hi = kPaThreads - 1;   // last t with scan[t] <= want
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (scan[mid] <= want) lo = mid;
-      else hi = mid - 1;
+  // the sequence that holds unit `begin`, and the unit it starts at
+  int seq = 0;
+  int64_t seq_at = 0;
+  {
+    const int64_t want = idiv(begin, hkv);  // in units of one head: only the sequence is looked for
+    int64_t at = 0;
+    for (int i = 0; i < a.n_seqs; i += 32) {
+      const int n = i + lane < a.n_seqs ? (int)units(blocks(i + lane)) : 0;
+      int64_t x = n;  // inclusive sums
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      const uint32_t here = __ballot_sync(0xffffffffu, want < at + x);
+      if (here) {
+        const int src = __ffs(here) - 1;
+        seq = i + src;
+        seq_at = (at + __shfl_sync(0xffffffffu, x - n, src)) * hkv;
+        break;
+      }
+      at += __shfl_sync(0xffffffffu, x, 31);
     }
-    int64_t at = scan[lo];
-    int i = lo * per;
-    for (; i < a.n_seqs - 1; ++i) {
-      const int64_t b = blocks(i);
-      if (at + b > want) break;
-      at += b;
-    }
-    sh_seq = i;
-    sh_first = at * hkv;
-    sh_flag = 0;
   }
+  if (tid == 0) sh_flag = 0;
   __syncthreads();
-  int seq = sh_seq;
-  int64_t seq_at = sh_first;  // global block where the sequence starts
 
   unsigned char *ring = smem + wt * C::GROUP;
   int64_t *rowbuf = reinterpret_cast<int64_t *>(smem + C::OFF_ROW) + wt * C::SLOTS * TN;
@@ -291,15 +306,18 @@ k_page_attn(const PageView pg, const AttnArgs a) {
     int nq, len;
     shape(seq, nq, len);
     const int64_t nb = nq > 0 ? ((int64_t)len + C::BLOCK - 1) / C::BLOCK : 0;
-    if (pos >= seq_at + nb * hkv) {  // on to the next sequence (empty ones among them)
-      seq_at += nb * hkv;
+    const int64_t nu = units(nb);
+    if (pos >= seq_at + nu * hkv) {  // on to the next sequence (empty ones among them)
+      seq_at += nu * hkv;
       ++seq;
       continue;
     }
-    const int kvh = (int)((pos - seq_at) / nb);
-    const int64_t item0 = seq_at + kvh * nb, item1 = item0 + nb;
+    const int kvh = (int)idiv(pos - seq_at, nu);
+    const int64_t item0 = seq_at + kvh * nu, item1 = item0 + nu;
     const int64_t stop = min(end, item1);
-    const int b0 = (int)(pos - item0), nblk = (int)(stop - pos);
+    // blocks of this item's part
+    const int b0 = (int)(chunked ? idiv(nb * (pos - item0), nu) : pos - item0);
+    const int nblk = (int)(chunked ? idiv(nb * (stop - item0), nu) : stop - item0) - b0;
     const int32_t *tab = a.table + (int64_t)seq * a.width;
 
     // ---- row lookups and copies, tile by tile.  Tile t of the group is
@@ -330,7 +348,7 @@ k_page_attn(const PageView pg, const AttnArgs a) {
     // In-page offset of the tile that is copied next: a tile inside one page and
     // below the length is one run of memory, copied from one address with constant
     // offsets; others row by row.
-    int in_page = (int)(((int64_t)b0 * C::BLOCK + wt * TN) % pg.rows);
+    int in_page = (int)((uint32_t)(b0 * C::BLOCK + wt * TN) % (uint32_t)pg.rows);
     const int in_step = C::BLOCK % pg.rows;
     auto copy = [&](int t) {
       // a thread copies one chunk column of every STEP-th row
@@ -402,8 +420,8 @@ k_page_attn(const PageView pg, const AttnArgs a) {
 #pragma unroll
     for (int t = 0; t < NS - 1; ++t) copy(t);
 
-    // ---- Q fragments of this warp's rows: for bf16 k-step s holds dims 16 s ..;
-    // for 8 bits k index (s, 2 qd + e) is dim 64 j + 16 qd + 4 s + e and
+    // ---- Q fragments of this warp's rows: for 16-bit rows k-step s holds dims 16 s ..;
+    // for 8-bit ones k index (s, 2 qd + e) is dim 64 j + 16 qd + 4 s + e and
     // (s, 2 qd + 8 + e) is 2 further on, s = 0 .. 3 of the 64 dims of block j
     uint32_t qf[MT][D / 16][4];
     float fr[MT][2];  // a score's factor by row: softmax scale in log2 units, f16 scaling
@@ -418,9 +436,8 @@ k_page_attn(const PageView pg, const AttnArgs a) {
         uint32_t top = 0u;
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
-          const int lo = KIND == DHS_PAGE_BF16 ? 16 * s + 2 * qd
-                                               : 64 * (s >> 2) + 16 * qd + 4 * (s & 3);
-          const int hi = lo + (KIND == DHS_PAGE_BF16 ? 8 : 2);
+          const int lo = C::B16 ? 16 * s + 2 * qd : 64 * (s >> 2) + 16 * qd + 4 * (s & 3);
+          const int hi = lo + (C::B16 ? 8 : 2);
           const uint32_t x = on ? *reinterpret_cast<const uint32_t *>(src + lo) : 0u;
           const uint32_t y = on ? *reinterpret_cast<const uint32_t *>(src + hi) : 0u;
           qf[mt][s][half] = x;
@@ -526,6 +543,27 @@ k_page_attn(const PageView pg, const AttnArgs a) {
               for (int x = 0; x < 4; ++x) o[mt][i][x] *= f;
         }
       }
+      const unsigned char *kc = kst, *vc = vst;  // the rows as the products read them
+      if (C::CONV) {
+        unsigned char *f16 = ring + C::RING;
+#pragma unroll
+        for (int u = 0; u < 2 * TN * C::CH / (WM * 32); ++u) {
+          const int e = (gl + u * WM * 32) % (TN * C::CH), x = e / C::CH, c = e % C::CH;
+          const int v = (gl + u * WM * 32) / (TN * C::CH);  // keys, then values
+          const uint4 w = *reinterpret_cast<const uint4 *>(kst + v * C::KV + e * 16);
+          uint4 lo, hi;
+          f16_pairs<KIND>(w.x, lo.x, lo.y);
+          f16_pairs<KIND>(w.y, lo.z, lo.w);
+          f16_pairs<KIND>(w.z, hi.x, hi.y);
+          f16_pairs<KIND>(w.w, hi.z, hi.w);
+          unsigned char *dst = f16 + v * TN * RC + x * RC;
+          *reinterpret_cast<uint4 *>(dst + (((2 * c) ^ (x & 7)) << 4)) = lo;
+          *reinterpret_cast<uint4 *>(dst + (((2 * c + 1) ^ (x & 7)) << 4)) = hi;
+        }
+        kc = f16;
+        vc = f16 + TN * RC;
+        group_sync();
+      }
       const float vdown = C::W == 1 ? __uint_as_float((uint32_t)(127 - max(vref, -100)) << 23) : 1.f;
 #pragma unroll
       for (int sub = 0; sub < TN / SUB; ++sub) {
@@ -538,7 +576,7 @@ k_page_attn(const PageView pg, const AttnArgs a) {
           for (int i = 0; i < SUB / 8; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[mt][i][e] = 0.f;
-        if (KIND == DHS_PAGE_BF16) {
+        if (C::B16) {
 #pragma unroll
           for (int i = 0; i < SUB / 16; ++i)
 #pragma unroll
@@ -547,11 +585,11 @@ k_page_attn(const PageView pg, const AttnArgs a) {
               const int x = s0 + i * 16 + (lane & 7) + ((lane >> 4) << 3);
               const int c = ks * 2 + ((lane >> 3) & 1);
               uint32_t b0r, b1r, b2r, b3r;
-              ldmatrix_x4(b0r, b1r, b2r, b3r, kst + x * RB + kchunk<C>(x, c) * 16);
+              ldmatrix_x4(b0r, b1r, b2r, b3r, kc + x * RC + ((c ^ (x & 7)) << 4));
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) {
-                mma_bf16_16816(s[mt][2 * i], qf[mt][ks], b0r, b1r);
-                mma_bf16_16816(s[mt][2 * i + 1], qf[mt][ks], b2r, b3r);
+                mma_kind<KIND>(s[mt][2 * i], qf[mt][ks], b0r, b1r);
+                mma_kind<KIND>(s[mt][2 * i + 1], qf[mt][ks], b2r, b3r);
               }
             }
         } else {
@@ -584,7 +622,7 @@ k_page_attn(const PageView pg, const AttnArgs a) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < NH; ++h) {
               float2 x = make_float2(s[mt][i][2 * h], s[mt][i][2 * h + 1]);
               if (C::W == 1) x = make_float2(x.x * ks.x, x.y * ks.y);
               if (masked) {
@@ -602,7 +640,7 @@ k_page_attn(const PageView pg, const AttnArgs a) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < NH; ++h) {
             top[mt][h] = fmaxf(top[mt][h], __shfl_xor_sync(0xffffffffu, top[mt][h], 1));
             top[mt][h] = fmaxf(top[mt][h], __shfl_xor_sync(0xffffffffu, top[mt][h], 2));
             top[mt][h] *= fr[mt][h];
@@ -612,7 +650,7 @@ k_page_attn(const PageView pg, const AttnArgs a) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < NH; ++h) {
               // (a row that has seen nothing keeps its zeros)
               const float m_new = fmaxf(mx[mt][h], top[mt][h]);
               const float f = mx[mt][h] == -CUDART_INF_F ? 0.f : ex2_approx(mx[mt][h] - m_new);
@@ -630,6 +668,10 @@ k_page_attn(const PageView pg, const AttnArgs a) {
         // the largest scale); l takes the weights unrounded.  -inf - -inf must not
         // arise in a row that has seen nothing yet
         uint32_t pf[MT][SUB / 16][4];
+        if (NH == 1) {
+#pragma unroll
+          for (int i = 0; i < SUB / 16; ++i) pf[0][i][1] = pf[0][i][3] = 0u;
+        }
 #pragma unroll
         for (int i = 0; i < SUB / 8; ++i) {
           float2 vs = make_float2(1.f, 1.f);
@@ -640,7 +682,7 @@ k_page_attn(const PageView pg, const AttnArgs a) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < NH; ++h) {
               const float b = mx[mt][h] == -CUDART_INF_F ? 0.f : -mx[mt][h];
               float2 p = make_float2(ex2_approx(fmaf(s[mt][i][2 * h], fr[mt][h], b)),
                                      ex2_approx(fmaf(s[mt][i][2 * h + 1], fr[mt][h], b)));
@@ -663,17 +705,17 @@ k_page_attn(const PageView pg, const AttnArgs a) {
         // O += P V
 #pragma unroll
         for (int i = 0; i < SUB / 16; ++i) {
-          if (KIND == DHS_PAGE_BF16) {
+          if (C::B16) {
 #pragma unroll
             for (int n = 0; n < D / 16; ++n) {
               const int x = s0 + i * 16 + (lane & 15);
               const int c = n * 2 + (lane >> 4);
               uint32_t b0r, b1r, b2r, b3r;
-              ldmatrix_x4_trans(b0r, b1r, b2r, b3r, vst + x * RB + vchunk<C>(x, c) * 16);
+              ldmatrix_x4_trans(b0r, b1r, b2r, b3r, vc + x * RC + ((c ^ (x & 7)) << 4));
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) {
-                mma_bf16_16816(o[mt][2 * n], pf[mt][i], b0r, b1r);
-                mma_bf16_16816(o[mt][2 * n + 1], pf[mt][i], b2r, b3r);
+                mma_kind<KIND>(o[mt][2 * n], pf[mt][i], b0r, b1r);
+                mma_kind<KIND>(o[mt][2 * n + 1], pf[mt][i], b2r, b3r);
               }
             }
           } else {
@@ -722,7 +764,7 @@ k_page_attn(const PageView pg, const AttnArgs a) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < NH; ++h) {
         l[mt][h] += __shfl_xor_sync(0xffffffffu, l[mt][h], 1);
         l[mt][h] += __shfl_xor_sync(0xffffffffu, l[mt][h], 2);
         const int m = (wm * MT + mt) * 16 + h * 8 + ql;
@@ -735,7 +777,7 @@ k_page_attn(const PageView pg, const AttnArgs a) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < NH; ++h) {
         const int m = (wm * MT + mt) * 16 + h * 8 + ql;
         float top = -CUDART_INF_F;
 #pragma unroll
@@ -750,7 +792,7 @@ k_page_attn(const PageView pg, const AttnArgs a) {
         for (int i = 0; i < D / 8; ++i) {
           const float x = nan ? CUDART_NAN_F : o[mt][i][2 * h] * f;
           const float y = nan ? CUDART_NAN_F : o[mt][i][2 * h + 1] * f;
-          if (KIND == DHS_PAGE_BF16) {
+          if (C::B16) {
             *reinterpret_cast<float2 *>(dst + 8 * i + 2 * qd) = make_float2(x, y);
           } else {
             dst[2 * qd * (D / 8) + i] = x;
@@ -819,8 +861,8 @@ k_page_attn(const PageView pg, const AttnArgs a) {
     }
     if (pos == item0 && tid == 0) {
       // for the join: the CTAs that share the item
-      auto owner = [&](int64_t blk) {  // largest b with range(b) <= blk
-        int b = (int)min((int64_t)n_cta - 1, ((blk + 1) * n_cta - 1) / total);
+      auto owner = [&](int64_t blk) {  // largest b with range(b) <= blk (a unit)
+        int b = (int)min((int64_t)n_cta - 1, idiv((blk + 1) * n_cta - 1, total_units));
         while (b > 0 && range(b) > blk) --b;
         while (b + 1 < n_cta && range(b + 1) <= blk) ++b;
         return b;
@@ -834,63 +876,89 @@ k_page_attn(const PageView pg, const AttnArgs a) {
 }
 
 // Joins an item's parts: out = sum_p w_p O_p / sum_p w_p l_p, w_p = 2^(m_p - max m).
-// One row is shared by SPLIT warps, each with every SPLIT-th part.
+// One row is shared by SPLIT warps, each with every SPLIT-th part and a running
+// maximum of its own; eight parts' loads are under way at a time, as it is their
+// latency that the join takes.
 template <int D, int SPLIT>
 __global__ void __launch_bounds__(128)
 k_page_join(const AttnArgs a, int hkv, int width_rows) {
-  constexpr int V = D / 32;  // dims of a lane
+  constexpr int V = D / 32, AHEAD = 8;  // dims of a lane
   __shared__ float red[4][D + 2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, part0 = warp % SPLIT;
   const int64_t e = (int64_t)blockIdx.x * (4 / SPLIT) + warp / SPLIT;
-  pdl_wait();
   const bool on = e < (int64_t)a.n_seqs * hkv * a.R;
   const int m = on ? (int)(e % a.R) : 0;
   const int64_t item = on ? e / a.R : 0;
-  const int2 pl = on ? a.plan[item] : make_int2(-1, -1);
   const int seq = (int)(item / hkv), kvh = (int)(item % hkv), j = m / a.G;
   int nq = a.q_lens ? a.q_lens[seq] : a.q_len;
   nq = max(0, min(nq, a.q_len));
+  const int len = max(0, min(a.seq_lens[seq], width_rows));
+  pdl_wait();
+  const int2 pl = on ? a.plan[item] : make_int2(-1, -1);
   const bool live = pl.x >= 0 && j < nq;
-  auto at = [&](int c) {
-    return a.parts + (((int64_t)c * 2 + (c == pl.x ? 1 : 0)) * a.R + m) * (D + 2);
-  };
   float top = -CUDART_INF_F, den = 0.f, acc[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.f;
-  if (live) {
-    for (int c = pl.x + lane; c <= pl.y; c += 32) top = fmaxf(top, at(c)[D]);
+  for (int c0 = pl.x + part0; live && c0 <= pl.y; c0 += AHEAD * SPLIT) {
+    float2 ml[AHEAD], o[AHEAD][V / 2];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-#pragma unroll 8
-    for (int c = pl.x + part0; c <= pl.y; c += SPLIT) {
-      const float *src = at(c);
-      const float2 x = *reinterpret_cast<const float2 *>(src + D);
+    for (int k = 0; k < AHEAD; ++k) {
+      const int c = c0 + k * SPLIT;
+      const float *src = a.parts + (((int64_t)c * 2 + (c == pl.x ? 1 : 0)) * a.R + m) * (D + 2);
+      const bool in = c <= pl.y;
+      ml[k] = in ? *reinterpret_cast<const float2 *>(src + D) : make_float2(-CUDART_INF_F, 0.f);
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i)
+        o[k][i] = in ? *reinterpret_cast<const float2 *>(src + lane * V + 2 * i)
+                     : make_float2(0.f, 0.f);
+    }
+    float now = top;
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) now = fmaxf(now, ml[k].x);
+    const float f0 = top == -CUDART_INF_F ? (den != den ? 1.f : 0.f) : ex2_approx(top - now);
+    den *= f0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] *= f0;
+    top = now;
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
       // (a part that saw nothing weighs nothing; one of NaN scores has m = -inf too)
-      const float f = x.x == -CUDART_INF_F ? (x.y != x.y ? 1.f : 0.f) : ex2_approx(x.x - top);
-      den += x.y * f;
+      const float f = ml[k].x == -CUDART_INF_F ? (ml[k].y != ml[k].y ? 1.f : 0.f)
+                                               : ex2_approx(ml[k].x - now);
+      den += ml[k].y * f;
 #pragma unroll
-      for (int i = 0; i < V; i += 2) {
-        const float2 y = *reinterpret_cast<const float2 *>(src + lane * V + i);
-        acc[i] += y.x * f;
-        acc[i + 1] += y.y * f;
+      for (int i = 0; i < V / 2; ++i) {
+        acc[2 * i] += o[k][i].x * f;
+        acc[2 * i + 1] += o[k][i].y * f;
       }
     }
   }
   if (SPLIT > 1) {
 #pragma unroll
     for (int i = 0; i < V; ++i) red[warp][lane * V + i] = acc[i];
-    if (lane == 0) red[warp][D] = den;
+    if (lane == 0) {
+      red[warp][D] = top;
+      red[warp][D + 1] = den;
+    }
     __syncthreads();
     if (part0 != 0) return;
+    float all = top;
 #pragma unroll
-    for (int w = 1; w < SPLIT; ++w) {
+    for (int w = 1; w < SPLIT; ++w) all = fmaxf(all, red[warp + w][D]);
+    den = 0.f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] += red[warp + w][lane * V + i];
-      den += red[warp + w][D];
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < SPLIT; ++w) {
+      const float t = red[warp + w][D], d = red[warp + w][D + 1];
+      const float f = t == -CUDART_INF_F ? (d != d ? 1.f : 0.f) : ex2_approx(t - all);
+      den += d * f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] += red[warp + w][lane * V + i] * f;
     }
+    top = all;
   }
   if (!live) return;
-  const int len = max(0, min(a.seq_lens[seq], width_rows));
   const int sees = len - nq + j + 1;
   const float inv = 1.f / den;
   const int64_t row = ((int64_t)seq * a.q_len + j) * a.hq + kvh * a.G + (m - j * a.G);
@@ -914,15 +982,17 @@ int64_t plan_bytes(int32_t n_seqs, int hkv) {
   return ((int64_t)n_seqs * hkv * 8 + 255) / 256 * 256;
 }
 
-// Calls f with the configuration for R rows.  16 rows fit one warp and four
+// Calls f with the configuration for R rows.  8 rows take half of a row tile's
+// softmax, 16 rows fit one warp and four
 // token groups stream at once; more rows take more warps of the same tile, and
 // above 64 two row tiles a warp.
 template <int D, int KIND, class F>
 auto pick_rows(int R, F f) {
-  if (R <= 16) return f(Cfg<D, KIND, 1, 1>());
-  if (R <= 32) return f(Cfg<D, KIND, 2, 1>());
-  if (R <= 64) return f(Cfg<D, KIND, 4, 1>());
-  return f(Cfg<D, KIND, 4, 2>());
+  if (R <= 8) return f(Cfg<D, KIND, 1, 1, 1>());
+  if (R <= 16) return f(Cfg<D, KIND, 1, 1, 2>());
+  if (R <= 32) return f(Cfg<D, KIND, 2, 1, 2>());
+  if (R <= 64) return f(Cfg<D, KIND, 4, 1, 2>());
+  return f(Cfg<D, KIND, 4, 2, 2>());
 }
 template <class F>
 auto pick(const PageView &pg, int R, F f) {

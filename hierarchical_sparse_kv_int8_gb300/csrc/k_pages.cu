@@ -84,7 +84,8 @@ __device__ __forceinline__ void dequantise(uint32_t c, float s, uint32_t &lo, ui
   for (int i = 0; i < 4; ++i) {
     const uint32_t b = (c >> (i * 8)) & 0xFFu;
     if (KIND == DHS_PAGE_INT8) {
-      x[i] = (float)(int8_t)b * s;
+      // 2^23 + (x + 128) as bits, less 2^23 + 128 (a conversion takes the slow pipe)
+      x[i] = __fsub_rn(__uint_as_float(0x4B000000u | (b ^ 0x80u)), 8388736.f) * s;
     } else {
       // the code's seven lower bits at a float's exponent and mantissa give the
       // value times 2^-120, subnormals included
