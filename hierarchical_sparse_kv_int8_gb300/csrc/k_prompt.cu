@@ -66,7 +66,11 @@ struct PrCfg {
   static constexpr int HALVES = D / 64;
   static constexpr int TILE = 128 * D * 2;          // a Q, K or V tile
   static constexpr int HALF = 128 * 128;            // 64 dims of its 128 rows
-  static constexpr int SLOTS = D == 128 ? 5 : 8;    // K and V tiles in flight
+  // K and V tiles in flight, in a ring each: who waits for a ring's copies waits for
+  // every one of them.  (A wait that skips a phase of its barrier, as for every other
+  // copy of a common ring, takes the phase before last for the one it waits for
+  // while the last is still open.)
+  static constexpr int KS = D == 128 ? 3 : 4, VS = D == 128 ? 2 : 4, SLOTS = KS + VS;
   static constexpr int OFF_KV = 2 * TILE;
   static constexpr int OFF_RED = OFF_KV + SLOTS * TILE;  // float [2 tiles][2 halves][128]
   static constexpr int OFF_BAR = OFF_RED + 2 * 2 * 128 * 4;
@@ -270,32 +274,43 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
       }
     }
   };
-  // K of the n-th tile is copy 2 n of the ring, V copy 2 n + 1
-  auto slot = [&](int c) { return c % C::SLOTS; };
-  auto phase = [&](int c) { return (uint32_t)((c / C::SLOTS) & 1); };
+  // slot of the n-th K or V tile, and the parity of its use of the slot
+  auto kslot = [&](int n) { return n % C::KS; };
+  auto vslot = [&](int n) { return C::KS + n % C::VS; };
+  auto kpar = [&](int n) { return (uint32_t)((n / C::KS) & 1); };
+  auto vpar = [&](int n) { return (uint32_t)((n / C::VS) & 1); };
 
   if (warp >= kMmaWarp) {
     if (warp == kLoadWarp) {
       // ------------------------------------------------------------- copies
       if (lane == 0 && nt > 0) {
         const int ntile = n1 > 0 ? 2 : 1;
+        int issued[2] = {0, 0};
         mbar_arrive_expect_tx(q_full, (uint32_t)(ntile * C::HALVES * a.G * a.tpt * 128));
         for (int i = 0; i < ntile; ++i)
           for (int h = 0; h < C::HALVES; ++h)
             tma_load_3d(smem + i * C::TILE + h * C::HALF, &mq, h * 64, kvh * a.G,
                         q0 + (i ? tok1 : tok0), q_full);
-        int c = 0;
-        for (; c < 2 * nt; ++c) {
-          if (c >= C::SLOTS) wait(&empty[slot(c)], phase(c) ^ 1u);
+        int n = 0;
+        for (; n < nt; ++n) {
+          for (int w = 0; w < 2; ++w) {  // K, then V
+            const int t = w ? vslot(n) : kslot(n);
+            if (n >= (w ? C::VS : C::KS)) wait(&empty[t], (w ? vpar(n) : kpar(n)) ^ 1u);
+            if (*abort_v) break;
+            mbar_arrive_expect_tx(&full[t], (uint32_t)C::TILE);
+            for (int h = 0; h < C::HALVES; ++h)
+              tma_load_3d(smem + C::OFF_KV + t * C::TILE + h * C::HALF, w ? &mv : &mk, h * 64, kvh,
+                          k0 + (t0 + n) * kPrN, &full[t]);
+            issued[w] = n + 1;
+          }
           if (*abort_v) break;
-          mbar_arrive_expect_tx(&full[slot(c)], (uint32_t)C::TILE);
-          for (int h = 0; h < C::HALVES; ++h)
-            tma_load_3d(smem + C::OFF_KV + slot(c) * C::TILE + h * C::HALF, (c & 1) ? &mv : &mk,
-                        h * 64, kvh, k0 + (t0 + (c >> 1)) * kPrN, &full[slot(c)]);
         }
         // every copy has landed before the CTA ends
         wait(q_full, 0u, true);
-        for (int i = max(0, c - C::SLOTS); i < c; ++i) wait(&full[slot(i)], phase(i), true);
+        for (int i = max(0, issued[0] - C::KS); i < issued[0]; ++i)
+          wait(&full[kslot(i)], kpar(i), true);
+        for (int i = max(0, issued[1] - C::VS); i < issued[1]; ++i)
+          wait(&full[vslot(i)], vpar(i), true);
       }
     } else if (warp == kMmaWarp) {
       // ------------------------------------------------------------- products
@@ -305,7 +320,7 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
         const uint32_t sQ = smem_u32(smem), sKV = smem_u32(smem + C::OFF_KV);
         auto qk = [&](int i, int n) {
           const uint64_t q = tc_desc_sw128(sQ + i * C::TILE, 16, 1024);
-          const uint64_t k = tc_desc_sw128(sKV + slot(2 * n) * C::TILE, 16, 1024);
+          const uint64_t k = tc_desc_sw128(sKV + kslot(n) * C::TILE, 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t o = ((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4;
@@ -314,19 +329,19 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
           warp_commit(&s_full[i]);
         };
         auto pv = [&](int i, int n) {
-          const uint64_t v = tc_desc_sw128(sKV + slot(2 * n + 1) * C::TILE, C::HALF, 1024);
+          const uint64_t v = tc_desc_sw128(sKV + vslot(n) * C::TILE, C::HALF, 1024);
 #pragma unroll
           for (int kk = 0; kk < kPrN / 16; ++kk)
             warp_mma_ta(2 * kPrN + i * D, i * kPrN + kk * 8, v + kk * 128, kIdescPV, n | kk);
-          warp_commit(&pv_done[i]);
+          if (n + 1 == (i ? n1 : n0)) warp_commit(&pv_done[i]);
         };
         wait(q_full, 0u);
-        wait(&full[slot(0)], phase(0));
+        wait(&full[kslot(0)], 0u);
         __syncwarp();
         tc_fence_after();
         if (n0 > 0) qk(0, 0);
         if (n1 > 0) qk(1, 0);
-        warp_commit(&empty[slot(0)]);
+        warp_commit(&empty[kslot(0)]);
         for (int n = 0; n < nt && !__any_sync(0xffffffffu, *abort_v); ++n) {
           wait(&clean[n % C::CLEAN], (uint32_t)((n / C::CLEAN) & 1));
           __syncwarp();
@@ -340,14 +355,14 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
               pv(i, n);
             }
             if (n + 1 < ni) {
-              wait(&full[slot(2 * n + 2)], phase(2 * n + 2));
+              wait(&full[kslot(n + 1)], kpar(n + 1));
               __syncwarp();
               tc_fence_after();
               qk(i, n + 1);
             }
           }
-          warp_commit(&empty[slot(2 * n + 1)]);
-          if (n + 1 < nt) warp_commit(&empty[slot(2 * n + 2)]);
+          warp_commit(&empty[vslot(n)]);
+          if (n + 1 < nt) warp_commit(&empty[kslot(n + 1)]);
         }
         warp_commit(mma_done);
         wait(mma_done, 0u, true);
@@ -356,12 +371,11 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
       // ------------------------------------------------------------- values
       const int common = off + tok0;  // keys that every row of the CTA sees
       for (int n = 0; n < nt; ++n) {
-        const int c = 2 * n + 1;
-        wait(&full[slot(c)], phase(c));
+        wait(&full[vslot(n)], vpar(n));
         if (__any_sync(0xffffffffu, *abort_v)) break;
         const int r0 = max(0, common - (t0 + n) * kPrN);
         if (r0 < kPrN) {
-          unsigned char *v = smem + C::OFF_KV + slot(c) * C::TILE;
+          unsigned char *v = smem + C::OFF_KV + vslot(n) * C::TILE;
           const int inside = nk - (t0 + n) * kPrN;  // rows of this sequence
           // row r's 64 dims of half h are the 128 bytes at h * HALF + r * 128
           bool found = false;
@@ -489,7 +503,7 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
     named_sync(pair, 64);
     l += red[(hg ^ 1) * 128 + m];
     if (ni > 0) {
-      wait(&pv_done[i], (uint32_t)((ni - 1) & 1));
+      wait(&pv_done[i], 0u);
       __syncwarp();
       tc_fence_after();
     }

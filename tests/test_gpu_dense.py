@@ -600,6 +600,34 @@ def test_prompt_masked_places_do_not_matter(torch, dhs, d):
     assert torch.isnan(out[:60]).all() and torch.isnan(out[260:]).all()
 
 
+def test_prompt_from_cold_memory(torch, dhs):
+    """The first tiles come from memory slowly and in any order: every run equals the
+    others bit by bit, and sampled rows the oracle."""
+    from oracle import dense_oracle as oracle
+    sizes = [1500, 1856, 300, 1100, 700]
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for hq, hkv, d in ((32, 8, 128), (8, 8, 64)):
+        n = sum(sizes)
+        q, k, v = (torch.randn((n, h, d), device="cuda").bfloat16() for h in (hq, hkv, hkv))
+        cu = torch.tensor([0] + sizes).cumsum(0).int().cuda()
+        ws = dhs.prompt_workspace(q, k, len(sizes))
+        runs = []
+        for _ in range(6):
+            out, lse = torch.zeros_like(q), torch.zeros((n, hq), device="cuda")
+            flush.zero_()
+            torch.cuda.synchronize()
+            dhs.prompt_attend(q, k, v, cu, cu, out, lse=lse, workspace=ws)
+            runs.append((out, lse))
+        for out, lse in runs[1:]:
+            assert torch.equal(out, runs[0][0]) and torch.equal(lse, runs[0][1])
+        for i, ln in enumerate(sizes):
+            at = int(cu[i])
+            for u in (0, ln // 3, ln - 1):
+                want = oracle.attend(_np(q[at + u:at + u + 1]), _np(k[at:at + u + 1]), _np(v[at:at + u + 1]),
+                                     1 / math.sqrt(d))
+                _close(_np(runs[0][0][at + u:at + u + 1]), _np(runs[0][1][at + u:at + u + 1]), want, d, u + 1)
+
+
 def test_prompt_minus_infinity_scores(torch, dhs):
     n, d = 140, 64
     q, k, v = (torch.randn((n, 1, d)).bfloat16().cuda() for _ in range(3))
