@@ -47,6 +47,7 @@ constexpr int kPrM = 128, kPrN = 128, kPrH = kPrN / 2;
 constexpr int kMmaWarp = 16, kLoadWarp = 17, kCleanWarp = 18;
 constexpr int kPrSpin = 1 << 20;
 constexpr float kPrRescale = 8.f;
+constexpr int kPrSplits = 64;      // key splits at most
 constexpr uint32_t kPrCols = 512;  // S0, S1 (P over them), O0, O1
 
 struct PromptArgs {
@@ -253,8 +254,9 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
   const int all = max(0, off + max(last0, last1));           // keys any row sees
   const int T = (all + kPrN - 1) / kPrN;
   // this CTA's key tiles, and those of either row tile
-  const int t0 = (int)((int64_t)T * blockIdx.y / a.nsplit);
-  const int t1 = (int)((int64_t)T * (blockIdx.y + 1) / a.nsplit);
+  // (T is below 2^24 and there are at most kPrSplits parts: 32 bits hold the products)
+  const int t0 = a.nsplit == 1 ? 0 : (int)((uint32_t)T * blockIdx.y / (uint32_t)a.nsplit);
+  const int t1 = a.nsplit == 1 ? T : (int)((uint32_t)T * (blockIdx.y + 1) / (uint32_t)a.nsplit);
   const int e0 = min(t1, (max(0, off + last0) + kPrN - 1) / kPrN);
   const int e1 = last1 >= tok1 ? min(t1, (max(0, off + last1) + kPrN - 1) / kPrN) : t0;
   const int n0 = max(0, e0 - t0), n1 = max(0, e1 - t0), nt = max(n0, n1);
@@ -377,9 +379,24 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
         if (r0 < kPrN) {
           unsigned char *v = smem + C::OFF_KV + vslot(n) * C::TILE;
           const int inside = nk - (t0 + n) * kPrN;  // rows of this sequence
-          // row r's 64 dims of half h are the 128 bytes at h * HALF + r * 128
-          bool found = false;
+          // Row r's 64 dims of half h are the 128 bytes at h * HALF + r * 128.  An
+          // exponent of ones plus one carries into the sign's place: eight values cost
+          // a dozen instructions, and the slow loop runs only if some are not finite.
+          uint32_t any = 0u;
+#pragma unroll 8
           for (int e = r0 * 8 + (warp - kCleanWarp) * 32 + lane; e < kPrN * 8; e += 64) {
+#pragma unroll
+            for (int h = 0; h < C::HALVES; ++h) {
+              const uint4 w = *reinterpret_cast<const uint4 *>(v + h * C::HALF + e * 16);
+              any |= (w.x & 0x7F807F80u) + 0x00800080u;
+              any |= (w.y & 0x7F807F80u) + 0x00800080u;
+              any |= (w.z & 0x7F807F80u) + 0x00800080u;
+              any |= (w.w & 0x7F807F80u) + 0x00800080u;
+            }
+          }
+          bool found = false;
+          for (int e = r0 * 8 + (warp - kCleanWarp) * 32 + lane;
+               (any & 0x80008000u) != 0u && e < kPrN * 8; e += 64) {
 #pragma unroll
             for (int h = 0; h < C::HALVES; ++h) {
               uint4 *at = reinterpret_cast<uint4 *>(v + h * C::HALF + e * 16);
@@ -507,12 +524,18 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
       __syncwarp();
       tc_fence_after();
     }
-    // every thread of the row tile's warps reads tensor memory; valid rows write
+    // Every thread of the row tile's warps reads tensor memory.  The rows go out
+    // through shared memory, over the row tile's queries (no product reads them any
+    // more), so that a store covers whole lines: from registers it would touch 32
+    // of them, and the last of a CTA's stores left 3 us after its last product.
     const int64_t row = (int64_t)(q0 + tok) * a.hq + kvh * a.G + h;
     const bool patch = *(volatile int *)&bad_values != 0;
     const int common = off + tok0;
     const float inv = 1.f / l;  // only scores of -inf: 0 / 0
     float *part = a.parts + ((int64_t)blockIdx.y * a.n_q * a.hq + row) * (D + 2);
+    // this warp's 32 rows x D / 2 columns, in bf16, over the row tile's own queries
+    constexpr int OB = D;  // bytes of half a row
+    unsigned char *stage = smem + i * C::TILE + (hg * 4 + (warp & 3)) * 32 * OB;
 #pragma unroll 1
     for (int c = 0; c < D / 2; c += 16) {
       const int col = hg * (D / 2) + c;
@@ -537,12 +560,12 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
           }
         }
       }
-      if (!valid) continue;
       if (a.nsplit > 1) {
+        if (valid)
 #pragma unroll
-        for (int x = 0; x < 16; x += 2)
-          *reinterpret_cast<float2 *>(part + col + x) =
-              make_float2(__uint_as_float(o[x]), __uint_as_float(o[x + 1]));
+          for (int x = 0; x < 16; x += 2)
+            *reinterpret_cast<float2 *>(part + col + x) =
+                make_float2(__uint_as_float(o[x]), __uint_as_float(o[x + 1]));
       } else {
 #pragma unroll
         for (int x = 0; x < 16; x += 8) {
@@ -553,7 +576,24 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
             w.z = pack_bf16(__uint_as_float(o[x + 4]) * inv, __uint_as_float(o[x + 5]) * inv);
             w.w = pack_bf16(__uint_as_float(o[x + 6]) * inv, __uint_as_float(o[x + 7]) * inv);
           }
-          *reinterpret_cast<uint4 *>(a.out + row * D + col + x) = w;
+          // 16-byte chunk, rotated by the row so that eight rows meet no bank twice
+          const int ch = (c + x) / 8;
+          *reinterpret_cast<uint4 *>(stage + lane * OB + ((ch + lane) % (OB / 16)) * 16) = w;
+        }
+      }
+    }
+    if (a.nsplit == 1) {
+      __syncwarp();
+      constexpr int CH = OB / 16;  // chunks of a row; 32 / CH rows a store
+      const int tok_i = i ? tok1 : tok0;
+#pragma unroll
+      for (int x = 0; x < 32; x += 32 / CH) {
+        const int r = x + lane / CH, ch = lane % CH;
+        const int mm = (warp & 3) * 32 + r, tl = mm / a.G;
+        if (tl < a.tpt && tok_i + tl < nq) {
+          const int64_t to = (int64_t)(q0 + tok_i + tl) * a.hq + kvh * a.G + (mm - tl * a.G);
+          *reinterpret_cast<uint4 *>(a.out + to * D + hg * (D / 2) + ch * 8) =
+              *reinterpret_cast<const uint4 *>(stage + r * OB + ((ch + r) % CH) * 16);
         }
       }
     }
@@ -636,7 +676,7 @@ int prompt_splits(int64_t n_q, int64_t n_k, int32_t n_seqs, int hq, int hkv, int
   const int64_t ctas = prompt_tiles(n_q, n_seqs, hq / hkv) * hkv;
   const int64_t fill = sms / std::max<int64_t>(1, ctas);
   const int64_t room = n_k / n_seqs / (4 * kPrN);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(fill, room), 64));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(fill, room), kPrSplits));
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
