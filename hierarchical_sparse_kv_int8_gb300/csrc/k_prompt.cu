@@ -59,6 +59,8 @@ struct PromptArgs {
   int32_t *err;
   int64_t n_q, n_k;
   int n_seqs, hq, hkv, G, tpt, nsplit;
+  int64_t most;              // row-tile pairs there can be
+  int out32;                 // out lies on 32-byte boundaries
   float scale_log2;
 };
 
@@ -76,10 +78,11 @@ struct PrCfg {
   static constexpr int OFF_RED = OFF_KV + SLOTS * TILE;  // float [2 tiles][2 halves][128]
   static constexpr int OFF_BAR = OFF_RED + 2 * 2 * 128 * 4;
   static constexpr int CLEAN = 4;                   // value tiles gone over and not yet used, at most
-  static constexpr int BARS = 2 + 2 * SLOTS + CLEAN + 6;
+  static constexpr int BARS = 3 + 2 * SLOTS + CLEAN + 8 + 4;
   static constexpr int OFF_TMEM = OFF_BAR + BARS * 8;
-  static constexpr int OFF_MISC = OFF_TMEM + 16;    // int [2]
-  static constexpr int SMEM = OFF_MISC + 16;
+  static constexpr int OFF_MISC = OFF_TMEM + 16;    // int [4]: abort, -, bad values by item parity
+  static constexpr int OFF_ITEM = OFF_MISC + 16;    // PromptItem [2]
+  static constexpr int SMEM = OFF_ITEM + 2 * 64;
 };
 static_assert(PrCfg<128>::SMEM <= 227 * 1024, "shared memory of the prompt kernel");
 
@@ -154,6 +157,96 @@ __device__ __forceinline__ bool prompt_seq(const PromptArgs &a, int i, int &q0, 
   return true;
 }
 
+// One piece of work: two row tiles of a sequence and the key tiles they walk.
+struct PromptItem {
+  int q0, nq, k0, nk;   // the sequence; q0 < 0: no more work
+  int tok0, kvh, part;  // row tile 0's first token, kv head, key split
+  int t0, n0, n1;       // first key tile, and how many either row tile walks
+};
+static_assert(sizeof(PromptItem) <= 64, "");
+
+// The items of CTA b: items are ordered by the tile's place in its sequence, the
+// last places (the longest walks) first, over all sequences, kv heads and key
+// splits; the CTAs take them in turn, forth and back, which balances them within
+// about one short item.  All lanes of a warp; the next item comes back in lane-uniform
+// registers.
+struct PromptSchedule {
+  const PromptArgs &a;
+  int lane, span, q0, nq, k0, nk, tiles, top;
+  int64_t items;
+
+  __device__ int load(int i) {
+    q0 = nq = k0 = nk = 0;
+    if (i < a.n_seqs) prompt_seq(a, i, q0, nq, k0, nk);
+    return (nq + span - 1) / span;
+  }
+  __device__ PromptSchedule(const PromptArgs &args, int l) : a(args), lane(l), span(2 * args.tpt) {
+    int64_t total = 0;
+    top = 0;
+    for (int i = 0; i < a.n_seqs; i += 32) {
+      tiles = load(i + lane);  // (32 sequences or fewer stay in registers)
+      total += (int64_t)__reduce_add_sync(0xffffffffu, (unsigned)tiles);
+      top = max(top, __reduce_max_sync(0xffffffffu, tiles));
+    }
+    items = min(total, a.most) * a.hkv * a.nsplit;
+  }
+  // tiles whose place in their sequence is j or later
+  __device__ int64_t from(int j) {
+    int64_t n = 0;
+    for (int i = 0; i < a.n_seqs; i += 32) {
+      const int x = a.n_seqs > 32 ? load(i + lane) : tiles;
+      n += (int64_t)__reduce_add_sync(0xffffffffu, (unsigned)max(0, x - j));
+    }
+    return n;
+  }
+  __device__ bool item(int k, PromptItem &it) {
+    const int64_t w = (int64_t)k * gridDim.x +
+                      (k & 1 ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
+    if (w >= items) return false;
+    const int64_t per = (int64_t)a.hkv * a.nsplit;
+    const int t = (int)(w / per), in = (int)(w - t * per);
+    it.kvh = in % a.hkv;
+    it.part = in / a.hkv;
+    it.q0 = it.nq = it.k0 = it.nk = 0;
+    // the place: from(place + 1) <= t < from(place)
+    int lo = 0, hi = top - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (from(mid) > t) lo = mid;
+      else hi = mid - 1;
+    }
+    // the sequence: the (t - from(place + 1))-th of those that have it
+    int nth = (int)(t - from(lo + 1));
+    for (int i = 0; i < a.n_seqs; i += 32) {
+      const int x = a.n_seqs > 32 ? load(i + lane) : tiles;
+      const uint32_t has = __ballot_sync(0xffffffffu, x > lo);
+      if (nth < __popc(has)) {
+        const bool me = x > lo && __popc(has & ((1u << lane) - 1u)) == nth;
+        const int src = __ffs(__ballot_sync(0xffffffffu, me)) - 1;
+        it.q0 = __shfl_sync(0xffffffffu, q0, src);
+        it.nq = __shfl_sync(0xffffffffu, nq, src);
+        it.k0 = __shfl_sync(0xffffffffu, k0, src);
+        it.nk = __shfl_sync(0xffffffffu, nk, src);
+        break;
+      }
+      nth -= __popc(has);
+    }
+    it.tok0 = lo * span;
+    const int off = it.nk - it.nq + 1, tok1 = it.tok0 + a.tpt;
+    const int last0 = min(tok1, it.nq) - 1, last1 = min(tok1 + a.tpt, it.nq) - 1;
+    // key tiles that any row sees, this split's, and either row tile's (T is below
+    // 2^24 and there are at most kPrSplits parts: 32 bits hold the products)
+    const int T = (max(0, off + max(last0, last1)) + kPrN - 1) / kPrN;
+    it.t0 = a.nsplit == 1 ? 0 : (int)((uint32_t)T * it.part / (uint32_t)a.nsplit);
+    const int t1 = a.nsplit == 1 ? T : (int)((uint32_t)T * (it.part + 1) / (uint32_t)a.nsplit);
+    const int e0 = min(t1, (max(0, off + last0) + kPrN - 1) / kPrN);
+    const int e1 = last1 >= tok1 ? min(t1, (max(0, off + last1) + kPrN - 1) / kPrN) : it.t0;
+    it.n0 = max(0, e0 - it.t0);
+    it.n1 = max(0, e1 - it.t0);
+    return true;
+  }
+};
+
 template <int D>
 __global__ void __launch_bounds__(kPrThreads, 1)
 k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -162,7 +255,10 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
   // no static shared memory: the dynamic part starts on the boundary it asks for
   extern __shared__ __align__(1024) unsigned char smem[];
   int *misc = reinterpret_cast<int *>(smem + C::OFF_MISC);
-  int &abort_flag = misc[0], &bad_values = misc[1];
+  volatile int *abort_v = misc, *bad_values = misc + 2;
+  auto item_of = [&](int k) -> PromptItem & {
+    return *reinterpret_cast<PromptItem *>(smem + C::OFF_ITEM + (k & 1) * 64);
+  };
   if ((smem_u32(smem) & 1023u) != 0u) {  // (the swizzle pattern follows address bits)
     page_error(a.err, DC_CAPACITY, DHS_SITE_PROMPT_ATTEND);
     return;
@@ -170,27 +266,29 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
-  uint64_t *q_full = bars, *full = bars + 1, *empty = full + C::SLOTS, *clean = empty + C::SLOTS;
-  uint64_t *s_full = clean + C::CLEAN, *p_full = s_full + 2, *pv_done = s_full + 4;
-  uint64_t *mma_done = s_full + 6;
+  uint64_t *q_full = bars, *q_empty = bars + 1, *mma_done = bars + 2, *full = bars + 3,
+           *empty = full + C::SLOTS, *clean = empty + C::SLOTS;
+  uint64_t *s_full = clean + C::CLEAN, *p_full = s_full + 2, *pv_done = s_full + 4,
+           *o_empty = s_full + 6, *item_full = s_full + 8, *item_empty = s_full + 10;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_TMEM);
-  volatile int *abort_v = &abort_flag;
-  // set up while the offsets are on their way
   if (tid == kLoadWarp * 32) {
     mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(mma_done, 1);
     for (int i = 0; i < C::SLOTS; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < C::CLEAN; ++i) mbar_init(&clean[i], 2);
-    mbar_init(mma_done, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], kPrSoftmax / 64);  // one arrival per warp
+      mbar_init(&p_full[i], kPrSoftmax / 64);   // one arrival per warp
       mbar_init(&pv_done[i], 1);
+      mbar_init(&o_empty[i], kPrSoftmax / 64);
+      mbar_init(&item_full[i], 1);
+      mbar_init(&item_empty[i], kPrSoftmax / 32 + 3);  // all warps but the loader's
     }
-    abort_flag = 0;
-    bad_values = 0;
+    for (int i = 0; i < 4; ++i) misc[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     fence_proxy_async_smem();
   }
@@ -200,67 +298,9 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
     tma_prefetch(&mk);
     tma_prefetch(&mv);
   }
-  // ---- which sequence and tile: row tiles of all sequences laid end to end, the
-  // last (longest) first, the kv heads of a tile next to one another.  Every warp
-  // looks for itself, 32 sequences at a time: first their number of tiles, then the
-  // sequence (32 sequences or fewer are read once).
-  const int kvh = blockIdx.x % a.hkv;
-  const int span = 2 * a.tpt;  // tokens of a CTA
-  int q0 = 0, nq = 0, k0 = 0, nk = 0, tile = -1;
-  {
-    auto tiles = [&](int i) {
-      q0 = nq = k0 = nk = 0;
-      if (i < a.n_seqs) prompt_seq(a, i, q0, nq, k0, nk);
-      return (nq + span - 1) / span;
-    };
-    int total = 0, n = 0;
-    for (int i = 0; i < a.n_seqs; i += 32) {
-      n = tiles(i + lane);
-      total += __reduce_add_sync(0xffffffffu, n);
-    }
-    const int want = total - 1 - (int)(blockIdx.x / a.hkv);
-    for (int i = 0, at = 0; i < a.n_seqs && want >= 0; i += 32) {
-      if (a.n_seqs > 32) n = tiles(i + lane);
-      int x = n;  // inclusive sums
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      const uint32_t here = __ballot_sync(0xffffffffu, want < at + x);
-      if (here) {
-        const int src = __ffs(here) - 1;
-        tile = want - at - __shfl_sync(0xffffffffu, x - n, src);
-        q0 = __shfl_sync(0xffffffffu, q0, src);
-        nq = __shfl_sync(0xffffffffu, nq, src);
-        k0 = __shfl_sync(0xffffffffu, k0, src);
-        nk = __shfl_sync(0xffffffffu, nk, src);
-        break;
-      }
-      at += __shfl_sync(0xffffffffu, x, 31);
-    }
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (tile < 0) {  // the grid covers the largest number of tiles there can be
-    if (warp == kMmaWarp) tmem_dealloc(*tmem_slot, kPrCols);
-    return;
-  }
-  const int tok0 = tile * span;              // of the sequence
-  const int off = nk - nq + 1;                  // query u sees keys 0 .. off + u - 1
-  const int tok1 = tok0 + a.tpt;                // row tile 1's first token
-  const int last0 = min(tok1, nq) - 1, last1 = min(tok1 + a.tpt, nq) - 1;
-  const int all = max(0, off + max(last0, last1));           // keys any row sees
-  const int T = (all + kPrN - 1) / kPrN;
-  // this CTA's key tiles, and those of either row tile
-  // (T is below 2^24 and there are at most kPrSplits parts: 32 bits hold the products)
-  const int t0 = a.nsplit == 1 ? 0 : (int)((uint32_t)T * blockIdx.y / (uint32_t)a.nsplit);
-  const int t1 = a.nsplit == 1 ? T : (int)((uint32_t)T * (blockIdx.y + 1) / (uint32_t)a.nsplit);
-  const int e0 = min(t1, (max(0, off + last0) + kPrN - 1) / kPrN);
-  const int e1 = last1 >= tok1 ? min(t1, (max(0, off + last1) + kPrN - 1) / kPrN) : t0;
-  const int n0 = max(0, e0 - t0), n1 = max(0, e1 - t0), nt = max(n0, n1);
-
   // All 512 columns are this CTA's, so they start at column 0 (lane 0), and the
   // addresses below are constants.
   constexpr uint32_t tmem = 0u;
@@ -276,109 +316,166 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
       }
     }
   };
-  // slot of the n-th K or V tile, and the parity of its use of the slot
-  auto kslot = [&](int n) { return n % C::KS; };
-  auto vslot = [&](int n) { return C::KS + n % C::VS; };
-  auto kpar = [&](int n) { return (uint32_t)((n / C::KS) & 1); };
-  auto vpar = [&](int n) { return (uint32_t)((n / C::VS) & 1); };
+  auto given_up = [&]() { return __any_sync(0xffffffffu, *abort_v) != 0; };
+  // Slot of the n-th K or V tile since the start, and the parity of its use.  (All
+  // counts below run over a CTA's items: every wait is for the phase after the one
+  // that its waiter waited for last.)
+  auto kslot = [&](uint32_t n) { return n % C::KS; };
+  auto vslot = [&](uint32_t n) { return C::KS + n % C::VS; };
+  auto kpar = [&](uint32_t n) { return (n / C::KS) & 1u; };
+  auto vpar = [&](uint32_t n) { return (n / C::VS) & 1u; };
+  auto item_par = [&](int k) { return (uint32_t)(k >> 1) & 1u; };
+  // the k-th item, read and released by every warp but the loader's
+  auto take = [&](int k) {
+    wait(&item_full[k & 1], item_par(k));
+    __syncwarp();
+    const PromptItem it = item_of(k);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&item_empty[k & 1]);
+    return it;
+  };
 
-  if (warp >= kMmaWarp) {
-    if (warp == kLoadWarp) {
-      // ------------------------------------------------------------- copies
+  if (warp == kLoadWarp) {
+    // --------------------------------------------------------- items and copies
+    PromptSchedule plan(a, lane);
+    uint32_t kn = 0, vn = 0, qn = 0;  // copies issued
+    for (int k = 0;; ++k) {
+      PromptItem it;
+      const bool more = plan.item(k, it);
+      if (!more) it.q0 = -1;
+      if (k >= 2) wait(&item_empty[k & 1], item_par(k) ^ 1u);
+      __syncwarp();
+      if (given_up()) break;
+      if (lane == 0) {
+        item_of(k) = it;
+        mbar_arrive(&item_full[k & 1]);
+      }
+      if (!more) break;
+      const int nt = max(it.n0, it.n1);
       if (lane == 0 && nt > 0) {
-        const int ntile = n1 > 0 ? 2 : 1;
-        int issued[2] = {0, 0};
-        mbar_arrive_expect_tx(q_full, (uint32_t)(ntile * C::HALVES * a.G * a.tpt * 128));
-        for (int i = 0; i < ntile; ++i)
-          for (int h = 0; h < C::HALVES; ++h)
-            tma_load_3d(smem + i * C::TILE + h * C::HALF, &mq, h * 64, kvh * a.G,
-                        q0 + (i ? tok1 : tok0), q_full);
-        int n = 0;
-        for (; n < nt; ++n) {
-          for (int w = 0; w < 2; ++w) {  // K, then V
-            const int t = w ? vslot(n) : kslot(n);
-            if (n >= (w ? C::VS : C::KS)) wait(&empty[t], (w ? vpar(n) : kpar(n)) ^ 1u);
-            if (*abort_v) break;
-            mbar_arrive_expect_tx(&full[t], (uint32_t)C::TILE);
+        const int ntile = it.n1 > 0 ? 2 : 1;
+        if (qn > 0) wait(q_empty, (qn - 1) & 1u);
+        if (!*abort_v) {
+          mbar_arrive_expect_tx(q_full, (uint32_t)(ntile * C::HALVES * a.G * a.tpt * 128));
+          for (int i = 0; i < ntile; ++i)
             for (int h = 0; h < C::HALVES; ++h)
-              tma_load_3d(smem + C::OFF_KV + t * C::TILE + h * C::HALF, w ? &mv : &mk, h * 64, kvh,
-                          k0 + (t0 + n) * kPrN, &full[t]);
-            issued[w] = n + 1;
-          }
+              tma_load_3d(smem + i * C::TILE + h * C::HALF, &mq, h * 64, it.kvh * a.G,
+                          it.q0 + it.tok0 + i * a.tpt, q_full);
+          ++qn;
+        }
+        for (int n = 0; n < 2 * nt && !*abort_v; ++n) {  // K, V, K, V, ...
+          const bool v = n & 1;
+          const uint32_t c = v ? vn : kn, t = v ? vslot(c) : kslot(c);
+          if (c >= (uint32_t)(v ? C::VS : C::KS)) wait(&empty[t], (v ? vpar(c) : kpar(c)) ^ 1u);
           if (*abort_v) break;
+          mbar_arrive_expect_tx(&full[t], (uint32_t)C::TILE);
+          for (int h = 0; h < C::HALVES; ++h)
+            tma_load_3d(smem + C::OFF_KV + t * C::TILE + h * C::HALF, v ? &mv : &mk, h * 64, it.kvh,
+                        it.k0 + (it.t0 + (n >> 1)) * kPrN, &full[t]);
+          if (v) ++vn;
+          else ++kn;
         }
-        // every copy has landed before the CTA ends
-        wait(q_full, 0u, true);
-        for (int i = max(0, issued[0] - C::KS); i < issued[0]; ++i)
-          wait(&full[kslot(i)], kpar(i), true);
-        for (int i = max(0, issued[1] - C::VS); i < issued[1]; ++i)
-          wait(&full[vslot(i)], vpar(i), true);
       }
-    } else if (warp == kMmaWarp) {
-      // ------------------------------------------------------------- products
-      if (nt > 0) {
-        constexpr uint32_t kIdescQK = tc_idesc_bf16(kPrM, kPrN, 0, 0);
-        constexpr uint32_t kIdescPV = tc_idesc_bf16(kPrM, D, 0, 1);
-        const uint32_t sQ = smem_u32(smem), sKV = smem_u32(smem + C::OFF_KV);
-        auto qk = [&](int i, int n) {
-          const uint64_t q = tc_desc_sw128(sQ + i * C::TILE, 16, 1024);
-          const uint64_t k = tc_desc_sw128(sKV + kslot(n) * C::TILE, 16, 1024);
+      __syncwarp();
+    }
+    if (lane == 0) {
+      // every copy has landed before the CTA ends
+      if (qn > 0) wait(q_full, (qn - 1) & 1u, true);
+      for (uint32_t i = kn > C::KS ? kn - C::KS : 0; i < kn; ++i) wait(&full[kslot(i)], kpar(i), true);
+      for (uint32_t i = vn > C::VS ? vn - C::VS : 0; i < vn; ++i) wait(&full[vslot(i)], vpar(i), true);
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ----------------------------------------------------------------- products
+    constexpr uint32_t kIdescQK = tc_idesc_bf16(kPrM, kPrN, 0, 0);
+    constexpr uint32_t kIdescPV = tc_idesc_bf16(kPrM, D, 0, 1);
+    const uint32_t sQ = smem_u32(smem), sKV = smem_u32(smem + C::OFF_KV);
+    auto qk = [&](int i, uint32_t c) {
+      const uint64_t q = tc_desc_sw128(sQ + i * C::TILE, 16, 1024);
+      const uint64_t k = tc_desc_sw128(sKV + kslot(c) * C::TILE, 16, 1024);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t o = ((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4;
-            warp_mma(i * kPrN, q + o, k + o, kIdescQK, kk);
-          }
-          warp_commit(&s_full[i]);
-        };
-        auto pv = [&](int i, int n) {
-          const uint64_t v = tc_desc_sw128(sKV + vslot(n) * C::TILE, C::HALF, 1024);
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t o = ((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4;
+        warp_mma(i * kPrN, q + o, k + o, kIdescQK, kk);
+      }
+      warp_commit(&s_full[i]);
+    };
+    auto pv = [&](int i, uint32_t c, int n) {
+      const uint64_t v = tc_desc_sw128(sKV + vslot(c) * C::TILE, C::HALF, 1024);
 #pragma unroll
-          for (int kk = 0; kk < kPrN / 16; ++kk)
-            warp_mma_ta(2 * kPrN + i * D, i * kPrN + kk * 8, v + kk * 128, kIdescPV, n | kk);
-          if (n + 1 == (i ? n1 : n0)) warp_commit(&pv_done[i]);
-        };
-        wait(q_full, 0u);
-        wait(&full[kslot(0)], 0u);
+      for (int kk = 0; kk < kPrN / 16; ++kk)
+        warp_mma_ta(2 * kPrN + i * D, i * kPrN + kk * 8, v + kk * 128, kIdescPV, n | kk);
+    };
+    uint32_t kn = 0, vn = 0, qn = 0, pn[2] = {0, 0}, on[2] = {0, 0};
+    for (int k = 0;; ++k) {
+      const PromptItem it = take(k);
+      if (given_up() || it.q0 < 0) break;
+      const int nt = max(it.n0, it.n1);
+      if (nt == 0) continue;
+      // S of a row tile may be written at once: the P that the last item's final
+      // product read there was issued before
+      wait(q_full, qn & 1u);
+      ++qn;
+      wait(&full[kslot(kn)], kpar(kn));
+      __syncwarp();
+      tc_fence_after();
+      if (it.n0 > 0) qk(0, kn);
+      if (it.n1 > 0) qk(1, kn);
+      warp_commit(&empty[kslot(kn)]);
+      if (nt == 1) warp_commit(q_empty);
+      ++kn;
+      for (int n = 0; n < nt && !given_up(); ++n) {
+        wait(&clean[vn % C::CLEAN], (vn / C::CLEAN) & 1u);
         __syncwarp();
-        tc_fence_after();
-        if (n0 > 0) qk(0, 0);
-        if (n1 > 0) qk(1, 0);
-        warp_commit(&empty[kslot(0)]);
-        for (int n = 0; n < nt && !__any_sync(0xffffffffu, *abort_v); ++n) {
-          wait(&clean[n % C::CLEAN], (uint32_t)((n / C::CLEAN) & 1));
-          __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int ni = i ? n1 : n0;
-            if (n < ni) {
-              wait(&p_full[i], (uint32_t)(n & 1));
-              __syncwarp();
-              tc_fence_after();
-              pv(i, n);
-            }
-            if (n + 1 < ni) {
-              wait(&full[kslot(n + 1)], kpar(n + 1));
-              __syncwarp();
-              tc_fence_after();
-              qk(i, n + 1);
+        for (int i = 0; i < 2; ++i) {
+          const int ni = i ? it.n1 : it.n0;
+          if (n < ni) {
+            // O of the last item has been read
+            if (n == 0 && on[i] > 0) wait(&o_empty[i], (on[i] - 1) & 1u);
+            wait(&p_full[i], pn[i] & 1u);
+            ++pn[i];
+            __syncwarp();
+            tc_fence_after();
+            pv(i, vn, n);
+            if (n + 1 == ni) {
+              warp_commit(&pv_done[i]);
+              ++on[i];
             }
           }
-          warp_commit(&empty[vslot(n)]);
-          if (n + 1 < nt) warp_commit(&empty[kslot(n + 1)]);
+          if (n + 1 < ni) {
+            wait(&full[kslot(kn)], kpar(kn));
+            __syncwarp();
+            tc_fence_after();
+            qk(i, kn);
+          }
         }
-        warp_commit(mma_done);
-        wait(mma_done, 0u, true);
+        warp_commit(&empty[vslot(vn)]);
+        ++vn;
+        if (n + 1 < nt) {
+          warp_commit(&empty[kslot(kn)]);
+          ++kn;
+          if (n + 2 == nt) warp_commit(q_empty);
+        }
       }
-    } else {
-      // ------------------------------------------------------------- values
-      const int common = off + tok0;  // keys that every row of the CTA sees
-      for (int n = 0; n < nt; ++n) {
-        wait(&full[vslot(n)], vpar(n));
-        if (__any_sync(0xffffffffu, *abort_v)) break;
-        const int r0 = max(0, common - (t0 + n) * kPrN);
+    }
+    warp_commit(mma_done);
+    wait(mma_done, 0u, true);
+    __syncwarp();
+  } else if (warp >= kCleanWarp) {
+    // ------------------------------------------------------------------- values
+    uint32_t vn = 0;
+    for (int k = 0;; ++k) {
+      const PromptItem it = take(k);
+      if (given_up() || it.q0 < 0) break;
+      const int common = it.nk - it.nq + 1 + it.tok0;  // keys that every row of the item sees
+      for (int n = 0; n < max(it.n0, it.n1); ++n, ++vn) {
+        wait(&full[vslot(vn)], vpar(vn));
+        if (given_up()) break;
+        const int r0 = max(0, common - (it.t0 + n) * kPrN);
         if (r0 < kPrN) {
-          unsigned char *v = smem + C::OFF_KV + vslot(n) * C::TILE;
-          const int inside = nk - (t0 + n) * kPrN;  // rows of this sequence
+          unsigned char *v = smem + C::OFF_KV + vslot(vn) * C::TILE;
+          const int inside = it.nk - (it.t0 + n) * kPrN;  // rows of this sequence
           // Row r's 64 dims of half h are the 128 bytes at h * HALF + r * 128.  An
           // exponent of ones plus one carries into the sign's place: eight values cost
           // a dozen instructions, and the slow loop runs only if some are not finite.
@@ -413,197 +510,184 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
               }
             }
           }
-          if (found) bad_values = 1;
+          if (found) bad_values[k & 1] = k + 1;
           fence_proxy_async_smem();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&clean[n % C::CLEAN]);
+        if (lane == 0) mbar_arrive(&clean[vn % C::CLEAN]);
       }
     }
     __syncwarp();
   } else {
-    // --------------------------------------------------------------- softmax
+    // ------------------------------------------------------------------ softmax
     const int i = warp >> 3, hg = (warp >> 2) & 1, m = tid & 127;
     const int tloc = m / a.G, h = m - tloc * a.G;
-    const int tok = (i ? tok1 : tok0) + tloc;
-    const bool valid = tloc < a.tpt && tok < nq;
-    const int seen = valid ? off + tok : 0;             // may be negative
-    const int least = off + (i ? tok1 : tok0);          // of this row tile's rows
-    const int ni = i ? n1 : n0;
+    const int pair = 1 + i * 4 + (warp & 3);  // barrier of the two warps of these rows
     const uint32_t lrow = (uint32_t)((warp & 3) * 32) << 16;
     // this thread's half of the row's scores, and of its output columns
     const uint32_t tS = tmem + lrow + i * kPrN, tO = tmem + lrow + 2 * kPrN + i * D + hg * (D / 2);
     float *red = reinterpret_cast<float *>(smem + C::OFF_RED) + i * 256;
-    const int pair = 1 + i * 4 + (warp & 3);            // barrier of the warps of these rows
     const float sl2 = a.scale_log2;
-    float m_run = -CUDART_INF_F, l = 0.f;
-    // (no early exit: the warps of a pair meet at their barriers, also after a wait has
-    // run out)
-    for (int n = 0; n < ni; ++n) {
-      wait(&s_full[i], (uint32_t)(n & 1));
-      __syncwarp();
-      tc_fence_after();
-      uint32_t s0[32], s1[32];
-      tmem_ld32(tS + hg * kPrH, s0);
-      tmem_ld32(tS + hg * kPrH + 32, s1);
-      tmem_wait_ld();
-      const int first = (t0 + n) * kPrN;
-      if (first + kPrN > least) {
-        const int lim = seen - first - hg * kPrH;  // columns this row sees
+    uint32_t sn = 0, on = 0;
+    for (int k = 0;; ++k) {
+      const PromptItem it = take(k);
+      // (the warps of a pair leave together: they meet at barriers below, also after a
+      // wait has run out)
+      if (named_or(pair, 64, *abort_v != 0) || it.q0 < 0) break;
+      const int off = it.nk - it.nq + 1, tok = it.tok0 + i * a.tpt + tloc;
+      const bool valid = tloc < a.tpt && tok < it.nq;
+      const int seen = valid ? off + tok : 0;             // may be negative
+      const int least = off + it.tok0 + i * a.tpt;        // of this row tile's rows
+      const int ni = i ? it.n1 : it.n0;
+      float m_run = -CUDART_INF_F, l = 0.f;
+      for (int n = 0; n < ni; ++n, ++sn) {
+        wait(&s_full[i], sn & 1u);
+        __syncwarp();
+        tc_fence_after();
+        uint32_t s0[32], s1[32];
+        tmem_ld32(tS + hg * kPrH, s0);
+        tmem_ld32(tS + hg * kPrH + 32, s1);
+        tmem_wait_ld();
+        const int first = (it.t0 + n) * kPrN;
+        if (first + kPrN > least) {
+          const int lim = seen - first - hg * kPrH;  // columns this row sees
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          if (c >= lim) s0[c] = 0xFF800000u;
-          if (c + 32 >= lim) s1[c] = 0xFF800000u;
+          for (int c = 0; c < 32; ++c) {
+            if (c >= lim) s0[c] = 0xFF800000u;
+            if (c + 32 >= lim) s1[c] = 0xFF800000u;
+          }
         }
-      }
-      float mx0 = -CUDART_INF_F, mx1 = mx0;
+        float mx0 = -CUDART_INF_F, mx1 = mx0;
 #pragma unroll
-      for (int c = 0; c < 32; c += 2) {  // (three-operand maxima)
-        mx0 = fmaxf(mx0, fmaxf(__uint_as_float(s0[c]), __uint_as_float(s0[c + 1])));
-        mx1 = fmaxf(mx1, fmaxf(__uint_as_float(s1[c]), __uint_as_float(s1[c + 1])));
-      }
-      float mx = fmaxf(mx0, mx1) * sl2;
-      // The two warps that share 32 rows meet here, which also separates the halves'
-      // reads of S from their writes of P.  Rows whose maximum grew much are rare:
-      // only then do the halves exchange their maxima.
-      if (named_or(pair, 64, mx > m_run + kPrRescale)) {
-        red[hg * 128 + m] = mx;
-        named_sync(pair, 64);
-        mx = fmaxf(mx, red[(hg ^ 1) * 128 + m]);
-        named_sync(pair, 64);
-        if (__any_sync(0xffffffffu, mx > m_run + kPrRescale)) {
-          const float m_new = fmaxf(m_run, mx);
-          const float f = m_run == -CUDART_INF_F ? 0.f : ex2_approx(m_run - m_new);
-          m_run = m_new;
-          l *= f;
-          if (n > 0) {  // (the product of tile n - 1 was complete before S of tile n)
+        for (int c = 0; c < 32; c += 2) {  // (three-operand maxima)
+          mx0 = fmaxf(mx0, fmaxf(__uint_as_float(s0[c]), __uint_as_float(s0[c + 1])));
+          mx1 = fmaxf(mx1, fmaxf(__uint_as_float(s1[c]), __uint_as_float(s1[c + 1])));
+        }
+        float mx = fmaxf(mx0, mx1) * sl2;
+        // The two warps that share 32 rows meet here, which also separates the halves'
+        // reads of S from their writes of P.  Rows whose maximum grew much are rare:
+        // only then do the halves exchange their maxima.
+        if (named_or(pair, 64, mx > m_run + kPrRescale)) {
+          red[hg * 128 + m] = mx;
+          named_sync(pair, 64);
+          mx = fmaxf(mx, red[(hg ^ 1) * 128 + m]);
+          named_sync(pair, 64);
+          if (__any_sync(0xffffffffu, mx > m_run + kPrRescale)) {
+            const float m_new = fmaxf(m_run, mx);
+            const float f = m_run == -CUDART_INF_F ? 0.f : ex2_approx(m_run - m_new);
+            m_run = m_new;
+            l *= f;
+            if (n > 0) {  // (the product of tile n - 1 was complete before S of tile n)
 #pragma unroll 1
-            for (int c = 0; c < D / 2; c += 16) {
-              uint32_t o[16];
-              tmem_ld16(tO + c, o);
-              tmem_wait_ld();
+              for (int c = 0; c < D / 2; c += 16) {
+                uint32_t o[16];
+                tmem_ld16(tO + c, o);
+                tmem_wait_ld();
 #pragma unroll
-              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-              tmem_st16(tO + c, o);
+                for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                tmem_st16(tO + c, o);
+              }
             }
           }
         }
-      }
-      // -inf - -inf must not arise in a row that has seen nothing
-      const float b = m_run == -CUDART_INF_F ? 0.f : -m_run;
-      float l0 = 0.f, l1 = 0.f;
-      uint32_t p[16];
-      // weights are rounded to bf16 for the product (at most 2^-8 of each); l is not
-      auto weights = [&](const uint32_t(&s)[32]) {
-#pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          float u, w;
-          fma_f32x2(u, w, __uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1]), sl2, sl2, b, b);
-          u = ex2_approx(u);
-          w = ex2_approx(w);
-          add_f32x2(l0, l1, u, w);
-          p[x] = pack_bf16(u, w);
-        }
-      };
-      weights(s0);
-      tmem_st16(tS + hg * (kPrH / 2), p);
-      weights(s1);
-      tmem_st16(tS + hg * (kPrH / 2) + 16, p);
-      l += l0 + l1;
-      tmem_wait_st();  // (of the rescaled O, too)
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[i]);
-    }
-    // the row's sum over both halves
-    red[hg * 128 + m] = l;
-    named_sync(pair, 64);
-    l += red[(hg ^ 1) * 128 + m];
-    if (ni > 0) {
-      wait(&pv_done[i], 0u);
-      __syncwarp();
-      tc_fence_after();
-    }
-    // Every thread of the row tile's warps reads tensor memory.  The rows go out
-    // through shared memory, over the row tile's queries (no product reads them any
-    // more), so that a store covers whole lines: from registers it would touch 32
-    // of them, and the last of a CTA's stores left 3 us after its last product.
-    const int64_t row = (int64_t)(q0 + tok) * a.hq + kvh * a.G + h;
-    const bool patch = *(volatile int *)&bad_values != 0;
-    const int common = off + tok0;
-    const float inv = 1.f / l;  // only scores of -inf: 0 / 0
-    float *part = a.parts + ((int64_t)blockIdx.y * a.n_q * a.hq + row) * (D + 2);
-    // this warp's 32 rows x D / 2 columns, in bf16, over the row tile's own queries
-    constexpr int OB = D;  // bytes of half a row
-    unsigned char *stage = smem + i * C::TILE + (hg * 4 + (warp & 3)) * 32 * OB;
-#pragma unroll 1
-    for (int c = 0; c < D / 2; c += 16) {
-      const int col = hg * (D / 2) + c;
-      uint32_t o[16];
-      if (ni > 0) {
-        tmem_ld16(tO + c, o);
-        tmem_wait_ld();
-      } else {
-#pragma unroll
-        for (int x = 0; x < 16; ++x) o[x] = 0u;
-      }
-      if (patch && valid) {
-        // values that were taken out, for the keys that this row sees in this CTA's tiles
-        const int lo = max(max(common, 0), t0 * kPrN), hi = min(seen, (t0 + ni) * kPrN);
-        for (int p = lo; p < hi; ++p) {
-          const uint16_t *src = a.v + (int64_t)(k0 + p) * a.vt + (int64_t)kvh * a.vh + col;
+        // -inf - -inf must not arise in a row that has seen nothing
+        const float b = m_run == -CUDART_INF_F ? 0.f : -m_run;
+        float l0 = 0.f, l1 = 0.f;
+        uint32_t p[16];
+        // weights are rounded to bf16 for the product (at most 2^-8 of each); l is not
+        auto weights = [&](const uint32_t(&s)[32]) {
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
+            float u, w;
+            fma_f32x2(u, w, __uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1]), sl2, sl2, b, b);
+            u = ex2_approx(u);
+            w = ex2_approx(w);
+            add_f32x2(l0, l1, u, w);
+            p[x] = pack_bf16(u, w);
+          }
+        };
+        weights(s0);
+        tmem_st16(tS + hg * (kPrH / 2), p);
+        weights(s1);
+        tmem_st16(tS + hg * (kPrH / 2) + 16, p);
+        l += l0 + l1;
+        tmem_wait_st();  // (of the rescaled O, too)
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[i]);
+      }
+      // the row's sum over both halves
+      red[hg * 128 + m] = l;
+      named_sync(pair, 64);
+      l += red[(hg ^ 1) * 128 + m];
+      uint32_t o[D / 2];
+      if (ni > 0) {
+        wait(&pv_done[i], on & 1u);
+        ++on;
+        __syncwarp();
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < D / 2; c += 32)
+          tmem_ld32(tO + c, *reinterpret_cast<uint32_t(*)[32]>(&o[c]));
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_empty[i]);
+      } else {
+#pragma unroll
+        for (int x = 0; x < D / 2; ++x) o[x] = 0u;
+      }
+      if (valid && bad_values[k & 1] == k + 1) {
+        // values that were taken out, for the keys that this row sees in this item's tiles
+        const int lo = max(max(off + it.tok0, 0), it.t0 * kPrN);
+        const int hi = min(seen, (it.t0 + ni) * kPrN);
+        for (int p = lo; p < hi; ++p) {
+          const uint16_t *src =
+              a.v + (int64_t)(it.k0 + p) * a.vt + (int64_t)it.kvh * a.vh + hg * (D / 2);
+#pragma unroll
+          for (int x = 0; x < D / 2; ++x) {
             const uint32_t u = (uint32_t)src[x] << 16;
             if ((u & 0x7F800000u) == 0x7F800000u)
               o[x] = __float_as_uint(__uint_as_float(o[x]) + __uint_as_float(u));
           }
         }
       }
-      if (a.nsplit > 1) {
-        if (valid)
+      if (valid) {
+        const int64_t row = (int64_t)(it.q0 + tok) * a.hq + it.kvh * a.G + h;
+        if (a.nsplit > 1) {
+          float *part = a.parts + ((int64_t)it.part * a.n_q * a.hq + row) * (D + 2);
 #pragma unroll
-          for (int x = 0; x < 16; x += 2)
-            *reinterpret_cast<float2 *>(part + col + x) =
+          for (int x = 0; x < D / 2; x += 2)
+            *reinterpret_cast<float2 *>(part + hg * (D / 2) + x) =
                 make_float2(__uint_as_float(o[x]), __uint_as_float(o[x + 1]));
-      } else {
+          if (hg == 0) *reinterpret_cast<float2 *>(part + D) = make_float2(m_run, l);
+        } else {
+          const float inv = 1.f / l;  // only scores of -inf: 0 / 0
+          uint16_t *to = a.out + row * D + hg * (D / 2);
 #pragma unroll
-        for (int x = 0; x < 16; x += 8) {
-          uint4 w = make_uint4(0u, 0u, 0u, 0u);
-          if (seen > 0) {
-            w.x = pack_bf16(__uint_as_float(o[x]) * inv, __uint_as_float(o[x + 1]) * inv);
-            w.y = pack_bf16(__uint_as_float(o[x + 2]) * inv, __uint_as_float(o[x + 3]) * inv);
-            w.z = pack_bf16(__uint_as_float(o[x + 4]) * inv, __uint_as_float(o[x + 5]) * inv);
-            w.w = pack_bf16(__uint_as_float(o[x + 6]) * inv, __uint_as_float(o[x + 7]) * inv);
+          for (int x = 0; x < D / 2; x += 16) {
+            uint32_t w[8];
+#pragma unroll
+            for (int y = 0; y < 8; ++y)
+              w[y] = seen > 0 ? pack_bf16(__uint_as_float(o[x + 2 * y]) * inv,
+                                          __uint_as_float(o[x + 2 * y + 1]) * inv)
+                              : 0u;
+            if (a.out32) {  // whole 32-byte sectors
+              asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(to + x),
+                           "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]),
+                           "r"(w[6]), "r"(w[7])
+                           : "memory");
+            } else {
+              *reinterpret_cast<uint4 *>(to + x) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4 *>(to + x + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+            }
           }
-          // 16-byte chunk, rotated by the row so that eight rows meet no bank twice
-          const int ch = (c + x) / 8;
-          *reinterpret_cast<uint4 *>(stage + lane * OB + ((ch + lane) % (OB / 16)) * 16) = w;
+          if (a.lse && hg == 0)
+            a.lse[row] = m_run == CUDART_INF_F ? m_run
+                         : l == 0.f            ? -CUDART_INF_F
+                                               : (m_run + log2f(l)) * 0.69314718055994531f;
         }
       }
-    }
-    if (a.nsplit == 1) {
-      __syncwarp();
-      constexpr int CH = OB / 16;  // chunks of a row; 32 / CH rows a store
-      const int tok_i = i ? tok1 : tok0;
-#pragma unroll
-      for (int x = 0; x < 32; x += 32 / CH) {
-        const int r = x + lane / CH, ch = lane % CH;
-        const int mm = (warp & 3) * 32 + r, tl = mm / a.G;
-        if (tl < a.tpt && tok_i + tl < nq) {
-          const int64_t to = (int64_t)(q0 + tok_i + tl) * a.hq + kvh * a.G + (mm - tl * a.G);
-          *reinterpret_cast<uint4 *>(a.out + to * D + hg * (D / 2) + ch * 8) =
-              *reinterpret_cast<const uint4 *>(stage + r * OB + ((ch + r) % CH) * 16);
-        }
-      }
-    }
-    if (valid && hg == 0) {
-      if (a.nsplit > 1)
-        *reinterpret_cast<float2 *>(part + D) = make_float2(m_run, l);
-      else if (a.lse)
-        a.lse[row] = m_run == CUDART_INF_F ? m_run
-                     : l == 0.f            ? -CUDART_INF_F
-                                           : (m_run + log2f(l)) * 0.69314718055994531f;
     }
   }
   tc_fence_before();
@@ -787,8 +871,10 @@ extern "C" int dhs_prompt_attend(const void *q, const void *k, const void *v,
   if (a.nsplit > 1 &&
       (!workspace || workspace_bytes < (int64_t)a.nsplit * n_q * q_heads * (d + 2) * 4))
     return DHS_ERR_INVALID;
-  const int64_t ctas = prompt_tiles(n_q, n_seqs, a.G) * kv_heads;
-  if (ctas > INT32_MAX) return DHS_ERR_CAPACITY;
+  a.most = prompt_tiles(n_q, n_seqs, a.G);
+  a.out32 = ((uintptr_t)out & 31u) == 0;
+  const int64_t items = a.most * kv_heads * a.nsplit;
+  if (items > INT32_MAX) return DHS_ERR_CAPACITY;
   CUtensorMap mq = {}, mk = {}, mv = {};
   if (!encode(enc, &mq, q, n_q, q_heads, (int)d, st[0], st[1], a.G, a.tpt)) return DHS_ERR_INVALID;
   if (n_k > 0 && (!encode(enc, &mk, k, n_k, kv_heads, (int)d, st[2], st[3], 1, kPrN) ||
@@ -800,7 +886,7 @@ extern "C" int dhs_prompt_attend(const void *q, const void *k, const void *v,
     static DeviceSmem granted;
     cudaError_t e = granted.ensure(k_prompt<D>, PrCfg<D>::SMEM, dev);
     if (e == cudaSuccess)
-      e = launch_prio(k_prompt<D>, dim3((unsigned)ctas, (unsigned)a.nsplit), dim3(kPrThreads),
+      e = launch_prio(k_prompt<D>, dim3((unsigned)std::min<int64_t>(items, sms)), dim3(kPrThreads),
                       (size_t)PrCfg<D>::SMEM, s, mq, mk, mv, a);
     if (e == cudaSuccess && a.nsplit > 1)
       e = launch_pdl(k_prompt_join<D>, dim3((unsigned)((n_q * q_heads + 3) / 4)), dim3(128), 0, s,
