@@ -172,8 +172,7 @@ static_assert(sizeof(PromptItem) <= 64, "");
 // registers.
 struct PromptSchedule {
   const PromptArgs &a;
-  int lane, span, q0, nq, k0, nk, tiles, top;
-  int64_t items;
+  int lane, span, q0, nq, k0, nk, tiles, top, items;
 
   __device__ int load(int i) {
     q0 = nq = k0 = nk = 0;
@@ -188,25 +187,23 @@ struct PromptSchedule {
       total += (int64_t)__reduce_add_sync(0xffffffffu, (unsigned)tiles);
       top = max(top, __reduce_max_sync(0xffffffffu, tiles));
     }
-    items = min(total, a.most) * a.hkv * a.nsplit;
+    items = (int)min(total, a.most) * a.hkv * a.nsplit;  // (the host keeps this in 31 bits)
   }
   // tiles whose place in their sequence is j or later
-  __device__ int64_t from(int j) {
-    int64_t n = 0;
-    for (int i = 0; i < a.n_seqs; i += 32) {
-      const int x = a.n_seqs > 32 ? load(i + lane) : tiles;
-      n += (int64_t)__reduce_add_sync(0xffffffffu, (unsigned)max(0, x - j));
-    }
-    return n;
+  __device__ int from(int j) {
+    if (a.n_seqs <= 32) return __reduce_add_sync(0xffffffffu, max(0, tiles - j));
+    int n = 0;
+    for (int i = 0; i < a.n_seqs; i += 32) n += max(0, load(i + lane) - j);
+    return __reduce_add_sync(0xffffffffu, n);
   }
   __device__ bool item(int k, PromptItem &it) {
     const int64_t w = (int64_t)k * gridDim.x +
                       (k & 1 ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
     if (w >= items) return false;
-    const int64_t per = (int64_t)a.hkv * a.nsplit;
-    const int t = (int)(w / per), in = (int)(w - t * per);
-    it.kvh = in % a.hkv;
-    it.part = in / a.hkv;
+    const uint32_t per = (uint32_t)(a.hkv * a.nsplit);
+    const int t = (int)((uint32_t)w / per), in = (int)((uint32_t)w % per);
+    it.part = a.nsplit == 1 ? 0 : (int)((uint32_t)in / (uint32_t)a.hkv);
+    it.kvh = in - it.part * a.hkv;
     it.q0 = it.nq = it.k0 = it.nk = 0;
     // the place: from(place + 1) <= t < from(place)
     int lo = 0, hi = top - 1;
@@ -216,7 +213,7 @@ struct PromptSchedule {
       else hi = mid - 1;
     }
     // the sequence: the (t - from(place + 1))-th of those that have it
-    int nth = (int)(t - from(lo + 1));
+    int nth = t - from(lo + 1);
     for (int i = 0; i < a.n_seqs; i += 32) {
       const int x = a.n_seqs > 32 ? load(i + lane) : tiles;
       const uint32_t has = __ballot_sync(0xffffffffu, x > lo);
@@ -530,15 +527,23 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
     const float sl2 = a.scale_log2;
     uint32_t sn = 0, on = 0;
     for (int k = 0;; ++k) {
-      const PromptItem it = take(k);
+      // the item stays in shared memory until its rows are written: few of its
+      // fields are wanted in the loop, where registers are short
+      wait(&item_full[k & 1], item_par(k));
+      __syncwarp();
+      volatile const PromptItem &it = item_of(k);
       // (the warps of a pair leave together: they meet at barriers below, also after a
       // wait has run out)
       if (named_or(pair, 64, *abort_v != 0) || it.q0 < 0) break;
-      const int off = it.nk - it.nq + 1, tok = it.tok0 + i * a.tpt + tloc;
-      const bool valid = tloc < a.tpt && tok < it.nq;
-      const int seen = valid ? off + tok : 0;             // may be negative
-      const int least = off + it.tok0 + i * a.tpt;        // of this row tile's rows
-      const int ni = i ? it.n1 : it.n0;
+      const int t0 = it.t0, ni = i ? it.n1 : it.n0;
+      int lim0;  // columns of tile 0 that this row's half sees
+      int least; // tiles from this one on have columns that some row does not see
+      {
+        const int off = it.nk - it.nq + 1, tok = it.tok0 + i * a.tpt + tloc;
+        const bool valid = tloc < a.tpt && tok < it.nq;
+        lim0 = (valid ? off + tok : 0) - hg * kPrH;
+        least = off + it.tok0 + i * a.tpt;
+      }
       float m_run = -CUDART_INF_F, l = 0.f;
       for (int n = 0; n < ni; ++n, ++sn) {
         wait(&s_full[i], sn & 1u);
@@ -548,9 +553,9 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
         tmem_ld32(tS + hg * kPrH, s0);
         tmem_ld32(tS + hg * kPrH + 32, s1);
         tmem_wait_ld();
-        const int first = (it.t0 + n) * kPrN;
+        const int first = (t0 + n) * kPrN;
         if (first + kPrN > least) {
-          const int lim = seen - first - hg * kPrH;  // columns this row sees
+          const int lim = lim0 - first;  // columns this row sees
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
             if (c >= lim) s0[c] = 0xFF800000u;
@@ -620,6 +625,12 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
       red[hg * 128 + m] = l;
       named_sync(pair, 64);
       l += red[(hg ^ 1) * 128 + m];
+      const int off = it.nk - it.nq + 1, tok = it.tok0 + i * a.tpt + tloc;
+      const int q0 = it.q0, k0 = it.k0, kvh = it.kvh, part_no = it.part, common = off + it.tok0;
+      const bool valid = tloc < a.tpt && tok < it.nq;
+      const int seen = valid ? off + tok : 0;  // may be negative
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&item_empty[k & 1]);
       uint32_t o[D / 2];
       if (ni > 0) {
         wait(&pv_done[i], on & 1u);
@@ -639,11 +650,11 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
       }
       if (valid && bad_values[k & 1] == k + 1) {
         // values that were taken out, for the keys that this row sees in this item's tiles
-        const int lo = max(max(off + it.tok0, 0), it.t0 * kPrN);
-        const int hi = min(seen, (it.t0 + ni) * kPrN);
+        const int lo = max(max(common, 0), t0 * kPrN);
+        const int hi = min(seen, (t0 + ni) * kPrN);
         for (int p = lo; p < hi; ++p) {
           const uint16_t *src =
-              a.v + (int64_t)(it.k0 + p) * a.vt + (int64_t)it.kvh * a.vh + hg * (D / 2);
+              a.v + (int64_t)(k0 + p) * a.vt + (int64_t)kvh * a.vh + hg * (D / 2);
 #pragma unroll
           for (int x = 0; x < D / 2; ++x) {
             const uint32_t u = (uint32_t)src[x] << 16;
@@ -653,9 +664,9 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
         }
       }
       if (valid) {
-        const int64_t row = (int64_t)(it.q0 + tok) * a.hq + it.kvh * a.G + h;
+        const int64_t row = (int64_t)(q0 + tok) * a.hq + kvh * a.G + h;
         if (a.nsplit > 1) {
-          float *part = a.parts + ((int64_t)it.part * a.n_q * a.hq + row) * (D + 2);
+          float *part = a.parts + ((int64_t)part_no * a.n_q * a.hq + row) * (D + 2);
 #pragma unroll
           for (int x = 0; x < D / 2; x += 2)
             *reinterpret_cast<float2 *>(part + hg * (D / 2) + x) =
@@ -752,15 +763,27 @@ int64_t prompt_tiles(int64_t n_q, int32_t n_seqs, int G) {
   return n_q / span + std::min<int64_t>(n_seqs, n_q);
 }
 
-// Key splits: when the row tiles leave SMs idle, as many as fill them, as long as a
-// split keeps four key tiles of an average sequence (a split costs the write and
-// read of its part, 4 D bytes a row).
+// Key splits: as many as make the longest CTA shortest.  With I row-tile pairs (times
+// kv heads) of T key tiles, n splits deal I n items of T / n tiles to the SMs in
+// ceil(I n / SMs) turns; an item costs some 3 tiles' time besides its tiles, a join
+// some 6.  (Two 500-token chunks over 32K keys, 32 pairs: 4 splits, 98 us instead of
+// 330.)
 int prompt_splits(int64_t n_q, int64_t n_k, int32_t n_seqs, int hq, int hkv, int sms) {
   if (n_q == 0 || n_seqs == 0) return 1;
-  const int64_t ctas = prompt_tiles(n_q, n_seqs, hq / hkv) * hkv;
-  const int64_t fill = sms / std::max<int64_t>(1, ctas);
-  const int64_t room = n_k / n_seqs / (4 * kPrN);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(fill, room), kPrSplits));
+  const int64_t items = prompt_tiles(n_q, n_seqs, hq / hkv) * hkv;
+  // an average row's keys: all of the sequence but half of its queries
+  const int64_t tiles =
+      std::max<int64_t>(0, n_k - std::min(n_q, n_k) / 2) / n_seqs / kPrN + 1;
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int n = 1; n <= kPrSplits && (n == 1 || tiles / n >= 4); ++n) {
+    const int64_t cost = (items * n + sms - 1) / sms * ((tiles + n - 1) / n + 3) + (n > 1 ? 6 : 0);
+    if (cost < least) {
+      least = cost;
+      best = n;
+    }
+  }
+  return best;
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
