@@ -1089,6 +1089,7 @@ extern "C" int dhs_page_attend(const dhs_pages *pages, const void *q, const int3
       return DHS_ERR_INVALID;
     static DeviceSmem granted;
     const int64_t rows = (int64_t)n_seqs * pg.hkv * a.R;
+    if (rows > INT32_MAX) return DHS_ERR_CAPACITY;
     const int width_rows =
         (int)std::min<int64_t>((int64_t)table_width * pg.rows, (int64_t)INT32_MAX - 1024);
     // few rows: four warps a row

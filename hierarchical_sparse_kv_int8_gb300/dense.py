@@ -203,7 +203,7 @@ class PageCache:
         if nbytes < 0:
             raise ValueError("attend does not serve n_seqs=%d, q_len=%d, q_heads=%d"
                              % (n_seqs, q_len, q_heads))
-        return torch.zeros(max(16, nbytes), dtype=torch.uint8, device=self.device)
+        return torch.empty(max(16, nbytes), dtype=torch.uint8, device=self.device)
 
     def attend(self, q, seq_lens, page_table, out, workspace, lse=None, q_lens=None,
                scale: float = 0.0, stream=None):
@@ -239,7 +239,7 @@ def prompt_workspace(q, k, n_seqs: int) -> Optional[torch.Tensor]:
                                                     k.shape[1], q.shape[2])
     if nbytes < 0:
         raise ValueError("prompt_attend does not serve q %s, k %s" % (tuple(q.shape), tuple(k.shape)))
-    return torch.zeros(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+    return torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
 
 
 def prompt_attend(q, k, v, cu_q, cu_k, out, lse=None, workspace=None, scale: float = 0.0,

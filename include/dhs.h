@@ -671,16 +671,16 @@ int dhs_page_read(const dhs_pages *pages, void *k, void *v, const int64_t *strid
  *   seq_lens  device int32 [n_seqs], the queries' own positions included
  *             (write their rows first); 0 for an idle slot
  *   scale     0 = 1/sqrt(head_dim); finite and not negative
- *   out       device bf16 like q
+ *   out       device bf16 like q, 16-byte aligned
  *   lse       device fp32 [n_seqs][q_len][q_heads] natural-log sum-exp, or NULL
  * A query that sees no position has out = 0 and lse = -inf.  q_len * (q_heads
- * / kv_heads) <= 128, q_len <= 8.  The result does not depend on the other
- * sequences' values.
- *   workspace  device, 16-byte aligned, at least dhs_page_attend_workspace()
- *              bytes; its first workspace_bytes are zero before the first call
- *              that uses it, and each call leaves ready for the next.  Calls
- *              that may overlap on the GPU (other streams, graphs replayed at the
- *              same time) each take one of their own. */
+ * / kv_heads) <= 128, q_len <= 8.  Scales of an 8-bit cache must not be negative.
+ * What rows a query does not see hold (infinities, NaN) never reaches it, nor do
+ * other sequences' values; with the same lengths the result repeats bit by bit.
+ *   workspace  device scratch, 16-byte aligned, at least
+ *              dhs_page_attend_workspace() bytes; what it holds before and after a
+ *              call does not matter.  Calls that may overlap on the GPU (other
+ *              streams, graphs replayed at the same time) each take one of their own */
 int dhs_page_attend(const dhs_pages *pages, const void *q, const int32_t *q_lens,
                     const int32_t *seq_lens, const int32_t *page_table, int32_t table_width,
                     int32_t n_seqs, int32_t q_len, int32_t q_heads, float scale, void *out,

@@ -472,6 +472,40 @@ def test_attend_far_pages(torch, dhs):
     assert torch.equal(ko, -vo) and (ko - k).abs().max() < 0.05
 
 
+def test_attend_ignores_scales_of_rows_it_does_not_see(torch, dhs):
+    """Unused rows of an 8-bit cache have NaN scales (the poison of every test here);
+    a visible row with a NaN scale makes its sequence NaN and no other."""
+    for side in ("k_scale", "v_scale"):
+        pc = Paged(torch, dhs, [50, 40], 16, 1, 64, INT8)
+        kv = pc.fill()
+        getattr(pc.cache, side)[int(pc.table[0, 1]), 0, 3] = math.nan
+        q = torch.randn((2, 1, 4, 64)).bfloat16().cuda()
+        out = torch.zeros_like(q)
+        pc.cache.attend(q, pc.seq_lens, pc.table, out, pc.cache.attend_workspace(2, 1, 4))
+        from oracle import dense_oracle as oracle
+        assert torch.isnan(out[0]).all()
+        _close(_np(out[1]), None, oracle.attend(_np(q[1]), *kv[1], 1 / 8), 64, 40, np.abs(kv[1][1]).max())
+
+
+def test_attend_scales_far_apart(torch, dhs):
+    """Value scales that grow by 2^40 along the sequence, zeros among them: each row's
+    result is as exact as its own largest terms."""
+    from oracle import dense_oracle as oracle
+    pc = Paged(torch, dhs, [640], 64, 1, 128, INT8)
+    kv = pc.fill()
+    grow = torch.exp2((torch.arange(640) // 16).float() - 20)
+    grow[100:130] = 0
+    pos = torch.arange(640)
+    page, row = pc.table.cpu()[0].long()[pos // 64].cuda(), (pos % 64).cuda()
+    pc.cache.v_scale[page, 0, row] *= grow.cuda()
+    v = kv[0][1] * grow.double().numpy()[:, None, None]
+    q = torch.randn((1, 2, 8, 128)).bfloat16().cuda()
+    out = torch.zeros_like(q)
+    pc.cache.attend(q, pc.seq_lens, pc.table, out, pc.cache.attend_workspace(1, 2, 8))
+    want = oracle.attend(_np(q[0]), kv[0][0], v, 1 / math.sqrt(128))
+    _close(_np(out[0]), None, want, 128, 640, np.abs(v).max())
+
+
 def test_attend_same_result_again_and_beside_others(torch, dhs):
     """Bits repeat; a sequence's result does not depend on its neighbours' values,
     and a workspace goes from one call to the next, whatever ran before."""
@@ -573,6 +607,46 @@ def test_prompt_long_chunk(torch, dhs):
     """Few queries against many keys: the keys are split and joined."""
     _prompt(torch, dhs, [(3, 9000), (17, 5000)], 4, 2, 128)
     _prompt(torch, dhs, [(3, 9000), (1, 3)], 2, 2, 64)
+
+
+def test_prompt_split_among_many(torch, dhs):
+    """Key splits of more items than SMs, sequences without queries or keys among them."""
+    sizes = [(37, 2900), (0, 700), (64, 3100), (5, 0), (1, 2600), (50, 3000), (33, 2500), (3, 1)]
+    q = torch.empty((sum(a for a, _ in sizes), 16, 64), dtype=torch.bfloat16, device="cuda")
+    k = torch.empty((sum(b for _, b in sizes), 8, 64), dtype=torch.bfloat16, device="cuda")
+    assert dhs.prompt_workspace(q, k, len(sizes)) is not None
+    _prompt(torch, dhs, sizes, 16, 8, 64)
+
+
+def test_prompt_refuses_a_small_workspace(torch, dhs):
+    q = torch.zeros((8, 2, 64), dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros((9000, 2, 64), dtype=torch.bfloat16, device="cuda")
+    cq, ck = (torch.tensor([0, n], dtype=torch.int32).cuda() for n in (8, 9000))
+    ws = dhs.prompt_workspace(q, k, 1)
+    for bad in (None, ws[:ws.numel() - 16]):
+        with pytest.raises(dhs.DhsError) as e:
+            dhs.prompt_attend(q, k, k, cq, ck, torch.empty_like(q), workspace=bad)
+        assert e.value.code == 1
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_outputs_at_sixteen_bytes(torch, dhs, d):
+    """Tensors that start 16 bytes into a 256-byte line."""
+    from oracle import dense_oracle as oracle
+    shift = lambda *s: torch.empty(math.prod(s) + 8, dtype=torch.bfloat16, device="cuda")[8:].view(s)  # noqa: E731
+    q, k, v, out = shift(70, 4, d), shift(70, 2, d), shift(70, 2, d), shift(70, 4, d)
+    for t in (q, k, v):
+        t.copy_(torch.randn(t.shape))
+    cu = torch.tensor([0, 70], dtype=torch.int32).cuda()
+    dhs.prompt_attend(q, k, v, cu, cu, out)
+    want = oracle.attend(_np(q), _np(k), _np(v), 1 / math.sqrt(d))
+    _close(_np(out), None, want, d, 70)
+    pc = Paged(torch, dhs, [70], 16, 2, d, BF16)
+    pc.cache.write(k, v, cu, pc.seq_lens, pc.table)
+    q1, o1 = shift(1, 1, 4, d), shift(1, 1, 4, d)
+    q1.copy_(torch.randn(q1.shape))
+    pc.cache.attend(q1, pc.seq_lens, pc.table, o1, pc.cache.attend_workspace(1, 1, 4))
+    _close(_np(o1[0]), None, oracle.attend(_np(q1[0]), _np(k), _np(v), 1 / math.sqrt(d)), d, 70)
 
 
 @pytest.mark.parametrize("d", [64, 128])
