@@ -409,6 +409,8 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
       if (given_up() || it.q0 < 0) break;
       const int nt = max(it.n0, it.n1);
       if (nt == 0) continue;
+      for (int i = 0; i < 2; ++i)
+        if ((i ? it.n1 : it.n0) > 0 && on[i] > 0) wait(&o_empty[i], (on[i] - 1) & 1u);
       // S of a row tile may be written at once: the P that the last item's final
       // product read there was issued before
       wait(q_full, qn & 1u);
@@ -421,7 +423,8 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
       warp_commit(&empty[kslot(kn)]);
       if (nt == 1) warp_commit(q_empty);
       ++kn;
-      for (int n = 0; n < nt && !given_up(); ++n) {
+      for (int n = 0; n < nt; ++n) {
+        if ((n & 15) == 15 && given_up()) break;
         wait(&clean[vn % C::CLEAN], (vn / C::CLEAN) & 1u);
         __syncwarp();
 #pragma unroll
@@ -429,7 +432,6 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
           const int ni = i ? it.n1 : it.n0;
           if (n < ni) {
             // O of the last item has been read
-            if (n == 0 && on[i] > 0) wait(&o_empty[i], (on[i] - 1) & 1u);
             wait(&p_full[i], pn[i] & 1u);
             ++pn[i];
             __syncwarp();
