@@ -133,7 +133,8 @@ struct Cfg {
   static constexpr int OFF_ROW = DATA;                           // int64 [WT][SLOTS][TN]
   static constexpr int OFF_MASK = OFF_ROW + WT * SLOTS * TN * 8; // uint32 [WT][SLOTS][2]
   static constexpr int OFF_ML = OFF_MASK + WT * SLOTS * 8;       // float [WT][ROWS][2]
-  static constexpr int SMEM = OFF_ML + WT * ROWS * 8;
+  static constexpr int OFF_TAB = OFF_ML + WT * ROWS * 8;         // int2 [ROWS]
+  static constexpr int SMEM = OFF_TAB + ROWS * 8;
   static constexpr int OCC = SMEM * 2 <= 226 * 1024 ? 2 : 1;
   static constexpr bool B16 = W == 2 || CONV;            // the products read 16-bit rows
   static constexpr int BLOCK = WT * TN;                  // positions of a block
@@ -166,7 +167,7 @@ struct AttnArgs {
   uint16_t *out;
   float *lse;
   int2 *plan;        // [n_seqs][hkv]: first and last CTA of an item in parts, or (-1, -1)
-  float *parts;      // [grid][2][R][D + 2]: O, m, l
+  float *parts;      // [grid][2][R][D + 4]: O, m, l, -
   int32_t *err;
   int width, n_seqs, q_len, hq, G, R;
   float scale_log2;
@@ -197,23 +198,32 @@ k_page_attn(const PageView pg, const AttnArgs a) {
       len = (int)max((int64_t)0, min((int64_t)len, most));
     }
   };
-  auto blocks = [&](int i) -> int64_t {
-    int nq, len;
-    shape(i, nq, len);
-    return nq > 0 ? ((int64_t)len + C::BLOCK - 1) / C::BLOCK : 0;
+  // Blocks (of one kv head) of sequence i + lane; with 32 sequences or fewer each lane
+  // keeps what it read.
+  const bool few = a.n_seqs <= 32;
+  int my_nq = 0, my_len = 0, my_n = 0;
+  bool known = false;
+  auto blocks = [&](int i) {
+    if (known) return my_n;
+    my_nq = my_len = 0;
+    if (i + lane < a.n_seqs) shape(i + lane, my_nq, my_len);
+    my_n = my_nq > 0 ? (int)(((uint32_t)my_len + C::BLOCK - 1) / C::BLOCK) : 0;
+    return my_n;
   };
 
-  // Blocks (of one kv head) and sequences with any: every warp adds up all of them,
-  // 32 at a time.
+  // All blocks, and the sequences with any: every warp adds up all of them.
   int64_t sum = 0;
   int some = 0;
   for (int i = 0; i < a.n_seqs; i += 32) {
-    const int n = i + lane < a.n_seqs ? (int)blocks(i + lane) : 0;
+    const int n = blocks(i);
     some += __popc(__ballot_sync(0xffffffffu, n > 0));
-    sum += n;  // (this lane's)
+    sum += few ? __reduce_add_sync(0xffffffffu, n) : n;  // (32 of them fit 32 bits)
   }
+  if (!few) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  }
+  known = few;
   const int64_t total = sum * hkv;
 
   // sequences without a block: their queries see nothing
@@ -252,7 +262,7 @@ k_page_attn(const PageView pg, const AttnArgs a) {
   int64_t total_units = total;
   if (chunked) {
     int64_t x = 0;
-    for (int i = lane; i < a.n_seqs; i += 32) x += units(blocks(i));
+    for (int i = 0; i < a.n_seqs; i += 32) x += units(blocks(i));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     total_units = x * hkv;
@@ -265,17 +275,17 @@ k_page_attn(const PageView pg, const AttnArgs a) {
   const int64_t begin = range(blockIdx.x), end = range(blockIdx.x + 1);
 
   // the sequence that holds unit `begin`, and the unit it starts at
-  int seq = 0;
+  int seq = 0, seq_nq = 0, seq_len = 0;
   int64_t seq_at = 0;
   {
     const int64_t want = idiv(begin, hkv);  // in units of one head: only the sequence is looked for
     int64_t at = 0;
     for (int i = 0; i < a.n_seqs; i += 32) {
-      const int n = i + lane < a.n_seqs ? (int)units(blocks(i + lane)) : 0;
-      int64_t x = n;  // inclusive sums
+      const int n = (int)units(blocks(i));
+      int x = n;  // inclusive sums
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
       }
       const uint32_t here = __ballot_sync(0xffffffffu, want < at + x);
@@ -283,6 +293,8 @@ k_page_attn(const PageView pg, const AttnArgs a) {
         const int src = __ffs(here) - 1;
         seq = i + src;
         seq_at = (at + __shfl_sync(0xffffffffu, x - n, src)) * hkv;
+        seq_nq = __shfl_sync(0xffffffffu, my_nq, src);
+        seq_len = __shfl_sync(0xffffffffu, my_len, src);
         break;
       }
       at += __shfl_sync(0xffffffffu, x, 31);
@@ -303,13 +315,12 @@ k_page_attn(const PageView pg, const AttnArgs a) {
   };
 
   for (int64_t pos = begin; pos < end && seq < a.n_seqs;) {
-    int nq, len;
-    shape(seq, nq, len);
-    const int64_t nb = nq > 0 ? ((int64_t)len + C::BLOCK - 1) / C::BLOCK : 0;
+    const int nq = seq_nq, len = seq_len;
+    const int64_t nb = nq > 0 ? (int64_t)(((uint32_t)len + C::BLOCK - 1) / C::BLOCK) : 0;
     const int64_t nu = units(nb);
     if (pos >= seq_at + nu * hkv) {  // on to the next sequence (empty ones among them)
       seq_at += nu * hkv;
-      ++seq;
+      if (++seq < a.n_seqs) shape(seq, seq_nq, seq_len);
       continue;
     }
     const int kvh = (int)idiv(pos - seq_at, nu);
@@ -323,25 +334,31 @@ k_page_attn(const PageView pg, const AttnArgs a) {
     // ---- row lookups and copies, tile by tile.  Tile t of the group is
     // positions (b0 + t) * BLOCK + wt * TN ...
     constexpr int LK = (TN + WM * 32 - 1) / (WM * 32);  // lookups of a thread
-    auto lookup = [&](int t, int64_t (&row)[LK]) {
+    // the page (-1: no position there), read ahead of the row that follows from it
+    auto lookup = [&](int t, int (&page)[LK]) {
 #pragma unroll
       for (int u = 0; u < LK; ++u) {
         const int x = gl + u * WM * 32;
         const int64_t p = (int64_t)(b0 + t) * C::BLOCK + wt * TN + x;
-        row[u] = -1;
-        if (t < nblk && x < TN && p < len) {
-          row[u] = page_row(pg, tab, (int)p, a.err, DHS_SITE_PAGE_ATTEND);
-          if (row[u] >= 0) row[u] += (int64_t)kvh * pg.rows;
-        }
+        page[u] = t < nblk && x < TN && p < len
+                      ? tab[(uint64_t)(uint32_t)p * pg.div_mul >> pg.div_shift]
+                      : INT32_MIN;
       }
     };
-    auto keep = [&](int t, const int64_t (&row)[LK]) {
+    auto keep = [&](int t, const int (&page)[LK]) {
       int64_t *dst = rowbuf + (t % C::SLOTS) * TN;
 #pragma unroll
       for (int u = 0; u < LK; ++u) {
         const int x = gl + u * WM * 32;
-        const uint32_t ok = __ballot_sync(0xffffffffu, row[u] >= 0);
-        if (x < TN) dst[x] = row[u];  // (-1: nothing there)
+        const uint32_t p = (uint32_t)((b0 + t) * C::BLOCK + wt * TN + x);
+        int64_t row = -1;  // nothing there
+        if (page[u] >= 0 && page[u] < pg.n_pages)
+          row = ((int64_t)page[u] * hkv + kvh) * pg.rows +
+                (p - (uint32_t)((uint64_t)p * pg.div_mul >> pg.div_shift) * pg.rows);
+        else if (page[u] != INT32_MIN)
+          page_error(a.err, DC_LOC_RANGE, DHS_SITE_PAGE_ATTEND);
+        const uint32_t ok = __ballot_sync(0xffffffffu, row >= 0);
+        if (x < TN) dst[x] = row;
         if (lane == 0 && (x >> 5) < 2) maskbuf[(t % C::SLOTS) * 2 + (x >> 5)] = ok;
       }
     };
@@ -410,11 +427,11 @@ k_page_attn(const PageView pg, const AttnArgs a) {
     };
 
     {
-      int64_t row[NS][LK];
+      int page[NS][LK];
 #pragma unroll
-      for (int t = 0; t < NS; ++t) lookup(t, row[t]);
+      for (int t = 0; t < NS; ++t) lookup(t, page[t]);
 #pragma unroll
-      for (int t = 0; t < NS; ++t) keep(t, row[t]);
+      for (int t = 0; t < NS; ++t) keep(t, page[t]);
     }
     group_sync();
 #pragma unroll
@@ -491,7 +508,7 @@ k_page_attn(const PageView pg, const AttnArgs a) {
     for (int t = 0; t < nblk; ++t) {
       cp_async_wait_group<NS - 2>();
       group_sync();
-      int64_t ahead[LK];
+      int ahead[LK];
       lookup(t + NS, ahead);
       copy(t + NS - 1);
       unsigned char *kst = ring + (t % NS) * C::STAGE, *vst = kst + C::KV;
@@ -774,6 +791,36 @@ k_page_attn(const PageView pg, const AttnArgs a) {
     cp_async_wait_all();
     __syncthreads();
     const bool patch = sh_flag != 0;
+    const bool whole = pos == item0 && stop == item1;
+    const int slot = pos > item0 ? 0 : 1;
+    float *part = a.parts + ((int64_t)blockIdx.x * 2 + slot) * a.R * (D + 4);
+    int2 *tab_of = reinterpret_cast<int2 *>(smem + C::OFF_TAB);
+    // a row's maximum and sum over the groups; its place (-1: an idle query) and the
+    // factor of its output (negative: it sees nothing)
+    if (tid < a.R) {
+      const int m = tid, j = m / a.G, sees = len - nq + j + 1;
+      float top = -CUDART_INF_F, den = 0.f;
+#pragma unroll
+      for (int g = 0; g < WT; ++g) top = fmaxf(top, ml[(g * C::ROWS + m) * 2]);
+#pragma unroll
+      for (int g = 0; g < WT; ++g) {
+        const float2 x = *reinterpret_cast<const float2 *>(ml + (g * C::ROWS + m) * 2);
+        const float f = x.x == -CUDART_INF_F ? (x.y != x.y ? 1.f : 0.f) : ex2_approx(x.x - top);
+        den += x.y * f;
+      }
+      const int at = j < nq ? j * a.hq + (m - j * a.G) : -1;
+      tab_of[m] = make_int2(at, __float_as_int(sees <= 0 ? -1.f : 1.f / den));  // (only -inf: 0 / 0)
+      if (j < nq) {
+        if (!whole) {
+          *reinterpret_cast<float2 *>(part + m * (D + 4) + D) = make_float2(top, den);
+        } else if (a.lse) {
+          a.lse[(int64_t)seq * a.q_len * a.hq + kvh * a.G + at] =
+              top == CUDART_INF_F ? top
+              : den == 0.f        ? -CUDART_INF_F
+                                  : (top + log2f(den)) * 0.69314718055994531f;
+        }
+      }
+    }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -802,34 +849,26 @@ k_page_attn(const PageView pg, const AttnArgs a) {
       }
     __syncthreads();
 
-    const bool whole = pos == item0 && stop == item1;
-    const int slot = pos > item0 ? 0 : 1;
-    float *part = a.parts + ((int64_t)blockIdx.x * 2 + slot) * a.R * (D + 2);
     if (tid == 0) sh_flag = 0;  // every thread has read it
     // one row's 4 dims at a time
+    uint16_t *out0 = a.out + ((int64_t)seq * a.q_len * a.hq + kvh * a.G) * D;
     for (int e = tid; e < a.R * (D / 4); e += kPaThreads) {
-      const int m = e / (D / 4), d4 = (e % (D / 4)) * 4, j = m / a.G;
-      if (j >= nq) continue;
-      float top = -CUDART_INF_F, den = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      const int m = e / (D / 4), d4 = (e % (D / 4)) * 4;
+      const int2 tb = tab_of[m];
+      if (tb.x < 0) continue;
+      float4 acc = *reinterpret_cast<const float4 *>(osm + m * C::OPAD + d4);
 #pragma unroll
-      for (int g = 0; g < WT; ++g) top = fmaxf(top, ml[(g * C::ROWS + m) * 2]);
-#pragma unroll
-      for (int g = 0; g < WT; ++g) {
-        const float2 x = *reinterpret_cast<const float2 *>(ml + (g * C::ROWS + m) * 2);
-        const float f = x.x == -CUDART_INF_F ? (x.y != x.y ? 1.f : 0.f) : ex2_approx(x.x - top);
-        den += x.y * f;
+      for (int g = 1; g < WT; ++g) {
         const float4 y = *reinterpret_cast<const float4 *>(osm + (g * C::ROWS + m) * C::OPAD + d4);
         acc.x += y.x;
         acc.y += y.y;
         acc.z += y.z;
         acc.w += y.w;
       }
-      const int sees = len - nq + j + 1;
       if (KIND == DHS_PAGE_BF16 && patch) {
         // the values taken out above, for the queries that see them
         const int64_t lo = max((int64_t)max(0, common), (int64_t)b0 * C::BLOCK);
-        const int64_t hi = min((int64_t)sees, (int64_t)(b0 + nblk) * C::BLOCK);
+        const int64_t hi = min((int64_t)len - nq + m / a.G + 1, (int64_t)(b0 + nblk) * C::BLOCK);
         for (int64_t p = lo; p < hi; ++p) {
           int64_t row = page_row(pg, tab, (int)p, a.err, DHS_SITE_PAGE_ATTEND);
           if (row < 0) continue;
@@ -843,20 +882,13 @@ k_page_attn(const PageView pg, const AttnArgs a) {
         }
       }
       if (whole) {
-        const float inv = sees <= 0 ? 0.f : 1.f / den;  // only -inf scores: 0 / 0
-        const int64_t row = ((int64_t)seq * a.q_len + j) * a.hq + kvh * a.G + (m - j * a.G);
-        *reinterpret_cast<uint2 *>(a.out + row * D + d4) =
-            sees <= 0 ? make_uint2(0u, 0u)
+        const float inv = __int_as_float(tb.y);
+        *reinterpret_cast<uint2 *>(out0 + (int64_t)tb.x * D + d4) =
+            inv < 0.f ? make_uint2(0u, 0u)
                       : make_uint2(pack_bf16(acc.x * inv, acc.y * inv),
                                    pack_bf16(acc.z * inv, acc.w * inv));
-        if (a.lse && d4 == 0)
-          a.lse[row] = top == CUDART_INF_F ? top
-                       : den == 0.f        ? -CUDART_INF_F
-                                           : (top + log2f(den)) * 0.69314718055994531f;
       } else {
-        *reinterpret_cast<float2 *>(part + m * (D + 2) + d4) = make_float2(acc.x, acc.y);
-        *reinterpret_cast<float2 *>(part + m * (D + 2) + d4 + 2) = make_float2(acc.z, acc.w);
-        if (d4 == 0) *reinterpret_cast<float2 *>(part + m * (D + 2) + D) = make_float2(top, den);
+        *reinterpret_cast<float4 *>(part + m * (D + 4) + d4) = acc;
       }
     }
     if (pos == item0 && tid == 0) {
@@ -904,7 +936,7 @@ k_page_join(const AttnArgs a, int hkv, int width_rows) {
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) {
       const int c = c0 + k * SPLIT;
-      const float *src = a.parts + (((int64_t)c * 2 + (c == pl.x ? 1 : 0)) * a.R + m) * (D + 2);
+      const float *src = a.parts + (((int64_t)c * 2 + (c == pl.x ? 1 : 0)) * a.R + m) * (D + 4);
       const bool in = c <= pl.y;
       ml[k] = in ? *reinterpret_cast<const float2 *>(src + D) : make_float2(-CUDART_INF_F, 0.f);
 #pragma unroll
@@ -1037,7 +1069,7 @@ extern "C" int64_t dhs_page_attend_workspace(const dhs_pages *pages, int32_t n_s
   const int R = q_len * (q_heads / pg.hkv), sms = device_sms(dev);
   if (sms < 1) return -1;
   return pick(pg, R, [&](auto c) -> int64_t {
-    return plan_bytes(n_seqs, pg.hkv) + (int64_t)sms * decltype(c)::OCC * 2 * R * (pg.d + 2) * 4;
+    return plan_bytes(n_seqs, pg.hkv) + (int64_t)sms * decltype(c)::OCC * 2 * R * (pg.d + 4) * 4;
   });
 }
 
@@ -1085,7 +1117,7 @@ extern "C" int dhs_page_attend(const dhs_pages *pages, const void *q, const int3
   return pick(pg, a.R, [&](auto c) -> int {
     using C = decltype(c);
     const int grid = sms * C::OCC;
-    if (workspace_bytes < plan_bytes(n_seqs, pg.hkv) + (int64_t)grid * 2 * a.R * (C::D + 2) * 4)
+    if (workspace_bytes < plan_bytes(n_seqs, pg.hkv) + (int64_t)grid * 2 * a.R * (C::D + 4) * 4)
       return DHS_ERR_INVALID;
     static DeviceSmem granted;
     const int64_t rows = (int64_t)n_seqs * pg.hkv * a.R;
