@@ -527,6 +527,7 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
     const uint32_t tS = tmem + lrow + i * kPrN, tO = tmem + lrow + 2 * kPrN + i * D + hg * (D / 2);
     float *red = reinterpret_cast<float *>(smem + C::OFF_RED) + i * 256;
     const float sl2 = a.scale_log2;
+    const uint64_t sl22 = pack_f32x2(sl2, sl2);
     uint32_t sn = 0, on = 0;
     for (int k = 0;; ++k) {
       // the item stays in shared memory until its rows are written: few of its
@@ -567,8 +568,8 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
         float mx0 = -CUDART_INF_F, mx1 = mx0;
 #pragma unroll
         for (int c = 0; c < 32; c += 2) {  // (three-operand maxima)
-          mx0 = fmaxf(mx0, fmaxf(__uint_as_float(s0[c]), __uint_as_float(s0[c + 1])));
-          mx1 = fmaxf(mx1, fmaxf(__uint_as_float(s1[c]), __uint_as_float(s1[c + 1])));
+          mx0 = max3(mx0, __uint_as_float(s0[c]), __uint_as_float(s0[c + 1]));
+          mx1 = max3(mx1, __uint_as_float(s1[c]), __uint_as_float(s1[c + 1]));
         }
         float mx = fmaxf(mx0, mx1) * sl2;
         // The two warps that share 32 rows meet here, which also separates the halves'
@@ -599,17 +600,19 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
         }
         // -inf - -inf must not arise in a row that has seen nothing
         const float b = m_run == -CUDART_INF_F ? 0.f : -m_run;
-        float l0 = 0.f, l1 = 0.f;
+        uint64_t l2 = pack_f32x2(0.f, 0.f);
+        const uint64_t b2 = pack_f32x2(b, b);
         uint32_t p[16];
         // weights are rounded to bf16 for the product (at most 2^-8 of each); l is not
         auto weights = [&](const uint32_t(&s)[32]) {
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
             float u, w;
-            fma_f32x2(u, w, __uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1]), sl2, sl2, b, b);
+            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[2 * x]),
+                                              __uint_as_float(s[2 * x + 1])), sl22, b2), u, w);
             u = ex2_approx(u);
             w = ex2_approx(w);
-            add_f32x2(l0, l1, u, w);
+            l2 = add_f32x2(l2, pack_f32x2(u, w));
             p[x] = pack_bf16(u, w);
           }
         };
@@ -617,7 +620,11 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
         tmem_st16(tS + hg * (kPrH / 2), p);
         weights(s1);
         tmem_st16(tS + hg * (kPrH / 2) + 16, p);
-        l += l0 + l1;
+        {
+          float l0, l1;
+          unpack_f32x2(l2, l0, l1);
+          l += l0 + l1;
+        }
         tmem_wait_st();  // (of the rescaled O, too)
         tc_fence_before();
         __syncwarp();

@@ -143,19 +143,32 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
-// Two fp32 numbers at a time: a * b + c and a + b, each rounded to nearest.
-__device__ __forceinline__ void fma_f32x2(float &x, float &y, float ax, float ay, float bx,
-                                          float by, float cx, float cy) {
-  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
-      " mov.b64 c, {%6, %7};\n fma.rn.f32x2 c, a, b, c;\n mov.b64 {%0, %1}, c;\n}\n"
-      : "=f"(x), "=f"(y)
-      : "f"(ax), "f"(ay), "f"(bx), "f"(by), "f"(cx), "f"(cy));
+// Two fp32 numbers in one 64-bit register pair, and a * b + c, a + b of such pairs,
+// each rounded to nearest.  (Kept packed: packing around every instruction costs
+// more moves than it saves.)
+__device__ __forceinline__ uint64_t pack_f32x2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(x), "f"(y));
+  return r;
 }
-__device__ __forceinline__ void add_f32x2(float &x, float &y, float ax, float ay) {
-  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n"
-      " add.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}\n"
-      : "+f"(x), "+f"(y)
-      : "f"(ax), "f"(ay));
+__device__ __forceinline__ void unpack_f32x2(uint64_t p, float &x, float &y) {
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(x), "=f"(y) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// The largest of three (a NaN only if all are).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 // Plain arrival on an mbarrier (release at CTA scope).
