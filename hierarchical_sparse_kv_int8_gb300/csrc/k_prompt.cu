@@ -4,32 +4,44 @@
 // q_heads / kv_heads heads of a token next to one another: 128 rows are tpt =
 // 128 / G tokens (the rest of the 128 idle when G does not divide it), so that
 // grouped heads share every key and value tile and the causal edge of a tile is
-// tpt positions wide.  A CTA owns two such row tiles (2 tpt consecutive tokens of
-// one sequence) and walks the keys they see in tiles of 128:
+// tpt positions wide.  An item of work is two such row tiles (2 tpt consecutive
+// tokens of one sequence), walking the keys that they see in tiles of 128:
 //   S_i = Q_i K^T (M 128, N 128, K D), P_i = 2^(c S_i - m_i), O_i += P_i V.
+// One CTA per SM walks a fixed list of items (PromptSchedule), so that the copies
+// and first products of an item run while the rows of the one before are written.
+//
 // Warps 0-7 and 8-15 are the softmax threads of row tile 0 and 1, two threads a
 // row, each with half of a tile's columns: they read S from tensor memory, keep the
 // row's maximum m (O is rescaled only when it grows by more than kPrRescale) and its
 // sum l in 32 bits, and write P in bf16 over S in tensor memory, from where the second
-// product reads it.  One thread of warp 16 issues all MMAs in the order  P0 V(t), Q0
-// K(t+1), P1 V(t), Q1 K(t+1): while one row tile's softmax runs, the tensor cores
-// work for the other.  S_i(t + 1) overwrites P_i(t), which the MMA issued just before
-// it has read: MMAs of a thread run in order.  (With one thread a row the softmax of
-// a tile took 2500 cycles against 1300 of the other tile's products, and bound the
-// kernel: 1.02 ms for 16384 tokens of 16 heads.)  One thread of warp 17 fetches Q and the ring of K and V
-// tiles with tiled TMA copies in the 128-byte-swizzled layout.
+// product reads it.  (With one thread a row the softmax of a tile took 2500 cycles
+// against the 1024 of the other row tile's products, and bound the kernel: 1.02 ms
+// where this one takes 0.64.)  Warp 16 issues all MMAs, for each value tile t in the
+// order  P0 V(t), Q0 K(t+1), P1 V(t), Q1 K(t+1): while one row tile's softmax runs,
+// the tensor cores work for the other.  S_i(t + 1) overwrites P_i(t), which the MMA
+// issued just before it reads: MMAs run in the order of their issue.  Warp 17 works
+// out the items and fetches Q and the rings of K and V tiles with tiled TMA copies in
+// the 128-byte-swizzled layout.
 //
 // A weight is 0 where a row does not see a key, but 0 times an infinity or a NaN is
 // not 0: warps 18-19 go over the value tiles at the causal edge and the sequence's
 // end before they are used, set what is not finite there to 0, and remember it; the
 // rows that do see such a value get it added at the end, value by value.
 //
-// With few row tiles the keys are split over nsplit CTAs, which leave (O, m, l) in
-// the workspace for a join.
+// With few row tiles the keys are split over several items, which leave (O, m, l) in
+// the workspace for a join (prompt_splits says when).
 //
 // Waits are bounded; one that runs out records an error and lets the CTA finish:
-// the loader then waits for its copies and the MMA thread for its products before
+// the loader then waits for its copies and the MMA warp for its products before
 // tensor memory is freed.
+//
+// Measured (16 heads of one kv head, 128 dims): 16384 tokens of one sequence 0.644 ms,
+// 1708 TFLOP/s, 89 % of the measured matrix rate; 8192 tokens 0.19 ms.  It runs into
+// the exponentials next: a tile's 128 x 128 cost an SM's special-function units 1024
+// cycles, just the time of the tile's two products at 128 dims, and twice that of the
+// products at 64 dims, where the same 16384 tokens reach 984 TFLOP/s.  16 ragged
+// sequences of up to 2048 tokens (32 heads over 8) reach 1043: an item costs some 3
+// tiles' time besides its tiles (the first S, the rows' writing).
 #include "pages_internal.cuh"
 #include "tc_util.cuh"
 
@@ -292,8 +304,10 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
   if (warp == kMmaWarp) tmem_alloc(tmem_slot, kPrCols);
   if (tid == kLoadWarp * 32 + 1) {
     tma_prefetch(&mq);
-    tma_prefetch(&mk);
-    tma_prefetch(&mv);
+    if (a.n_k > 0) {  // (without keys their maps are not made)
+      tma_prefetch(&mk);
+      tma_prefetch(&mv);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -409,6 +423,7 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
       if (given_up() || it.q0 < 0) break;
       const int nt = max(it.n0, it.n1);
       if (nt == 0) continue;
+      // the last item's O has been read
       for (int i = 0; i < 2; ++i)
         if ((i ? it.n1 : it.n0) > 0 && on[i] > 0) wait(&o_empty[i], (on[i] - 1) & 1u);
       // S of a row tile may be written at once: the P that the last item's final
@@ -431,7 +446,6 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
         for (int i = 0; i < 2; ++i) {
           const int ni = i ? it.n1 : it.n0;
           if (n < ni) {
-            // O of the last item has been read
             wait(&p_full[i], pn[i] & 1u);
             ++pn[i];
             __syncwarp();
@@ -638,8 +652,7 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
       const int q0 = it.q0, k0 = it.k0, kvh = it.kvh, part_no = it.part, common = off + it.tok0;
       const bool valid = tloc < a.tpt && tok < it.nq;
       const int seen = valid ? off + tok : 0;  // may be negative
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&item_empty[k & 1]);
+      bool bad = false;
       uint32_t o[D / 2];
       if (ni > 0) {
         wait(&pv_done[i], on & 1u);
@@ -651,13 +664,17 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
           tmem_ld32(tO + c, *reinterpret_cast<uint32_t(*)[32]>(&o[c]));
         tmem_wait_ld();
         tc_fence_before();
+        // (read before this item's place is given up: the one after next uses it again)
+        bad = bad_values[k & 1] == k + 1;
         __syncwarp();
         if (lane == 0) mbar_arrive(&o_empty[i]);
       } else {
 #pragma unroll
         for (int x = 0; x < D / 2; ++x) o[x] = 0u;
       }
-      if (valid && bad_values[k & 1] == k + 1) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&item_empty[k & 1]);
+      if (valid && bad) {
         // values that were taken out, for the keys that this row sees in this item's tiles
         const int lo = max(max(common, 0), t0 * kPrN);
         const int hi = min(seen, (t0 + ni) * kPrN);
@@ -761,7 +778,8 @@ k_prompt_join(const PromptArgs a) {
 }
 
 bool prompt_args(int64_t n_q, int64_t n_k, int32_t n_seqs, int32_t hq, int32_t hkv, int32_t d) {
-  return n_q >= 0 && n_k >= 0 && n_q <= INT32_MAX && n_k <= INT32_MAX && n_seqs >= 0 && hkv >= 1 &&
+  // (a tile's positions run up to 256 past the last token, in 32 bits)
+  return n_q >= 0 && n_k >= 0 && n_q <= INT32_MAX - 256 && n_k <= INT32_MAX - 256 && n_seqs >= 0 && hkv >= 1 &&
          hkv <= kPageMaxHeads && hq >= 1 && hq % hkv == 0 && hq / hkv <= 128 &&
          (d == 64 || d == 128);
 }
@@ -856,7 +874,7 @@ extern "C" int dhs_prompt_attend(const void *q, const void *k, const void *v,
                                  int32_t *err, dhs_stream stream) {
   using namespace dhs;
   if (!prompt_args(n_q, n_k, n_seqs, q_heads, kv_heads, head_dim) || !(scale >= 0.f) ||
-      scale > 3e38f || workspace_bytes < 0)
+      scale > 1e38f || workspace_bytes < 0)
     return DHS_ERR_INVALID;
   if (n_q == 0 || n_seqs == 0) return DHS_OK;
   if (!q || !out || !cu_q || !cu_k || (n_k > 0 && (!k || !v)) || ((uintptr_t)q & 15u) ||

@@ -670,7 +670,7 @@ int dhs_page_read(const dhs_pages *pages, void *k, void *v, const int64_t *strid
  *             n_i on are not touched
  *   seq_lens  device int32 [n_seqs], the queries' own positions included
  *             (write their rows first); 0 for an idle slot
- *   scale     0 = 1/sqrt(head_dim); finite and not negative
+ *   scale     0 = 1/sqrt(head_dim); at most 1e38, not negative
  *   out       device bf16 like q, 16-byte aligned
  *   lse       device fp32 [n_seqs][q_len][q_heads] natural-log sum-exp, or NULL
  * A query that sees no position has out = 0 and lse = -inf.  q_len * (q_heads
@@ -701,7 +701,8 @@ int64_t dhs_page_attend_workspace(const dhs_pages *pages, int32_t n_seqs, int32_
  *              n_k; query rows outside every sequence are not touched
  *   out        device bf16 [n_q][q_heads][head_dim], 16-byte aligned
  *   lse        device fp32 [n_q][q_heads] natural-log sum-exp, or NULL
- * q_heads / kv_heads <= 128.  A query that sees no key has out = 0 and lse = -inf;
+ * n_q and n_k are at most 2^31 - 257, scale as in dhs_page_attend, q_heads / kv_heads
+ * at most 128.  A query that sees no key has out = 0 and lse = -inf;
  * what a key that a query does not see holds (infinities, NaN) never reaches it.
  *   workspace  as in dhs_page_attend, of dhs_prompt_attend_workspace() bytes;
  *              NULL with 0 bytes where that is 0 */

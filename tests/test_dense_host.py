@@ -108,6 +108,16 @@ def test_prompt_refusals(dhs):
         assert lib.dhs_prompt_attend_workspace(*a) == -1, a
 
 
+def test_limits_of_scale_and_tokens(dhs):
+    """Larger scales are infinite once they are in log2 units; a tile's positions run past
+    the last token in 32 bits."""
+    lib = dhs.load()
+    assert _attend(lib, scale=2e38) == INVALID and _prompt(lib, scale=2e38) == INVALID
+    for n in ((1 << 31) - 1, (1 << 31) - 256):
+        assert _prompt(lib, nq=n) == INVALID and _prompt(lib, nk=n) == INVALID
+        assert lib.dhs_prompt_attend_workspace(n, 4, 1, 8, 2, 128) == -1
+
+
 def test_binding_refuses_cpu_tensors_and_wrong_types(dhs):
     import torch
     x = torch.zeros((4, 2, 64, 128), dtype=torch.bfloat16)
