@@ -31,7 +31,9 @@
 // off by 2^-40 of it below), a key's scale multiplies its column of scores.  A
 // value's scale multiplies its column of weights over a common power of two, which
 // follows the largest scale read so far: f16 then holds a weight times scale to 2^-11,
-// or to 2^-31 of the largest weight times the largest scale.  (Codes to bf16 instead,
+// or to 2^-31 of the largest weight times the largest scale that the row sees (2^-27
+// next to a scale of up to 2^4 times that which the row does not see; the values of
+// larger ones are added when the warps' parts are merged).  (Codes to bf16 instead,
 // with scaled bf16 weights, took 4 instructions a pair on the half-rate integer
 // pipe instead of 1.5 to 2, and bound the kernel.)
 // The fragments are read so that no transposition is needed: a thread's 16
@@ -43,6 +45,15 @@
 // NaN is not 0, so among the last q_len - 1 positions, the only ones that some
 // queries of a sequence see and others do not, values that are not finite are
 // set to 0 in shared memory and added afterwards to the queries that see them.
+//
+// Measured, 32 sequences of 65536 positions, 128 dims, one kv head, in us (and % of the
+// measured copy bandwidth): bf16 8 rows 165 (96), 32 rows 173 (91), 64 rows 225 (70),
+// 128 rows 510; int8 8 rows 101 (81), 32 rows 181, 64 rows 316, 128 rows 805.  Up to 32
+// rows of bf16 the bytes bound it, in 8 bits the conversion to f16 does, and with more
+// rows the mma.sync products and the registers that 128 rows leave for nothing else
+// (serving decodes and verifies with 1 to 32 rows).  One sequence of 4096: 9.3 us, of
+// which the join takes 4 to 5 and the way from the lengths through the page table to
+// the first rows most of the rest.
 #include "pages_internal.cuh"
 #include "tc_util.cuh"
 
@@ -113,7 +124,7 @@ struct Cfg {
   static constexpr int RB = D * W;                       // bytes of a row
   static constexpr int CH = RB / 16;                     // 16-byte chunks of a row
   // 8-bit tiles that four warps read are turned into f16 in shared memory once (32 x
-  // 64K int8, 128 rows: 916 -> 875 us; with two warps 185 -> 225 us, so not there)
+  // 64K int8, 128 rows: 916 -> 875 us when it came in; 2 warps: 185 -> 225, so not there)
   static constexpr bool CONV = W == 1 && WM > 2;
   // positions of a group's tile: 8 KB of keys and values per warp of the group
   static constexpr int TN0 = 8192 * WM / (2 * RB);
@@ -134,7 +145,8 @@ struct Cfg {
   static constexpr int OFF_MASK = OFF_ROW + WT * SLOTS * TN * 8; // uint32 [WT][SLOTS][2]
   static constexpr int OFF_ML = OFF_MASK + WT * SLOTS * 8;       // float [WT][ROWS][2]
   static constexpr int OFF_TAB = OFF_ML + WT * ROWS * 8;         // int2 [ROWS]
-  static constexpr int SMEM = OFF_TAB + ROWS * 8;
+  static constexpr int OFF_LATE = OFF_TAB + ROWS * 8;            // float [ROWS][kMaxKmax]
+  static constexpr int SMEM = OFF_LATE + (W == 1 ? ROWS * kMaxKmax * 4 : 0);
   static constexpr int OCC = SMEM * 2 <= 226 * 1024 ? 2 : 1;
   static constexpr bool B16 = W == 2 || CONV;            // the products read 16-bit rows
   static constexpr int BLOCK = WT * TN;                  // positions of a block
@@ -161,6 +173,20 @@ __device__ __forceinline__ int64_t idiv(int64_t a, int64_t b) {
   return ((uint64_t)a | (uint64_t)b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
 
+__device__ __forceinline__ float2 f16_floats(uint32_t two) {
+  float2 r;
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "r"(two));
+  return r;
+}
+// code x of the four in w
+template <int KIND>
+__device__ __forceinline__ float code_value(uint32_t w, int x) {
+  const uint32_t c = (w >> (8 * x)) & 0xFFu;
+  return KIND == DHS_PAGE_INT8 ? (float)(int8_t)c : f16_floats(e4m3_f16(c)).x;
+}
+
 struct AttnArgs {
   const uint16_t *q;
   const int32_t *q_lens, *seq_lens, *table;
@@ -179,7 +205,8 @@ k_page_attn(const PageView pg, const AttnArgs a) {
   constexpr int D = C::D, MT = C::MT, WM = C::WM, WT = C::WT, TN = C::TN, NS = C::NS, RB = C::RB;
   constexpr int KIND = C::KIND, SUB = C::SUB, NH = C::NH, RC = C::RC;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ int sh_flag;
+  __shared__ int sh_flag;       // values that are not finite were taken out
+  __shared__ uint32_t sh_late;  // positions from `common` on that were left out
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int wm = warp % WM, wt = warp / WM;      // rows of this warp, token group
   const int gl = wm * 32 + lane;                 // thread within the group
@@ -300,7 +327,10 @@ k_page_attn(const PageView pg, const AttnArgs a) {
       at += __shfl_sync(0xffffffffu, x, 31);
     }
   }
-  if (tid == 0) sh_flag = 0;
+  if (tid == 0) {
+    sh_flag = 0;
+    sh_late = 0u;
+  }
   __syncthreads();
 
   unsigned char *ring = smem + wt * C::GROUP;
@@ -512,7 +542,7 @@ k_page_attn(const PageView pg, const AttnArgs a) {
       lookup(t + NS, ahead);
       copy(t + NS - 1);
       unsigned char *kst = ring + (t % NS) * C::STAGE, *vst = kst + C::KV;
-      const float *sc = reinterpret_cast<const float *>(vst + C::KV);
+      float *sc = reinterpret_cast<float *>(vst + C::KV);
       const int p0 = (int)((int64_t)(b0 + t) * C::BLOCK) + wt * TN;
       const uint32_t ok0 = maskbuf[(t % C::SLOTS) * 2];
       const uint32_t ok1 = TN > 32 ? maskbuf[(t % C::SLOTS) * 2 + 1] : 0xffffffffu;
@@ -539,6 +569,32 @@ k_page_attn(const PageView pg, const AttnArgs a) {
         __syncwarp();
       }
       if (C::W == 1) {
+        if (nq > 1 && p0 + TN > common) {
+          // Scales that only some rows see (the last q_len - 1) and that are 2^5 times those
+          // that all see, or the first of them: following one would cost the rows that do
+          // not see it their weights.  Where the power of two does not cover them already,
+          // their positions' values are left for the merge.  (Each warp of the group does
+          // the same.  This costs 1 to 3 %, also where q_len is 1; a power of two of each
+          // row's own cost 4 to 16 %.)
+          int e[2] = {-127, -127}, ref = -127;
+#pragma unroll
+          for (int u = 0; u < (TN + 31) / 32; ++u) {
+            const int x = lane + u * 32;
+            const uint32_t b = x < TN ? __float_as_uint(sc[TN + x]) : 0u;
+            e[u] = (int)((b < 0x7F800000u ? b : 0u) >> 23) - 127;
+            if (p0 + x <= max(p0, common - 1)) ref = max(ref, e[u]);
+          }
+          ref = __reduce_max_sync(0xffffffffu, ref);
+#pragma unroll
+          for (int u = 0; u < (TN + 31) / 32; ++u) {
+            const int x = lane + u * 32;
+            if (p0 + x >= max(common, 0) && e[u] > ref + 4 && e[u] >= vref + kVrefMax) {
+              sc[TN + x] = 0.f;
+              atomicOr(&sh_late, 1u << (p0 + x - common));
+            }
+          }
+          __syncwarp();
+        }
         // the tile's largest value scale (as bits; not one that is not finite)
         uint32_t top = 0u;
 #pragma unroll
@@ -681,8 +737,8 @@ k_page_attn(const PageView pg, const AttnArgs a) {
             }
         }
         // weights, rounded for the product with V: to bf16 (at most 2^-8 of each) or,
-        // times the value's scale, to f16 (2^-11, or 2^-31 of the largest weight times
-        // the largest scale); l takes the weights unrounded.  -inf - -inf must not
+        // times the value's scale, to f16 (2^-11, or as said at the top); l takes the
+        // weights unrounded.  -inf - -inf must not
         // arise in a row that has seen nothing yet
         uint32_t pf[MT][SUB / 16][4];
         if (NH == 1) {
@@ -791,6 +847,8 @@ k_page_attn(const PageView pg, const AttnArgs a) {
     cp_async_wait_all();
     __syncthreads();
     const bool patch = sh_flag != 0;
+    const uint32_t late = C::W == 1 ? sh_late : 0u;
+    float *late_w = reinterpret_cast<float *>(smem + C::OFF_LATE);  // a row's weights
     const bool whole = pos == item0 && stop == item1;
     const int slot = pos > item0 ? 0 : 1;
     float *part = a.parts + ((int64_t)blockIdx.x * 2 + slot) * a.R * (D + 4);
@@ -807,6 +865,23 @@ k_page_attn(const PageView pg, const AttnArgs a) {
         const float2 x = *reinterpret_cast<const float2 *>(ml + (g * C::ROWS + m) * 2);
         const float f = x.x == -CUDART_INF_F ? (x.y != x.y ? 1.f : 0.f) : ex2_approx(x.x - top);
         den += x.y * f;
+      }
+      if (late) {
+        const uint16_t *src =
+            a.q + (((int64_t)seq * a.q_len + j) * a.hq + kvh * a.G + (m - j * a.G)) * D;
+        for (int i = 0; i < kMaxKmax - 1; ++i) {
+          if (!(late >> i & 1u) || common + i >= sees) continue;
+          const int64_t row = page_row(pg, tab, common + i, nullptr, 0) + (int64_t)kvh * pg.rows;
+          float x = 0.f;
+          for (int c = 0; c < D; c += 4) {
+            const uint32_t w = *reinterpret_cast<const uint32_t *>(pg.k + row * RB + c);
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              x = fmaf(__uint_as_float((uint32_t)src[c + y] << 16), code_value<KIND>(w, y), x);
+          }
+          late_w[m * kMaxKmax + i] = ex2_approx(x * pg.ks[row] * a.scale_log2 -
+                                                (top == -CUDART_INF_F ? 0.f : top));
+        }
       }
       const int at = j < nq ? j * a.hq + (m - j * a.G) : -1;
       tab_of[m] = make_int2(at, __float_as_int(sees <= 0 ? -1.f : 1.f / den));  // (only -inf: 0 / 0)
@@ -849,7 +924,10 @@ k_page_attn(const PageView pg, const AttnArgs a) {
       }
     __syncthreads();
 
-    if (tid == 0) sh_flag = 0;  // every thread has read it
+    if (tid == 0) {  // every thread has read them
+      sh_flag = 0;
+      sh_late = 0u;
+    }
     // one row's 4 dims at a time
     uint16_t *out0 = a.out + ((int64_t)seq * a.q_len * a.hq + kvh * a.G) * D;
     for (int e = tid; e < a.R * (D / 4); e += kPaThreads) {
@@ -864,6 +942,18 @@ k_page_attn(const PageView pg, const AttnArgs a) {
         acc.y += y.y;
         acc.z += y.z;
         acc.w += y.w;
+      }
+      if (C::W == 1 && late) {
+        for (int i = 0; i < kMaxKmax - 1; ++i) {
+          if (!(late >> i & 1u) || common + i >= len - nq + m / a.G + 1) continue;
+          const int64_t row = page_row(pg, tab, common + i, nullptr, 0) + (int64_t)kvh * pg.rows;
+          const uint32_t w = *reinterpret_cast<const uint32_t *>(pg.v + row * RB + d4);
+          const float p = late_w[m * kMaxKmax + i], vs = pg.vs[row];
+          acc.x += p * (vs * code_value<KIND>(w, 0));
+          acc.y += p * (vs * code_value<KIND>(w, 1));
+          acc.z += p * (vs * code_value<KIND>(w, 2));
+          acc.w += p * (vs * code_value<KIND>(w, 3));
+        }
       }
       if (KIND == DHS_PAGE_BF16 && patch) {
         // the values taken out above, for the queries that see them
@@ -1015,9 +1105,8 @@ int64_t plan_bytes(int32_t n_seqs, int hkv) {
 }
 
 // Calls f with the configuration for R rows.  8 rows take half of a row tile's
-// softmax, 16 rows fit one warp and four
-// token groups stream at once; more rows take more warps of the same tile, and
-// above 64 two row tiles a warp.
+// softmax, 16 rows fit one warp and four token groups stream at once; more rows take
+// more warps of the same tile, and above 64 two row tiles a warp.
 template <int D, int KIND, class F>
 auto pick_rows(int R, F f) {
   if (R <= 8) return f(Cfg<D, KIND, 1, 1, 1>());
@@ -1082,7 +1171,7 @@ extern "C" int dhs_page_attend(const dhs_pages *pages, const void *q, const int3
   using namespace dhs;
   PageView pg;
   if (!attend_args(pages, n_seqs, q_len, q_heads, &pg) || table_width < 0 || !(scale >= 0.f) ||
-      scale > 3e38f || workspace_bytes < 0)
+      scale > 1e38f || workspace_bytes < 0)
     return DHS_ERR_INVALID;
   if (n_seqs == 0) return DHS_OK;
   if (!q || !seq_lens || !page_table || !out || !workspace || ((uintptr_t)q & 15u) ||

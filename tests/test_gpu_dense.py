@@ -506,6 +506,29 @@ def test_attend_scales_far_apart(torch, dhs):
     _close(_np(out[0]), None, want, 128, 640, np.abs(v).max())
 
 
+@pytest.mark.parametrize("kind", [INT8, E4M3])
+@pytest.mark.parametrize("hq,d", [(2, 128), (4, 64), (8, 128), (16, 64), (32, 128)])
+def test_attend_large_scales_that_some_queries_do_not_see(torch, dhs, kind, hq, d):
+    """The last rows' value scales are 2^60 times the others': the queries before them are
+    as exact as without (their tolerance counts only values that they see)."""
+    from oracle import dense_oracle as oracle
+    for where in (1, 3):
+        pc = Paged(torch, dhs, [2, 3, 64, 65, 66, 67, 129, 130, 700], 64, 1, d, kind)
+        kv = pc.fill()
+        for i, n in enumerate(pc.lens):
+            for p in range(max(0, n - where), n):
+                pc.cache.v_scale[int(pc.table[i, p // 64]), 0, p % 64] *= 2.0 ** 60
+                kv[i][1][p] *= 2.0 ** 60
+        q = torch.randn((9, 4, hq, d)).bfloat16().cuda()
+        out = torch.zeros_like(q)
+        pc.cache.attend(q, pc.seq_lens, pc.table, out, pc.cache.attend_workspace(9, 4, hq))
+        pc.cache.check()
+        for i, n in enumerate(pc.lens):
+            want = oracle.attend(_np(q[i]), *kv[i], 1 / math.sqrt(d))
+            vmax = [np.abs(kv[i][1][:max(0, n - 3 + u)]).max(initial=0.0) for u in range(4)]
+            _close(_np(out[i]), None, want, d, n, np.array(vmax)[:, None, None])
+
+
 def test_attend_same_result_again_and_beside_others(torch, dhs):
     """Bits repeat; a sequence's result does not depend on its neighbours' values,
     and a workspace goes from one call to the next, whatever ran before."""
@@ -672,6 +695,28 @@ def test_prompt_masked_places_do_not_matter(torch, dhs, d):
     assert np.isfinite(got[130:, 2:][:, :, clear]).all()
     _close(got[130:131, :2], None, [w[130:131, :2] for w in want], d, 200)
     assert torch.isnan(out[:60]).all() and torch.isnan(out[260:]).all()
+
+
+def test_prompt_infinite_values_of_many_sequences(torch, dhs):
+    """Some 400 short sequences (several to a CTA, most with one row tile), half of them
+    with an infinite value: it reaches the rows that see it and no other sequence's."""
+    from oracle import dense_oracle as oracle
+    g = torch.Generator().manual_seed(11)
+    sizes = torch.randint(1, 40, (400,), generator=g).tolist()
+    sizes[100], sizes[200] = 150, 300
+    cu = np.concatenate([[0], np.cumsum(sizes)])
+    q, k, v = (torch.randn((int(cu[-1]), h, 64), generator=g).bfloat16() for h in (2, 1, 1))
+    for i in range(0, 400, 2):
+        v[cu[i] + sizes[i] * 2 // 3, 0, i % 64] = math.inf
+    off = torch.tensor(cu, dtype=torch.int32).cuda()
+    qd, kd, vd = q.cuda(), k.cuda(), v.cuda()
+    out = torch.full_like(qd, 77.0)
+    dhs.prompt_attend(qd, kd, vd, off, off, out, workspace=dhs.prompt_workspace(qd, kd, 400))
+    for i in range(400):
+        r = slice(cu[i], cu[i + 1])
+        want = oracle.attend(_np(q[r]), _np(k[r]), _np(v[r]), 1 / 8)
+        assert np.array_equal(np.isposinf(_np(out[r])), np.isposinf(want[0])), i
+        _close(_np(out[r]), None, want, 64, sizes[i])
 
 
 def test_prompt_from_cold_memory(torch, dhs):
@@ -881,3 +926,32 @@ def test_calls_on_another_stream(torch, dhs):
     for i in range(2):
         want = oracle.attend(2 * _np(q[i]), *kv[i], 1 / math.sqrt(128))
         _close(_np(out[i]), None, want, 128, 2000)
+
+
+def test_two_calls_at_once(torch, dhs):
+    """The same calls on two streams at a time, each with a workspace of its own."""
+    pc = Paged(torch, dhs, [9000, 300, 4000], 64, 2, 128, INT8)
+    pc.fill()
+    q = torch.randn((3, 2, 8, 128)).bfloat16().cuda()
+    x, kv = torch.randn((700, 8, 128)).bfloat16().cuda(), torch.randn((6000, 2, 128)).bfloat16().cuda()
+    cq, ck = (torch.tensor(c, dtype=torch.int32).cuda() for c in ([0, 300, 700], [0, 5000, 6000]))
+
+    def calls(stream):
+        with torch.cuda.stream(stream):
+            a, b = torch.empty_like(q), torch.empty_like(x)
+            ws, pw = pc.cache.attend_workspace(3, 2, 8), dhs.prompt_workspace(x, kv, 2)
+            for _ in range(4):
+                pc.cache.attend(q, pc.seq_lens, pc.table, a, ws)
+                dhs.prompt_attend(x, kv, kv, cq, ck, b, workspace=pw)
+            return a, b, ws, pw
+
+    torch.cuda.synchronize()
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    alone = calls(one)
+    torch.cuda.synchronize()
+    for s in (one, two):
+        s.wait_stream(torch.cuda.current_stream())
+    got = [calls(s) for s in (one, two)]
+    torch.cuda.synchronize()
+    for g in got:
+        assert torch.equal(g[0], alone[0]) and torch.equal(g[1], alone[1])
