@@ -36,12 +36,13 @@
 // tensor memory is freed.
 //
 // Measured (16 heads of one kv head, 128 dims): 16384 tokens of one sequence 0.644 ms,
-// 1708 TFLOP/s, 89 % of the measured matrix rate; 8192 tokens 0.19 ms.  It runs into
-// the exponentials next: a tile's 128 x 128 cost an SM's special-function units 1024
-// cycles, just the time of the tile's two products at 128 dims, and twice that of the
-// products at 64 dims, where the same 16384 tokens reach 984 TFLOP/s.  16 ragged
-// sequences of up to 2048 tokens (32 heads over 8) reach 1043: an item costs some 3
-// tiles' time besides its tiles (the first S, the rows' writing).
+// 1708 TFLOP/s, 89 % of the measured matrix rate; 8192 tokens 0.18 ms.  At 64 dims a
+// tile's products take half the time and its softmax the same: 16384 tokens reach 992
+// TFLOP/s with the tensor pipe busy for 39 % of the cycles, the issue slots for 52 and
+// the exponentials' pipe for 39: what bounds it is the chain of a tile's softmax (read S,
+// maximum, exponentials, write P) of which two run side by side.  16 ragged sequences of
+// up to 2048 tokens (32 heads over 8) reach 1043: an item costs some 3 tiles' time
+// besides its tiles (the first S, the rows' writing).
 #include "pages_internal.cuh"
 #include "tc_util.cuh"
 
@@ -802,7 +803,8 @@ k_prompt_join(const PromptArgs a) {
 
 bool prompt_args(int64_t n_q, int64_t n_k, int32_t n_seqs, int32_t hq, int32_t hkv, int32_t d) {
   // (a tile's positions run up to 256 past the last token, in 32 bits)
-  return n_q >= 0 && n_k >= 0 && n_q <= INT32_MAX - 256 && n_k <= INT32_MAX - 256 && n_seqs >= 0 && hkv >= 1 &&
+  constexpr int64_t most = INT32_MAX - 256;
+  return n_q >= 0 && n_k >= 0 && n_q <= most && n_k <= most && n_seqs >= 0 && hkv >= 1 &&
          hkv <= kPageMaxHeads && hq >= 1 && hq % hkv == 0 && hq / hkv <= 128 &&
          (d == 64 || d == 128);
 }
