@@ -9,7 +9,6 @@ library its tensors must stay alive until the stream has passed it.
 from __future__ import annotations
 
 import ctypes
-from contextlib import nullcontext
 from typing import Optional
 
 import torch
@@ -32,15 +31,20 @@ class Pages(ctypes.Structure):
                 ("head_dim", ctypes.c_int32), ("kind", ctypes.c_int32)]
 
 
-try:  # the current stream's handle without building a Stream object (a decode step makes
-    # several calls of a few microseconds each)
+# A decode step makes several calls of a few microseconds each, so what a call does on
+# the host counts: the current stream's handle and device without torch's wrappers, no
+# array of strides for contiguous rows, no context where the device is the current one
+# (7.9 -> XX us for a write from Python, of which the launch is 2).
+try:
     from torch._C import _cuda_getCurrentRawStream as _current_stream
+    from torch._C import _cuda_getDevice as _current_device
 except ImportError:
+    _current_device = torch.cuda.current_device
+
     def _current_stream(index):
         return torch.cuda.current_stream(index).cuda_stream
 
 _BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
-_HERE = nullcontext()
 
 
 def _lib():
@@ -99,7 +103,7 @@ def _on(index):
     """The context in which a call runs on device ``index``."""
     if index < 0:
         raise ValueError("CUDA tensors expected")
-    return _HERE if torch.cuda.current_device() == index else torch.cuda.device(index)
+    return torch.cuda.device(index)
 
 
 def _raw(stream, index):
@@ -172,17 +176,20 @@ class PageCache:
 
     def _copy(self, fn, what, k, v, cu, seq_lens, page_table, stream):
         ix = self._index
+        if _current_device() != ix:
+            with _on(ix):
+                return self._copy(fn, what, k, v, cu, seq_lens, page_table, stream)
         tok, h, d, kt, kh = _rows(k, "k", ix)
         tv, hv, dv, vt, vh = _rows(v, "v", ix)
         if (tv, hv, dv) != (tok, h, d) or h != self.kv_heads or d != self.head_dim:
             raise ValueError("k and v: [tokens, %d, %d] expected, not %s and %s" % (
                 self.kv_heads, self.head_dim, tuple(k.shape), tuple(v.shape)))
         n = seq_lens.shape[0]
-        with _on(ix):
-            rc = fn(self._ref, k.data_ptr(), v.data_ptr(), _Strides4(kt, kh, vt, vh), tok,
-                    _plain(cu, "cu", _I32, (n + 1,), ix),
-                    _plain(seq_lens, "seq_lens", _I32, (n,), ix), _table(page_table, n, ix),
-                    page_table.shape[1], n, self._err, _raw(stream, ix))
+        strides = None if kt == vt == h * d and kh == vh == d else _Strides4(kt, kh, vt, vh)
+        rc = fn(self._ref, k.data_ptr(), v.data_ptr(), strides, tok,
+                _plain(cu, "cu", _I32, (n + 1,), ix),
+                _plain(seq_lens, "seq_lens", _I32, (n,), ix), _table(page_table, n, ix),
+                page_table.shape[1], n, self._err, _raw(stream, ix))
         if rc:
             _raise(rc, what)
 
@@ -210,19 +217,21 @@ class PageCache:
         """Attention of the newest tokens over the cache (dhs_page_attend):
         ``q`` and ``out`` [n_seqs, q_len, q_heads, head_dim]."""
         ix, shape = self._index, q.shape
+        if _current_device() != ix:
+            with _on(ix):
+                return self.attend(q, seq_lens, page_table, out, workspace, lse, q_lens, scale, stream)
         if len(shape) != 4 or shape[3] != self.head_dim:
             raise ValueError("q: [n_seqs, q_len, q_heads, %d] expected, not %s"
                              % (self.head_dim, tuple(shape)))
         n, qn, hq, _ = shape
         space, nbytes = _space(workspace, ix)
-        with _on(ix):
-            rc = self._lib.dhs_page_attend(
-                self._ref, _plain(q, "q", _BF16, shape, ix),
-                None if q_lens is None else _plain(q_lens, "q_lens", _I32, (n,), ix),
-                _plain(seq_lens, "seq_lens", _I32, (n,), ix), _table(page_table, n, ix),
-                page_table.shape[1], n, qn, hq, scale, _plain(out, "out", _BF16, shape, ix),
-                None if lse is None else _plain(lse, "lse", _F32, (n, qn, hq), ix), space, nbytes,
-                self._err, _raw(stream, ix))
+        rc = self._lib.dhs_page_attend(
+            self._ref, _plain(q, "q", _BF16, shape, ix),
+            None if q_lens is None else _plain(q_lens, "q_lens", _I32, (n,), ix),
+            _plain(seq_lens, "seq_lens", _I32, (n,), ix), _table(page_table, n, ix),
+            page_table.shape[1], n, qn, hq, scale, _plain(out, "out", _BF16, shape, ix),
+            None if lse is None else _plain(lse, "lse", _F32, (n, qn, hq), ix), space, nbytes,
+            self._err, _raw(stream, ix))
         if rc:
             _raise(rc, "dhs_page_attend")
 
@@ -247,6 +256,9 @@ def prompt_attend(q, k, v, cu_q, cu_k, out, lse=None, workspace=None, scale: flo
     """Causal attention of packed sequences (dhs_prompt_attend): ``q`` [n_q, q_heads,
     head_dim], ``k`` and ``v`` [n_k, kv_heads, head_dim], ``out`` like ``q``."""
     ix = q.get_device()
+    if ix < 0 or _current_device() != ix:
+        with _on(ix):
+            return prompt_attend(q, k, v, cu_q, cu_k, out, lse, workspace, scale, errors, stream)
     nq, hq, d, qt, qh = _rows(q, "q", ix)
     nk, hkv, dk, kt, kh = _rows(k, "k", ix)
     nv, hv, dv, vt, vh = _rows(v, "v", ix)
@@ -257,12 +269,13 @@ def prompt_attend(q, k, v, cu_q, cu_k, out, lse=None, workspace=None, scale: flo
     if n < 0:
         raise ValueError("cu_q: [n_seqs + 1] expected")
     space, nbytes = _space(workspace, ix)
-    with _on(ix):
-        rc = _lib().dhs_prompt_attend(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), _Strides6(qt, qh, kt, kh, vt, vh), nq, nk,
-            _plain(cu_q, "cu_q", _I32, (n + 1,), ix), _plain(cu_k, "cu_k", _I32, (n + 1,), ix), n, hq,
-            hkv, d, scale, _plain(out, "out", _BF16, q.shape, ix),
-            None if lse is None else _plain(lse, "lse", _F32, (nq, hq), ix), space, nbytes,
-            None if errors is None else _plain(errors, "errors", _I32, (2,), ix), _raw(stream, ix))
+    strides = (None if kt == vt == hkv * d and qt == hq * d and qh == kh == vh == d
+               else _Strides6(qt, qh, kt, kh, vt, vh))
+    rc = _lib().dhs_prompt_attend(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), strides, nq, nk,
+        _plain(cu_q, "cu_q", _I32, (n + 1,), ix), _plain(cu_k, "cu_k", _I32, (n + 1,), ix), n, hq,
+        hkv, d, scale, _plain(out, "out", _BF16, q.shape, ix),
+        None if lse is None else _plain(lse, "lse", _F32, (nq, hq), ix), space, nbytes,
+        None if errors is None else _plain(errors, "errors", _I32, (2,), ix), _raw(stream, ix))
     if rc:
         _raise(rc, "dhs_prompt_attend")
