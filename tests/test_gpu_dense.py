@@ -955,3 +955,49 @@ def test_two_calls_at_once(torch, dhs):
     torch.cuda.synchronize()
     for g in got:
         assert torch.equal(g[0], alone[0]) and torch.equal(g[1], alone[1])
+
+
+def test_prompt_bad_offsets_among_many(torch, dhs):
+    """One offset out of range among 300 sequences: the two that it belongs to are left
+    alone and reported, the others are as without it."""
+    n, t = 300, 5
+    q, k = torch.randn((n * t, 4, 64)).bfloat16().cuda(), torch.randn((n * t, 2, 64)).bfloat16().cuda()
+    cu = torch.arange(0, n * t + 1, t, dtype=torch.int32)
+    bad = cu.clone()
+    bad[150] = 10 ** 9
+    ws, err = dhs.prompt_workspace(q, k, n), torch.zeros(2, dtype=torch.int32, device="cuda")
+    outs = []
+    for c in (cu, bad):
+        out = torch.full_like(q, 77.0)
+        dhs.prompt_attend(q, k, k, cu.cuda(), c.cuda(), out, workspace=ws, errors=err)
+        outs.append(out)
+    with pytest.raises(dhs.DhsError):
+        dhs.check_errors(err)
+    r = slice(149 * t, 151 * t)
+    assert torch.all(outs[1][r] == 77)
+    outs[1][r] = outs[0][r]
+    assert torch.equal(outs[0], outs[1])
+
+
+def test_prompt_past_2_to_the_31_elements(torch, dhs):
+    """q and out of more than 2^31 elements: the last sequences are right, and as in a call
+    of their own."""
+    from oracle import dense_oracle as oracle
+    n, t, hq, hkv, d = 500, 33, 1024, 8, 128
+    q = torch.empty((n * t, hq, d), dtype=torch.bfloat16, device="cuda")
+    assert q.numel() > 1 << 31
+    for i in range(0, n * t, 1650):
+        q[i:i + 1650] = torch.randn((1650, hq, d), device="cuda")
+    k, v = (torch.randn((n * t, hkv, d), device="cuda").bfloat16() for _ in range(2))
+    cu = torch.arange(0, n * t + 1, t, dtype=torch.int32, device="cuda")
+    out = torch.full_like(q, 77.0)
+    dhs.prompt_attend(q, k, v, cu, cu, out, workspace=dhs.prompt_workspace(q, k, n))
+    last = slice((n - 2) * t, n * t)
+    own = torch.empty_like(out[last])
+    dhs.prompt_attend(q[last], k[last], v[last], cu[:3], cu[:3], own,
+                      workspace=dhs.prompt_workspace(q[last], k[last], 2))
+    r = slice((n - 1) * t, n * t)
+    want = oracle.attend(_np(q[r, 1020:]), _np(k[r, 7:]), _np(v[r, 7:]), 1 / math.sqrt(d))
+    _close(_np(out[r, 1020:]), None, want, d, t)
+    assert not (out[:2 * t] == 77).any()
+    assert torch.equal(out[last], own)
