@@ -48,7 +48,7 @@
 //
 // Measured, 32 sequences of 65536 positions, 128 dims, one kv head, in us (and % of the
 // measured copy bandwidth): bf16 8 rows 165 (96), 32 rows 173 (91), 64 rows 225 (70),
-// 128 rows 510; int8 8 rows 101 (81), 32 rows 181, 64 rows 316, 128 rows 805.  Up to 32
+// 128 rows 510; int8 8 rows 99 (82), 32 rows 181, 64 rows 316, 128 rows 801.  Up to 32
 // rows of bf16 the bytes bound it, in 8 bits the conversion to f16 does, and with more
 // rows the mma.sync products and the registers that 128 rows leave for nothing else
 // (serving decodes and verifies with 1 to 32 rows).  One sequence of 4096: 9.3 us, of
@@ -115,10 +115,11 @@ __device__ __forceinline__ void cp_async_4_zfill(void *dst, const void *src, int
                "r"(bytes));
 }
 
-template <int D_, int KIND_, int WM_, int MT_, int NH_>
+template <int D_, int KIND_, int WM_, int MT_, int NH_, bool SOME_ = KIND_ != DHS_PAGE_BF16>
 struct Cfg {
   static constexpr int D = D_, KIND = KIND_, WM = WM_, MT = MT_;
   static constexpr int NH = NH_;                         // 8-row halves of a row tile in use
+  static constexpr bool SOME = SOME_;  // value scales that only some rows see are looked for
   static constexpr int WT = kPaWarps / WM;
   static constexpr int W = KIND == DHS_PAGE_BF16 ? 2 : 1;
   static constexpr int RB = D * W;                       // bytes of a row
@@ -146,7 +147,7 @@ struct Cfg {
   static constexpr int OFF_ML = OFF_MASK + WT * SLOTS * 8;       // float [WT][ROWS][2]
   static constexpr int OFF_TAB = OFF_ML + WT * ROWS * 8;         // int2 [ROWS]
   static constexpr int OFF_LATE = OFF_TAB + ROWS * 8;            // float [ROWS][kMaxKmax]
-  static constexpr int SMEM = OFF_LATE + (W == 1 ? ROWS * kMaxKmax * 4 : 0);
+  static constexpr int SMEM = OFF_LATE + (SOME ? ROWS * kMaxKmax * 4 : 0);
   static constexpr int OCC = SMEM * 2 <= 226 * 1024 ? 2 : 1;
   static constexpr bool B16 = W == 2 || CONV;            // the products read 16-bit rows
   static constexpr int BLOCK = WT * TN;                  // positions of a block
@@ -569,13 +570,12 @@ k_page_attn(const PageView pg, const AttnArgs a) {
         __syncwarp();
       }
       if (C::W == 1) {
-        if (nq > 1 && p0 + TN > common) {
+        if (C::SOME && nq > 1 && p0 + TN > common) {
           // Scales that only some rows see (the last q_len - 1) and that are 2^5 times those
           // that all see, or the first of them: following one would cost the rows that do
           // not see it their weights.  Where the power of two does not cover them already,
           // their positions' values are left for the merge.  (Each warp of the group does
-          // the same.  This costs 1 to 3 %, also where q_len is 1; a power of two of each
-          // row's own cost 4 to 16 %.)
+          // the same.  This costs 1 to 3 %; a power of two of each row's own cost 4 to 16.)
           int e[2] = {-127, -127}, ref = -127;
 #pragma unroll
           for (int u = 0; u < (TN + 31) / 32; ++u) {
@@ -847,7 +847,7 @@ k_page_attn(const PageView pg, const AttnArgs a) {
     cp_async_wait_all();
     __syncthreads();
     const bool patch = sh_flag != 0;
-    const uint32_t late = C::W == 1 ? sh_late : 0u;
+    const uint32_t late = C::SOME ? sh_late : 0u;
     float *late_w = reinterpret_cast<float *>(smem + C::OFF_LATE);  // a row's weights
     const bool whole = pos == item0 && stop == item1;
     const int slot = pos > item0 ? 0 : 1;
@@ -866,7 +866,7 @@ k_page_attn(const PageView pg, const AttnArgs a) {
         const float f = x.x == -CUDART_INF_F ? (x.y != x.y ? 1.f : 0.f) : ex2_approx(x.x - top);
         den += x.y * f;
       }
-      if (late) {
+      if (C::SOME && late) {
         const uint16_t *src =
             a.q + (((int64_t)seq * a.q_len + j) * a.hq + kvh * a.G + (m - j * a.G)) * D;
         for (int i = 0; i < kMaxKmax - 1; ++i) {
@@ -943,7 +943,7 @@ k_page_attn(const PageView pg, const AttnArgs a) {
         acc.z += y.z;
         acc.w += y.w;
       }
-      if (C::W == 1 && late) {
+      if (C::SOME && late) {
         for (int i = 0; i < kMaxKmax - 1; ++i) {
           if (!(late >> i & 1u) || common + i >= len - nq + m / a.G + 1) continue;
           const int64_t row = page_row(pg, tab, common + i, nullptr, 0) + (int64_t)kvh * pg.rows;
@@ -1106,9 +1106,13 @@ int64_t plan_bytes(int32_t n_seqs, int hkv) {
 
 // Calls f with the configuration for R rows.  8 rows take half of a row tile's
 // softmax, 16 rows fit one warp and four token groups stream at once; more rows take
-// more warps of the same tile, and above 64 two row tiles a warp.
+// more warps of the same tile, and above 64 two row tiles a warp.  With one token a
+// sequence every row sees every position, and up to 16 rows of 8 bits, the usual
+// decode, leave out what looks for others (128 x 100K int8: 451 -> 446 us).
 template <int D, int KIND, class F>
-auto pick_rows(int R, F f) {
+auto pick_rows(int R, int q_len, F f) {
+  if (KIND != DHS_PAGE_BF16 && q_len == 1 && R <= 16)
+    return R <= 8 ? f(Cfg<D, KIND, 1, 1, 1, false>()) : f(Cfg<D, KIND, 1, 1, 2, false>());
   if (R <= 8) return f(Cfg<D, KIND, 1, 1, 1>());
   if (R <= 16) return f(Cfg<D, KIND, 1, 1, 2>());
   if (R <= 32) return f(Cfg<D, KIND, 2, 1, 2>());
@@ -1116,14 +1120,14 @@ auto pick_rows(int R, F f) {
   return f(Cfg<D, KIND, 4, 2, 2>());
 }
 template <class F>
-auto pick(const PageView &pg, int R, F f) {
+auto pick(const PageView &pg, int R, int q_len, F f) {
   switch ((pg.d == 128 ? 4 : 0) + pg.kind) {
-    case 0: return pick_rows<64, DHS_PAGE_BF16>(R, f);
-    case 1: return pick_rows<64, DHS_PAGE_INT8>(R, f);
-    case 2: return pick_rows<64, DHS_PAGE_E4M3>(R, f);
-    case 4: return pick_rows<128, DHS_PAGE_BF16>(R, f);
-    case 5: return pick_rows<128, DHS_PAGE_INT8>(R, f);
-    default: return pick_rows<128, DHS_PAGE_E4M3>(R, f);
+    case 0: return pick_rows<64, DHS_PAGE_BF16>(R, q_len, f);
+    case 1: return pick_rows<64, DHS_PAGE_INT8>(R, q_len, f);
+    case 2: return pick_rows<64, DHS_PAGE_E4M3>(R, q_len, f);
+    case 4: return pick_rows<128, DHS_PAGE_BF16>(R, q_len, f);
+    case 5: return pick_rows<128, DHS_PAGE_INT8>(R, q_len, f);
+    default: return pick_rows<128, DHS_PAGE_E4M3>(R, q_len, f);
   }
 }
 
@@ -1157,7 +1161,7 @@ extern "C" int64_t dhs_page_attend_workspace(const dhs_pages *pages, int32_t n_s
   }
   const int R = q_len * (q_heads / pg.hkv), sms = device_sms(dev);
   if (sms < 1) return -1;
-  return pick(pg, R, [&](auto c) -> int64_t {
+  return pick(pg, R, q_len, [&](auto c) -> int64_t {
     return plan_bytes(n_seqs, pg.hkv) + (int64_t)sms * decltype(c)::OCC * 2 * R * (pg.d + 4) * 4;
   });
 }
@@ -1203,7 +1207,7 @@ extern "C" int dhs_page_attend(const dhs_pages *pages, const void *q, const int3
   a.R = q_len * a.G;
   a.scale_log2 = (scale == 0.f ? 1.f / sqrtf((float)pg.d) : scale) * 1.4426950408889634f;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return pick(pg, a.R, [&](auto c) -> int {
+  return pick(pg, a.R, q_len, [&](auto c) -> int {
     using C = decltype(c);
     const int grid = sms * C::OCC;
     if (workspace_bytes < plan_bytes(n_seqs, pg.hkv) + (int64_t)grid * 2 * a.R * (C::D + 4) * 4)
