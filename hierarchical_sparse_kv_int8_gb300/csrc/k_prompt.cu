@@ -16,7 +16,7 @@
 // sum l in 32 bits, and write P in bf16 over S in tensor memory, from where the second
 // product reads it.  (With one thread a row the softmax of a tile took 2500 cycles
 // against the 1024 of the other row tile's products, and bound the kernel: 1.02 ms
-// where this one takes 0.64.)  Warp 16 issues all MMAs, for each value tile t in the
+// then, 0.73 with two.)  Warp 16 issues all MMAs, for each value tile t in the
 // order  P0 V(t), Q0 K(t+1), P1 V(t), Q1 K(t+1): while one row tile's softmax runs,
 // the tensor cores work for the other.  S_i(t + 1) overwrites P_i(t), which the MMA
 // issued just before it reads: MMAs run in the order of their issue.  Warp 17 works
@@ -35,14 +35,14 @@
 // the loader then waits for its copies and the MMA warp for its products before
 // tensor memory is freed.
 //
-// Measured (16 heads of one kv head, 128 dims): 16384 tokens of one sequence 0.644 ms,
-// 1708 TFLOP/s, 89 % of the measured matrix rate; 8192 tokens 0.18 ms.  At 64 dims a
-// tile's products take half the time and its softmax the same: 16384 tokens reach 992
-// TFLOP/s with the tensor pipe busy for 39 % of the cycles, the issue slots for 52 and
-// the exponentials' pipe for 39: what bounds it is the chain of a tile's softmax (read S,
-// maximum, exponentials, write P) of which two run side by side.  16 ragged sequences of
-// up to 2048 tokens (32 heads over 8) reach 1043: an item costs some 3 tiles' time
-// besides its tiles (the first S, the rows' writing).
+// Measured (16 heads of one kv head, 128 dims): 16384 tokens of one sequence 0.60 ms,
+// 1830 TFLOP/s, 95 % of the measured matrix rate; 8192 tokens 0.166 ms.  At 64 dims Q K^T
+// takes half the time, P V as long as at 128 and a tile's softmax the same: 16384 tokens
+// reach 1110 TFLOP/s with the tensor pipe busy for 44 % of the cycles, the issue slots
+// for 54 and the exponentials' pipe for 44: what bounds it is the chain of a tile's
+// softmax (read S, maximum, exponentials, write P), of which two run side by side.  16
+// ragged sequences of up to 2048 tokens (32 heads over 8) reach 1180: an item costs some 3
+// tiles' time besides its tiles (the first S, the rows' writing).
 #include "pages_internal.cuh"
 #include "tc_util.cuh"
 
@@ -822,7 +822,7 @@ int64_t prompt_tiles(int64_t n_q, int32_t n_seqs, int G) {
 // Key splits: as many as make the longest CTA shortest.  With I row-tile pairs (times
 // kv heads) of T key tiles, n splits deal I n items of T / n tiles to the SMs in
 // ceil(I n / SMs) turns; an item costs some 3 tiles' time besides its tiles, a join
-// some 6.  (Two 500-token chunks over 32K keys, 32 pairs: 4 splits, 98 us instead of
+// some 6.  (Two 500-token chunks over 32K keys, 32 pairs: 4 splits, 92 us instead of
 // 330.)
 int prompt_splits(int64_t n_q, int64_t n_k, int32_t n_seqs, int hq, int hkv, int sms) {
   if (n_q == 0 || n_seqs == 0) return 1;
