@@ -47,11 +47,11 @@
 // set to 0 in shared memory and added afterwards to the queries that see them.
 //
 // Measured, 32 sequences of 65536 positions, 128 dims, one kv head, in us (and % of the
-// measured copy bandwidth): bf16 8 rows 165 (96), 32 rows 173 (91), 64 rows 225 (70),
-// 128 rows 510; int8 8 rows 99 (82), 32 rows 181, 64 rows 316, 128 rows 801.  Up to 32
+// measured copy bandwidth): bf16 8 rows 167 (95), 32 rows 173 (91), 64 rows 225 (70),
+// 128 rows 510; int8 8 rows 99 (82), 32 rows 178, 64 rows 316, 128 rows 833.  Up to 32
 // rows of bf16 the bytes bound it, in 8 bits the conversion to f16 does, and with more
 // rows the mma.sync products and the registers that 128 rows leave for nothing else
-// (serving decodes and verifies with 1 to 32 rows).  One sequence of 4096: 9.3 us, of
+// (serving decodes and verifies with 1 to 32 rows).  One sequence of 4096: 9.0 us, of
 // which the join takes 4 to 5 and the way from the lengths through the page table to
 // the first rows most of the rest.
 #include "pages_internal.cuh"
@@ -239,15 +239,42 @@ k_page_attn(const PageView pg, const AttnArgs a) {
     return my_n;
   };
 
+  // The same of sequences i + 32 u + lane, whose loads are under way together (1024
+  // sequences of 200: 53 -> 38 us).
+  auto blocks8 = [&](int i, int (&n)[8], bool record) {
+    int nq[8], len[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int at = i + 32 * u + lane;
+      nq[u] = at >= a.n_seqs ? 0 : a.q_lens ? a.q_lens[at] : a.q_len;
+      len[u] = at >= a.n_seqs ? 0 : a.seq_lens[at];
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (record && (nq[u] < 0 || nq[u] > a.q_len || len[u] < 0 || len[u] > most))
+        page_error(a.err, DC_ROW_RANGE, DHS_SITE_PAGE_ATTEND);
+      len[u] = (int)max((int64_t)0, min((int64_t)len[u], most));
+      n[u] = nq[u] > 0 ? (int)(((uint32_t)len[u] + C::BLOCK - 1) / C::BLOCK) : 0;
+    }
+  };
+
   // All blocks, and the sequences with any: every warp adds up all of them.
   int64_t sum = 0;
   int some = 0;
-  for (int i = 0; i < a.n_seqs; i += 32) {
-    const int n = blocks(i);
-    some += __popc(__ballot_sync(0xffffffffu, n > 0));
-    sum += few ? __reduce_add_sync(0xffffffffu, n) : n;  // (32 of them fit 32 bits)
-  }
-  if (!few) {
+  if (few) {
+    const int n = blocks(0);
+    some = __popc(__ballot_sync(0xffffffffu, n > 0));
+    sum = __reduce_add_sync(0xffffffffu, n);  // (32 of them fit 32 bits)
+  } else {
+    for (int i = 0; i < a.n_seqs; i += 256) {
+      int n[8];
+      blocks8(i, n, true);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        some += __popc(__ballot_sync(0xffffffffu, n[u] > 0));
+        sum += n[u];
+      }
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   }
@@ -308,25 +335,36 @@ k_page_attn(const PageView pg, const AttnArgs a) {
   {
     const int64_t want = idiv(begin, hkv);  // in units of one head: only the sequence is looked for
     int64_t at = 0;
-    for (int i = 0; i < a.n_seqs; i += 32) {
-      const int n = (int)units(blocks(i));
-      int x = n;  // inclusive sums
+    int base = 0;  // its 32 neighbours
+    if (!few) {
+      bool found = false;
+      for (int i = 0; i < a.n_seqs && !found; i += 256) {
+        int n[8];
+        blocks8(i, n, false);
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        for (int u = 0; u < 8; ++u) {
+          const int all = __reduce_add_sync(0xffffffffu, (int)units(n[u]));
+          if (!found && want < at + all) {
+            found = true;
+            base = i + 32 * u;
+          }
+          if (!found) at += all;
+        }
       }
-      const uint32_t here = __ballot_sync(0xffffffffu, want < at + x);
-      if (here) {
-        const int src = __ffs(here) - 1;
-        seq = i + src;
-        seq_at = (at + __shfl_sync(0xffffffffu, x - n, src)) * hkv;
-        seq_nq = __shfl_sync(0xffffffffu, my_nq, src);
-        seq_len = __shfl_sync(0xffffffffu, my_len, src);
-        break;
-      }
-      at += __shfl_sync(0xffffffffu, x, 31);
     }
+    const int n = (int)units(blocks(base));
+    int x = n;  // inclusive sums
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    const uint32_t here = __ballot_sync(0xffffffffu, want < at + x);
+    const int src = max(0, __ffs(here) - 1);
+    seq = base + src;
+    seq_at = (at + __shfl_sync(0xffffffffu, x - n, src)) * hkv;
+    seq_nq = __shfl_sync(0xffffffffu, my_nq, src);
+    seq_len = __shfl_sync(0xffffffffu, my_len, src);
   }
   if (tid == 0) {
     sh_flag = 0;
@@ -361,6 +399,35 @@ k_page_attn(const PageView pg, const AttnArgs a) {
     const int b0 = (int)(chunked ? idiv(nb * (pos - item0), nu) : pos - item0);
     const int nblk = (int)(chunked ? idiv(nb * (stop - item0), nu) : stop - item0) - b0;
     const int32_t *tab = a.table + (int64_t)seq * a.width;
+
+    // ---- Q fragments of this warp's rows: for 16-bit rows k-step s holds dims 16 s ..;
+    // for 8-bit ones k index (s, 2 qd + e) is dim 64 j + 16 qd + 4 s + e and (s, 2 qd + 8 + e)
+    // is 2 further on, s = 0 .. 3 of the 64 dims of block j
+    uint32_t qf[MT][D / 16][4];
+    auto load_q = [&]() {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int m = (wm * MT + mt) * 16 + half * 8 + ql, j = m / a.G;
+          const bool on = m < a.R && j < nq;
+          const uint16_t *src =
+              a.q + (((int64_t)seq * a.q_len + j) * a.hq + kvh * a.G + (m - j * a.G)) * D;
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s) {
+            const int lo = C::B16 ? 16 * s + 2 * qd : 64 * (s >> 2) + 16 * qd + 4 * (s & 3);
+            const int hi = lo + (C::B16 ? 8 : 2);
+            qf[mt][s][half] = on ? *reinterpret_cast<const uint32_t *>(src + lo) : 0u;
+            qf[mt][s][2 + half] = on ? *reinterpret_cast<const uint32_t *>(src + hi) : 0u;
+          }
+        }
+    };
+    // 8 bits: under way with the lookups and first copies, as the rows' largest elements
+    // are wanted before the first tile (189 short sequences 74 -> 69 us); bf16 after them
+    // (400 short sequences 94 us, before them 100), and so 128 rows of 8 bits, whose
+    // registers are short (32 x 64K 833 us, before them 842)
+    constexpr bool kEarly = C::W == 1 && MT == 1;
+    if (kEarly) load_q();
 
     // ---- row lookups and copies, tile by tile.  Tile t of the group is
     // positions (b0 + t) * BLOCK + wt * TN ...
@@ -468,33 +535,24 @@ k_page_attn(const PageView pg, const AttnArgs a) {
 #pragma unroll
     for (int t = 0; t < NS - 1; ++t) copy(t);
 
-    // ---- Q fragments of this warp's rows: for 16-bit rows k-step s holds dims 16 s ..;
-    // for 8-bit ones k index (s, 2 qd + e) is dim 64 j + 16 qd + 4 s + e and
-    // (s, 2 qd + 8 + e) is 2 further on, s = 0 .. 3 of the 64 dims of block j
-    uint32_t qf[MT][D / 16][4];
-    float fr[MT][2];  // a score's factor by row: softmax scale in log2 units, f16 scaling
+    if (!kEarly) load_q();
+
+    // ---- Q in f16 and what a score is multiplied by
+    float fr[MT][2];  // by row: softmax scale in log2 units, f16 scaling
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const int m = (wm * MT + mt) * 16 + half * 8 + ql, j = m / a.G;
-        const bool on = m < a.R && j < nq;
-        const uint16_t *src =
-            a.q + (((int64_t)seq * a.q_len + j) * a.hq + kvh * a.G + (m - j * a.G)) * D;
-        uint32_t top = 0u;
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          const int lo = C::B16 ? 16 * s + 2 * qd : 64 * (s >> 2) + 16 * qd + 4 * (s & 3);
-          const int hi = lo + (C::B16 ? 8 : 2);
-          const uint32_t x = on ? *reinterpret_cast<const uint32_t *>(src + lo) : 0u;
-          const uint32_t y = on ? *reinterpret_cast<const uint32_t *>(src + hi) : 0u;
-          qf[mt][s][half] = x;
-          qf[mt][s][2 + half] = y;
-          top = max(top, max(max(x & 0x7FFFu, (x >> 16) & 0x7FFFu),
-                             max(y & 0x7FFFu, (y >> 16) & 0x7FFFu)));
-        }
         fr[mt][half] = a.scale_log2;
         if (C::W == 1) {
+          uint32_t top = 0u;
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t x = qf[mt][s][2 * k + half];
+              top = max(top, max(x & 0x7FFFu, (x >> 16) & 0x7FFFu));
+            }
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
           // the largest element goes to [2^14, 2^15) (infinities and NaN stay)
