@@ -24,6 +24,8 @@
 // instructions a value.)
 #include "pages_internal.cuh"
 
+#include <algorithm>
+
 namespace dhs {
 namespace {
 
@@ -243,6 +245,30 @@ int tokens_per_cta(int64_t n_tok) {
   return (int)(per < 1 ? 1 : (per > kPgTok ? kPgTok : per));
 }
 
+// Whether a row of d elements at i st + j sh and one at off + i' st + j' sh share an
+// element, for any 0 <= i, i' < n and 0 <= j, j' < h; with off = 0 (the rows themselves)
+// a row and itself do not count.  For every difference of heads the nearest difference
+// of tokens on either side decides.
+bool rows_meet(int64_t n, int64_t h, int64_t st, int64_t sh, int64_t d, int64_t off, bool same) {
+  if (same && (h == 1 || sh >= d) && (n == 1 || st >= (h - 1) * sh + d)) return false;
+  const __int128 extent = (__int128)(n - 1) * st + (__int128)(h - 1) * sh + d;
+  if (!same && (off >= extent || off <= -extent)) return false;
+  for (int64_t dj = same ? 0 : 1 - h; dj < h; ++dj) {
+    const int64_t want = -(off + dj * sh);  // what di st has to miss by d
+    const int64_t lo = st > 0 ? want / st - (want % st < 0) : 0;
+    for (int64_t di = lo; di <= lo + 1; ++di) {
+      int64_t x = std::max(1 - n, std::min(n - 1, di));
+      if (same && dj == 0 && x == 0) {
+        if (n == 1) continue;
+        x = 1;
+      }
+      const int64_t miss = x * st - want;
+      if (miss < d && miss > -d) return true;
+    }
+  }
+  return false;
+}
+
 int page_copy(bool write, const dhs_pages *pages, void *k, void *v, const int64_t *strides,
               int64_t n_tok, const int32_t *cu, const int32_t *lens, const int32_t *table,
               int32_t width, int32_t n_seqs, int32_t *err, dhs_stream stream) {
@@ -265,10 +291,17 @@ int page_copy(bool write, const dhs_pages *pages, void *k, void *v, const int64_
     r.kh = strides[1];
     r.vt = strides[2];
     r.vh = strides[3];
-    // rows that are written must not lie over one another
-    if (!write)
-      for (int i = 0; i < 4; ++i)
-        if ((i & 1 ? pg.hkv > 1 : n_tok > 1) && strides[i] < pg.d) return DHS_ERR_INVALID;
+  }
+  // rows that are written must not lie over one another (between keys and values of
+  // different strides the caller sees to that)
+  if (!write) {
+    const int64_t off = (int64_t)((uintptr_t)v - (uintptr_t)k) / 2;
+    const bool one = n_tok == 1, single = pg.hkv == 1;
+    if (rows_meet(n_tok, pg.hkv, r.kt, r.kh, pg.d, 0, true) ||
+        rows_meet(n_tok, pg.hkv, r.vt, r.vh, pg.d, 0, true) ||
+        ((one || r.kt == r.vt) && (single || r.kh == r.vh) &&
+         rows_meet(n_tok, pg.hkv, r.kt, r.kh, pg.d, off, false)))
+      return DHS_ERR_INVALID;
   }
   const int per = tokens_per_cta(n_tok);
   const unsigned grid = (unsigned)((n_tok + per - 1) / per);

@@ -655,7 +655,8 @@ int dhs_page_write(const dhs_pages *pages, const void *k, const void *v, const i
 /* The inverse: packed token cu[i] + u of k and v (addressed as in
  * dhs_page_write) receives the cached row, code * scale rounded to bf16.
  * Padding tokens are left as they were; rows that cannot be read (see err)
- * become zeros. */
+ * become zeros.  No two rows of k, no two of v, and no row of k and one of v may
+ * share an element (refused, but for k and v of different strides). */
 int dhs_page_read(const dhs_pages *pages, void *k, void *v, const int64_t *strides,
                   int64_t n_tokens, const int32_t *cu, const int32_t *seq_lens,
                   const int32_t *page_table, int32_t table_width, int32_t n_seqs, int32_t *err,

@@ -57,6 +57,45 @@ def test_read_refuses_overlapping_rows(dhs):
     assert _copy(lib, "dhs_page_read", strides=(256, 128, 256, 64)) == INVALID
 
 
+def _rows_meet(first, second, d, same):
+    """By every pair of rows (their first elements)."""
+    return any(abs(a - b) < d for i, a in enumerate(first) for j, b in enumerate(second)
+               if not (same and i == j))
+
+
+def _starts(n, h, st, sh):
+    return [i * st + j * sh for i in range(n) for j in range(h)]
+
+
+@pytest.mark.parametrize("n,h,d", [(4, 2, 64), (3, 4, 64), (1, 3, 128), (5, 1, 128), (2, 2, 64)])
+def test_read_refuses_rows_that_share_elements(dhs, n, h, d):
+    """All layouts of a grid of strides in which two rows of k, two of v, or a row of
+    each of the same strides meet: one of two heads over the next token, one token apart
+    as heads are, and values among the keys."""
+    lib = dhs.load()
+    p = _pages(kv_heads=h, head_dim=d)
+    seen = [0, 0]
+    grid = [0, 8, d // 2, d - 8, d, d + 8, 2 * d - 8, 2 * d, 3 * d, h * d, h * d + 8, 8 * d]
+    for st in grid:
+        for sh in grid:
+            own = _starts(n, h, st, sh)
+            if _rows_meet(own, own, d, True):
+                seen[0] += 1
+                assert _copy(lib, "dhs_page_read", p, n=n, strides=(st, sh, 8 * d * h, 8 * d), v=A + (1 << 20)) == INVALID
+                assert _copy(lib, "dhs_page_read", p, n=n, strides=(8 * d * h, 8 * d, st, sh), v=A + (1 << 20)) == INVALID
+                continue
+            for off in (0, 8, -8, d - 8, d, -d, 2 * d, st, -st, sh, st + sh - 8, st - sh, 2 * sh - st):
+                if _rows_meet(own, [x + off for x in own], d, False):
+                    seen[1] += 1
+                    assert _copy(lib, "dhs_page_read", p, n=n, k=1 << 30, v=(1 << 30) + 2 * off,
+                                 strides=(st, sh, st, sh)) == INVALID, (st, sh, off)
+    assert (n * h == 1 or seen[0]) and seen[1]
+
+
+def test_read_refuses_one_tensor_for_keys_and_values(dhs):
+    assert _copy(dhs.load(), "dhs_page_read") == INVALID
+
+
 def _attend(lib, p=None, q=A, lens=A, table=A, width=3, seqs=2, q_len=1, hq=8, scale=0.0, out=A, ws=A,
             nbytes=1 << 40):
     p = p if p is not None else _pages()

@@ -1001,3 +1001,36 @@ def test_prompt_past_2_to_the_31_elements(torch, dhs):
     _close(_np(out[r, 1020:]), None, want, d, t)
     assert not (out[:2 * t] == 77).any()
     assert torch.equal(out[last], own)
+
+
+# ------------------------------------------------------------------ where rows may lie
+@pytest.mark.parametrize("n,h", [(4, 2), (3, 4), (1, 3), (5, 1)])
+def test_read_into_every_layout_whose_rows_do_not_meet(torch, dhs, n, h):
+    """A grid of strides: a layout in which no two rows meet receives every row, heads
+    among the tokens and values among the keys included; the others are refused."""
+    d = 64
+    pc = Paged(torch, dhs, [n], 16, h, d, BF16)
+    kv = pc.fill()[0]
+    cu = torch.tensor([0, n], dtype=torch.int32).cuda()
+    served = refused = 0
+    grid = [8, d - 8, d, d + 8, 2 * d, 3 * d, h * d, 8 * d]
+    for st in grid:
+        for sh in grid:
+            for off in (8, d, -d, 2 * d, st, sh, st + sh, 64 * d):
+                buf = torch.full((128 * d,), 5.0, dtype=torch.bfloat16, device="cuda")
+                first = 2 * d
+                rows = [first + x + i * st + j * sh for x in (0, off) for i in range(n) for j in range(h)]
+                ko, vo = (buf.as_strided((n, h, d), (st, sh, 1), first + x) for x in (0, off))
+                gaps = np.diff(np.sort(rows))
+                if gaps.min() < d:
+                    refused += 1
+                    with pytest.raises(dhs.DhsError) as e:
+                        pc.cache.read(ko, vo, cu, pc.seq_lens, pc.table)
+                    assert e.value.code == 1
+                    continue
+                served += 1
+                pc.cache.read(ko, vo, cu, pc.seq_lens, pc.table)
+                assert np.array_equal(_np(ko), kv[0]) and np.array_equal(_np(vo), kv[1])
+                assert (buf == 5.0).sum().item() >= buf.numel() - 2 * n * h * d
+    pc.cache.check()
+    assert served and refused
