@@ -31,9 +31,11 @@
 // With few row tiles the keys are split over several items, which leave (O, m, l) in
 // the workspace for a join (prompt_splits says when).
 //
-// Waits are bounded; one that runs out records an error and lets the CTA finish:
-// the loader then waits for its copies and the MMA warp for its products before
-// tensor memory is freed.
+// Waits are bounded, by a time that follows the work a wait may last for
+// (prompt_wait_us); one that runs out records an error and lets the CTA finish: rows that
+// are not written yet stay as they were, the loader waits for its copies and the MMA
+// warp for its products before tensor memory is freed.  With key splits each CTA leaves
+// word of it for the join, which then writes no row at all.
 //
 // Measured (16 heads of one kv head, 128 dims): 16384 tokens of one sequence 0.60 ms,
 // 1830 TFLOP/s, 95 % of the measured matrix rate; 8192 tokens 0.166 ms.  At 64 dims Q K^T
@@ -58,7 +60,20 @@ constexpr int kPrSoftmax = 512;  // two row tiles, two warpgroups each
 constexpr int kPrThreads = kPrSoftmax + 128;
 constexpr int kPrM = 128, kPrN = 128, kPrH = kPrN / 2;
 constexpr int kMmaWarp = 16, kLoadWarp = 17, kCleanWarp = 18;
-constexpr int kPrSpin = 1 << 20;
+// Microseconds that a wait lasts at most (see prompt_wait_us), and that the last ones of
+// a CTA do, for copies and products in flight.  In a build for tests the first is a
+// variable.
+constexpr uint32_t kPrLastUs = 2000000;
+#ifdef DHS_TEST_WAITS
+}  // namespace
+}  // namespace dhs
+extern "C" uint32_t dhs_prompt_wait_us;
+uint32_t dhs_prompt_wait_us = 2000000;
+namespace dhs {
+namespace {
+#else
+constexpr uint32_t dhs_prompt_wait_us = 2000000;
+#endif
 constexpr float kPrRescale = 8.f;
 constexpr int kPrSplits = 64;      // key splits at most
 constexpr uint32_t kPrCols = 512;  // S0, S1 (P over them), O0, O1
@@ -69,9 +84,11 @@ struct PromptArgs {
   const int32_t *cu_q, *cu_k;
   uint16_t *out;
   float *lse, *parts;
+  int32_t *status;           // [CTAs] in the workspace: a wait of the CTA ran out
   int32_t *err;
   int64_t n_q, n_k;
-  int n_seqs, hq, hkv, G, tpt, nsplit;
+  int n_seqs, hq, hkv, G, tpt, nsplit, ctas;
+  uint32_t wait_us;
   int64_t most;              // row-tile pairs there can be
   int out32;                 // out lies on 32-byte boundaries
   float scale_log2;
@@ -152,6 +169,13 @@ __device__ __forceinline__ bool named_or(int id, int count, bool on) {
       : "r"(id), "r"(count), "r"((uint32_t)on)
       : "memory");
   return r != 0;
+}
+
+// Time in units of 1.024 us, of which the low 32 bits last for 73 minutes.
+__device__ __forceinline__ uint32_t global_us() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %globaltimer;\n" : "=l"(t));
+  return (uint32_t)(t >> 10);
 }
 
 // A sequence's queries and keys; false (recorded) for offsets out of range.
@@ -293,6 +317,7 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
     return *reinterpret_cast<PromptItem *>(smem + C::OFF_ITEM + (k & 1) * 64);
   };
   if ((smem_u32(smem) & 1023u) != 0u) {  // (the swizzle pattern follows address bits)
+    if (a.nsplit > 1 && threadIdx.x == 0) a.status[blockIdx.x] = 1;
     page_error(a.err, DC_CAPACITY, DHS_SITE_PROMPT_ATTEND);
     return;
   }
@@ -345,15 +370,16 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
   constexpr uint32_t tmem = 0u;
 
   auto wait = [&](uint64_t *bar, uint32_t parity, bool force = false) {
-    int spins = 0;
-    while (!mbar_try_wait(bar, parity)) {
+    if (mbar_try_wait(bar, parity)) return;
+    const uint32_t since = global_us();  // (a poll that fails has waited for some 5 us)
+    do {
       if (!force && *abort_v) return;
-      if (++spins > kPrSpin) {
+      if (global_us() - since >= (force ? kPrLastUs : a.wait_us)) {
         page_error(a.err, DC_TIMEOUT, DHS_SITE_PROMPT_ATTEND);
         *abort_v = 1;
         return;
       }
-    }
+    } while (!mbar_try_wait(bar, parity));
   };
   auto given_up = [&]() { return __any_sync(0xffffffffu, *abort_v) != 0; };
   // Slot of the n-th K or V tile since the start, and the parity of its use.  (All
@@ -672,14 +698,7 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[i]);
       }
-      // the row's sum over both halves
       red[hg * 128 + m] = l;
-      named_sync(pair, 64);
-      l += red[(hg ^ 1) * 128 + m];
-      const int off = it.nk - it.nq + 1, tok = it.tok0 + i * a.tpt + tloc;
-      const int q0 = it.q0, k0 = it.k0, kvh = it.kvh, part_no = it.part, common = off + it.tok0;
-      const bool valid = tloc < a.tpt && tok < it.nq;
-      const int seen = valid ? off + tok : 0;  // may be negative
       bool bad = false;
       uint32_t o[D / 2];
       if (ni > 0) {
@@ -700,6 +719,14 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
 #pragma unroll
         for (int x = 0; x < D / 2; ++x) o[x] = 0u;
       }
+      // Rows of an item for which a wait ran out (whoever's it was: it is known by the
+      // time what it waited for arrives here) are not written, nor half of them.
+      const bool lost = named_or(pair, 64, *abort_v != 0);
+      l += red[(hg ^ 1) * 128 + m];  // the row's sum over both halves
+      const int off = it.nk - it.nq + 1, tok = it.tok0 + i * a.tpt + tloc;
+      const int q0 = it.q0, k0 = it.k0, kvh = it.kvh, part_no = it.part, common = off + it.tok0;
+      const bool valid = tloc < a.tpt && tok < it.nq && !lost;
+      const int seen = valid ? off + tok : 0;  // may be negative
       __syncwarp();
       if (lane == 0) mbar_arrive(&item_empty[k & 1]);
       if (valid && bad) {
@@ -759,6 +786,7 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
   __syncthreads();
   tc_fence_after();
   if (warp == kMmaWarp) tmem_dealloc(*tmem_slot, kPrCols);
+  if (a.nsplit > 1 && tid == 0) a.status[blockIdx.x] = *abort_v;
 }
 
 // Joins the parts of a row: sum_s w_s O_s / sum_s w_s l_s, w_s = 2^(m_s - max m).
@@ -778,6 +806,8 @@ k_prompt_join(const PromptArgs a) {
   const bool some = nk - nq + (int)(tok - q0) + 1 > 0;
   const float *p = a.parts + row * (D + 2);
   const int64_t step = rows * (D + 2);
+  int lost = 0;
+  for (int c = lane; c < a.ctas; c += 32) lost |= a.status[c];
   float top = -CUDART_INF_F, den = 0.f, acc[V];
 #pragma unroll
   for (int x = 0; x < V; ++x) acc[x] = 0.f;
@@ -794,6 +824,7 @@ k_prompt_join(const PromptArgs a) {
       acc[x + 1] += o.y * f;
     }
   }
+  if (__any_sync(0xffffffffu, lost != 0)) return;  // (which parts are missing is not known)
   const float inv = 1.f / den;
 #pragma unroll
   for (int x = 0; x < V; x += 2)
@@ -840,6 +871,22 @@ int prompt_splits(int64_t n_q, int64_t n_k, int32_t n_seqs, int hq, int hkv, int
     }
   }
   return best;
+}
+
+// Bytes of the parts' workspace: (O, m, l) of every row and split, then a word a CTA.
+int64_t prompt_bytes(int nsplit, int64_t n_q, int hq, int d, int sms) {
+  return nsplit > 1 ? (int64_t)nsplit * n_q * hq * (d + 2) * 4 + (int64_t)sms * 4 : 0;
+}
+
+// How long a wait may take.  Some last as long as an item (a row tile without work waits
+// for the next one) or as the search for one among all sequences: beside two seconds,
+// 20 us for each key tile there can be, which takes 0.3 to 0.5 us, and 5 us for each
+// sequence, which takes some 0.1; half an hour at most.
+uint32_t prompt_wait_us(int64_t n_k, int32_t n_seqs) {
+  const uint64_t least = dhs_prompt_wait_us;
+  return (uint32_t)std::min<uint64_t>(
+      least + least * (uint64_t)(n_k / kPrN + 1) / 100000 + least * (uint64_t)n_seqs / 400000,
+      1800000000u);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
@@ -892,7 +939,7 @@ extern "C" int64_t dhs_prompt_attend_workspace(int64_t n_q, int64_t n_k, int32_t
   const int sms = device_sms(dev);
   if (sms < 1) return -1;
   const int n = prompt_splits(n_q, n_k, n_seqs, q_heads, kv_heads, sms);
-  return n > 1 ? (int64_t)n * n_q * q_heads * (head_dim + 2) * 4 : 0;
+  return prompt_bytes(n, n_q, q_heads, head_dim, sms);
 }
 
 extern "C" int dhs_prompt_attend(const void *q, const void *k, const void *v,
@@ -947,13 +994,16 @@ extern "C" int dhs_prompt_attend(const void *q, const void *k, const void *v,
   a.tpt = kPrM / a.G;
   a.nsplit = prompt_splits(n_q, n_k, n_seqs, q_heads, kv_heads, sms);
   a.scale_log2 = (scale == 0.f ? 1.f / sqrtf((float)d) : scale) * 1.4426950408889634f;
-  if (a.nsplit > 1 &&
-      (!workspace || workspace_bytes < (int64_t)a.nsplit * n_q * q_heads * (d + 2) * 4))
-    return DHS_ERR_INVALID;
+  const int64_t bytes = prompt_bytes(a.nsplit, n_q, q_heads, head_dim, sms);
+  if (bytes > 0 && (!workspace || workspace_bytes < bytes)) return DHS_ERR_INVALID;
+  a.wait_us = prompt_wait_us(n_k, n_seqs);
   a.most = prompt_tiles(n_q, n_seqs, a.G);
   a.out32 = ((uintptr_t)out & 31u) == 0;
   const int64_t items = a.most * kv_heads * a.nsplit;
   if (items > INT32_MAX) return DHS_ERR_CAPACITY;
+  a.ctas = (int)std::min<int64_t>(items, sms);
+  a.status = bytes > 0 ? reinterpret_cast<int32_t *>(static_cast<unsigned char *>(workspace) + bytes) - sms
+                       : nullptr;
   CUtensorMap mq = {}, mk = {}, mv = {};
   if (!encode(enc, &mq, q, n_q, q_heads, (int)d, st[0], st[1], a.G, a.tpt)) return DHS_ERR_INVALID;
   if (n_k > 0 && (!encode(enc, &mk, k, n_k, kv_heads, (int)d, st[2], st[3], 1, kPrN) ||
@@ -965,7 +1015,7 @@ extern "C" int dhs_prompt_attend(const void *q, const void *k, const void *v,
     static DeviceSmem granted;
     cudaError_t e = granted.ensure(k_prompt<D>, PrCfg<D>::SMEM, dev);
     if (e == cudaSuccess)
-      e = launch_prio(k_prompt<D>, dim3((unsigned)std::min<int64_t>(items, sms)), dim3(kPrThreads),
+      e = launch_prio(k_prompt<D>, dim3((unsigned)a.ctas), dim3(kPrThreads),
                       (size_t)PrCfg<D>::SMEM, s, mq, mk, mv, a);
     if (e == cudaSuccess && a.nsplit > 1)
       e = launch_pdl(k_prompt_join<D>, dim3((unsigned)((n_q * q_heads + 3) / 4)), dim3(128), 0, s,
