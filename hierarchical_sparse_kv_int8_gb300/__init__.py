@@ -135,6 +135,7 @@ _SIGS.update({
     "dhs_prompt_attend": ([_P] * 4 + [_I64] * 2 + [_P] * 2 + [_I32] * 4 +
                           [ctypes.c_float, _P, _P, _P, _I64, _P, _P], ctypes.c_int),
     "dhs_prompt_attend_workspace": ([_I64, _I64, _I32, _I32, _I32, _I32], _I64),
+    "dhs_prompt_errors": ([_P, _P], ctypes.c_int),
 })
 
 

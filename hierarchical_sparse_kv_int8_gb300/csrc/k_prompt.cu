@@ -178,6 +178,13 @@ __device__ __forceinline__ uint32_t global_us() {
   return (uint32_t)(t >> 10);
 }
 
+// What calls without a record of their own find, one for each device.
+__device__ int32_t device_record[2];
+
+__device__ __forceinline__ void prompt_error(const PromptArgs &a, int code) {
+  page_error(a.err, code, DHS_SITE_PROMPT_ATTEND);
+}
+
 // A sequence's queries and keys; false (recorded) for offsets out of range.
 __device__ __forceinline__ bool prompt_seq(const PromptArgs &a, int i, int &q0, int &nq, int &k0,
                                            int &nk, bool record = true) {
@@ -185,7 +192,7 @@ __device__ __forceinline__ bool prompt_seq(const PromptArgs &a, int i, int &q0, 
   k0 = a.cu_k[i];
   const int64_t q1 = a.cu_q[i + 1], k1 = a.cu_k[i + 1];
   if (q0 < 0 || q1 < q0 || q1 > a.n_q || k0 < 0 || k1 < k0 || k1 > a.n_k) {
-    if (record) page_error(a.err, DC_ROW_RANGE, DHS_SITE_PROMPT_ATTEND);
+    if (record) prompt_error(a, DC_ROW_RANGE);
     nq = nk = 0;
     return false;
   }
@@ -318,7 +325,7 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
   };
   if ((smem_u32(smem) & 1023u) != 0u) {  // (the swizzle pattern follows address bits)
     if (a.nsplit > 1 && threadIdx.x == 0) a.status[blockIdx.x] = 1;
-    page_error(a.err, DC_CAPACITY, DHS_SITE_PROMPT_ATTEND);
+    prompt_error(a, DC_CAPACITY);
     return;
   }
   // (a warp's number by a shuffle: the compiler then knows that the roles' branches are
@@ -375,7 +382,7 @@ k_prompt(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtenso
     do {
       if (!force && *abort_v) return;
       if (global_us() - since >= (force ? kPrLastUs : a.wait_us)) {
-        page_error(a.err, DC_TIMEOUT, DHS_SITE_PROMPT_ATTEND);
+        prompt_error(a, DC_TIMEOUT);
         *abort_v = 1;
         return;
       }
@@ -911,6 +918,24 @@ EncodeTiled encoder() {
   return reinterpret_cast<EncodeTiled>(f);
 }
 
+// The device's record (its address asked for once; chosen in the kernel it would cost
+// registers where there are none), or nullptr.
+int32_t *record_of(int dev) {
+  static std::atomic<int32_t *> known[kMaxDevices];
+  if (dev < 0 || dev >= kMaxDevices) return nullptr;
+  int32_t *p = known[dev].load(std::memory_order_acquire);
+  if (!p) {
+    void *at = nullptr;
+    if (cudaGetSymbolAddress(&at, device_record) != cudaSuccess) {
+      cudaGetLastError();
+      return nullptr;
+    }
+    p = static_cast<int32_t *>(at);
+    known[dev].store(p, std::memory_order_release);
+  }
+  return p;
+}
+
 // [tokens][heads][d] of bf16, boxes of 64 dims x box_heads x box_tokens.
 bool encode(EncodeTiled f, CUtensorMap *m, const void *p, int64_t tokens, int heads, int d,
             int64_t st, int64_t sh, int box_heads, int box_tokens) {
@@ -974,7 +999,8 @@ extern "C" int dhs_prompt_attend(const void *q, const void *k, const void *v,
   }
   const int sms = device_sms(dev);
   EncodeTiled enc = encoder();
-  if (sms < 1 || !enc) return DHS_ERR_CUDA;
+  if (!err) err = record_of(dev);
+  if (sms < 1 || !enc || !err) return DHS_ERR_CUDA;
   PromptArgs a;
   a.v = static_cast<const uint16_t *>(v);
   a.vt = st[4];
@@ -1024,6 +1050,25 @@ extern "C" int dhs_prompt_attend(const void *q, const void *k, const void *v,
   };
   const cudaError_t e = d == 128 ? go(std::integral_constant<int, 128>())
                                  : go(std::integral_constant<int, 64>());
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return DHS_ERR_CUDA;
+  }
+  return DHS_OK;
+}
+
+extern "C" int dhs_prompt_errors(int32_t *found, dhs_stream stream) {
+  using namespace dhs;
+  if (!found) return DHS_ERR_INVALID;
+  static const int32_t none[2] = {0, 0};
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e =
+      cudaMemcpyFromSymbolAsync(found, device_record, sizeof none, 0, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess && found[0] != 0) {
+    e = cudaMemcpyToSymbolAsync(device_record, none, sizeof none, 0, cudaMemcpyHostToDevice, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  }
   if (e != cudaSuccess) {
     cudaGetLastError();
     return DHS_ERR_CUDA;

@@ -112,9 +112,17 @@ def _raw(stream, index):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def check_errors(errors, stream=None):
+def check_errors(errors=None, stream=None):
     """Waits for ``stream``, raises DhsError (code 5) if a call recorded a bad
-    page, length or offset in ``errors`` (int32[2]), and clears the record."""
+    page, length or offset in ``errors`` (int32[2]), and clears the record.
+    Without ``errors``: what :func:`prompt_attend` calls without a record of their own
+    found on the current device."""
+    if errors is None:
+        found = (ctypes.c_int32 * 2)()
+        rc = _lib().dhs_prompt_errors(found, _raw(stream, _current_device()))
+        if rc:
+            _raise(rc, "dhs_prompt_errors")
+        return _found(*found)
     with _on(errors.get_device()):
         s = torch.cuda.current_stream() if stream is None else stream
         if isinstance(s, int):
@@ -123,6 +131,10 @@ def check_errors(errors, stream=None):
             code, site = errors.tolist()
             if code:
                 errors.zero_()
+    _found(code, site)
+
+
+def _found(code, site):
     if code:
         _raise(5, "%s: %s" % (_SITE.get(site, "?"), _CHECK.get(code, "check %d" % code)))
 
@@ -254,7 +266,9 @@ def prompt_workspace(q, k, n_seqs: int) -> Optional[torch.Tensor]:
 def prompt_attend(q, k, v, cu_q, cu_k, out, lse=None, workspace=None, scale: float = 0.0,
                   errors=None, stream=None):
     """Causal attention of packed sequences (dhs_prompt_attend): ``q`` [n_q, q_heads,
-    head_dim], ``k`` and ``v`` [n_k, kv_heads, head_dim], ``out`` like ``q``."""
+    head_dim], ``k`` and ``v`` [n_k, kv_heads, head_dim], ``out`` like ``q``.  Bad offsets
+    are recorded in ``errors`` (int32[2] on the device) and raised by
+    ``check_errors(errors)``; without it in the device's own record, by ``check_errors()``."""
     ix = q.get_device()
     if ix < 0 or _current_device() != ix:
         with _on(ix):

@@ -606,7 +606,9 @@ int64_t dhs_policy_free_pages(const dhs_policy *p);
  * page, length or offset leaves the rows in question out, never follows them,
  * and records what it found unless err[0] already holds a record: err[0] = 1
  * for a length or offset outside its range, 2 for a page outside [0, n_pages),
- * 4 for a bounded wait that ran out; err[1] = the call, DHS_SITE_*. */
+ * 4 for a bounded wait that ran out; err[1] = the call, DHS_SITE_*.  A dhs_page_*
+ * call with NULL keeps no record; dhs_prompt_attend with NULL keeps it in the one
+ * that dhs_prompt_errors reads. */
 enum { DHS_PAGE_BF16 = 0, DHS_PAGE_INT8 = 1, DHS_PAGE_E4M3 = 2 };
 enum { DHS_SITE_PAGE_WRITE = 1, DHS_SITE_PAGE_READ = 2, DHS_SITE_PAGE_ATTEND = 3,
        DHS_SITE_PROMPT_ATTEND = 4 };
@@ -714,6 +716,9 @@ int dhs_prompt_attend(const void *q, const void *k, const void *v, const int64_t
                       int64_t workspace_bytes, int32_t *err, dhs_stream stream);
 int64_t dhs_prompt_attend_workspace(int64_t n_q, int64_t n_k, int32_t n_seqs, int32_t q_heads,
                                     int32_t kv_heads, int32_t head_dim);
+/* What dhs_prompt_attend calls with err = NULL found on the current device, into
+ * host int32[2] laid out as err: waits for the stream, and clears the record. */
+int dhs_prompt_errors(int32_t *found, dhs_stream stream);
 
 #ifdef __cplusplus
 }

@@ -147,6 +147,10 @@ def test_prompt_refusals(dhs):
         assert lib.dhs_prompt_attend_workspace(*a) == -1, a
 
 
+def test_prompt_errors_refuses_no_place(dhs):
+    assert dhs.load().dhs_prompt_errors(None, None) == INVALID
+
+
 def test_limits_of_scale_and_tokens(dhs):
     """Larger scales are infinite once they are in log2 units; a tile's positions run past
     the last token in 32 bits."""

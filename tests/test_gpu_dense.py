@@ -1034,3 +1034,40 @@ def test_read_into_every_layout_whose_rows_do_not_meet(torch, dhs, n, h):
                 assert (buf == 5.0).sum().item() >= buf.numel() - 2 * n * h * d
     pc.cache.check()
     assert served and refused
+
+
+# ------------------------------------------------------------------ what the checks find
+def test_prompt_errors_without_a_record_are_kept(torch, dhs):
+    """In one record of the device, also for a first call that is captured; calls with a
+    record of their own stay out of it."""
+    dhs.check_errors()
+    q = torch.randn((20, 4, 64)).bfloat16().cuda()
+    good, bad = (torch.tensor(x, dtype=torch.int32).cuda() for x in ([0, 12, 20], [0, 25, 20]))
+    out = torch.full_like(q, 77.0)
+    err = torch.zeros(2, dtype=torch.int32, device="cuda")
+    dhs.prompt_attend(q, q, q, bad, bad, out, errors=err)
+    dhs.check_errors()
+    with pytest.raises(dhs.DhsError):
+        dhs.check_errors(err)
+    dhs.prompt_attend(q, q, q, bad, bad, out)
+    dhs.prompt_attend(q, q, q, good, good, out, errors=err)
+    dhs.check_errors(err)
+    with pytest.raises(dhs.DhsError) as e:
+        dhs.check_errors()
+    assert e.value.code == 5 and "dhs_prompt_attend" in str(e.value) and "offset" in str(e.value)
+    dhs.check_errors()                            # the record is taken once
+    cu, side = bad.clone(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        dhs.prompt_attend(q, q, q, cu, cu, out)
+    graph.replay()
+    with pytest.raises(dhs.DhsError):
+        dhs.check_errors()
+    cu.copy_(good)
+    want = out.clone()
+    out.fill_(77.0)
+    graph.replay()
+    dhs.check_errors(stream=torch.cuda.current_stream())
+    dhs.prompt_attend(q, q, q, good, good, want)
+    assert torch.equal(out, want) and not (out == 77.0).any()
