@@ -1154,8 +1154,9 @@ k_page_join(const AttnArgs a, int hkv, int width_rows) {
 
 bool attend_args(const dhs_pages *pages, int32_t n_seqs, int32_t q_len, int32_t q_heads,
                  PageView *pg) {
-  return page_view(pages, pg) && n_seqs >= 0 && q_len >= 1 && q_len <= kMaxKmax && q_heads >= 1 &&
-         q_heads % pg->hkv == 0 && (int64_t)q_len * (q_heads / pg->hkv) <= 128;
+  return page_view(pages, pg) && n_seqs >= 0 && n_seqs <= kMaxSeqs && q_len >= 1 &&
+         q_len <= kMaxKmax && q_heads >= 1 && q_heads % pg->hkv == 0 &&
+         (int64_t)q_len * (q_heads / pg->hkv) <= 128;
 }
 
 int64_t plan_bytes(int32_t n_seqs, int hkv) {

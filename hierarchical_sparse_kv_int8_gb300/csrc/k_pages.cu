@@ -273,7 +273,8 @@ int page_copy(bool write, const dhs_pages *pages, void *k, void *v, const int64_
               int64_t n_tok, const int32_t *cu, const int32_t *lens, const int32_t *table,
               int32_t width, int32_t n_seqs, int32_t *err, dhs_stream stream) {
   PageView pg;
-  if (!page_view(pages, &pg) || n_tok < 0 || n_seqs < 0 || width < 0) return DHS_ERR_INVALID;
+  if (!page_view(pages, &pg) || n_tok < 0 || n_seqs < 0 || n_seqs > kMaxSeqs || width < 0)
+    return DHS_ERR_INVALID;
   if (n_tok == 0 || n_seqs == 0) return DHS_OK;
   if (!k || !v || !cu || !lens || !table || width < 1 || ((uintptr_t)k & 15u) ||
       ((uintptr_t)v & 15u))

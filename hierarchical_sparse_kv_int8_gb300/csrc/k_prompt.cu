@@ -846,9 +846,9 @@ k_prompt_join(const PromptArgs a) {
 bool prompt_args(int64_t n_q, int64_t n_k, int32_t n_seqs, int32_t hq, int32_t hkv, int32_t d) {
   // (a tile's positions run up to 256 past the last token, in 32 bits)
   constexpr int64_t most = INT32_MAX - 256;
-  return n_q >= 0 && n_k >= 0 && n_q <= most && n_k <= most && n_seqs >= 0 && hkv >= 1 &&
-         hkv <= kPageMaxHeads && hq >= 1 && hq % hkv == 0 && hq / hkv <= 128 &&
-         (d == 64 || d == 128);
+  return n_q >= 0 && n_k >= 0 && n_q <= most && n_k <= most && n_seqs >= 0 &&
+         n_seqs <= kMaxSeqs && hkv >= 1 && hkv <= kPageMaxHeads && hq >= 1 && hq % hkv == 0 &&
+         hq / hkv <= 128 && (d == 64 || d == 128);
 }
 
 // Most row-tile pairs n_q tokens of n_seqs sequences can make.
@@ -1028,7 +1028,8 @@ extern "C" int dhs_prompt_attend(const void *q, const void *k, const void *v,
   const int64_t items = a.most * kv_heads * a.nsplit;
   if (items > INT32_MAX) return DHS_ERR_CAPACITY;
   a.ctas = (int)std::min<int64_t>(items, sms);
-  a.status = bytes > 0 ? reinterpret_cast<int32_t *>(static_cast<unsigned char *>(workspace) + bytes) - sms
+  a.status = bytes > 0 ? reinterpret_cast<int32_t *>(static_cast<unsigned char *>(workspace) +
+                                                     bytes) - sms
                        : nullptr;
   CUtensorMap mq = {}, mk = {}, mv = {};
   if (!encode(enc, &mq, q, n_q, q_heads, (int)d, st[0], st[1], a.G, a.tpt)) return DHS_ERR_INVALID;

@@ -10,6 +10,8 @@ namespace dhs {
 
 constexpr int kPageMaxHeads = 1024;
 constexpr int kMaxDevices = 64;
+// Sequences of a call at most: loops over them run up to 1024 past the last, in 32 bits.
+constexpr int kMaxSeqs = INT32_MAX - 1024;
 
 // Streaming multiprocessors of a device (asked once), 0 on failure.
 int device_sms(int dev);
@@ -91,7 +93,7 @@ __device__ __forceinline__ int seq_of(const int32_t *cu, int n, int64_t tok) {
   if (tok < cu[0]) return -1;
   int lo = 0, hi = n;  // cu[lo] <= tok; hi is n or cu[hi] > tok
   while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
+    const int mid = lo + ((hi - lo + 1) >> 1);  // (n may be more than 2^30)
     if (cu[mid] <= tok) lo = mid;
     else hi = mid - 1;
   }

@@ -147,6 +147,19 @@ def test_prompt_refusals(dhs):
         assert lib.dhs_prompt_attend_workspace(*a) == -1, a
 
 
+def test_limit_of_sequences(dhs):
+    """Loops over the sequences and the search among them run past the last in 32 bits."""
+    lib = dhs.load()
+    p = ctypes.byref(_pages())
+    for n in ((1 << 31) - 1, (1 << 31) - 1024):
+        assert _copy(lib, "dhs_page_write", seqs=n) == INVALID
+        assert _copy(lib, "dhs_page_read", seqs=n, v=A << 20) == INVALID
+        assert _attend(lib, seqs=n) == INVALID
+        assert lib.dhs_page_attend_workspace(p, n, 1, 8) == -1
+        assert _prompt(lib, seqs=n) == INVALID
+        assert lib.dhs_prompt_attend_workspace(4, 4, n, 8, 2, 128) == -1
+
+
 def test_prompt_errors_refuses_no_place(dhs):
     assert dhs.load().dhs_prompt_errors(None, None) == INVALID
 

@@ -1071,3 +1071,21 @@ def test_prompt_errors_without_a_record_are_kept(torch, dhs):
     dhs.check_errors(stream=torch.cuda.current_stream())
     dhs.prompt_attend(q, q, q, good, good, want)
     assert torch.equal(out, want) and not (out == 77.0).any()
+
+
+def test_write_and_read_of_the_last_of_2_30_sequences(torch, dhs):
+    """The search among more than 2^30 sequences (all empty but the last; the arrays take
+    13 GB) stays within 32 bits."""
+    n = (1 << 30) + 5
+    pc = Paged(torch, dhs, [1], 16, 1, 64, BF16)
+    cu = torch.zeros(n + 1, dtype=torch.int32, device="cuda")
+    lens, table = torch.zeros(n, dtype=torch.int32, device="cuda"), torch.full((n, 1), -1, dtype=torch.int32, device="cuda")
+    cu[n], lens[n - 1], table[n - 1, 0] = 1, 1, pc.table[0, 0]
+    k = torch.randn((1, 1, 64)).bfloat16().cuda()
+    ko, vo = torch.zeros_like(k), torch.zeros_like(k)
+    pc.cache.write(k, -k, cu, lens, table)
+    pc.cache.read(ko, vo, cu, lens, table)
+    pc.cache.check()
+    assert torch.equal(ko, k) and torch.equal(vo, -k)
+    page = int(pc.table[0, 0])
+    assert torch.equal(pc.cache.k[page, 0, 0], k[0, 0])
