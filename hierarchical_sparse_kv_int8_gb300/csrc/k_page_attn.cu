@@ -1238,7 +1238,8 @@ extern "C" int dhs_page_attend(const dhs_pages *pages, const void *q, const int3
     return DHS_ERR_INVALID;
   if (n_seqs == 0) return DHS_OK;
   if (!q || !seq_lens || !page_table || !out || !workspace || ((uintptr_t)q & 15u) ||
-      ((uintptr_t)out & 15u) || ((uintptr_t)workspace & 15u))
+      ((uintptr_t)out & 15u) || ((uintptr_t)workspace & 15u) ||
+      !words(q_lens, seq_lens, page_table, lse, err))
     return DHS_ERR_INVALID;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {

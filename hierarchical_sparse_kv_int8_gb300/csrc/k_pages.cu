@@ -277,7 +277,7 @@ int page_copy(bool write, const dhs_pages *pages, void *k, void *v, const int64_
     return DHS_ERR_INVALID;
   if (n_tok == 0 || n_seqs == 0) return DHS_OK;
   if (!k || !v || !cu || !lens || !table || width < 1 || ((uintptr_t)k & 15u) ||
-      ((uintptr_t)v & 15u))
+      ((uintptr_t)v & 15u) || !words(cu, lens, table, err))
     return DHS_ERR_INVALID;
   if (n_tok > INT32_MAX) return DHS_ERR_CAPACITY;
   TokenRows r;

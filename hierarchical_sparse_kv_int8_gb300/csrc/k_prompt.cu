@@ -980,7 +980,7 @@ extern "C" int dhs_prompt_attend(const void *q, const void *k, const void *v,
   if (n_q == 0 || n_seqs == 0) return DHS_OK;
   if (!q || !out || !cu_q || !cu_k || (n_k > 0 && (!k || !v)) || ((uintptr_t)q & 15u) ||
       ((uintptr_t)k & 15u) || ((uintptr_t)v & 15u) || ((uintptr_t)out & 15u) ||
-      ((uintptr_t)workspace & 15u))
+      ((uintptr_t)workspace & 15u) || !words(cu_q, cu_k, lse, err))
     return DHS_ERR_INVALID;
   const int64_t d = head_dim;
   int64_t st[6] = {q_heads * d, d, kv_heads * d, d, kv_heads * d, d};

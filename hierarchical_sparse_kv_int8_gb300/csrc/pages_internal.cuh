@@ -42,10 +42,17 @@ struct PageView {
   int div_shift;
 };
 
+// Whether arrays of 32-bit words (NULL: none) lie where words may lie.
+template <typename... P>
+bool words(const P *...p) {
+  return (((uintptr_t)p | ...) & 3u) == 0;
+}
+
 inline bool page_view(const dhs_pages *p, PageView *out) {
   if (!p || !p->k || !p->v || ((uintptr_t)p->k & 15u) || ((uintptr_t)p->v & 15u)) return false;
   if (p->kind < DHS_PAGE_BF16 || p->kind > DHS_PAGE_E4M3) return false;
   if (p->kind != DHS_PAGE_BF16 && (!p->k_scale || !p->v_scale)) return false;
+  if (p->kind != DHS_PAGE_BF16 && !words(p->k_scale, p->v_scale)) return false;
   if (p->page_rows < 1 || p->kv_heads < 1 || p->kv_heads > kPageMaxHeads || p->n_pages < 1 ||
       p->n_pages > INT32_MAX || (p->head_dim != 64 && p->head_dim != 128))
     return false;

@@ -600,8 +600,8 @@ int64_t dhs_policy_free_pages(const dhs_policy *p);
  * The calls need no context, allocate nothing, synchronise nothing and can be
  * captured into a CUDA graph; lengths, offsets and page tables are read on the
  * device, so a captured graph follows them.  Pointers and stream belong to the
- * current device.  head_dim is 64 or 128; q, k, v and out are bf16; n_seqs is at
- * most 2^31 - 1025.
+ * current device; int32 and fp32 arrays are 4-byte aligned.  head_dim is 64 or 128; q, k, v
+ * and out are bf16; n_seqs is at most 2^31 - 1025.
  *
  * `err` of every call is a device int32[2] or NULL: a kernel that finds a bad
  * page, length or offset leaves the rows in question out, never follows them,

@@ -147,6 +147,29 @@ def test_prompt_refusals(dhs):
         assert lib.dhs_prompt_attend_workspace(*a) == -1, a
 
 
+def test_arrays_of_words_off_their_boundary(dhs):
+    lib = dhs.load()
+    good = ctypes.byref(_pages())
+    for bad in (A + 1, A + 2, A + 3):
+        for b in (dict(k_scale=bad), dict(v_scale=bad)):
+            assert _copy(lib, "dhs_page_write", _pages(**b)) == INVALID
+            assert _copy(lib, "dhs_page_read", _pages(**b), v=A << 20) == INVALID
+            assert _attend(lib, _pages(**b)) == INVALID
+            assert lib.dhs_page_attend_workspace(ctypes.byref(_pages(**b)), 2, 1, 8) == -1
+        for i in range(4):
+            cu, lens, table, err = (bad if x == i else A for x in range(4))
+            for name in ("dhs_page_write", "dhs_page_read"):
+                assert getattr(lib, name)(good, A, A << 20, None, 4, cu, lens, table, 3, 2, err, None) == INVALID
+        for i in range(5):
+            q_lens, lens, table, lse, err = (bad if x == i else A for x in range(5))
+            assert lib.dhs_page_attend(good, A, q_lens, lens, table, 3, 2, 1, 8, 0.0, A, lse, A, 1 << 40, err,
+                                       None) == INVALID
+        for i in range(4):
+            cq, ck, lse, err = (bad if x == i else A for x in range(4))
+            assert lib.dhs_prompt_attend(A, A, A, None, 4, 4, cq, ck, 1, 8, 2, 128, 0.0, A, lse, A, 1 << 40, err,
+                                         None) == INVALID
+
+
 def test_limit_of_sequences(dhs):
     """Loops over the sequences and the search among them run past the last in 32 bits."""
     lib = dhs.load()
