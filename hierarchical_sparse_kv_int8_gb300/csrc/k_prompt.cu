@@ -804,7 +804,11 @@ k_prompt_join(const PromptArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / 32, rows = a.n_q * a.hq;
   pdl_wait();
-  if (row >= rows) return;
+  // (which parts are missing is not known; each warp reading all words for itself, beside
+  // its parts, took up to 3 us longer)
+  int lost = 0;
+  for (int c = threadIdx.x; c < a.ctas; c += 128) lost |= a.status[c];
+  if (__syncthreads_or(lost) || row >= rows) return;
   const int64_t tok = row / a.hq;
   const int i = seq_of(a.cu_q, a.n_seqs, tok);
   if (i < 0) return;
@@ -813,8 +817,6 @@ k_prompt_join(const PromptArgs a) {
   const bool some = nk - nq + (int)(tok - q0) + 1 > 0;
   const float *p = a.parts + row * (D + 2);
   const int64_t step = rows * (D + 2);
-  int lost = 0;
-  for (int c = lane; c < a.ctas; c += 32) lost |= a.status[c];
   float top = -CUDART_INF_F, den = 0.f, acc[V];
 #pragma unroll
   for (int x = 0; x < V; ++x) acc[x] = 0.f;
@@ -831,7 +833,6 @@ k_prompt_join(const PromptArgs a) {
       acc[x + 1] += o.y * f;
     }
   }
-  if (__any_sync(0xffffffffu, lost != 0)) return;  // (which parts are missing is not known)
   const float inv = 1.f / den;
 #pragma unroll
   for (int x = 0; x < V; x += 2)
