@@ -307,9 +307,12 @@ k_page_attn(const PageView pg, const AttnArgs a) {
   int n_cta = (int)min(min((int64_t)gridDim.x, total), n_parts);
   // Few long items: a CTA whose blocks belong to two items fills and drains its ring
   // twice (some 4 us), and the others wait for it.  Then each CTA takes one chunk of
-  // at most `most_blocks` blocks of one item, of which there are at most n_cta: 8
-  // items of 22,000 positions on 304 CTAs take 30.0 us instead of 31.2.  Chunks are up
-  // to items / n_cta longer than even shares (3% there); 32 items lose 6% by them.
+  // at most `most_blocks` blocks of one item, of which there are at most n_cta.  Chunks
+  // are up to items / n_cta longer than even shares, so many items lose by them.  Both
+  // sides, 128 dims, 1 to 32 rows, one item of 8K, 32K or 100K positions and the others of
+  // half that to that, means over 8 or 12 such batches: 2 items +0.1 % (-7 to +9), 3 -2.2,
+  // 4 -5.1, 6 -3.7, 8 -2.0, 9 -2.3, 10 -1.3, 12 -3.4, 16 -2.4, 24 -2.0, 32 -2.6 (-7 to 0),
+  // 48 +0.8 (-3 to +3).  The rule stops at 9 and leaves some 2 % at 10 to 32.
   const bool chunked = items > 1 && items * 32 <= n_cta;
   const int64_t most_blocks =
       chunked ? idiv(total + n_cta - items - 1, max((int64_t)1, n_cta - items)) : 1;

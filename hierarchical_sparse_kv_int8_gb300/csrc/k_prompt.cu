@@ -38,13 +38,16 @@
 // word of it for the join, which then writes no row at all.
 //
 // Measured (16 heads of one kv head, 128 dims): 16384 tokens of one sequence 0.60 ms,
-// 1830 TFLOP/s, 95 % of the measured matrix rate; 8192 tokens 0.166 ms.  At 64 dims Q K^T
+// 1830 TFLOP/s, 95 % of the measured matrix rate, in calls with pauses between; 0.66 ms
+// and 86 % (98 % of the rate held for seconds) in calls without, where the power limit
+// lowers the clock; 8192 tokens 0.166 ms.  At 64 dims Q K^T
 // takes half the time, P V as long as at 128 and a tile's softmax the same: 16384 tokens
 // reach 1110 TFLOP/s with the tensor pipe busy for 44 % of the cycles, the issue slots
 // for 54 and the exponentials' pipe for 44: what bounds it is the chain of a tile's
 // softmax (read S, maximum, exponentials, write P), of which two run side by side.  16
-// ragged sequences of up to 2048 tokens (32 heads over 8) reach 1180: an item costs some 3
-// tiles' time besides its tiles (the first S, the rows' writing).
+// ragged sequences of up to 2048 tokens (32 heads over 8) reach 1180 (1090 in calls
+// without pauses): an item costs some 3 tiles' time besides its tiles (the first S, the
+// rows' writing).
 #include "pages_internal.cuh"
 #include "tc_util.cuh"
 
@@ -862,7 +865,9 @@ int64_t prompt_tiles(int64_t n_q, int32_t n_seqs, int G) {
 // kv heads) of T key tiles, n splits deal I n items of T / n tiles to the SMs in
 // ceil(I n / SMs) turns; an item costs some 3 tiles' time besides its tiles, a join
 // some 6.  (Two 500-token chunks over 32K keys, 32 pairs: 4 splits, 92 us instead of
-// 330.)
+// 330.)  The average stands for every sequence: 500 tokens over 100K keys (8 heads over 2,
+// 128 dims) take 147 us by themselves and 980 beside 30 prompts of 50 tokens, which lower
+// it to no split.
 int prompt_splits(int64_t n_q, int64_t n_k, int32_t n_seqs, int hq, int hkv, int sms) {
   if (n_q == 0 || n_seqs == 0) return 1;
   const int64_t items = prompt_tiles(n_q, n_seqs, hq / hkv) * hkv;

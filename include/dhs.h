@@ -656,7 +656,7 @@ int dhs_page_write(const dhs_pages *pages, const void *k, const void *v, const i
                    dhs_stream stream);
 
 /* The inverse: packed token cu[i] + u of k and v (addressed as in
- * dhs_page_write) receives the cached row, code * scale rounded to bf16.
+ * dhs_page_write) receives the cached row, code * scale in fp32 rounded to bf16.
  * Padding tokens are left as they were; rows that cannot be read (see err)
  * become zeros.  No two rows of k, no two of v, and no row of k and one of v may
  * share an element (refused, but for k and v of different strides). */
