@@ -316,12 +316,34 @@ NCU_NAMES = {"index_score": "k_index_score", "topk": "k_topk", "union_probe": "k
              "commit": "k_commit"}
 
 
-def csrc_hash() -> str:
-    """sha256 over the kernel sources (file name, then bytes; sorted), 16 hex digits."""
+CSRC = os.path.join(ROOT, "hierarchical_sparse_kv_int8_gb300", "csrc")
+
+
+def profiled_sources():
+    """What the kernels of NCU_NAMES are built from: the files of csrc/ that define one,
+    and the headers of csrc/ that they include."""
     import glob
+    import re
+    names = tuple(n.rstrip("<") for n in NCU_NAMES.values())
+    todo = [f for f in sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+            if any(k.startswith(names) for k in re.findall(
+                r"__global__[^;{]*?\b(k_\w+)\s*\(", open(f).read()))]
+    got = set()
+    while todo:
+        f = todo.pop()
+        if f not in got and os.path.exists(f):
+            got.add(f)
+            todo += [os.path.join(CSRC, i) for i in
+                     re.findall(r'#include "([^"/]+)"', open(f).read())]
+    return sorted(got)
+
+
+def csrc_hash() -> str:
+    """sha256 over the profiled kernels' sources (file name, then bytes; sorted), 16 hex
+    digits: other kernels of the library come and go without it."""
     import hashlib
     h = hashlib.sha256()
-    for f in sorted(glob.glob(os.path.join(ROOT, "hierarchical_sparse_kv_int8_gb300", "csrc", "*"))):
+    for f in profiled_sources():
         h.update(os.path.basename(f).encode())
         h.update(open(f, "rb").read())
     return h.hexdigest()[:16]

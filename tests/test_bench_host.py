@@ -78,6 +78,29 @@ def test_csrc_hash_is_stable():
     int(h, 16)
 
 
+def test_csrc_hash_follows_the_profiled_kernels_only(tmp_path, monkeypatch):
+    """Their files and the headers these include move it; files of other kernels do not."""
+    import os
+    import shutil
+    names = [os.path.basename(f) for f in bench.profiled_sources()]
+    assert {"k_select.cu", "k_resolve.cu", "k_attn.cu", "k_uattn.cu", "k_uattn_tc.cu", "k_state.cu",
+            "dhs_internal.cuh", "ptx_util.cuh", "tc_util.cuh"} <= set(names)
+    assert not {"k_prompt.cu", "k_pages.cu", "k_page_attn.cu", "pages_internal.cuh", "dhs_api.cu"} & set(names)
+    shutil.copytree(bench.CSRC, tmp_path / "csrc")
+    monkeypatch.setattr(bench, "CSRC", str(tmp_path / "csrc"))
+    was = bench.csrc_hash()
+    for f in sorted(os.listdir(tmp_path / "csrc")):
+        p = tmp_path / "csrc" / f
+        text = p.read_text()
+        p.write_text(text + "\n// another line\n")
+        assert (bench.csrc_hash() != was) == (f in names), f
+        p.write_text(text)
+    (tmp_path / "csrc" / "k_new.cu").write_text('#include "tc_util.cuh"\n__global__ void k_new() {}\n')
+    assert bench.csrc_hash() == was
+    (tmp_path / "csrc" / "k_new.cu").write_text("__global__ void k_commit_more(int x) {}\n")
+    assert bench.csrc_hash() != was
+
+
 def test_reference_arm_line(capsys):
     """The reference arm times the oracle on one request's round per step, on
     a pool of one process per host core, and prints the contract's line with
