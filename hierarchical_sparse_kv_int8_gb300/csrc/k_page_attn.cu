@@ -48,7 +48,7 @@
 //
 // Measured, 32 sequences of 65536 positions, 128 dims, one kv head, in us (and % of the
 // measured copy bandwidth): bf16 8 rows 167 (95), 32 rows 173 (91), 64 rows 225 (70),
-// 128 rows 510; int8 8 rows 99 (82), 32 rows 178, 64 rows 316, 128 rows 833.  Up to 32
+// 128 rows 510; int8 8 rows 99 (82), 32 rows 178, 64 rows 316, 128 rows 801.  Up to 32
 // rows of bf16 the bytes bound it, in 8 bits the conversion to f16 does, and with more
 // rows the mma.sync products and the registers that 128 rows leave for nothing else
 // (serving decodes and verifies with 1 to 32 rows).  One sequence of 4096: 9.0 us, of
@@ -200,6 +200,89 @@ struct AttnArgs {
   float scale_log2;
 };
 
+// More than 32 sequences.  Their lengths are read eight to a lane, under way together (1024
+// sequences of 200: 53 -> 38 us).
+struct SeqLens {
+  const int32_t *q_lens, *seq_lens;
+  int q_len, n_seqs, most;
+};
+// Blocks (of one kv head) of sequences i + 32 u + this lane.
+template <int BLOCK>
+__device__ __forceinline__ void blocks_of_8(const SeqLens &a, int i, int (&n)[8], int32_t *err) {
+  const int lane = threadIdx.x & 31;
+  int nq[8], len[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const int at = i + 32 * u + lane;
+    nq[u] = at >= a.n_seqs ? 0 : a.q_lens ? a.q_lens[at] : a.q_len;
+    len[u] = at >= a.n_seqs ? 0 : a.seq_lens[at];
+  }
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    if (nq[u] < 0 || nq[u] > a.q_len || len[u] < 0 || len[u] > a.most)
+      page_error(err, DC_ROW_RANGE, DHS_SITE_PAGE_ATTEND);
+    len[u] = max(0, min(len[u], a.most));
+    n[u] = nq[u] > 0 ? (int)(((uint32_t)len[u] + BLOCK - 1) / BLOCK) : 0;
+  }
+}
+// This lane's share of all blocks, and the sequences with any.
+template <int BLOCK>
+__device__ __forceinline__ longlong2 count_blocks(const SeqLens &a, int32_t *err) {
+  int64_t sum = 0;
+  int some = 0;
+  for (int i = 0; i < a.n_seqs; i += 256) {
+    int n[8];
+    blocks_of_8<BLOCK>(a, i, n, err);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      some += __popc(__ballot_sync(0xffffffffu, n[u] > 0));
+      sum += n[u];
+    }
+  }
+  return make_longlong2(sum, some);
+}
+// The 32 neighbours (their first) among whom unit `want` is, and the units before them.
+// (chunk: blocks of a unit)
+template <int BLOCK>
+__device__ __forceinline__ longlong2 find_neighbours(const SeqLens &a, int64_t want,
+                                                     int64_t chunk) {
+  int base = 0;
+  bool found = false;
+  int64_t at = 0;
+  for (int i = 0; i < a.n_seqs && !found; i += 256) {
+    int n[8];
+    blocks_of_8<BLOCK>(a, i, n, nullptr);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int units = chunk == 1 ? n[u] : (int)idiv(n[u] + chunk - 1, chunk);
+      const int all = __reduce_add_sync(0xffffffffu, units);
+      if (!found && want < at + all) {
+        found = true;
+        base = i + 32 * u;
+      }
+      if (!found) at += all;
+    }
+  }
+  return make_longlong2(base, at);
+}
+// The same as calls: with these loops inside it, the kernel's code for few sequences lies
+// apart, which costs where it has to come from memory (L2 flushed before each call: one
+// sequence of 4096 19 us with them, 15 without; 16 of 64K in int8 78 and 73; 61 of 8000 in
+// e4m3 107 and 103).
+template <int BLOCK>
+__device__ __noinline__ longlong2 count_blocks_call(const int32_t *q_lens, const int32_t *seq_lens,
+                                                    int q_len, int n_seqs, int most,
+                                                    int32_t *err) {
+  return count_blocks<BLOCK>(SeqLens{q_lens, seq_lens, q_len, n_seqs, most}, err);
+}
+template <int BLOCK>
+__device__ __noinline__ longlong2 find_neighbours_call(const int32_t *q_lens,
+                                                       const int32_t *seq_lens, int q_len,
+                                                       int n_seqs, int most, int64_t want,
+                                                       int64_t chunk) {
+  return find_neighbours<BLOCK>(SeqLens{q_lens, seq_lens, q_len, n_seqs, most}, want, chunk);
+}
+
 template <class C>
 __global__ void __launch_bounds__(kPaThreads, C::OCC)
 k_page_attn(const PageView pg, const AttnArgs a) {
@@ -239,25 +322,9 @@ k_page_attn(const PageView pg, const AttnArgs a) {
     return my_n;
   };
 
-  // The same of sequences i + 32 u + lane, whose loads are under way together (1024
-  // sequences of 200: 53 -> 38 us).
-  auto blocks8 = [&](int i, int (&n)[8], bool record) {
-    int nq[8], len[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int at = i + 32 * u + lane;
-      nq[u] = at >= a.n_seqs ? 0 : a.q_lens ? a.q_lens[at] : a.q_len;
-      len[u] = at >= a.n_seqs ? 0 : a.seq_lens[at];
-    }
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      if (record && (nq[u] < 0 || nq[u] > a.q_len || len[u] < 0 || len[u] > most))
-        page_error(a.err, DC_ROW_RANGE, DHS_SITE_PAGE_ATTEND);
-      len[u] = (int)max((int64_t)0, min((int64_t)len[u], most));
-      n[u] = nq[u] > 0 ? (int)(((uint32_t)len[u] + C::BLOCK - 1) / C::BLOCK) : 0;
-    }
-  };
-
+  // (128 rows of bf16 have no register for the calls' sake: 498 us for 32 x 64K, 542 with them)
+  constexpr bool kCalls = !(C::W == 2 && MT == 2);
+  const SeqLens seqs{a.q_lens, a.seq_lens, a.q_len, a.n_seqs, (int)most};
   // All blocks, and the sequences with any: every warp adds up all of them.
   int64_t sum = 0;
   int some = 0;
@@ -266,15 +333,11 @@ k_page_attn(const PageView pg, const AttnArgs a) {
     some = __popc(__ballot_sync(0xffffffffu, n > 0));
     sum = __reduce_add_sync(0xffffffffu, n);  // (32 of them fit 32 bits)
   } else {
-    for (int i = 0; i < a.n_seqs; i += 256) {
-      int n[8];
-      blocks8(i, n, true);
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        some += __popc(__ballot_sync(0xffffffffu, n[u] > 0));
-        sum += n[u];
-      }
-    }
+    const longlong2 r = kCalls ? count_blocks_call<C::BLOCK>(a.q_lens, a.seq_lens, a.q_len,
+                                                             a.n_seqs, (int)most, a.err)
+                               : count_blocks<C::BLOCK>(seqs, a.err);
+    sum = r.x;
+    some = (int)r.y;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   }
@@ -340,20 +403,12 @@ k_page_attn(const PageView pg, const AttnArgs a) {
     int64_t at = 0;
     int base = 0;  // its 32 neighbours
     if (!few) {
-      bool found = false;
-      for (int i = 0; i < a.n_seqs && !found; i += 256) {
-        int n[8];
-        blocks8(i, n, false);
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int all = __reduce_add_sync(0xffffffffu, (int)units(n[u]));
-          if (!found && want < at + all) {
-            found = true;
-            base = i + 32 * u;
-          }
-          if (!found) at += all;
-        }
-      }
+      const longlong2 r =
+          kCalls ? find_neighbours_call<C::BLOCK>(a.q_lens, a.seq_lens, a.q_len, a.n_seqs,
+                                                  (int)most, want, most_blocks)
+                 : find_neighbours<C::BLOCK>(seqs, want, most_blocks);
+      base = (int)r.x;
+      at = r.y;
     }
     const int n = (int)units(blocks(base));
     int x = n;  // inclusive sums
@@ -428,7 +483,7 @@ k_page_attn(const PageView pg, const AttnArgs a) {
     // 8 bits: under way with the lookups and first copies, as the rows' largest elements
     // are wanted before the first tile (189 short sequences 74 -> 69 us); bf16 after them
     // (400 short sequences 94 us, before them 100), and so 128 rows of 8 bits, whose
-    // registers are short (32 x 64K 833 us, before them 842)
+    // registers are short (32 x 64K took 833 us then, before them 842)
     constexpr bool kEarly = C::W == 1 && MT == 1;
     if (kEarly) load_q();
 
