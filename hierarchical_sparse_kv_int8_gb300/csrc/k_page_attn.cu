@@ -267,8 +267,9 @@ __device__ __forceinline__ longlong2 find_neighbours(const SeqLens &a, int64_t w
 }
 // The same as calls: with these loops inside it, the kernel's code for few sequences lies
 // apart, which costs where it has to come from memory (L2 flushed before each call: one
-// sequence of 4096 19 us with them, 15 without; 16 of 64K in int8 78 and 73; 61 of 8000 in
-// e4m3 107 and 103).
+// sequence of 4096 18.7 us with them, 16.9 without; 16 of 64K in int8 77 and 73, 8 of up to
+// 32K in bf16, 4 tokens each, 41.5 and 39.5).  More than 32 pay for it with 1 to 5 % (61 of
+// 8000 in e4m3 106.8 and 107.7, 1024 of 200 in int8, 32 rows each, 63 and 66).
 template <int BLOCK>
 __device__ __noinline__ longlong2 count_blocks_call(const int32_t *q_lens, const int32_t *seq_lens,
                                                     int q_len, int n_seqs, int most,
