@@ -50,10 +50,9 @@
 // measured copy bandwidth): bf16 8 rows 167 (95), 32 rows 173 (91), 64 rows 225 (70),
 // 128 rows 510; int8 8 rows 99 (82), 32 rows 178, 64 rows 316, 128 rows 801.  Up to 32
 // rows of bf16 the bytes bound it, in 8 bits the conversion to f16 does, and with more
-// rows the mma.sync products and the registers that 128 rows leave for nothing else
-// (serving decodes and verifies with 1 to 32 rows).  One sequence of 4096: 9.0 us, of
-// which the join takes 4 to 5 and the way from the lengths through the page table to
-// the first rows most of the rest.
+// rows the mma.sync products and the registers that 128 rows leave for nothing else.  One
+// sequence of 4096: 9.0 us, of which the join takes 4 to 5 and the way from the lengths
+// through the page table to the first rows most of the rest.
 #include "pages_internal.cuh"
 #include "tc_util.cuh"
 
