@@ -20,7 +20,8 @@ from . import _build
 
 __all__ = ["Arenas", "Config", "Context", "DhsError", "build", "load", "LOC_RING", "LOC_OPT",
            "LOC_HOT", "LOC_STAGE", "BUF", "ROLE_FULL", "ROLE_FOLLOWER", "PageCache", "PAGE_BF16",
-           "PAGE_INT8", "PAGE_E4M3", "prompt_attend", "prompt_workspace", "check_errors"]
+           "PAGE_INT8", "PAGE_E4M3", "prompt_attend", "prompt_workspace", "check_errors", "Rotation",
+           "ROTATE_HALVES", "ROTATE_NEIGHBOURS", "rotate"]
 
 LOC_RING, LOC_OPT, LOC_HOT, LOC_STAGE = 0, 1, 2, 3
 LOC_TIER_SHIFT = 28
@@ -129,6 +130,10 @@ _P, _I32, _I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
 _SIGS.update({
     "dhs_page_write": ([_P, _P, _P, _P, _I64, _P, _P, _P, _I32, _I32, _P, _P], ctypes.c_int),
     "dhs_page_read": ([_P, _P, _P, _P, _I64, _P, _P, _P, _I32, _I32, _P, _P], ctypes.c_int),
+    "dhs_rotation_turns": ([_P, _I32, _P], ctypes.c_int),
+    "dhs_rotate": ([_P, _P, _P, ctypes.c_float, _I32, _I64, _P, _P], ctypes.c_int),
+    "dhs_page_append": ([_P] * 6 + [ctypes.c_float, _I64] + [_P] * 4 + [_I32, _I32, _P, _P],
+                        ctypes.c_int),
     "dhs_page_attend": ([_P] * 5 + [_I32] * 4 + [ctypes.c_float, _P, _P, _P, _I64, _P, _P],
                         ctypes.c_int),
     "dhs_page_attend_workspace": ([_P, _I32, _I32, _I32], _I64),
@@ -533,7 +538,8 @@ class Context:
                                              _dptr(lse), _stream(stream)), "dhs_round_host")
 
 
-_DENSE = ("PageCache", "PAGE_BF16", "PAGE_INT8", "PAGE_E4M3", "prompt_attend", "prompt_workspace",
+_DENSE = ("Rotation", "ROTATE_HALVES", "ROTATE_NEIGHBOURS", "rotate",
+          "PageCache", "PAGE_BF16", "PAGE_INT8", "PAGE_E4M3", "prompt_attend", "prompt_workspace",
           "check_errors")
 
 

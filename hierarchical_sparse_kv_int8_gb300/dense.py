@@ -1,4 +1,4 @@
-"""Dense attention over a paged cache: binding of ``dhs_page_*`` and
+"""Dense attention over a paged cache: binding of ``dhs_page_*``, ``dhs_rotate`` and
 ``dhs_prompt_attend`` (see include/dhs.h for what each call computes).
 
 Tensors are checked for type, shape, layout and device and passed on; nothing
@@ -18,10 +18,11 @@ _KIND = {torch.bfloat16: PAGE_BF16, torch.int8: PAGE_INT8, torch.float8_e4m3fn: 
 _DTYPE = {v: k for k, v in _KIND.items()}
 _CHECK = {1: "a length or offset outside its range", 2: "a page outside the cache",
           4: "a bounded wait that ran out"}
-_SITE = {1: "dhs_page_write", 2: "dhs_page_read", 3: "dhs_page_attend", 4: "dhs_prompt_attend"}
+_SITE = {1: "dhs_page_write", 2: "dhs_page_read", 3: "dhs_page_attend", 4: "dhs_prompt_attend",
+         5: "dhs_page_append", 6: "dhs_page_chunk"}
+ROTATE_HALVES, ROTATE_NEIGHBOURS = 0, 1
 
-
-_Strides4, _Strides6 = ctypes.c_int64 * 4, ctypes.c_int64 * 6
+_Strides2, _Strides4, _Strides6 = ctypes.c_int64 * 2, ctypes.c_int64 * 4, ctypes.c_int64 * 6
 
 
 class Pages(ctypes.Structure):
@@ -29,6 +30,17 @@ class Pages(ctypes.Structure):
                 ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
                 ("page_rows", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("kind", ctypes.c_int32)]
+
+
+class _Turns(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("n_pairs", ctypes.c_int32), ("pairing", ctypes.c_int32),
+                ("amplitude", ctypes.c_float)]
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("norm", ctypes.c_void_p)] + [
+        (n, ctypes.c_int64) for n in ("x_token", "x_head", "out_token", "out_head")] + [
+        ("heads", ctypes.c_int32)]
 
 
 # A decode step makes several calls of a few microseconds each, so what a call does on
@@ -91,6 +103,27 @@ def _rows(t, name, index):
     return n, h, d, (st if n > 1 else h * d), (sh if h > 1 else d)
 
 
+def _heads(name, x, out, norm, index):
+    """Tokens, elements and the description of a tensor's heads and where they go."""
+    n, h, d, xt, xh = _rows(x, name, index)
+    ot = oh = 0
+    if out is not None:
+        if out.shape != x.shape:
+            raise ValueError("%s_out: %s expected, not %s" % (name, tuple(x.shape), tuple(out.shape)))
+        _, _, _, ot, oh = _rows(out, name + "_out", index)
+    return n, d, _Heads(x.data_ptr(), None if out is None else out.data_ptr(),
+                        None if norm is None else _plain(norm, name + "_norm", _F32, (d,), index),
+                        xt, xh, ot, oh, h)
+
+
+def _turns(rotation, index):
+    if rotation is None:
+        return None
+    if rotation._index != index:
+        raise ValueError("rotation: on cuda:%s expected, not cuda:%s" % (index, rotation._index))
+    return rotation._ref
+
+
 def _space(t, index):
     if t is None:
         return None, 0
@@ -137,6 +170,61 @@ def check_errors(errors=None, stream=None):
 def _found(code, site):
     if code:
         _raise(5, "%s: %s" % (_SITE.get(site, "?"), _CHECK.get(code, "check %d" % code)))
+
+
+class Rotation:
+    """A position rotation for :func:`rotate` and :meth:`PageCache.append`, laid out once.
+
+    ``freqs``: the angle that pair i of a head's row turns by per position, in radians (fp64,
+    on any device); a multiple of 4 of them, at most half a head's elements, the rest of which
+    stay as they are.  ``pairing``: ``ROTATE_HALVES`` for pairs (i, i + len(freqs)),
+    ``ROTATE_NEIGHBOURS`` for (2 i, 2 i + 1).  ``amplitude`` multiplies sines and cosines.
+    """
+
+    def __init__(self, freqs, pairing: int = ROTATE_HALVES, amplitude: float = 1.0, device=None):
+        host = torch.as_tensor(freqs).detach()
+        if device is None:
+            device = host.device if host.is_cuda else "cuda"
+        host = host.to("cpu", torch.float64).contiguous()
+        if host.dim() != 1 or pairing not in (ROTATE_HALVES, ROTATE_NEIGHBOURS):
+            raise ValueError("freqs: [n_pairs], pairing: ROTATE_HALVES or ROTATE_NEIGHBOURS expected")
+        turns = torch.empty(host.shape, dtype=torch.int64)
+        rc = _lib().dhs_rotation_turns(host.data_ptr(), host.numel(), turns.data_ptr())
+        if rc:
+            _raise(rc, "dhs_rotation_turns")
+        self.turns, self.pairing, self.amplitude = turns.to(device), pairing, amplitude
+        self._index = self.turns.get_device()
+        with _on(self._index):
+            torch.cuda.current_stream().synchronize()  # (calls on any stream may follow)
+        self._desc = _Turns(self.turns.data_ptr(), host.numel(), pairing, amplitude)
+        self._ref = ctypes.byref(self._desc)
+
+
+def rotate(q, k, positions, rotation, q_out, k_out, q_norm=None, k_norm=None, eps: float = 1e-6,
+           stream=None):
+    """Norm and rotation of every head (dhs_rotate): ``q`` and ``k`` [tokens, heads, head_dim]
+    bf16 into ``q_out`` and ``k_out`` (which may be ``q`` and ``k``); ``k`` and ``k_out`` or ``q``
+    and ``q_out`` may be None.  ``positions`` int32 [tokens]; ``q_norm`` and ``k_norm`` fp32
+    [head_dim] or None; ``rotation`` a :class:`Rotation` or None."""
+    some = k if q is None else q
+    ix = some.get_device()
+    if ix < 0 or _current_device() != ix:
+        with _on(ix):
+            return rotate(q, k, positions, rotation, q_out, k_out, q_norm, k_norm, eps, stream)
+    hq = hk = None
+    n, d = some.shape[0], some.shape[-1]
+    if q is not None:
+        n, d, hq = _heads("q", q, q_out, q_norm, ix)
+    if k is not None:
+        nk, dk, hk = _heads("k", k, k_out, k_norm, ix)
+        if (nk, dk) != (n, d):
+            raise ValueError("k: [%d, kv_heads, %d] expected, not %s" % (n, d, tuple(k.shape)))
+    rc = _lib().dhs_rotate(_turns(rotation, ix), None if hq is None else ctypes.byref(hq),
+                           None if hk is None else ctypes.byref(hk), eps, d, n,
+                           None if positions is None else _plain(positions, "positions", _I32, (n,), ix),
+                           _raw(stream, ix))
+    if rc:
+        _raise(rc, "dhs_rotate")
 
 
 class PageCache:
@@ -208,6 +296,37 @@ class PageCache:
     def write(self, k, v, cu, seq_lens, page_table, stream=None):
         """Store packed tokens' rows (dhs_page_write)."""
         self._copy(self._lib.dhs_page_write, "dhs_page_write", k, v, cu, seq_lens, page_table, stream)
+
+    def append(self, q, k, v, cu, seq_lens, page_table, q_out, rotation=None, q_norm=None,
+               k_norm=None, eps: float = 1e-6, positions=None, k_out=None, stream=None):
+        """Norm and rotation of packed tokens' queries and keys, the queries into ``q_out``, keys
+        and values into the pages (dhs_page_append).  ``q`` and ``q_out`` may be None; ``k_out``
+        takes the keys in bf16 as well; ``positions`` int32 [tokens] to rotate by instead of
+        the tokens' own.  The norms and ``rotation`` as in :func:`rotate`."""
+        ix = self._index
+        if _current_device() != ix:
+            with _on(ix):
+                return self.append(q, k, v, cu, seq_lens, page_table, q_out, rotation, q_norm, k_norm,
+                                   eps, positions, k_out, stream)
+        tok, d, hk = _heads("k", k, k_out, k_norm, ix)
+        tv, hv, dv, vt, vh = _rows(v, "v", ix)
+        if d != self.head_dim or hk.heads != self.kv_heads or (tv, hv, dv) != (tok, hk.heads, d):
+            raise ValueError("k and v: [tokens, %d, %d] expected, not %s and %s" % (
+                self.kv_heads, self.head_dim, tuple(k.shape), tuple(v.shape)))
+        hq = None
+        if q is not None:
+            nq, dq, hq = _heads("q", q, q_out, q_norm, ix)
+            if (nq, dq) != (tok, d):
+                raise ValueError("q: [%d, q_heads, %d] expected, not %s" % (tok, d, tuple(q.shape)))
+        n = seq_lens.shape[0]
+        rc = self._lib.dhs_page_append(
+            self._ref, _turns(rotation, ix), None if hq is None else ctypes.byref(hq),
+            ctypes.byref(hk), v.data_ptr(), _Strides2(vt, vh), eps, tok,
+            None if positions is None else _plain(positions, "positions", _I32, (tok,), ix),
+            _plain(cu, "cu", _I32, (n + 1,), ix), _plain(seq_lens, "seq_lens", _I32, (n,), ix),
+            _table(page_table, n, ix), page_table.shape[1], n, self._err, _raw(stream, ix))
+        if rc:
+            _raise(rc, "dhs_page_append")
 
     def read(self, k_out, v_out, cu, seq_lens, page_table, stream=None):
         """Cached rows of packed tokens, as bf16 (dhs_page_read)."""

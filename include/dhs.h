@@ -597,6 +597,9 @@ int64_t dhs_policy_free_pages(const dhs_policy *p);
  *   dhs_page_write     the new tokens' keys and values into the pages
  *   dhs_page_attend    the newest 1-8 tokens of every sequence over the pages
  *   dhs_page_read      cached rows back, for the next chunk of a long prompt
+ * and, where the layer's queries and keys still lack their norm and rotation,
+ *   dhs_rotate         both, for every head, before dhs_prompt_attend
+ *   dhs_page_append    both on the way into the pages, in dhs_page_write's place
  * The calls need no context, allocate nothing, synchronise nothing and can be
  * captured into a CUDA graph; lengths, offsets and page tables are read on the
  * device, so a captured graph follows them.  Pointers and stream belong to the
@@ -612,7 +615,7 @@ int64_t dhs_policy_free_pages(const dhs_policy *p);
  * that dhs_prompt_errors reads. */
 enum { DHS_PAGE_BF16 = 0, DHS_PAGE_INT8 = 1, DHS_PAGE_E4M3 = 2 };
 enum { DHS_SITE_PAGE_WRITE = 1, DHS_SITE_PAGE_READ = 2, DHS_SITE_PAGE_ATTEND = 3,
-       DHS_SITE_PROMPT_ATTEND = 4 };
+       DHS_SITE_PROMPT_ATTEND = 4, DHS_SITE_PAGE_APPEND = 5, DHS_SITE_PAGE_CHUNK = 6 };
 
 /* The cache: caller-owned device memory, k and v 16-byte aligned.
  *   k, v              [n_pages][kv_heads][page_rows][head_dim] elements of
@@ -664,6 +667,65 @@ int dhs_page_read(const dhs_pages *pages, void *k, void *v, const int64_t *strid
                   int64_t n_tokens, const int32_t *cu, const int32_t *seq_lens,
                   const int32_t *page_table, int32_t table_width, int32_t n_seqs, int32_t *err,
                   dhs_stream stream);
+
+/* A position rotation: pair i < n_pairs of a head's row turns by the angle of its token's
+ * position times frequency i, (a, b) -> A (a cos - b sin, b cos + a sin).
+ *   turns      device uint64 [n_pairs], 8-byte aligned: the frequencies in turns per position,
+ *              as dhs_rotation_turns gives them (so far positions keep their angles)
+ *   n_pairs    a multiple of 4, at most head_dim / 2; elements from 2 n_pairs on stay
+ *   pairing    which elements pair i is: (i, n_pairs + i) or (2 i, 2 i + 1)
+ *   amplitude  A, 1 for a plain rotation; above 0, at most 1e38 */
+enum { DHS_ROTATE_HALVES = 0, DHS_ROTATE_NEIGHBOURS = 1 };
+typedef struct {
+  const uint64_t *turns;
+  int32_t n_pairs;
+  int32_t pairing;
+  float amplitude;
+} dhs_rotation;
+
+/* Host: frequencies in radians per position (|f| < 2^32) as turns in 64-bit fixed point,
+ * round(f / 2 pi 2^64) mod 2^64. */
+int dhs_rotation_turns(const double *freqs, int32_t n, uint64_t *turns);
+
+/* A tensor's heads, as they come and as they go.  x and out: device bf16, 16-byte aligned,
+ * element e of head h of token t at t * x_token + h * x_head + e (in elements, multiples of 8,
+ * not negative; out likewise).  norm: device fp32 [head_dim], 16-byte aligned, the weights of
+ * a norm x / sqrt(mean(x^2) + eps) * norm before the rotation, or NULL for none.  out may be x
+ * with the same strides.  No two rows of out may share an element, nor a row of out and
+ * another one that the call reads or writes (refused where x and out have the same strides). */
+typedef struct {
+  const void *x;
+  void *out;
+  const float *norm;
+  int64_t x_token, x_head, out_token, out_head;
+  int32_t heads; /* 1 .. 131072 */
+} dhs_heads;
+
+/* Norm and rotation of the heads of n_tokens tokens: q and k, or one of them (the other
+ * NULL).  rot NULL: no rotation.  positions: device int32 [n_tokens], any values, NULL
+ * without a rotation.  Everything is in fp32 and rounded once, to bf16.  eps is at least 0,
+ * at most 1e38 (with 0, a row of zeros becomes NaN). */
+int dhs_rotate(const dhs_rotation *rot, const dhs_heads *q, const dhs_heads *k, float eps,
+               int32_t head_dim, int64_t n_tokens, const int32_t *positions, dhs_stream stream);
+
+/* The same with the keys going on into the cache, and values with them: tokens, pages and
+ * the rows that are left alone as in dhs_page_write.
+ *   q          the queries' heads, out included, or NULL
+ *   k          the keys' heads, as many as the cache has; out NULL unless they are wanted in
+ *              bf16 as well
+ *   v          device bf16, 16-byte aligned; v_strides: host int64[2], a token's and a head's
+ *              in elements, multiples of 8; NULL: contiguous
+ *   positions  device int32 [n_tokens] to rotate by, or NULL: each token's own, which is where
+ *              it goes in any case
+ * q's and k's out of padding tokens, and of tokens that err tells of, are left as they were.
+ * Keys in 8 bits: scale = max|y| / Q and code = y / scale as in dhs_page_write, of the fp32
+ * row y after norm and rotation, the quotient in fp32 too; values, and keys without either, as
+ * dhs_page_write stores them. */
+int dhs_page_append(const dhs_pages *pages, const dhs_rotation *rot, const dhs_heads *q,
+                    const dhs_heads *k, const void *v, const int64_t *v_strides, float eps,
+                    int64_t n_tokens, const int32_t *positions, const int32_t *cu,
+                    const int32_t *seq_lens, const int32_t *page_table, int32_t table_width,
+                    int32_t n_seqs, int32_t *err, dhs_stream stream);
 
 /* Attention of the newest tokens of every sequence over its cached rows, for
  * head h (kv head h / (q_heads / kv_heads)) and query j < n_i:

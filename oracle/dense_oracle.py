@@ -85,3 +85,56 @@ def attend(q, k, v, scale):
                 lse[u, h] = m + np.log(z) if np.isfinite(m) else m
                 reach[u, h] = (np.abs(kk) @ np.abs(q[u, h])).max() * scale
     return out, lse, wt, reach
+
+
+def _half_turn_bits():
+    """1 / 2 pi to 400 bits after the point, as a whole number (pi by Machin's formula)."""
+    bits = 460
+
+    def arctan_of_one_over(x):
+        t = (1 << bits) // x
+        s, n, sign = t, 3, -1
+        while t:
+            t //= x * x
+            s += sign * (t // n)
+            n, sign = n + 2, -sign
+        return s
+
+    pi = 4 * (4 * arctan_of_one_over(5) - arctan_of_one_over(239))
+    return (1 << (bits + 400)) // (2 * pi)
+
+
+_TURN = _half_turn_bits()
+
+
+def turns(freq, position=1):
+    """position * freq radians in turns, as a fraction in [0, 1) exact to some 2^-300."""
+    from fractions import Fraction as F
+    t = F(float(freq)) * int(position) * F(_TURN, 1 << 400)
+    return t - math.floor(t)
+
+
+def rotate(x, weight, eps, positions, freqs, halves, amplitude=1.0):
+    """Heads x [tokens, heads, d] after their norm (weight [d] or None) and rotation by
+    positions [tokens] (freqs [pairs], possibly none); and what error bounds are made of, the
+    sum of magnitudes |a| + |b| that each result is made of."""
+    y = np.array(x, np.float64)
+    if weight is not None:
+        with np.errstate(invalid="ignore"):
+            y = y / np.sqrt((y * y).mean(-1, keepdims=True) + eps) * np.asarray(weight, np.float64)
+    mag = np.abs(y)
+    n = len(freqs)
+    out = y.copy()
+    first = np.arange(n) * (1 if halves else 2)
+    second = first + (n if halves else 1)
+    for t, p in enumerate(positions):
+        if not n:
+            break
+        ang = np.array([2 * math.pi * float(turns(f, p)) for f in freqs])
+        c, s = amplitude * np.cos(ang), amplitude * np.sin(ang)
+        a, b = y[t][:, first], y[t][:, second]
+        with np.errstate(invalid="ignore"):
+            out[t][:, first], out[t][:, second] = a * c - b * s, b * c + a * s
+        both = amplitude * (np.abs(a) + np.abs(b))
+        mag[t][:, first], mag[t][:, second] = both, both
+    return out, mag
