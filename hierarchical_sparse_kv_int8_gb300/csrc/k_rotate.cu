@@ -14,17 +14,20 @@
 // all of their heads.
 //
 // HBM bounds it: each row is read once and written once, with nothing in between that
-// another row needs.  A lane holds 8 values of a row: 4 and their 4 partners half a rotation
-// away, or 4 pairs of neighbours, so that the rotation needs no exchange between lanes and
-// the norm one reduction over the row's 8 or 16 lanes.  A warp's rows are all of one of
-// queries, keys and values.
+// another row needs.  What stands in the way is the work per value, so a row's 8 or 16 lanes
+// keep their token: what they multiply by (sines, cosines and the norm's weights in one) is
+// made once and stays in registers over the heads of a chunk.  A lane holds 8 values of a
+// row: 4 and their 4 partners half a rotation away, or 4 pairs of neighbours, so that the
+// rotation needs no exchange between lanes and the norm one reduction over the row.
+// (TIMES)
 #include "pages_quant.cuh"
+#include "tc_util.cuh"
 
 namespace dhs {
 namespace {
 
 constexpr int kRoThreads = 256;
-constexpr int kRoTok = 16;   // tokens of a CTA at most
+constexpr int kRoAhead = 4;  // rows of a lane under way at a time
 constexpr int kNoPages = -1;
 
 struct HeadRows {
@@ -42,7 +45,8 @@ struct RotateArgs {
   int32_t *err;
   int64_t n_tok;
   float amplitude, eps;
-  int pairs, halves, per_cta, width, n_seqs;
+  int pairs, halves, width, n_seqs;
+  int chunk, qc, kc;  // heads of a chunk; chunks of queries and of keys
 };
 
 // Codes of eight values in 32 bits over the scale's reciprocal, rounded to nearest with
@@ -64,179 +68,198 @@ __device__ __forceinline__ void codes_of(const float (&y)[8], float by, uint32_t
   }
 }
 
-template <int D, int KIND>
+// CTA (x, y): tokens x * TOK .., chunk y of the heads of queries, then keys, then values.
+template <int D, int KIND, bool HALVES>
 __global__ void __launch_bounds__(kRoThreads)
 k_rotate(const PageView pg, const RotateArgs a) {
-  constexpr int L = D / 8, RW = 32 / L, ROWS = kRoThreads / L;  // lanes of a row, rows of a warp, CTA
-  __shared__ int64_t dst[kRoTok];
-  __shared__ int at_pos[kRoTok];
-  __shared__ __align__(16) float sh_cos[kRoTok][D / 2], sh_sin[kRoTok][D / 2];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % L;
-  const int64_t t0 = (int64_t)blockIdx.x * a.per_cta;
-  const int nt = (int)min((int64_t)a.per_cta, a.n_tok - t0);
+  constexpr int L = D / 8, TOK = kRoThreads / L, U = kRoAhead;  // lanes of a row, tokens
+  __shared__ int64_t dst[TOK];
+  __shared__ int at_pos[TOK];
+  const int sub = threadIdx.x % L, mine = threadIdx.x / L;
+  const int64_t t0 = (int64_t)blockIdx.x * TOK, tok = t0 + mine;
+  const bool there = tok < a.n_tok;
+  const int c = blockIdx.y;
+  const bool value = c >= a.qc + a.kc, key = !value && c >= a.qc;
+  const HeadRows &r = value ? a.v : key ? a.k : a.q;
+  const int h0 = (c - (value ? a.qc + a.kc : key ? a.qc : 0)) * a.chunk;
+  const int h1 = min(h0 + a.chunk, r.heads);
 
-  // slots of rows: queries, keys, values, each rounded up to whole warps
-  auto whole = [](int n) { return (n + RW - 1) / RW * RW; };
-  const int nq = nt * a.q.heads, nk = nt * a.k.heads, nv = nt * a.v.heads;
-  const int k0 = whole(nq), v0 = k0 + whole(nk), total = v0 + whole(nv);
-  const int step = ROWS * gridDim.y;
-
-  // where this lane's 8 values lie, without and with a rotation by halves
-  const int quads = a.pairs / 4;
-  const bool split = a.halves && sub < quads;
-  const int e0 = !a.halves ? 8 * sub : split ? 4 * sub : 2 * a.pairs + 8 * (sub - quads);
+  // where this lane's 8 values lie: two fours, of which a rotation by halves has pairs
+  const int quads = value ? 0 : a.pairs / 4;
+  const bool turned = sub < quads, split = HALVES && turned;
+  const int e0 = !HALVES || value ? 8 * sub : split ? 4 * sub : 2 * a.pairs + 8 * (sub - quads);
   const int e1 = split ? a.pairs + 4 * sub : e0 + 4;
 
-  // the row of a slot: its token and head
-  auto row_of = [&](int slot, int &t, int &h) -> const HeadRows & {
-    const HeadRows &r = slot < k0 ? a.q : slot < v0 ? a.k : a.v;
-    const int x = slot - (slot < k0 ? 0 : slot < v0 ? k0 : v0) + lane / L;
-    t = (int)((uint32_t)x / (uint32_t)r.heads);
-    h = x - t * r.heads;
-    return r;
-  };
-  auto load = [&](int slot, uint2 (&u)[2]) {
-    u[0] = u[1] = make_uint2(0u, 0u);
-    if (slot >= total) return;
-    int t, h;
-    const HeadRows &r = row_of(slot, t, h);
-    if (t >= nt) return;
-    const unsigned char *at = r.x + 2 * ((t0 + t) * r.xt + h * r.xh);
-    const bool value = slot >= v0;
-    u[0] = *reinterpret_cast<const uint2 *>(at + 2 * (value ? 8 * sub : e0));
-    u[1] = *reinterpret_cast<const uint2 *>(at + 2 * (value ? 8 * sub + 4 : e1));
-  };
-
-  int slot = (int)blockIdx.y * ROWS + warp * RW;
-  uint2 u[2];
-  load(slot, u);  // under way with the lookups
-
-  if (threadIdx.x < nt) {
-    int pos = 0;
-    int64_t to = 0;
-    if (KIND != kNoPages)
-      to = place(pg, a.cu, a.lens, a.table, a.width, a.n_seqs, t0 + threadIdx.x, a.err,
-                 DHS_SITE_PAGE_APPEND, &pos);
-    dst[threadIdx.x] = to;
-    at_pos[threadIdx.x] = a.positions ? a.positions[t0 + threadIdx.x] : pos;
-  }
-  if (a.pairs > 0) {
-    __syncthreads();
-    for (int e = threadIdx.x; e < nt * a.pairs; e += kRoThreads) {
-      const int t = e / a.pairs, i = e - t * a.pairs;
-      const uint64_t turn = a.turns[i] * (uint64_t)(int64_t)at_pos[t];
-      float s, c;
-      sincospif((float)(int32_t)(uint32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31
-      sh_cos[t][i] = c * a.amplitude;
-      sh_sin[t][i] = s * a.amplitude;
+  const unsigned char *from = r.x + 2 * ((there ? tok : 0) * r.xt + h0 * r.xh);
+  uint2 u[U][2];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const bool on = there && h + i < h1;
+      const unsigned char *at = from + (int64_t)(h - h0 + i) * r.xh * 2;
+      u[i][0] = on ? *reinterpret_cast<const uint2 *>(at + 2 * e0) : make_uint2(0u, 0u);
+      u[i][1] = on ? *reinterpret_cast<const uint2 *>(at + 2 * e1) : make_uint2(0u, 0u);
     }
-  }
-  __syncthreads();
+  };
+  load(h0);  // under way with the lookups
 
-  for (; slot < total; slot += step) {
-    uint2 next[2];
-    load(slot + step, next);
-    int t, h;
-    const HeadRows &r = row_of(slot, t, h);
-    const int64_t base = t < nt ? dst[t] : -2;
-    const bool on = t < nt && base >= 0;
-    const bool key = slot >= k0 && slot < v0, value = slot >= v0;  // (of the whole warp)
-    const uint32_t w[4] = {u[0].x, u[0].y, u[1].x, u[1].y};
-    const bool raw = !r.norm && (value || a.pairs == 0);  // the row goes as it came, bit by bit
-    float y[8];
+  if (KIND != kNoPages || a.pairs > 0) {
+    if (threadIdx.x < TOK && t0 + threadIdx.x < a.n_tok) {
+      int pos = 0;
+      int64_t to = 0;
+      if (KIND != kNoPages)
+        to = place(pg, a.cu, a.lens, a.table, a.width, a.n_seqs, t0 + threadIdx.x, a.err,
+                   DHS_SITE_PAGE_APPEND, &pos);
+      dst[threadIdx.x] = to;
+      at_pos[threadIdx.x] = a.positions ? a.positions[t0 + threadIdx.x] : pos;
+    }
+    __syncthreads();
+  }
+  const int64_t base = !there ? -2 : KIND == kNoPages ? 0 : dst[mine];
+  const bool on = base >= 0;
+  const bool raw = !r.norm && (value || a.pairs == 0);  // rows go as they come, bit by bit
+
+  // out = y C + (its partners) S: the weights, and the rotation, of this lane's values
+  uint64_t C[4], S[4];
+  if (!raw) {
+    float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f}, cw[8], sw[8];
+    if (r.norm) {
+      *reinterpret_cast<float4 *>(w) = *reinterpret_cast<const float4 *>(r.norm + e0);
+      *reinterpret_cast<float4 *>(w + 4) = *reinterpret_cast<const float4 *>(r.norm + e1);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      cw[i] = w[i];
+      sw[i] = 0.f;
+    }
+    if (turned && there) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t turn = a.turns[4 * sub + i] * (uint64_t)(int64_t)at_pos[mine];
+        float sn, cs;
+        sincospif((float)(int32_t)(uint32_t)(turn >> 32) * 4.656612873077393e-10f, &sn, &cs);  // 2^-31
+        sn *= a.amplitude;
+        cs *= a.amplitude;
+        const int p = HALVES ? i : 2 * i, q = HALVES ? 4 + i : 2 * i + 1;
+        cw[p] = w[p] * cs;
+        sw[p] = -w[q] * sn;
+        cw[q] = w[q] * cs;
+        sw[q] = w[p] * sn;
+      }
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      y[2 * i] = __uint_as_float(w[i] << 16);
-      y[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      C[i] = pack_f32x2(cw[2 * i], cw[2 * i + 1]);
+      S[i] = pack_f32x2(sw[2 * i], sw[2 * i + 1]);
     }
-    if (!value) {
-      if (r.norm) {
-        auto squares = [&](float g) {
-          float ss = 0.f;
+  }
+
+  // one row: heads are of the whole CTA, so every lane takes part in the reductions
+  auto finish = [&](int h, const uint2 (&x)[2]) {
+    const uint32_t w[4] = {x[0].x, x[0].y, x[1].x, x[1].y};
+    uint64_t y[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float z = y[i] * g;
-            ss = fmaf(z, z, ss);
-          }
+    for (int i = 0; i < 4; ++i)
+      y[i] = pack_f32x2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    uint2 b0 = x[0], b1 = x[1];
+    if (!raw) {
+      if (r.norm) {
+        auto squares = [&]() {
+          uint64_t two = mul_f32x2(y[0], y[0]);
+#pragma unroll
+          for (int i = 1; i < 4; ++i) two = fma_f32x2(y[i], y[i], two);
+          float ss, s1;
+          unpack_f32x2(two, ss, s1);
+          ss += s1;
 #pragma unroll
           for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
           return ss;
         };
-        const float ss = squares(1.f);
-        float f = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+        auto times = [&](float f) {
+          const uint64_t two = pack_f32x2(f, f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[i] = mul_f32x2(y[i], two);
+        };
+        float ss = squares(), eps = a.eps;
         // squares that leave the range of 32 bits (2^100 and more; below 2^-90 where eps does
         // not outweigh them): once more of the row times 2^-70 or 2^100
-        const bool big = !(ss < 1.2676506e30f), small = ss < 8.077936e-28f && a.eps < 7.8886e-31f;
+        const bool big = !(ss < 1.2676506e30f), small = ss < 8.077936e-28f && eps < 7.8886e-31f;
         if (__any_sync(0xffffffffu, big || small)) {
           const float g = big ? 8.470329472543003e-22f : small ? 1.2676506002282294e30f : 1.f;
-          f = rsqrtf(fmaf(squares(g), 1.f / D, a.eps * g * g)) * g;
+          times(g);
+          ss = squares();
+          eps = eps * g * g;
         }
-        const float4 g0 = *reinterpret_cast<const float4 *>(r.norm + e0);
-        const float4 g1 = *reinterpret_cast<const float4 *>(r.norm + e1);
-        y[0] *= f * g0.x;
-        y[1] *= f * g0.y;
-        y[2] *= f * g0.z;
-        y[3] *= f * g0.w;
-        y[4] *= f * g1.x;
-        y[5] *= f * g1.y;
-        y[6] *= f * g1.z;
-        y[7] *= f * g1.w;
+        times(rsqrtf(fmaf(ss, 1.f / D, eps)));
       }
-      if (sub < quads && t < nt) {
-        const float4 c4 = *reinterpret_cast<const float4 *>(&sh_cos[t][4 * sub]);
-        const float4 s4 = *reinterpret_cast<const float4 *>(&sh_sin[t][4 * sub]);
-        const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+      uint64_t z[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float &p = a.halves ? y[i] : y[2 * i], &q = a.halves ? y[4 + i] : y[2 * i + 1];
-          const float x = p;
-          p = x * c[i] - q * s[i];
-          q = q * c[i] + x * s[i];
-        }
-      }
-    }
-    const uint2 b0 = raw ? u[0] : make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
-    const uint2 b1 = raw ? u[1] : make_uint2(pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
-    if (!value) {
-      if (on && r.out) {
-        unsigned char *at = r.out + 2 * ((t0 + t) * r.ot + h * r.oh);
-        *reinterpret_cast<uint2 *>(at + 2 * e0) = b0;
-        *reinterpret_cast<uint2 *>(at + 2 * e1) = b1;
-      }
-    }
-    if (KIND != kNoPages && (key || value)) {
-      const int64_t row = base + (int64_t)h * pg.rows;
-      unsigned char *out = value ? pg.v : pg.k;
-      const int f0 = value ? 8 * sub : e0, f1 = value ? f0 + 4 : e1;
-      if (KIND == DHS_PAGE_BF16) {
-        if (on) {
-          *reinterpret_cast<uint2 *>(out + (row * D + f0) * 2) = b0;
-          *reinterpret_cast<uint2 *>(out + (row * D + f1) * 2) = b1;
-        }
-      } else {
-        uint32_t top = 0u;  // (as bits an infinity or a NaN is the largest)
+      for (int i = 0; i < 4; ++i) z[i] = mul_f32x2(y[i], C[i]);
+      if (turned) {
+        if (HALVES) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+          for (int i = 0; i < 4; ++i) z[i] = fma_f32x2(y[i ^ 2], S[i], z[i]);
+        } else {
 #pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float big = __uint_as_float(top);
-        const bool bad = top >= 0x7F800000u;
-        const float s = (bad || big < kTiny) ? 0.f
-                                             : __fdiv_rn(big, KIND == DHS_PAGE_INT8 ? 127.f : 448.f);
-        uint32_t code[2] = {0u, 0u};
-        if (s > 0.f) {
-          if (raw) quantise<KIND, 8>(w, big, s, code);
-          else codes_of<KIND>(y, __frcp_rn(s), code);
-        }
-        if (on) {
-          *reinterpret_cast<uint32_t *>(out + row * D + f0) = code[0];
-          *reinterpret_cast<uint32_t *>(out + row * D + f1) = code[1];
-          if (sub == 0) (value ? pg.vs : pg.ks)[row] = bad ? __uint_as_float(0x7FC00000u) : s;
+          for (int i = 0; i < 4; ++i) {
+            float p, q;
+            unpack_f32x2(y[i], p, q);
+            z[i] = fma_f32x2(pack_f32x2(q, p), S[i], z[i]);
+          }
         }
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = z[i];
+      float p[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) unpack_f32x2(y[i], p[2 * i], p[2 * i + 1]);
+      b0 = make_uint2(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]));
+      b1 = make_uint2(pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7]));
     }
-    u[0] = next[0];
-    u[1] = next[1];
+    const bool live = on && h < h1;
+    if (live && r.out) {
+      unsigned char *at = r.out + 2 * (tok * r.ot + h * r.oh);
+      *reinterpret_cast<uint2 *>(at + 2 * e0) = b0;
+      *reinterpret_cast<uint2 *>(at + 2 * e1) = b1;
+    }
+    if (KIND == kNoPages || !(key || value)) return;
+    const int64_t row = base + (int64_t)h * pg.rows;
+    unsigned char *out = value ? pg.v : pg.k;
+    if (KIND == DHS_PAGE_BF16) {
+      if (live) {
+        *reinterpret_cast<uint2 *>(out + (row * D + e0) * 2) = b0;
+        *reinterpret_cast<uint2 *>(out + (row * D + e1) * 2) = b1;
+      }
+      return;
+    }
+    float p[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) unpack_f32x2(y[i], p[2 * i], p[2 * i + 1]);
+    uint32_t top = 0u;  // (as bits an infinity or a NaN is the largest)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(p[i]) & 0x7FFFFFFFu);
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float big = __uint_as_float(top);
+    const bool bad = top >= 0x7F800000u;
+    const float s = (bad || big < kTiny) ? 0.f
+                                         : __fdiv_rn(big, KIND == DHS_PAGE_INT8 ? 127.f : 448.f);
+    uint32_t code[2] = {0u, 0u};
+    if (s > 0.f) {
+      if (raw) quantise<KIND, 8>(w, big, s, code);
+      else codes_of<KIND>(p, __frcp_rn(s), code);
+    }
+    if (live) {
+      *reinterpret_cast<uint32_t *>(out + row * D + e0) = code[0];
+      *reinterpret_cast<uint32_t *>(out + row * D + e1) = code[1];
+      if (sub == 0) (value ? pg.vs : pg.ks)[row] = bad ? __uint_as_float(0x7FC00000u) : s;
+    }
+  };
+  for (int h = h0; h < h1; h += U) {
+    if (h > h0) load(h);
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (h + i < h1) finish(h + i, u[i]);
   }
 }
 
@@ -289,30 +312,34 @@ bool rotation_ok(const dhs_rotation *rot, int d, RotateArgs *a) {
 }
 
 int launch(const PageView &pg, RotateArgs &a, int d, int kind, dhs_stream stream) {
-  // enough CTAs to fill the GPU first (heads over several where tokens are few), then more
-  // tokens of a CTA, which share its sines and cosines
-  const int rows_cta = kRoThreads / (d / 8);
-  int64_t per = a.n_tok / (8 * 152);
-  a.per_cta = (int)(per < 1 ? 1 : (per > kRoTok ? kRoTok : per));
-  const int64_t grid = (a.n_tok + a.per_cta - 1) / a.per_cta;
-  const int64_t rows = (int64_t)a.per_cta * (a.q.heads + a.k.heads + a.v.heads);
-  const int64_t split = std::max<int64_t>(
-      1, std::min((rows + rows_cta - 1) / rows_cta, (4 * 152 + grid - 1) / grid));
+  // Chunks as long as the GPU stays full (their sines, cosines and lookups are made once),
+  // one row each where tokens are few: 8 CTAs' lanes a row on each of 152 SMs.
+  const int64_t heads = (int64_t)a.q.heads + a.k.heads + a.v.heads;
+  const int64_t fill = a.n_tok * heads / (152 * 8 * (kRoThreads / (d / 8)));
+  a.chunk = (int)std::max<int64_t>(std::min<int64_t>(std::max<int64_t>(fill, 1), 32),
+                                   (heads + 59999) / 60000);
+  auto chunks = [&](int n) { return (n + a.chunk - 1) / a.chunk; };
+  a.qc = chunks(a.q.heads);
+  a.kc = chunks(a.k.heads);
+  const int tok = kRoThreads / (d / 8);
+  const dim3 grid((unsigned)((a.n_tok + tok - 1) / tok),
+                  (unsigned)(a.qc + a.kc + chunks(a.v.heads)));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  auto go = [&](auto kern) {
-    return launch_prio(kern, dim3((unsigned)grid, (unsigned)split), dim3(kRoThreads), 0, s, pg, a);
+  auto go = [&](auto dim, auto k) {
+    constexpr int D = decltype(dim)::value, K = decltype(k)::value;
+    return a.halves ? launch_prio(k_rotate<D, K, true>, grid, dim3(kRoThreads), 0, s, pg, a)
+                    : launch_prio(k_rotate<D, K, false>, grid, dim3(kRoThreads), 0, s, pg, a);
   };
-  cudaError_t e;
-  switch ((d == 128 ? 4 : 0) + kind) {
-    case -1: e = go(k_rotate<64, kNoPages>); break;
-    case 0: e = go(k_rotate<64, DHS_PAGE_BF16>); break;
-    case 1: e = go(k_rotate<64, DHS_PAGE_INT8>); break;
-    case 2: e = go(k_rotate<64, DHS_PAGE_E4M3>); break;
-    case 3: e = go(k_rotate<128, kNoPages>); break;
-    case 4: e = go(k_rotate<128, DHS_PAGE_BF16>); break;
-    case 5: e = go(k_rotate<128, DHS_PAGE_INT8>); break;
-    default: e = go(k_rotate<128, DHS_PAGE_E4M3>); break;
-  }
+  auto kinds = [&](auto dim) {
+    switch (kind) {
+      case DHS_PAGE_BF16: return go(dim, std::integral_constant<int, DHS_PAGE_BF16>());
+      case DHS_PAGE_INT8: return go(dim, std::integral_constant<int, DHS_PAGE_INT8>());
+      case DHS_PAGE_E4M3: return go(dim, std::integral_constant<int, DHS_PAGE_E4M3>());
+      default: return go(dim, std::integral_constant<int, kNoPages>());
+    }
+  };
+  const cudaError_t e = d == 128 ? kinds(std::integral_constant<int, 128>())
+                                 : kinds(std::integral_constant<int, 64>());
   if (e != cudaSuccess) {
     cudaGetLastError();
     return DHS_ERR_CUDA;

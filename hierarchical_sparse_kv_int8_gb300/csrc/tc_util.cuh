@@ -143,7 +143,7 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
-// Two fp32 numbers in one 64-bit register pair, and a * b + c, a + b of such pairs,
+// Two fp32 numbers in one 64-bit register pair, and a * b + c, a + b, a * b of such pairs,
 // each rounded to nearest.  (Kept packed: packing around every instruction costs
 // more moves than it saves.)
 __device__ __forceinline__ uint64_t pack_f32x2(float x, float y) {
@@ -162,6 +162,11 @@ __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c
 __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 // The largest of three (a NaN only if all are).
