@@ -9,6 +9,7 @@ library its tensors must stay alive until the stream has passed it.
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional
 
 import torch
@@ -43,6 +44,10 @@ class _Heads(ctypes.Structure):
         ("heads", ctypes.c_int32)]
 
 
+_HEADS = struct.Struct("=QQQqqqqi4x")  # its bytes, which cost a third of its object
+assert _HEADS.size == ctypes.sizeof(_Heads)
+
+
 # A decode step makes several calls of a few microseconds each, so what a call does on
 # the host counts: the current stream's handle and device without torch's wrappers, no
 # array of strides for contiguous rows, no context where the device is the current one
@@ -59,9 +64,15 @@ except ImportError:
 _BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
 
 
+_loaded = None
+
+
 def _lib():
-    from . import load
-    return load()
+    global _loaded
+    if _loaded is None:
+        from . import load
+        _loaded = load()
+    return _loaded
 
 
 def _raise(code, what):
@@ -103,17 +114,26 @@ def _rows(t, name, index):
     return n, h, d, (st if n > 1 else h * d), (sh if h > 1 else d)
 
 
+def _strides(name, t, index):
+    """Token and head stride of a packed bf16 tensor; like _rows, sooner for the usual one."""
+    if t.dtype is _BF16 and t.is_contiguous() and t.get_device() == index and t.dim() == 3:
+        _, h, d = t.shape
+        return h * d, d
+    return _rows(t, name, index)[3:]
+
+
 def _heads(name, x, out, norm, index):
-    """Tokens, elements and the description of a tensor's heads and where they go."""
-    n, h, d, xt, xh = _rows(x, name, index)
-    ot = oh = 0
+    """A dhs_heads: a tensor's heads, [tokens, heads, head_dim], and where they go."""
+    xt, xh = _strides(name, x, index)
+    shape, at, ot, oh = x.shape, None, 0, 0
     if out is not None:
-        if out.shape != x.shape:
-            raise ValueError("%s_out: %s expected, not %s" % (name, tuple(x.shape), tuple(out.shape)))
-        _, _, _, ot, oh = _rows(out, name + "_out", index)
-    return n, d, _Heads(x.data_ptr(), None if out is None else out.data_ptr(),
-                        None if norm is None else _plain(norm, name + "_norm", _F32, (d,), index),
-                        xt, xh, ot, oh, h)
+        if out.shape != shape:
+            raise ValueError("%s_out: %s expected, not %s" % (name, tuple(shape), tuple(out.shape)))
+        ot, oh = _strides(name + "_out", out, index)
+        at = out.data_ptr()
+    return _HEADS.pack(x.data_ptr(), at or 0,
+                       0 if norm is None else _plain(norm, name + "_norm", _F32, shape[2:], index),
+                       xt, xh, ot, oh, shape[1])
 
 
 def _turns(rotation, index):
@@ -211,16 +231,12 @@ def rotate(q, k, positions, rotation, q_out, k_out, q_norm=None, k_norm=None, ep
     if ix < 0 or _current_device() != ix:
         with _on(ix):
             return rotate(q, k, positions, rotation, q_out, k_out, q_norm, k_norm, eps, stream)
-    hq = hk = None
-    n, d = some.shape[0], some.shape[-1]
-    if q is not None:
-        n, d, hq = _heads("q", q, q_out, q_norm, ix)
-    if k is not None:
-        nk, dk, hk = _heads("k", k, k_out, k_norm, ix)
-        if (nk, dk) != (n, d):
-            raise ValueError("k: [%d, kv_heads, %d] expected, not %s" % (n, d, tuple(k.shape)))
-    rc = _lib().dhs_rotate(_turns(rotation, ix), None if hq is None else ctypes.byref(hq),
-                           None if hk is None else ctypes.byref(hk), eps, d, n,
+    hq = None if q is None else _heads("q", q, q_out, q_norm, ix)
+    hk = None if k is None else _heads("k", k, k_out, k_norm, ix)
+    n, _, d = some.shape
+    if hk is not None and (k.shape[0] != n or k.shape[2] != d):
+        raise ValueError("k: [%d, kv_heads, %d] expected, not %s" % (n, d, tuple(k.shape)))
+    rc = _lib().dhs_rotate(_turns(rotation, ix), hq, hk, eps, d, n,
                            None if positions is None else _plain(positions, "positions", _I32, (n,), ix),
                            _raw(stream, ix))
     if rc:
@@ -308,20 +324,21 @@ class PageCache:
             with _on(ix):
                 return self.append(q, k, v, cu, seq_lens, page_table, q_out, rotation, q_norm, k_norm,
                                    eps, positions, k_out, stream)
-        tok, d, hk = _heads("k", k, k_out, k_norm, ix)
-        tv, hv, dv, vt, vh = _rows(v, "v", ix)
-        if d != self.head_dim or hk.heads != self.kv_heads or (tv, hv, dv) != (tok, hk.heads, d):
+        hk = _heads("k", k, k_out, k_norm, ix)
+        vt, vh = _strides("v", v, ix)
+        tok, h, d = k.shape
+        if d != self.head_dim or h != self.kv_heads or v.shape != k.shape:
             raise ValueError("k and v: [tokens, %d, %d] expected, not %s and %s" % (
                 self.kv_heads, self.head_dim, tuple(k.shape), tuple(v.shape)))
         hq = None
         if q is not None:
-            nq, dq, hq = _heads("q", q, q_out, q_norm, ix)
-            if (nq, dq) != (tok, d):
+            hq = _heads("q", q, q_out, q_norm, ix)
+            if q.shape[0] != tok or q.shape[2] != d:
                 raise ValueError("q: [%d, q_heads, %d] expected, not %s" % (tok, d, tuple(q.shape)))
         n = seq_lens.shape[0]
         rc = self._lib.dhs_page_append(
-            self._ref, _turns(rotation, ix), None if hq is None else ctypes.byref(hq),
-            ctypes.byref(hk), v.data_ptr(), _Strides2(vt, vh), eps, tok,
+            self._ref, _turns(rotation, ix), hq, hk, v.data_ptr(),
+            None if vt == h * d and vh == d else _Strides2(vt, vh), eps, tok,
             None if positions is None else _plain(positions, "positions", _I32, (tok,), ix),
             _plain(cu, "cu", _I32, (n + 1,), ix), _plain(seq_lens, "seq_lens", _I32, (n,), ix),
             _table(page_table, n, ix), page_table.shape[1], n, self._err, _raw(stream, ix))
