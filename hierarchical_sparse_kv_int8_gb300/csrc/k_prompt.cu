@@ -49,9 +49,8 @@
 // without pauses): an item costs some 3 tiles' time besides its tiles (the first S, the
 // rows' writing).
 #include "pages_internal.cuh"
-#include "tc_util.cuh"
+#include "attn_tc.cuh"
 
-#include <cuda.h>
 #include <math_constants.h>
 
 #include <algorithm>
@@ -118,68 +117,6 @@ struct PrCfg {
   static constexpr int SMEM = OFF_ITEM + 2 * 64;
 };
 static_assert(PrCfg<128>::SMEM <= 227 * 1024, "shared memory of the prompt kernel");
-
-// The MMAs of this file are issued by a whole warp whose elected lane carries
-// them out: the operands are then warp-uniform values that the compiler keeps
-// where the instruction reads them.  (Issued from a branch of one lane, each MMA
-// took over 70 cycles of moves, more than the 64 it runs for.)
-// D[tmem] (+)= A[smem] * B[smem]
-__device__ __forceinline__ void warp_mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                         uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred e, p;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// D[tmem] (+)= A[tmem] * B[smem]: A's 128 rows are lanes, two elements a column.
-__device__ __forceinline__ void warp_mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                            uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred e, p;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void warp_commit(void *bar) {
-  asm volatile(
-      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
-          smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z,
-                                            void *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-      "[%1, {%2, %3, %4}], [%5];\n" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-      : "memory");
-}
-
-__device__ __forceinline__ void tma_prefetch(const CUtensorMap *map) {
-  asm volatile("prefetch.tensormap [%0];\n" ::"l"(map) : "memory");
-}
-
-// Barrier `id` over `count` threads that also says whether any of them had `on`.
-__device__ __forceinline__ bool named_or(int id, int count, bool on) {
-  uint32_t r;
-  __syncwarp();
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 q, %3, 0;\n barrier.red.or.pred p, %1, %2, q;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(r)
-      : "r"(id), "r"(count), "r"((uint32_t)on)
-      : "memory");
-  return r != 0;
-}
-
-// Time in units of 1.024 us, of which the low 32 bits last for 73 minutes.
-__device__ __forceinline__ uint32_t global_us() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %globaltimer;\n" : "=l"(t));
-  return (uint32_t)(t >> 10);
-}
 
 // What calls without a record of their own find, one for each device.
 __device__ int32_t device_record[2];
@@ -900,28 +837,6 @@ uint32_t prompt_wait_us(int64_t n_k, int32_t n_seqs) {
   return (uint32_t)std::min<uint64_t>(
       least + least * (uint64_t)(n_k / kPrN + 1) / 100000 + least * (uint64_t)n_seqs / 400000,
       1800000000u);
-}
-
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                 const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                 const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// The driver's tensor-map encoder (looked up once), or nullptr.
-EncodeTiled encoder() {
-  static std::atomic<void *> known{nullptr};
-  void *f = known.load(std::memory_order_acquire);
-  if (!f) {
-    cudaDriverEntryPointQueryResult res;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &res) != cudaSuccess ||
-        res != cudaDriverEntryPointSuccess) {
-      cudaGetLastError();
-      return nullptr;
-    }
-    known.store(f, std::memory_order_release);
-  }
-  return reinterpret_cast<EncodeTiled>(f);
 }
 
 // The device's record (its address asked for once; chosen in the kernel it would cost

@@ -383,6 +383,42 @@ class PageCache:
         if rc:
             _raise(rc, "dhs_page_attend")
 
+    def chunk_workspace(self, n_tokens: int, n_seqs: int, q_heads: int):
+        """A new workspace for :meth:`attend_chunk` calls of these sizes.  Calls that may
+        overlap on the GPU (other streams, other graphs) each need their own."""
+        with _on(self._index):
+            nbytes = self._lib.dhs_page_chunk_workspace(self._ref, n_tokens, n_seqs, q_heads)
+        if nbytes < 0:
+            raise ValueError("attend_chunk does not serve n_tokens=%d, n_seqs=%d, q_heads=%d"
+                             % (n_tokens, n_seqs, q_heads))
+        return torch.empty(max(16, nbytes), dtype=torch.uint8, device=self.device)
+
+    def attend_chunk(self, q, cu, seq_lens, page_table, out, workspace, lse=None, window: int = 0,
+                     sinks: int = 0, scale: float = 0.0, stream=None):
+        """Attention of packed new tokens over the cache (dhs_page_chunk): ``q`` and ``out``
+        [tokens, q_heads, head_dim].  With a ``window`` a token sees that many positions up to
+        its own, and the first ``sinks`` ones."""
+        ix = self._index
+        if _current_device() != ix:
+            with _on(ix):
+                return self.attend_chunk(q, cu, seq_lens, page_table, out, workspace, lse, window,
+                                         sinks, scale, stream)
+        qt, qh = _strides("q", q, ix)
+        tok, hq, d = q.shape
+        if d != self.head_dim:
+            raise ValueError("q: [tokens, q_heads, %d] expected, not %s" % (self.head_dim, tuple(q.shape)))
+        n = seq_lens.shape[0]
+        space, nbytes = _space(workspace, ix)
+        rc = self._lib.dhs_page_chunk(
+            self._ref, q.data_ptr(), None if qt == hq * d and qh == d else _Strides2(qt, qh), tok,
+            _plain(cu, "cu", _I32, (n + 1,), ix), _plain(seq_lens, "seq_lens", _I32, (n,), ix),
+            _table(page_table, n, ix), page_table.shape[1], n, hq, window, sinks, scale,
+            _plain(out, "out", _BF16, q.shape, ix),
+            None if lse is None else _plain(lse, "lse", _F32, (tok, hq), ix), space, nbytes,
+            self._err, _raw(stream, ix))
+        if rc:
+            _raise(rc, "dhs_page_chunk")
+
     def check(self, stream=None):
         """Raises DhsError if a call on this cache found a bad page or length."""
         check_errors(self.errors, stream)

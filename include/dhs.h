@@ -596,6 +596,7 @@ int64_t dhs_policy_free_pages(const dhs_policy *p);
  *   dhs_prompt_attend  the prompt's causal attention, packed sequences
  *   dhs_page_write     the new tokens' keys and values into the pages
  *   dhs_page_attend    the newest 1-8 tokens of every sequence over the pages
+ *   dhs_page_chunk     any number of new tokens of every sequence over the pages
  *   dhs_page_read      cached rows back, for the next chunk of a long prompt
  * and, where the layer's queries and keys still lack their norm and rotation,
  *   dhs_rotate         both, for every head, before dhs_prompt_attend
@@ -755,6 +756,34 @@ int dhs_page_attend(const dhs_pages *pages, const void *q, const int32_t *q_lens
 /* Bytes the call needs on the current device, -1 for arguments it refuses. */
 int64_t dhs_page_attend_workspace(const dhs_pages *pages, int32_t n_seqs, int32_t q_len,
                                   int32_t q_heads);
+
+/* Attention of a chunk of new tokens of every sequence over its cached rows, packed as
+ * dhs_page_write takes them: token cu[i] + u is position seq_lens[i] - (cu[i + 1] - cu[i]) + u
+ * (its own row, and the chunk's others, are written first).  Any numbers of tokens go
+ * together: chunks of prompts, whole prompts, and sequences that decode one token.
+ *   q          device bf16 [n_tokens][q_heads][head_dim], 16-byte aligned.  q_strides: host
+ *              int64[2], in elements, of a token and a head, multiples of 8; NULL: contiguous
+ *   window     0: a token at position p sees positions 0 .. p; else p - window + 1 .. p
+ *   sinks      with a window: and positions 0 .. sinks - 1, where they are not after p
+ *   scale      as in dhs_page_attend
+ *   out        device bf16 [n_tokens][q_heads][head_dim], 16-byte aligned
+ *   lse        device fp32 [n_tokens][q_heads] natural-log sum-exp, or NULL
+ *   workspace  as in dhs_page_attend, of dhs_page_chunk_workspace() bytes
+ * A token that sees no position has out = 0 and lse = -inf.  Rows of padding tokens (before
+ * cu[0] or from cu[n_seqs] on) and of sequences whose offsets or length are out of range are
+ * left as they were; positions on a page outside the cache are left out.  Page table entries
+ * of which no new token of the sequence sees a position are not read, so pages behind the
+ * window may be given away.  What a token does not see (infinities, NaN) never reaches it;
+ * scales of an 8-bit cache as in dhs_page_attend; with the same lengths the result repeats bit
+ * by bit.  n_tokens is at most 2^31 - 257, q_heads / kv_heads at most 128. */
+int dhs_page_chunk(const dhs_pages *pages, const void *q, const int64_t *q_strides,
+                   int64_t n_tokens, const int32_t *cu, const int32_t *seq_lens,
+                   const int32_t *page_table, int32_t table_width, int32_t n_seqs, int32_t q_heads,
+                   int32_t window, int32_t sinks, float scale, void *out, float *lse,
+                   void *workspace, int64_t workspace_bytes, int32_t *err, dhs_stream stream);
+/* Bytes the call needs on the current device, -1 for arguments it refuses. */
+int64_t dhs_page_chunk_workspace(const dhs_pages *pages, int64_t n_tokens, int32_t n_seqs,
+                                 int32_t q_heads);
 
 /* Causal attention of packed sequences.  Sequence i has queries cu_q[i] ..
  * cu_q[i + 1] - 1 and keys cu_k[i] .. cu_k[i + 1] - 1; its queries are its last
