@@ -136,6 +136,8 @@ _SIGS.update({
                         ctypes.c_int),
     "dhs_page_attend": ([_P] * 5 + [_I32] * 4 + [ctypes.c_float, _P, _P, _P, _I64, _P, _P],
                         ctypes.c_int),
+    "dhs_page_attend_window": ([_P] * 5 + [_I32] * 6 + [ctypes.c_float, _P, _P, _P, _I64, _P, _P],
+                               ctypes.c_int),
     "dhs_page_attend_workspace": ([_P, _I32, _I32, _I32], _I64),
     "dhs_page_chunk": ([_P] * 3 + [_I64] + [_P] * 3 + [_I32] * 5 +
                        [ctypes.c_float, _P, _P, _P, _I64, _P, _P], ctypes.c_int),

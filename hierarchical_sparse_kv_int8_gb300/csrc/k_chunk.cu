@@ -288,7 +288,7 @@ struct ChunkSchedule {
         int ns = 0, w0 = 0;  // tiles of the sinks, the window's first
         if (a.window > 0) {
           ns = (int)(((int64_t)a.sinks + kChN - 1) / kChN);
-          w0 = max(ns, max(0, p0 - a.window + 1) / kChN);
+          w0 = max(ns, (int)(max((int64_t)0, (int64_t)p0 - a.window + 1) / kChN));
         }
         auto listed = [&](int e) { return min(e, ns) + max(0, e - w0); };
         const int l0 = listed(e0), nt = listed(e1);
@@ -807,7 +807,7 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
         const int tok = i * a.tpt + tloc, ntok = it.ntok, p0 = it.p0;
         lim0 = (tloc < a.tpt && tok < ntok ? p0 + tok + 1 : 0) - hg * kChH;
         least = p0 + i * a.tpt + 1;
-        if (WIN) wend = p0 + min((i + 1) * a.tpt, ntok) - a.window;
+        if (WIN) wend = max(p0, -1024) + min((i + 1) * a.tpt, ntok) - a.window;
       }
       float m_run = -CUDART_INF_F, l = 0.f;
       for (int n = 0; n < ni; ++n, ++sn) {
@@ -1233,7 +1233,7 @@ extern "C" int dhs_page_chunk(const dhs_pages *pages, const void *q, const int64
   a.tpt = kChM / a.G;
   a.box = 1;
   while (a.box < 32 && a.pg.rows % (2 * a.box) == 0) a.box *= 2;
-  a.window = window;
+  a.window = std::min(window, INT32_MAX - 1024);  // (no sequence is longer)
   a.sinks = sinks;
   a.cap = window > 0 ? std::min<int64_t>((int64_t)window + sinks + 2 * a.tpt + 2 * kChN, (int64_t)1 << 31)
                      : (int64_t)1 << 31;

@@ -361,27 +361,34 @@ class PageCache:
         return torch.empty(max(16, nbytes), dtype=torch.uint8, device=self.device)
 
     def attend(self, q, seq_lens, page_table, out, workspace, lse=None, q_lens=None,
-               scale: float = 0.0, stream=None):
+               scale: float = 0.0, stream=None, window: int = 0, sinks: int = 0):
         """Attention of the newest tokens over the cache (dhs_page_attend):
-        ``q`` and ``out`` [n_seqs, q_len, q_heads, head_dim]."""
+        ``q`` and ``out`` [n_seqs, q_len, q_heads, head_dim].  With a ``window`` a token sees
+        that many positions up to its own, and the first ``sinks`` ones
+        (dhs_page_attend_window)."""
         ix, shape = self._index, q.shape
         if _current_device() != ix:
             with _on(ix):
-                return self.attend(q, seq_lens, page_table, out, workspace, lse, q_lens, scale, stream)
+                return self.attend(q, seq_lens, page_table, out, workspace, lse, q_lens, scale, stream,
+                                   window, sinks)
         if len(shape) != 4 or shape[3] != self.head_dim:
             raise ValueError("q: [n_seqs, q_len, q_heads, %d] expected, not %s"
                              % (self.head_dim, tuple(shape)))
         n, qn, hq, _ = shape
         space, nbytes = _space(workspace, ix)
-        rc = self._lib.dhs_page_attend(
+        if window or sinks:
+            fn, what, extra = self._lib.dhs_page_attend_window, "dhs_page_attend_window", (window, sinks)
+        else:
+            fn, what, extra = self._lib.dhs_page_attend, "dhs_page_attend", ()
+        rc = fn(
             self._ref, _plain(q, "q", _BF16, shape, ix),
             None if q_lens is None else _plain(q_lens, "q_lens", _I32, (n,), ix),
             _plain(seq_lens, "seq_lens", _I32, (n,), ix), _table(page_table, n, ix),
-            page_table.shape[1], n, qn, hq, scale, _plain(out, "out", _BF16, shape, ix),
+            page_table.shape[1], n, qn, hq, *extra, scale, _plain(out, "out", _BF16, shape, ix),
             None if lse is None else _plain(lse, "lse", _F32, (n, qn, hq), ix), space, nbytes,
             self._err, _raw(stream, ix))
         if rc:
-            _raise(rc, "dhs_page_attend")
+            _raise(rc, what)
 
     def chunk_workspace(self, n_tokens: int, n_seqs: int, q_heads: int):
         """A new workspace for :meth:`attend_chunk` calls of these sizes.  Calls that may

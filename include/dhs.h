@@ -753,7 +753,16 @@ int dhs_page_attend(const dhs_pages *pages, const void *q, const int32_t *q_lens
                     int32_t n_seqs, int32_t q_len, int32_t q_heads, float scale, void *out,
                     float *lse, void *workspace, int64_t workspace_bytes, int32_t *err,
                     dhs_stream stream);
-/* Bytes the call needs on the current device, -1 for arguments it refuses. */
+/* The same with a sliding window: a query at position p sees positions p - window + 1 .. p
+ * (window >= 1) and 0 .. sinks - 1.  Page table entries of which no query of the sequence
+ * sees a position are not read, so pages behind the window may be given away. */
+int dhs_page_attend_window(const dhs_pages *pages, const void *q, const int32_t *q_lens,
+                           const int32_t *seq_lens, const int32_t *page_table,
+                           int32_t table_width, int32_t n_seqs, int32_t q_len, int32_t q_heads,
+                           int32_t window, int32_t sinks, float scale, void *out, float *lse,
+                           void *workspace, int64_t workspace_bytes, int32_t *err,
+                           dhs_stream stream);
+/* Bytes either call needs on the current device, -1 for arguments it refuses. */
 int64_t dhs_page_attend_workspace(const dhs_pages *pages, int32_t n_seqs, int32_t q_len,
                                   int32_t q_heads);
 

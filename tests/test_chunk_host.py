@@ -41,3 +41,22 @@ def test_chunk_refusals(dhs):
     p = ctypes.byref(_pages())
     for bad in ((-1, 2, 8), (4, -1, 8), (4, 2, 0), (4, 2, 7), (4, 2, 258), ((1 << 31) - 256, 2, 8)):
         assert lib.dhs_page_chunk_workspace(p, *bad) == -1, bad
+
+
+def _window(lib, p=None, q=A, ql=None, lens=A, table=A, width=3, seqs=2, q_len=2, hq=8, window=9, sinks=0,
+            scale=0.0, out=A, lse=A, ws=A, nbytes=1 << 40, err=None):
+    return lib.dhs_page_attend_window(ctypes.byref(p or _pages()), q, ql, lens, table, width, seqs, q_len, hq,
+                                      window, sinks, scale, out, lse, ws, nbytes, err, None)
+
+
+def test_window_refusals(dhs):
+    lib = dhs.load()
+    for b in BAD_PAGES:
+        assert _window(lib, _pages(**b)) == INVALID, b
+    for b in [dict(q=None), dict(q=A + 8), dict(ql=A + 2), dict(lens=None), dict(lens=A + 2),
+              dict(table=None), dict(width=-1), dict(seqs=-1), dict(q_len=0), dict(q_len=9), dict(hq=7),
+              dict(hq=0), dict(hq=2 * 65), dict(window=0), dict(window=-3), dict(sinks=-1),
+              dict(scale=-1.0), dict(scale=math.nan), dict(out=None), dict(out=A + 8), dict(lse=A + 1),
+              dict(ws=None), dict(ws=A + 8), dict(nbytes=-1), dict(err=A + 2)]:
+        assert _window(lib, **b) == INVALID, b
+    assert _window(lib, seqs=0, q=None, lens=None) == 0

@@ -28,6 +28,17 @@ def _window_attend(oracle, q, k, v, scale, window, sinks):
                  for j in range(4))
 
 
+def give_away(pc, new, window, sinks):
+    """Pages of which no new token sees a position leave the table."""
+    table = pc.table.cpu()
+    for i, (a, t) in enumerate(zip(new, pc.lens)):
+        for g in range(-(-t // pc.rows)):
+            lo, hi = g * pc.rows, min(t, (g + 1) * pc.rows)   # its positions
+            if lo >= sinks and hi - 1 <= t - a - window:
+                table[i, g] = -9 if g % 2 else pc.n_pages + 5
+    pc.table = table.cuda()
+
+
 def _chunk(torch, dhs, pc, kv, new, hq, window=0, sinks=0, scale=0.0, seed=5, qmul=1.0, pad=(0, 0),
            strided=False, workspace=None, lse=True, check=True):
     from oracle import dense_oracle as oracle
@@ -72,4 +83,6 @@ def test_chunk_window(torch, dhs, kind, window, sinks):
     lens, new = [600, 700, 1, 130, 300], [200, 1, 1, 130, 9]
     d, hkv, hq, rows = (128, 1, 8, 16) if window % 2 else (64, 2, 6, 48)
     pc = Paged(torch, dhs, lens, rows, hkv, d, kind)
-    _chunk(torch, dhs, pc, pc.fill(), new, hq, window=window, sinks=sinks)
+    kv = pc.fill()
+    give_away(pc, new, window, sinks)
+    _chunk(torch, dhs, pc, kv, new, hq, window=window, sinks=sinks)

@@ -1,0 +1,134 @@
+"""Attention of the newest tokens with a sliding window and first positions that stay visible,
+on the GPU against the fp64 oracle (tolerances as for the attention without one)."""
+import math
+
+import numpy as np
+import pytest
+
+from test_gpu_chunk import _window_attend, give_away
+from test_gpu_dense import BF16, E4M3, INT8, KINDS, Paged, _close, _np, dhs, torch  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def _attend(torch, pc, kv, q_len, hq, window, sinks, q_lens=None, seed=5, qmul=1.0, q=None, workspace=None):
+    from oracle import dense_oracle as oracle
+    n, d = len(pc.lens), pc.d
+    g = torch.Generator().manual_seed(seed)
+    if q is None:
+        q = (torch.randn((n, q_len, hq, d), generator=g) * qmul).bfloat16().cuda()
+    out = torch.full_like(q, 77.0)
+    lse = torch.full((n, q_len, hq), 77.0, dtype=torch.float32, device="cuda")
+    ws = pc.cache.attend_workspace(n, q_len, hq) if workspace is None else workspace
+    ql = None if q_lens is None else torch.tensor(q_lens, dtype=torch.int32).cuda()
+    pc.cache.attend(q, pc.seq_lens, pc.table, out, ws, lse=lse, q_lens=ql, window=window, sinks=sinks)
+    pc.cache.check()
+    for i in range(n):
+        nq = q_len if q_lens is None else q_lens[i]
+        want = _window_attend(oracle, _np(q[i, :nq]), kv[i][0], kv[i][1], 1 / math.sqrt(d), window, sinks)
+        vmax = np.nanmax(np.abs(kv[i][1])) if pc.kind != BF16 and pc.lens[i] else 0.0
+        if nq:
+            _close(_np(out[i, :nq]), _np(lse[i, :nq]), want, d, max(1, pc.lens[i]), vmax)
+        assert torch.all(out[i, nq:] == 77) and torch.all(lse[i, nq:] == 77)
+    return out, lse
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("hq,hkv,d,rows,q_len", [
+    (8, 1, 128, 64, 1), (16, 1, 128, 16, 4), (6, 2, 64, 7, 8), (5, 1, 64, 64, 8), (12, 1, 128, 100, 5),
+    (64, 1, 128, 32, 2), (3, 3, 128, 1, 2)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (3, 2), (64, 4), (130, 0), (257, 65), (5000, 3)])
+def test_window(torch, dhs, kind, hq, hkv, d, rows, q_len, window, sinks):
+    lens = [0, 1, 5, 64, 130, 700, 1025]
+    pc = Paged(torch, dhs, lens, rows, hkv, d, kind)
+    kv = pc.fill()
+    give_away(pc, [q_len] * len(lens), window, sinks)
+    _attend(torch, pc, kv, q_len, hq, window, sinks)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_window_fewer_queries_than_room_and_many_sequences(torch, dhs, kind):
+    lens = [(i * 37) % 400 for i in range(70)]
+    q_lens = [i % 5 for i in range(70)]
+    pc = Paged(torch, dhs, lens, 16, 2, 64, kind)
+    kv = pc.fill()
+    give_away(pc, [4] * 70, 50, 3)
+    _attend(torch, pc, kv, 4, 8, 50, 3, q_lens=q_lens)
+
+
+def test_window_of_a_long_sequence(torch, dhs):
+    pc = Paged(torch, dhs, [70000, 33], 64, 1, 128, INT8)
+    kv = pc.fill()
+    _attend(torch, pc, kv, 1, 16, 2147483647, 2147483647)
+    give_away(pc, [1, 1], 4096, 4)      # (from here on the rest is not there)
+    _attend(torch, pc, kv, 1, 16, 4096, 4)
+
+
+@pytest.mark.parametrize("window,sinks", [(3, 0), (3, 1), (70, 2), (128, 0)])
+@pytest.mark.parametrize("q_len", [1, 4, 8])
+def test_window_edges_hide_what_is_not_finite(torch, dhs, window, sinks, q_len):
+    """bf16: every position around the window's edges and the sinks' end in turn holds infinities
+    and NaN; the queries that see it get them, the others nothing."""
+    from oracle import dense_oracle as oracle
+    t, hq, d, rows = 300, 4, 64, 16
+    first = t - q_len
+    spots = sorted({p for p in list(range(first - window - 1, first - window + q_len + 2)) +
+                    list(range(first - 1, t)) + [0, 1, 2, 3] if 0 <= p < t})
+    for p in spots:
+        pc = Paged(torch, dhs, [t], rows, 1, d, BF16)
+        kv = pc.fill()
+        page = int(pc.table[0, p // rows])
+        for c, row in ((math.inf, 3), (-math.inf, 9), (math.nan, 20)):
+            pc.cache.v[page, 0, p % rows, row] = c
+            kv[0][1][p, 0, row] = c
+        _attend(torch, pc, kv, q_len, hq, window, sinks)
+        pc.cache.k[page, 0, p % rows] = math.nan     # now the scores as well
+        kv[0][0][p] = math.nan
+        q = torch.randn((1, q_len, hq, d), generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+        out = torch.empty_like(q)
+        pc.cache.attend(q, pc.seq_lens, pc.table, out, pc.cache.attend_workspace(1, q_len, hq), window=window,
+                        sinks=sinks)
+        for j in range(q_len):
+            pos = first + j
+            seen = p <= pos and (p > pos - window or p < sinks)
+            assert bool(torch.isnan(out[0, j]).all()) == seen, (p, j)
+            if not seen:
+                want = _window_attend(oracle, _np(q[0, :j + 1]), kv[0][0][:pos + 1], kv[0][1][:pos + 1],
+                                      1 / math.sqrt(d), window, sinks)
+                _close(_np(out[0, j:j + 1]), None, [x[j:j + 1] for x in want], d, t)
+
+
+@pytest.mark.parametrize("kind", [INT8, E4M3])
+@pytest.mark.parametrize("hq,d", [(2, 128), (8, 64), (16, 128)])
+def test_window_large_scales_that_some_queries_do_not_see(torch, dhs, kind, hq, d):
+    """A value's scale 2^20 times the others', or NaN, at either edge of the window: rows that do
+    not see it keep their precision."""
+    t, rows, q_len, window, sinks = 333, 16, 8, 100, 2
+    first = t - q_len
+    for p in (first - window, first - window + 1, first - window + 4, first - window + q_len - 1, t - window,
+              first, first + 3, t - 1, 1):
+        for s in (2.0 ** 14, math.nan):
+            pc = Paged(torch, dhs, [t], rows, 1, d, kind)
+            kv = pc.fill()
+            page = int(pc.table[0, p // rows])
+            if s == s:
+                kv[0][1][p] *= s / float(pc.cache.v_scale[page, 0, p % rows])
+            else:
+                kv[0][1][p] = s
+            pc.cache.v_scale[page, 0, p % rows] = s
+            from oracle import dense_oracle as oracle
+            q = torch.randn((1, q_len, hq, d), generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+            out = torch.empty_like(q)
+            pc.cache.attend(q, pc.seq_lens, pc.table, out, pc.cache.attend_workspace(1, q_len, hq),
+                            window=window, sinks=sinks)
+            pc.cache.check()
+            for j in range(q_len):
+                pos = first + j
+                keep = [x for x in range(pos + 1) if x > pos - window or x < sinks]
+                want = oracle.attend(_np(q[0, j:j + 1]), kv[0][0][keep], kv[0][1][keep], 1 / math.sqrt(d))
+                seen = p in keep
+                if seen and s != s:
+                    assert torch.isnan(out[0, j]).all(), (p, j)
+                    continue
+                vmax = np.abs(kv[0][1][keep]).max()
+                _close(_np(out[0, j:j + 1]), None, want, d, t, vmax)
