@@ -16,17 +16,17 @@
 // the products, the softmax and its bounded waits are those of the prompt kernel, and so are
 // their reasons.)
 //
-// Pages.  A tile of 128 positions comes in four quarters of 32, each in boxes of the largest
-// power of two that divides the page's rows (32 at most): a box lies in one page, whichever page
-// size there is.  A lane looks up the page of each position; a box of which no position
+// Pages.  A tile of 128 positions comes in boxes of the largest power of two that divides the
+// page's rows: a box lies in one page, whichever page size there is.  A box of which no position
 // is wanted, or whose page is not in the cache, is fetched from beyond the cache's end, which
 // TMA fills with zeros, and so nothing is read that the page table does not name.
 //
-// bf16: the boxes go straight into the 128-byte-swizzled tiles that the MMAs read (warp 17);
-// warps 18-19 set values to 0 that are not finite and that some row does not see (0 times an
-// infinity is not 0), and the rows that see them get them added at the end.
-// 8 bits: warp 18 fetches the codes of keys and warp 19 those of values into rings of
-// quarters, and they turn them into bf16, exactly, in the MMAs' tiles.  A key's scale
+// bf16: the boxes go straight into the 128-byte-swizzled tiles that the MMAs read (warps 17
+// and 19: an issued copy takes a warp some 55 cycles); warp 18 sets values to 0 that are not
+// finite and that some row does not see (0 times an infinity is not 0), and the rows that see
+// them get them added at the end.
+// 8 bits: three warps fetch the codes of keys and three those of values, and turn them into
+// bf16, exactly, in the MMAs' tiles.  A key's scale
 // multiplies its column of scores in 32 bits and a value's its column of weights before their
 // one rounding to bf16, so that neither codes nor scales are rounded.
 //
@@ -48,9 +48,10 @@ namespace dhs {
 namespace {
 
 constexpr int kChSoftmax = 512;  // two row tiles, two warpgroups each
-constexpr int kChThreads = kChSoftmax + 128;
 constexpr int kChM = 128, kChN = 128, kChH = kChN / 2;
-constexpr int kChMma = 16, kChLoad = 17, kChKeys = 18, kChValues = 19;
+constexpr int kChMma = 16, kChLoad = 17;
+constexpr int kChClean = 18, kChLoadV = 19;  // bf16
+constexpr int kChTurn = 18;                  // 8 bits: the first of six
 // Microseconds that a wait lasts at most, and that a CTA's last ones do, for copies and
 // products in flight.  In a build for tests the first is a variable.
 constexpr uint32_t kChLastUs = 2000000;
@@ -98,24 +99,25 @@ struct ChCfg {
   // 32 rows of codes: of 64 bytes one after another, or, where each comes in a box of its own,
   // on the 128-byte boundaries that TMA writes to
   static constexpr int QUARTER = 32 * 128;
-  static constexpr int RK = W8 ? 4 : 0, RV = W8 ? (D == 64 ? 4 : 3) : 0;  // quarters in flight
+  static constexpr int TURN = W8 ? 3 : 0;     // warps that turn keys' codes, and values'
+  static constexpr int THREADS = kChSoftmax + (W8 ? 256 : 128);
   // What the softmax threads know of a key tile: positions whose page is not in the cache, and
-  // scales.  bf16: tile m's entry is filled when its slot is free of tile m - KS, that is when the
-  // softmax of tile m - KS - 1 is over; 8 bits: a tile sooner, with its codes.
-  static constexpr int NE = D == 64 ? 8 : 4;
+  // scales.  Tile m's is filled when its slot is free of tile m - KS, or, in 8 bits with its
+  // codes, a tile sooner; by then the softmax is over with tile m - KS - 2 or m - KS - 3.
+  static constexpr int NE = 8;
   static constexpr int ENTRY = 16 + (W8 ? 2 * 128 * 4 : 0);
   static constexpr int OFF_KV = 2 * TILE;
   static constexpr int OFF_RAW = OFF_KV + SLOTS * TILE;
-  static constexpr int OFF_RED = OFF_RAW + (RK + RV) * QUARTER;  // float [2 tiles][2 halves][128]
+  static constexpr int OFF_RED = OFF_RAW + 2 * TURN * QUARTER;  // float [2 tiles][2 halves][128]
   static constexpr int OFF_ENTRY = OFF_RED + 2 * 2 * 128 * 4;
   static constexpr int OFF_BAR = OFF_ENTRY + NE * ENTRY;
   static constexpr int CLEAN = 4;             // value tiles gone over and not yet used, at most
-  static constexpr int BARS = 3 + 2 * SLOTS + CLEAN + NE + RK + RV + 8 + 4;
+  static constexpr int BARS = 3 + 2 * SLOTS + (W8 ? 0 : CLEAN) + NE + 2 * TURN + 8 + 4;
   static constexpr int OFF_TMEM = OFF_BAR + BARS * 8;
   static constexpr int OFF_MISC = OFF_TMEM + 16;  // int [4]: abort, -, bad values by item parity
   static constexpr int OFF_ITEM = OFF_MISC + 16;  // ChunkItem [2]
   static constexpr int SMEM = OFF_ITEM + 2 * 64;
-  static_assert(NE >= KS + (W8 ? 2 : 1), "entries of key tiles");
+  static_assert(NE >= KS + (W8 ? 3 : 2), "entries of key tiles");
   static_assert(SMEM <= 227 * 1024, "shared memory of the chunk kernel");
 };
 
@@ -173,7 +175,8 @@ __device__ __forceinline__ bool chunk_seq(const ChunkArgs &a, int i, int &q0, in
 struct ChunkItem {
   int row0, ntok, seq, kvh;  // the first token's row (< 0: no more work), tokens of the item
   int p0;                    // the first token's position
-  int j0, n0, n1;            // of the list: first tile, and how many either row tile walks
+  int j0, n0, n1;            // of the list: first tile, and how many either row tile walks (one
+                             // row tile of two tiles and more: see `dual` below)
   int ns, gap;
   int slot;                  // of the parts, or -1: the whole item
   int tiles;                 // key tiles of this CTA before this piece
@@ -332,7 +335,7 @@ struct ChunkSchedule {
 };
 
 template <int D, int KIND, bool WIN>
-__global__ void __launch_bounds__(kChThreads, 1)
+__global__ void __launch_bounds__(ChCfg<D, KIND>::THREADS, 1)
 k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
         const __grid_constant__ CUtensorMap mv, const __grid_constant__ ChunkArgs a) {
   using C = ChCfg<D, KIND>;
@@ -356,9 +359,9 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
 
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
   uint64_t *q_full = bars, *q_empty = bars + 1, *mma_done = bars + 2, *full = bars + 3,
-           *empty = full + C::SLOTS, *clean = empty + C::SLOTS, *known = clean + C::CLEAN,
+           *empty = full + C::SLOTS, *clean = empty + C::SLOTS, *known = clean + (W8 ? 0 : C::CLEAN),
            *raw = known + C::NE;
-  uint64_t *s_full = raw + C::RK + C::RV, *p_full = s_full + 2, *pv_done = s_full + 4,
+  uint64_t *s_full = raw + 2 * C::TURN, *p_full = s_full + 2, *pv_done = s_full + 4,
            *o_empty = s_full + 6, *item_full = s_full + 8, *item_empty = s_full + 10;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_TMEM);
   if (tid == kChLoad * 32) {
@@ -366,19 +369,20 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
     mbar_init(q_empty, 1);
     mbar_init(mma_done, 1);
     for (int i = 0; i < C::SLOTS; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], W8 ? 4 : 1);          // 8 bits: a tile's quarters
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < C::CLEAN; ++i) mbar_init(&clean[i], 2);
-    for (int i = 0; i < C::NE; ++i) mbar_init(&known[i], W8 ? 2 : 1);
-    for (int i = 0; i < C::RK + C::RV; ++i) mbar_init(&raw[i], 1);
+    if (!W8)
+      for (int i = 0; i < C::CLEAN; ++i) mbar_init(&clean[i], 1);
+    for (int i = 0; i < C::NE; ++i) mbar_init(&known[i], W8 ? 8 : 1);
+    for (int i = 0; i < 2 * C::TURN; ++i) mbar_init(&raw[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], kChSoftmax / 64);   // one arrival per warp
       mbar_init(&pv_done[i], 1);
       mbar_init(&o_empty[i], kChSoftmax / 64);
       mbar_init(&item_full[i], 1);
-      mbar_init(&item_empty[i], kChSoftmax / 32 + 3);  // all warps but the loader's
+      mbar_init(&item_empty[i], C::THREADS / 32 - 1);  // all warps but the loader's
     }
     for (int i = 0; i < 4; ++i) misc[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -390,22 +394,25 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
     tma_prefetch(&mk);
     tma_prefetch(&mv);
   }
+  pdl_trigger();  // the join may be placed; it waits for this grid's end
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   constexpr uint32_t tmem = 0u;  // all 512 columns are this CTA's
 
+  // (whether what is waited for has come)
   auto wait = [&](uint64_t *bar, uint32_t parity, bool force = false) {
-    if (mbar_try_wait(bar, parity)) return;
+    if (mbar_try_wait(bar, parity)) return true;
     const uint32_t since = global_us();
     do {
-      if (!force && *abort_v) return;
+      if (!force && *abort_v) return false;
       if (global_us() - since >= (force ? kChLastUs : a.wait_us)) {
         page_error(a.err, DC_TIMEOUT, DHS_SITE_PAGE_CHUNK);
         *abort_v = 1;
-        return;
+        return false;
       }
     } while (!mbar_try_wait(bar, parity));
+    return true;
   };
   auto given_up = [&]() { return __any_sync(0xffffffffu, *abort_v) != 0; };
   // Slot of the n-th K or V tile since the start, and the parity of its use.  (All counts run
@@ -428,36 +435,53 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
     if (lane == 0) mbar_arrive(&item_empty[k & 1]);
     return it;
   };
-  // Where this lane's position of a quarter lives (row -1: not wanted, or not there) and, in a
-  // box's first lane, what to fetch: a page (n_pages: zeros) and the row in it.
-  struct Look {
-    int64_t row;
-    int page, in;
-    uint32_t bad;  // of the quarter's positions: wanted and not there
-  };
-  auto look = [&](const ChunkItem &it, int pos0) {
-    Look l;
-    const int pos = pos0 + lane, last = it.p0 + it.ntok - 1;
-    const bool want = pos <= last && (!WIN || pos > it.p0 - a.window || pos < a.sinks);
+  // The page of position `pos` of a piece's sequence as the table has it (INT32_MIN: none of
+  // the positions up to `to` is wanted) and the row in it; asked for a tile ahead of its use.
+  auto ask = [&](const ChunkItem &it, int pos, int to, int &in) {
+    const bool want = pos <= it.p0 + it.ntok - 1 && (!WIN || to > it.p0 - a.window || pos < a.sinks);
     const int pg = (int)((uint64_t)(uint32_t)pos * a.pg.div_mul >> a.pg.div_shift);
-    l.in = pos - pg * a.pg.rows;
-    const int page = want ? a.table[(int64_t)it.seq * a.width + pg] : -1;
-    const bool ok = want && page >= 0 && page < a.pg.n_pages;
-    if (want && !ok) page_error(a.err, DC_LOC_RANGE, DHS_SITE_PAGE_CHUNK);
-    l.bad = __ballot_sync(0xffffffffu, want && !ok);
-    l.row = ok ? ((int64_t)page * a.pg.hkv + it.kvh) * a.pg.rows + l.in : -1;
-    // a box is in one page: any of its positions that is there tells which
-    const uint32_t here = __ballot_sync(0xffffffffu, ok);
-    const uint32_t in_box = (here >> (lane & ~(a.box - 1))) & (a.box == 32 ? ~0u : (1u << a.box) - 1u);
-    const int p = __shfl_sync(0xffffffffu, page, (lane & ~(a.box - 1)) + max(0, __ffs(in_box) - 1));
-    l.page = in_box ? p : (int)a.pg.n_pages;
-    return l;
+    in = pos - pg * a.pg.rows;
+    return want ? a.table[(int64_t)it.seq * a.width + pg] : INT32_MIN;
+  };
+  auto there = [&](int page) { return page >= 0 && page < a.pg.n_pages; };
+  // bf16: the boxes of a key or value tile; a lane has box lane, lane + 32, ...
+  const int boxes = kChN / a.box;
+  struct Boxes {
+    int page[4], in[4];
+  };
+  auto ask_tile = [&](const ChunkItem &it, int n, Boxes &b) {
+    const int t0 = tile_of(it.ns, it.gap, it.j0 + n) * kChN;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      b.page[r] = INT32_MIN;
+      if (lane + 32 * r < boxes) {
+        const int pos = t0 + (lane + 32 * r) * a.box;
+        b.page[r] = ask(it, pos, pos + a.box - 1, b.in[r]);
+      }
+    }
+  };
+  auto fetch_tile = [&](const ChunkItem &it, const CUtensorMap *map, uint32_t slot, const Boxes &b) {
+    if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)C::TILE);
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (lane + 32 * r < boxes) {
+        const int page = there(b.page[r]) ? b.page[r] : (int)a.pg.n_pages;
+        for (int h = 0; h < C::HALVES; ++h)
+          tma_load_4d(smem + C::OFF_KV + slot * C::TILE + h * C::HALF + (lane + 32 * r) * a.box * 128,
+                      map, h * 64, b.in[r], it.kvh, page, &full[slot]);
+      }
+    __syncwarp();
   };
 
+  // (8 bits: of the 80 registers a thread at launch, 512 x 96 and 256 x 48 are made; every warp
+  // of a warpgroup asks in the same place)
+  if (warp >= kChMma) {
+  if (W8) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;\n");
   if (warp == kChLoad) {
-    // ------------------------------------------------- pieces and Q, in bf16 also K and V
+    // --------------------------------------------------- pieces and Q, in bf16 also K
     ChunkSchedule plan(a, lane);
-    uint32_t kn = 0, vn = 0, qn = 0, tiles = 0;
+    uint32_t kn = 0, qn = 0, tiles = 0;
     for (int k = 0;; ++k) {
       ChunkItem it = {};
       const bool more = plan.next(it);
@@ -487,49 +511,29 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
       }
       __syncwarp();
       if (given_up()) break;
-      if (!W8) {
+      if (!W8 && nt > 0) {
+        Boxes now, next;
+        ask_tile(it, 0, next);
         for (int n = 0; n < nt; ++n) {
-          const int t0 = tile_of(it.ns, it.gap, it.j0 + n) * kChN;
-          int page[4], in[4];
-          uint32_t bad[4];
+          now = next;
+          if (n + 1 < nt) ask_tile(it, n + 1, next);
+          if (kn >= (uint32_t)C::KS) wait(&empty[kslot(kn)], kpar(kn) ^ 1u);
+          if (given_up()) break;
+          // wanted positions that are not there
+          uint32_t *e = bad_of(kn);
+          if (lane < 4) e[lane] = 0u;
+          __syncwarp();
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const Look l = look(it, t0 + 32 * q);
-            page[q] = l.page;
-            in[q] = l.in;
-            bad[q] = l.bad;
-          }
-          bool stop = false;
-#pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            const uint32_t c = v ? vn : kn, t = v ? vslot(c) : kslot(c);
-            if (c >= (uint32_t)(v ? C::VS : C::KS)) wait(&empty[t], (v ? vpar(c) : kpar(c)) ^ 1u);
-            if (given_up()) {
-              stop = true;
-              break;
+          for (int r = 0; r < 4; ++r)
+            if (lane + 32 * r < boxes && now.page[r] != INT32_MIN && !there(now.page[r])) {
+              page_error(a.err, DC_LOC_RANGE, DHS_SITE_PAGE_CHUNK);
+              for (int x = (lane + 32 * r) * a.box; x < (lane + 32 * r + 1) * a.box; ++x)
+                atomicOr(&e[x >> 5], 1u << (x & 31));
             }
-            if (lane == 0) {
-              if (!v) {
-                uint32_t *e = bad_of(c);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) e[q] = bad[q];
-                mbar_arrive(&known[c % C::NE]);
-              }
-              mbar_arrive_expect_tx(&full[t], (uint32_t)C::TILE);
-            }
-            __syncwarp();
-            if ((lane & (a.box - 1)) == 0) {
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                for (int h = 0; h < C::HALVES; ++h)
-                  tma_load_4d(smem + C::OFF_KV + t * C::TILE + h * C::HALF + (32 * q + lane) * 128,
-                              v ? &mv : &mk, h * 64, in[q], it.kvh, page[q], &full[t]);
-            }
-            __syncwarp();
-            if (v) ++vn;
-            else ++kn;
-          }
-          if (stop) break;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&known[kn % C::NE]);
+          fetch_tile(it, &mk, kslot(kn), now);
+          ++kn;
         }
         if (given_up()) break;
       }
@@ -540,7 +544,6 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
       // every copy has landed before the CTA ends
       if (qn > 0) wait(q_full, (qn - 1) & 1u, true);
       for (uint32_t i = kn > C::KS ? kn - C::KS : 0; i < kn; ++i) wait(&full[kslot(i)], kpar(i), true);
-      for (uint32_t i = vn > C::VS ? vn - C::VS : 0; i < vn; ++i) wait(&full[vslot(i)], vpar(i), true);
     }
     __syncwarp();
   } else if (warp == kChMma) {
@@ -548,8 +551,8 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
     constexpr uint32_t kIdescQK = tc_idesc_bf16(kChM, kChN, 0, 0);
     constexpr uint32_t kIdescPV = tc_idesc_bf16(kChM, D, 0, 1);
     const uint32_t sQ = smem_u32(smem), sKV = smem_u32(smem + C::OFF_KV);
-    auto qk = [&](int i, uint32_t c) {
-      const uint64_t q = tc_desc_sw128(sQ + i * C::TILE, 16, 1024);
+    auto qk = [&](int i, uint32_t c, int of) {  // row tile i, whose Q is the `of`-th
+      const uint64_t q = tc_desc_sw128(sQ + of * C::TILE, 16, 1024);
       const uint64_t k = tc_desc_sw128(sKV + kslot(c) * C::TILE, 16, 1024);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
@@ -570,32 +573,78 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
       if (given_up() || it.row0 < 0) break;
       const int nt = max(it.n0, it.n1);
       if (nt == 0) continue;
+      const bool dual = it.n1 == 0 && nt > 1;
+      auto values_in = [&]() {
+        if (W8) wait(&full[vslot(vn)], vpar(vn));
+        else wait(&clean[vn % C::CLEAN], (vn / C::CLEAN) & 1u);
+      };
+      auto key_in = [&](uint32_t c) {
+        wait(&full[kslot(c)], kpar(c));
+        __syncwarp();
+        tc_fence_after();
+      };
+      auto weights_in = [&](int i) {
+        wait(&p_full[i], pn[i] & 1u);
+        ++pn[i];
+        __syncwarp();
+        tc_fence_after();
+      };
       // the last piece's O has been read
       for (int i = 0; i < 2; ++i)
-        if ((i ? it.n1 : it.n0) > 0 && on[i] > 0) wait(&o_empty[i], (on[i] - 1) & 1u);
+        if ((dual || (i ? it.n1 : it.n0) > 0) && on[i] > 0) wait(&o_empty[i], (on[i] - 1) & 1u);
       wait(q_full, qn & 1u);
       ++qn;
-      wait(&full[kslot(kn)], kpar(kn));
-      __syncwarp();
-      tc_fence_after();
-      if (it.n0 > 0) qk(0, kn);
-      if (it.n1 > 0) qk(1, kn);
+      key_in(kn);
+      if (dual) {
+        // one row tile: its even and odd key tiles are walked as two, side by side, and
+        // put together by the softmax threads
+        qk(0, kn, 0);
+        warp_commit(&empty[kslot(kn)]);
+        ++kn;
+        key_in(kn);
+        qk(1, kn, 0);
+        warp_commit(&empty[kslot(kn)]);
+        ++kn;
+        if (nt == 2) warp_commit(q_empty);
+        for (int n = 0; n < nt; ++n) {
+          if ((n & 15) == 15 && given_up()) break;
+          values_in();
+          auto step = [&](int i) {
+            weights_in(i);
+            pv(i, vn, n >> 1);
+            if (n + 2 >= nt) {
+              warp_commit(&pv_done[i]);
+              ++on[i];
+            }
+            warp_commit(&empty[vslot(vn)]);
+            ++vn;
+            if (n + 2 < nt) {
+              key_in(kn);
+              qk(i, kn, 0);
+              warp_commit(&empty[kslot(kn)]);
+              ++kn;
+              if (n + 3 == nt) warp_commit(q_empty);
+            }
+          };
+          if (n & 1) step(1);
+          else step(0);
+        }
+        continue;
+      }
+      if (it.n0 > 0) qk(0, kn, 0);
+      if (it.n1 > 0) qk(1, kn, 1);
       warp_commit(&empty[kslot(kn)]);
       if (nt == 1) warp_commit(q_empty);
       ++kn;
       for (int n = 0; n < nt; ++n) {
         if ((n & 15) == 15 && given_up()) break;
-        if (W8) wait(&full[vslot(vn)], vpar(vn));
-        else wait(&clean[vn % C::CLEAN], (vn / C::CLEAN) & 1u);
+        values_in();
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int ni = i ? it.n1 : it.n0;
           if (n < ni) {
-            wait(&p_full[i], pn[i] & 1u);
-            ++pn[i];
-            __syncwarp();
-            tc_fence_after();
+            weights_in(i);
             pv(i, vn, n);
             if (n + 1 == ni) {
               warp_commit(&pv_done[i]);
@@ -603,10 +652,8 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
             }
           }
           if (n + 1 < ni) {
-            wait(&full[kslot(kn)], kpar(kn));
-            __syncwarp();
-            tc_fence_after();
-            qk(i, kn);
+            key_in(kn);
+            qk(i, kn, i);
           }
         }
         warp_commit(&empty[vslot(vn)]);
@@ -621,87 +668,105 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
     warp_commit(mma_done);
     wait(mma_done, 0u, true);
     __syncwarp();
-  } else if (W8 && warp >= kChKeys) {
-    // ------------------------------------------- 8-bit keys (warp 18) and values (19)
-    const bool v = warp == kChValues;
-    const int RING = v ? C::RV : C::RK;
-    unsigned char *ring = smem + C::OFF_RAW + (v ? C::RK * C::QUARTER : 0);
-    uint64_t *ringf = raw + (v ? C::RK : 0);
+  } else if (W8 && warp >= kChTurn) {
+    // ---------------- 8 bits: keys (warps 18, 20, 21) and values (19, 22, 23) into bf16
+    // A warp has every third quarter and room for one: its codes are fetched while the other
+    // two warps work.
+    const bool v = warp == 19 || warp >= 22;
+    const uint32_t mine = warp < 20 ? 0 : warp < 22 ? warp - 19 : warp - 21;
+    unsigned char *room = smem + C::OFF_RAW + ((v ? C::TURN : 0) + mine) * C::QUARTER;
+    uint64_t *landed = &raw[(v ? C::TURN : 0) + mine];
     const float *scales = v ? a.pg.vs : a.pg.ks;
     const int pitch = D == 64 && a.box == 1 ? 128 : D;
-    uint32_t tn = 0, issued = 0, used = 0;  // tiles, quarters
+    // 16 codes at a time: chunk y of a row's 64 dims.  8 lanes that go together have rows x and
+    // x ^ 5, so that they meet no bank twice, neither among the codes (128-byte rows are swizzled)
+    // nor where the 32 bytes go as bf16.
+    const int y = lane & 3, xl = (lane >> 3) ^ (lane & 4 ? 5 : 0);
+    const uint32_t from = xl * pitch + (D == 128 ? y ^ xl : y) * 16;
+    const uint32_t to0 = xl * 128 + (((2 * y) ^ xl) << 4), to1 = to0 ^ 16;
+    uint32_t tn = 0, used = 0, issued = 0;  // tiles; quarters of this warp
     for (int k = 0;; ++k) {
       const ChunkItem it = take(k);
       if (given_up() || it.row0 < 0) break;
-      const int nt = max(it.n0, it.n1), quarters = 4 * nt;
-      auto issue = [&](int x) {
-        if (x < quarters) {
-          const uint32_t t = tn + (uint32_t)(x >> 2);
-          const int q = x & 3;
-          const Look l = look(it, tile_of(it.ns, it.gap, it.j0 + (x >> 2)) * kChN + 32 * q);
-          cp_async_4_or_0(scales_of(t) + (v ? 128 : 0) + 32 * q + lane, scales + max((int64_t)0, l.row),
-                          l.row >= 0 ? 4 : 0);
-          if (!v && lane == 0) bad_of(t)[q] = l.bad;
-          const uint32_t at = issued % RING;
-          if (lane == 0) mbar_arrive_expect_tx(&ringf[at], (uint32_t)(32 * D));
+      const uint32_t end = 4 * (tn + max(it.n0, it.n1));
+      auto place = [&](uint32_t g) {  // this lane's position of quarter g
+        return tile_of(it.ns, it.gap, it.j0 + (int)((g >> 2) - tn)) * kChN + 32 * (int)(g & 3) + lane;
+      };
+      // the first quarter of this warp's in the piece, its pages and those of the next
+      uint32_t g = 4 * tn + (mine + 3 - (4 * tn) % 3) % 3;
+      int in = 0, in1 = 0, page = INT32_MIN, page1 = INT32_MIN;
+      if (g < end) page = ask(it, place(g), place(g), in);
+      if (g + 3 < end) page1 = ask(it, place(g + 3), place(g + 3), in1);
+      auto fetch = [&](uint32_t g) {  // codes and scales of quarter g, whose page is known
+        if (g < end) {
+          const bool ok = there(page);
+          const uint32_t c = g >> 2;
+          const int q = g & 3;
+          if (page != INT32_MIN && !ok) page_error(a.err, DC_LOC_RANGE, DHS_SITE_PAGE_CHUNK);
+          const uint32_t bad = __ballot_sync(0xffffffffu, page != INT32_MIN && !ok);
+          if (!v && lane == 0) bad_of(c)[q] = bad;
+          const int64_t row = ok ? ((int64_t)page * a.pg.hkv + it.kvh) * a.pg.rows + in : 0;
+          cp_async_4_or_0(scales_of(c) + (v ? 128 : 0) + 32 * q + lane, scales + row, ok ? 4 : 0);
+          // a box is in one page: any of its positions that is there tells which
+          const int first = lane & ~(a.box - 1);
+          const uint32_t all = a.box == 32 ? ~0u : (1u << a.box) - 1u;
+          const uint32_t in_box = (__ballot_sync(0xffffffffu, ok) >> first) & all;
+          const int of = __shfl_sync(0xffffffffu, page, first + max(0, __ffs(in_box) - 1));
+          if (lane == 0) mbar_arrive_expect_tx(landed, (uint32_t)(32 * D));
           __syncwarp();
-          if ((lane & (a.box - 1)) == 0)
-            tma_load_4d(ring + at * C::QUARTER + lane * pitch, v ? &mv : &mk, 0, l.in, it.kvh, l.page,
-                        &ringf[at]);
+          if (lane == first)
+            tma_load_4d(room + lane * pitch, v ? &mv : &mk, 0, in, it.kvh,
+                        in_box ? of : (int)a.pg.n_pages, landed);
           ++issued;
         }
         cp_async_commit();
+        page = page1;
+        in = in1;
+        page1 = g + 6 < end ? ask(it, place(g + 6), place(g + 6), in1) : INT32_MIN;
       };
-      const uint32_t t_item = tn;
-      for (int x = 0; x < RING; ++x) issue(x);
-      bool stop = false;
-      for (int n = 0; n < nt; ++n) {
-        const uint32_t c = t_item + n, slot = v ? vslot(c) : kslot(c);
+      fetch(g);
+      for (; g < end; g += 3) {
+        const uint32_t c = g >> 2, slot = v ? vslot(c) : kslot(c);
+        wait(landed, used & 1u);
         if (c >= (uint32_t)(v ? C::VS : C::KS)) wait(&empty[slot], (v ? vpar(c) : kpar(c)) ^ 1u);
-        if (given_up()) {
-          stop = true;
-          break;
-        }
-        unsigned char *tile = smem + C::OFF_KV + slot * C::TILE;
-        for (int q = 0; q < 4; ++q) {
-          wait(&ringf[used % RING], (used / RING) & 1u);
-          __syncwarp();
-          const unsigned char *src = ring + (used % RING) * C::QUARTER;
-          // 16 codes at a time: row x, chunk y of D / 16, whose 32 bytes as bf16 are two
-          // neighbouring chunks of a half; lanes of the upper half take them the other way
-          // round, so that 8 lanes meet no bank twice
-          constexpr int CH = D / 16, N = CH;
-          uint4 w[N];
+        __syncwarp();
+        if (given_up()) break;
+        ++used;
+        unsigned char *dst = smem + C::OFF_KV + slot * C::TILE + (g & 3) * (32 * 128);
+        constexpr int B = D == 128 ? 4 : 2;  // chunks at a time: half of the quarter
+        uint4 w[B];
+        auto read = [&](int part) {
 #pragma unroll
-          for (int u = 0; u < N; ++u)
-            w[u] = *reinterpret_cast<const uint4 *>(src + (u * 32 + lane) / CH * pitch +
-                                                    (u * 32 + lane) % CH * 16);
+          for (int e = 0; e < B; ++e)
+            w[e] = *reinterpret_cast<const uint4 *>(
+                room + (D == 128 ? (from ^ ((e & 1) * 64)) + (2 * part + (e >> 1)) * 1024
+                                 : from + (2 * part + e) * 8 * pitch));
+        };
+        auto write = [&](int part) {
 #pragma unroll
-          for (int u = 0; u < N; ++u) {
-            const int e = u * 32 + lane, x = 32 * q + e / CH, y = e % CH;
+          for (int e = 0; e < B; ++e) {
             uint4 lo, hi;
-            lo.x = two_codes<KIND>(w[u].x, false);
-            lo.y = two_codes<KIND>(w[u].x, true);
-            lo.z = two_codes<KIND>(w[u].y, false);
-            lo.w = two_codes<KIND>(w[u].y, true);
-            hi.x = two_codes<KIND>(w[u].z, false);
-            hi.y = two_codes<KIND>(w[u].z, true);
-            hi.z = two_codes<KIND>(w[u].w, false);
-            hi.w = two_codes<KIND>(w[u].w, true);
-            const bool up = D == 128 && (y & 4);
-            unsigned char *dst = tile + (up ? C::HALF : 0) + x * 128;
-            const int c0 = 2 * (y & 3);
-            *reinterpret_cast<uint4 *>(dst + (((c0 + up) ^ (x & 7)) << 4)) = up ? hi : lo;
-            *reinterpret_cast<uint4 *>(dst + (((c0 + !up) ^ (x & 7)) << 4)) = up ? lo : hi;
+            lo.x = two_codes<KIND>(w[e].x, false);
+            lo.y = two_codes<KIND>(w[e].x, true);
+            lo.z = two_codes<KIND>(w[e].y, false);
+            lo.w = two_codes<KIND>(w[e].y, true);
+            hi.x = two_codes<KIND>(w[e].z, false);
+            hi.y = two_codes<KIND>(w[e].z, true);
+            hi.z = two_codes<KIND>(w[e].w, false);
+            hi.w = two_codes<KIND>(w[e].w, true);
+            unsigned char *at = dst + (D == 128 ? (e & 1) * C::HALF + (2 * part + (e >> 1)) * 1024
+                                                : (2 * part + e) * 1024);
+            *reinterpret_cast<uint4 *>(at + to0) = lo;
+            *reinterpret_cast<uint4 *>(at + to1) = hi;
           }
-          ++used;
-          __syncwarp();  // every lane has read the quarter
-          // (tn stays the piece's first tile while its quarters are asked for)
-          issue(4 * n + q + RING);
-        }
-        // this tile's scales are in: RING quarters were asked for after its last one
-        if (v) cp_async_wait_group<C::RV>();
-        else cp_async_wait_group<C::RK>();
+        };
+        read(0);
+        write(0);
+        read(1);
+        __syncwarp();  // every lane has its codes
+        fetch(g + 3);
+        write(1);
+        cp_async_wait_group<1>();  // this quarter's scales are in (the next one's may be under way)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -709,14 +774,36 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
           mbar_arrive(&known[c % C::NE]);
         }
       }
-      tn += nt;
-      if (stop) break;
+      tn += max(it.n0, it.n1);
+      if (given_up()) break;
     }
     cp_async_wait_all();
     // every copy has landed before the CTA ends
-    for (; used < issued; ++used) wait(&ringf[used % RING], (used / RING) & 1u, true);
+    if (used < issued) wait(landed, used & 1u, true);
     __syncwarp();
-  } else if (!W8 && warp >= kChKeys) {
+  } else if (!W8 && warp == kChLoadV) {
+    // ------------------------------------------------------------- bf16: V's copies
+    uint32_t vn = 0;
+    for (int k = 0;; ++k) {
+      const ChunkItem it = take(k);
+      if (given_up() || it.row0 < 0) break;
+      const int nt = max(it.n0, it.n1);
+      Boxes now, next;
+      if (nt > 0) ask_tile(it, 0, next);
+      for (int n = 0; n < nt; ++n) {
+        now = next;
+        if (n + 1 < nt) ask_tile(it, n + 1, next);
+        if (vn >= (uint32_t)C::VS) wait(&empty[vslot(vn)], vpar(vn) ^ 1u);
+        if (given_up()) break;
+        fetch_tile(it, &mv, vslot(vn), now);
+        ++vn;
+      }
+      if (given_up()) break;
+    }
+    if (lane == 0)
+      for (uint32_t i = vn > C::VS ? vn - C::VS : 0; i < vn; ++i) wait(&full[vslot(i)], vpar(i), true);
+    __syncwarp();
+  } else if (!W8 && warp == kChClean) {
     // ------------------------------------------------------------------- values
     uint32_t vn = 0;
     for (int k = 0;; ++k) {
@@ -739,7 +826,7 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
           auto some = [&](int x) { return x >= r0 || (WIN && x < r1 && t0 + x >= a.sinks); };
           uint32_t any = 0u;
 #pragma unroll 8
-          for (int e = (warp - kChKeys) * 32 + lane; e < kChN * 8; e += 64) {
+          for (int e = lane; e < kChN * 8; e += 32) {
             if (!some(e >> 3)) continue;
 #pragma unroll
             for (int h = 0; h < C::HALVES; ++h) {
@@ -751,8 +838,7 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
             }
           }
           bool found = false;
-          for (int e = (warp - kChKeys) * 32 + lane; (any & 0x80008000u) != 0u && e < kChN * 8;
-               e += 64) {
+          for (int e = lane; (any & 0x80008000u) != 0u && e < kChN * 8; e += 32) {
             if (!some(e >> 3)) continue;
 #pragma unroll
             for (int h = 0; h < C::HALVES; ++h) {
@@ -778,11 +864,14 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
       }
     }
     __syncwarp();
+  }
   } else {
+    if (W8) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;\n");
     // ------------------------------------------------------------------ softmax
     const int i = warp >> 3, hg = (warp >> 2) & 1, m = tid & 127;
     const int tloc = m / a.G, h = m - tloc * a.G;
     const int pair = 1 + i * 4 + (warp & 3);  // barrier of the two warps of these rows
+    const int rows = 9 + (warp & 3);          // of these and the other row tile's
     const uint32_t lrow = (uint32_t)((warp & 3) * 32) << 16;
     // this thread's half of the row's scores, and of its output columns
     const uint32_t tS = tmem + lrow + i * kChN, tO = tmem + lrow + 2 * kChN + i * D + hg * (D / 2);
@@ -796,22 +885,28 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
       wait(&item_full[k & 1], item_par(k));
       __syncwarp();
       volatile const ChunkItem &it = item_of(k);
-      // (the warps of a pair leave together: they meet at barriers below, also after a wait
-      // has run out)
-      if (named_or(pair, 64, *abort_v != 0) || it.row0 < 0) break;
-      const int ni = i ? it.n1 : it.n0;
+      // (the warps of these rows leave together: they meet at barriers below, also after a
+      // wait has run out)
+      if (named_or(rows, 128, *abort_v != 0) || it.row0 < 0) break;
+      // one row tile of several key tiles: row tile 0's threads have the even tiles, row tile
+      // 1's the odd ones, of the same rows
+      const bool dual = it.n1 == 0 && it.n0 > 1;
+      const int ni = dual ? (it.n0 + 1 - i) >> 1 : i ? it.n1 : it.n0, ti = dual ? 0 : i;
+      const int tstep = dual ? 2 : 1;
+      int tile = it.j0 + (dual ? i : 0);      // of the list
+      uint32_t en = (uint32_t)(it.tiles + (dual ? i : 0));  // the key tile's entry
       int lim0;  // columns of tile 0 that this row's half sees
       int least; // tiles from this one on have columns that some row does not see
       int wend = 0;  // tiles before this position have columns behind some row's window
       {
-        const int tok = i * a.tpt + tloc, ntok = it.ntok, p0 = it.p0;
+        const int tok = ti * a.tpt + tloc, ntok = it.ntok, p0 = it.p0;
         lim0 = (tloc < a.tpt && tok < ntok ? p0 + tok + 1 : 0) - hg * kChH;
-        least = p0 + i * a.tpt + 1;
-        if (WIN) wend = max(p0, -1024) + min((i + 1) * a.tpt, ntok) - a.window;
+        least = p0 + ti * a.tpt + 1;
+        if (WIN) wend = max(p0, -1024) + min((ti + 1) * a.tpt, ntok) - a.window;
       }
       float m_run = -CUDART_INF_F, l = 0.f;
-      for (int n = 0; n < ni; ++n, ++sn) {
-        const uint32_t en = (uint32_t)(it.tiles + n);  // the key tile's entry
+      const int ns = WIN ? it.ns : 0, gap = WIN ? it.gap : 0;
+      for (int n = 0; n < ni; ++n, ++sn, en += tstep, tile += tstep) {
         wait(&known[en % C::NE], (en / C::NE) & 1u);
         wait(&s_full[i], sn & 1u);
         __syncwarp();
@@ -820,7 +915,7 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
         tmem_ld32(tS + hg * kChH, s0);
         tmem_ld32(tS + hg * kChH + 32, s1);
         tmem_wait_ld();
-        const int first = tile_of(it.ns, it.gap, it.j0 + n) * kChN;
+        const int first = (WIN ? tile_of(ns, gap, tile) : tile) * kChN;
         const float *sc = scales_of(en) + hg * kChH;
         const uint2 out_of = *reinterpret_cast<const uint2 *>(bad_of(en) + hg * 2);
         const bool masked = first + kChN > least || (out_of.x | out_of.y) != 0u ||
@@ -902,6 +997,7 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
         // weights (8 bits: times their value's scale) are rounded to bf16 for the product, at
         // most 2^-8 of each; l takes them unrounded
         auto weights = [&](const uint32_t(&s)[32], const float *by, uint32_t hid) {
+          float4 f4;
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
             float u, w;
@@ -912,14 +1008,17 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
             uint64_t two = pack_f32x2(u, w);
             l2 = add_f32x2(l2, two);
             if (W8) {
-              const float2 f = *reinterpret_cast<const float2 *>(by + 2 * x);
-              unpack_f32x2(mul_f32x2(two, pack_f32x2(f.x, f.y)), u, w);
-              if (masked) {  // (a scale that is not finite at a hidden place)
-                if (hid >> (2 * x) & 1u) u = 0.f;
-                if (hid >> (2 * x + 1) & 1u) w = 0.f;
-              }
+              if (x % 2 == 0) f4 = *reinterpret_cast<const float4 *>(by + 2 * x);
+              unpack_f32x2(mul_f32x2(two, x % 2 ? pack_f32x2(f4.z, f4.w) : pack_f32x2(f4.x, f4.y)), u, w);
             }
             p[x] = pack_bf16(u, w);
+          }
+          if (W8 && masked) {  // (a scale that is not finite at a hidden place)
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              if (hid >> (2 * x) & 1u) p[x] &= 0xFFFF0000u;
+              if (hid >> (2 * x + 1) & 1u) p[x] &= 0x0000FFFFu;
+            }
           }
         };
         weights(s0, sc + 128, hid0);
@@ -938,39 +1037,79 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
       }
       red[hg * 128 + m] = l;
       bool bad = false;
-      uint32_t o[D / 2];
       if (ni > 0) {
         wait(&pv_done[i], on & 1u);
         ++on;
         __syncwarp();
         tc_fence_after();
+      }
+      if (dual && i == 1) {
+        // this half's maximum, sum and O go to the threads of row tile 0
+        named_sync(pair, 64);
+        l += red[(hg ^ 1) * 128 + m];
+        named_sync(pair, 64);
+        red[hg * 128 + m] = hg ? l : m_run;
+        tc_fence_before();
+        named_sync(rows, 128);  // they may read
+        named_sync(rows, 128);  // they have read
+        if (lane == 0) {
+          mbar_arrive(&o_empty[1]);
+          mbar_arrive(&item_empty[k & 1]);
+        }
+        continue;
+      }
+      uint32_t o[D / 2];
+      if (ni > 0) {
 #pragma unroll
         for (int c = 0; c < D / 2; c += 32)
           tmem_ld32(tO + c, *reinterpret_cast<uint32_t(*)[32]>(&o[c]));
         tmem_wait_ld();
         tc_fence_before();
-        // (read before this piece's place is given up: the one after next uses it again)
-        bad = !W8 && bad_values[k & 1] == k + 1;
         __syncwarp();
         if (lane == 0) mbar_arrive(&o_empty[i]);
       } else {
 #pragma unroll
         for (int x = 0; x < D / 2; ++x) o[x] = 0u;
       }
+      if (dual) named_sync(rows, 128);  // the other half is there
       // Rows of a piece for which a wait ran out (whoever's it was: it is known by the time
       // what it waited for arrives here) are not written, nor half of them.
       const bool lost = named_or(pair, 64, *abort_v != 0);
       l += red[(hg ^ 1) * 128 + m];  // the row's sum over both halves
-      const int tok = i * a.tpt + tloc, ntok = it.ntok, p0 = it.p0, slot = it.slot;
-      const int row0 = it.row0, kvh = it.kvh, seq = it.seq, j0 = it.j0, ns = it.ns, gap = it.gap;
+      // (read before this piece's place is given up: the one after next uses it again)
+      bad = !W8 && bad_values[k & 1] == k + 1;
+      if (dual) {
+        tc_fence_after();
+        const float m1 = red[256 + m], l1 = red[256 + 128 + m];
+        const float top = fmaxf(m_run, m1);
+        // (tiles that a row does not see weigh nothing; NaN scores have m = -inf too)
+        const float f0 = m_run == -CUDART_INF_F ? (l != l ? 1.f : 0.f) : ex2_approx(m_run - top);
+        const float f1 = m1 == -CUDART_INF_F ? (l1 != l1 ? 1.f : 0.f) : ex2_approx(m1 - top);
+        m_run = top;
+        l = l * f0 + l1 * f1;
+#pragma unroll
+        for (int c = 0; c < D / 2; c += 16) {
+          uint32_t x[16];
+          tmem_ld16(tO + D + c, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            o[c + e] = __float_as_uint(__uint_as_float(o[c + e]) * f0 + __uint_as_float(x[e]) * f1);
+        }
+        tc_fence_before();
+        named_sync(rows, 128);  // read
+      }
+      const int tok = ti * a.tpt + tloc, ntok = it.ntok, p0 = it.p0, slot = it.slot;
+      const int row0 = it.row0, kvh = it.kvh, seq = it.seq, j0 = it.j0;
+      const int walked = dual ? it.n0 : ni;
       const bool valid = tloc < a.tpt && tok < ntok && !lost;
       __syncwarp();
       if (lane == 0) mbar_arrive(&item_empty[k & 1]);
       if (valid && bad) {
         // values that were taken out, for the positions of this piece's tiles that this row sees
         const int pos = p0 + tok, last = p0 + ntok - 1;
-        for (int n = 0; n < ni; ++n) {
-          const int t0 = tile_of(ns, gap, j0 + n) * kChN;
+        for (int n = 0; n < walked; ++n) {
+          const int t0 = (WIN ? tile_of(ns, gap, j0 + n) : j0 + n) * kChN;
           const int from = WIN ? max(t0, 0) : max(t0, p0 + 1);
           for (int t = from; t < min(t0 + kChN, pos + 1); ++t) {
             if (WIN && t < a.sinks && t <= p0) continue;              // (every row sees it)
@@ -1123,8 +1262,8 @@ int64_t chunk_bytes(int n, int d) {
   return (int64_t)n * 2 * 256 * (d * 4 + 8) + (int64_t)n * (2 * 16 + 16) + 32;
 }
 
-// The cache's rows [page][kv head][page row][d], boxes of `box` rows: 64 bf16 swizzled, or a
-// row's codes.
+// The cache's rows [page][kv head][page row][d], boxes of `box` rows: 64 bf16, or a row's
+// codes; swizzled where that is 128 bytes.
 bool encode_pages(EncodeTiled f, CUtensorMap *m, void *p, const PageView &pg, int box) {
   const bool w8 = pg.kind != DHS_PAGE_BF16;
   const cuuint64_t rb = (cuuint64_t)pg.d * (w8 ? 1 : 2);
@@ -1135,7 +1274,7 @@ bool encode_pages(EncodeTiled f, CUtensorMap *m, void *p, const PageView &pg, in
   const cuuint32_t one[4] = {1, 1, 1, 1};
   return f(m, w8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, p, dims,
            strides, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-           w8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+           w8 && pg.d == 64 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1232,7 +1371,8 @@ extern "C" int dhs_page_chunk(const dhs_pages *pages, const void *q, const int64
   a.G = q_heads / a.pg.hkv;
   a.tpt = kChM / a.G;
   a.box = 1;
-  while (a.box < 32 && a.pg.rows % (2 * a.box) == 0) a.box *= 2;
+  const int most_box = a.pg.kind == DHS_PAGE_BF16 ? 128 : 32;  // (a tile, a quarter)
+  while (a.box < most_box && a.pg.rows % (2 * a.box) == 0) a.box *= 2;
   a.window = std::min(window, INT32_MAX - 1024);  // (no sequence is longer)
   a.sinks = sinks;
   a.cap = window > 0 ? std::min<int64_t>((int64_t)window + sinks + 2 * a.tpt + 2 * kChN, (int64_t)1 << 31)
@@ -1254,7 +1394,7 @@ extern "C" int dhs_page_chunk(const dhs_pages *pages, const void *q, const int64
     static DeviceSmem granted;
     cudaError_t e = granted.ensure(kern, C::SMEM, dev);
     if (e == cudaSuccess)
-      e = launch_prio(kern, dim3((unsigned)sms), dim3(kChThreads), (size_t)C::SMEM, s, mq, mk, mv, a);
+      e = launch_prio(kern, dim3((unsigned)sms), dim3(C::THREADS), (size_t)C::SMEM, s, mq, mk, mv, a);
     return e;
   };
   auto kinds = [&](auto dim, auto win) -> cudaError_t {
