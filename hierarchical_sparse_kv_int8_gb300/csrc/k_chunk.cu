@@ -112,9 +112,9 @@ struct ChCfg {
   static constexpr int OFF_ENTRY = OFF_RED + 2 * 2 * 128 * 4;
   static constexpr int OFF_BAR = OFF_ENTRY + NE * ENTRY;
   static constexpr int CLEAN = 4;             // value tiles gone over and not yet used, at most
-  static constexpr int BARS = 3 + 2 * SLOTS + (W8 ? 0 : CLEAN) + NE + 2 * TURN + 8 + 4;
+  static constexpr int BARS = 3 + 2 * SLOTS + (W8 ? 0 : CLEAN) + 2 * TURN + 8 + 4 + 8;
   static constexpr int OFF_TMEM = OFF_BAR + BARS * 8;
-  static constexpr int OFF_MISC = OFF_TMEM + 16;  // int [4]: abort, -, bad values by item parity
+  static constexpr int OFF_MISC = OFF_TMEM + 16;  // int [4]: abort, whether pages were missing, bad values by item parity
   static constexpr int OFF_ITEM = OFF_MISC + 16;  // ChunkItem [2]
   static constexpr int SMEM = OFF_ITEM + 2 * 64;
   static_assert(NE >= KS + (W8 ? 3 : 2), "entries of key tiles");
@@ -189,30 +189,34 @@ __device__ __forceinline__ int tile_of(int ns, int gap, int n) { return n < ns ?
 struct ChunkSchedule {
   const ChunkArgs &a;
   int lane, span, n_cta, hkv;
-  int64_t begin, end, total;
+  int64_t begin, end, share;
+  int rest;                        // all costs: share * n_cta + rest
   // the item to come: sequence, kv head, place in the sequence, where its cost starts
   int seq, kvh, r, q0, nq, off, R;
   int base, my_q0, my_nq, my_off;  // this lane's of 32 sequences
-  int64_t at, per;
+  int64_t at, per, m;
   // for the join
   int4 first;
   int first_pos, cont;
 
+  // the items r < m of a sequence cost max(o, 0) + (r + 1) span, later ones the cap
+  __device__ int64_t below_cap(int o) const {
+    if (a.window == 0) return INT32_MAX;
+    const int64_t left = a.cap - 1 - max(o, 0);
+    return left < span ? 0 : (int64_t)((uint32_t)left / (uint32_t)span);
+  }
   // cost of a sequence's first j items
-  __device__ int64_t upto(int j, int o) const {
-    const int64_t o1 = max(o, 0);
-    // items r < m cost o1 + (r + 1) span, later ones the cap
-    const int64_t m = a.cap > o1 + span ? (a.cap - 1 - o1) / span : 0;
+  __device__ int64_t upto(int j, int o, int64_t m) const {
     const int64_t x = min((int64_t)j, m);
-    return x * o1 + (int64_t)span * (x * (x + 1) / 2) + (j - x) * a.cap + (int64_t)j * kChOver;
+    return x * max(o, 0) + (int64_t)span * (x * (x + 1) / 2) + (j - x) * a.cap + (int64_t)j * kChOver;
   }
   __device__ int64_t cost_of(int i, bool record) const {
     int x0, n, o;
     if (i >= a.n_seqs || !chunk_seq(a, i, x0, n, o, record)) return 0;
-    return upto((n + span - 1) / span, o) * hkv;
+    return upto((int)((uint32_t)(n + span - 1) / (uint32_t)span), o, below_cap(o)) * hkv;
   }
   __device__ int64_t border(int b) const {
-    return total / n_cta * b + total % n_cta * b / n_cta;
+    return share * b + (int64_t)((uint32_t)rest * (uint32_t)b / (uint32_t)n_cta);
   }
   __device__ void enter(int i) {  // sequence i is the one to come
     seq = i;
@@ -225,8 +229,9 @@ struct ChunkSchedule {
     q0 = __shfl_sync(0xffffffffu, my_q0, i - base);
     nq = __shfl_sync(0xffffffffu, my_nq, i - base);
     off = __shfl_sync(0xffffffffu, my_off, i - base);
-    R = (nq + span - 1) / span;
-    per = upto(R, off);
+    R = (int)((uint32_t)(nq + span - 1) / (uint32_t)span);
+    m = below_cap(off);
+    per = upto(R, off, m);
   }
   __device__ ChunkSchedule(const ChunkArgs &args, int l) : a(args), lane(l) {
     span = 2 * a.tpt;
@@ -234,19 +239,24 @@ struct ChunkSchedule {
     first = make_int4(0, 0, 0, -1);
     first_pos = cont = 0;
     base = -64;
-    total = 0;
-    for (int i = 0; i < a.n_seqs; i += 32) total += cost_of(i + lane, true);
+    int64_t total = 0, mine = 0;
+    for (int i = 0; i < a.n_seqs; i += 32) {
+      mine = cost_of(i + lane, true);
+      total += mine;
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     n_cta = (int)min((int64_t)gridDim.x, (total + kChLeast - 1) / kChLeast);
     seq = a.n_seqs;
     at = begin = end = 0;
     if ((int)blockIdx.x >= n_cta) return;
+    share = (total | n_cta) >> 32 ? total / n_cta : (int64_t)((uint32_t)total / (uint32_t)n_cta);
+    rest = (int)(total - share * n_cta);
     begin = border(blockIdx.x);
     end = border(blockIdx.x + 1);
     // the sequence in which the share begins
     for (int i = 0; i < a.n_seqs; i += 32) {
-      const int64_t c = cost_of(i + lane, false);
+      const int64_t c = a.n_seqs <= 32 ? mine : cost_of(i + lane, false);
       int64_t x = c;  // inclusive sums
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -263,25 +273,27 @@ struct ChunkSchedule {
       at += __shfl_sync(0xffffffffu, x, 31);
     }
     if (seq >= a.n_seqs) return;
-    kvh = (int)((begin - at) / per);
+    kvh = (int)(((begin - at) | per) >> 32 ? (begin - at) / per
+                                           : (int64_t)((uint32_t)(begin - at) / (uint32_t)per));
     at += kvh * per;
     int lo = 0, hi = R - 1;  // the last item that starts at or before `begin`
     while (lo < hi) {
       const int mid = (int)(((int64_t)lo + hi + 1) >> 1);
-      if (at + upto(mid, off) <= begin) lo = mid;
+      if (at + upto(mid, off, m) <= begin) lo = mid;
       else hi = mid - 1;
     }
     r = lo;
-    at += upto(r, off);
+    at += upto(r, off, m);
   }
   // (of an item of nt tiles that starts at `at` and costs c) the tile at which border x cuts it
   __device__ int cut(int64_t x, int64_t c, int nt) const {
-    const int t = (int)((int64_t)nt * (x - at) / c);
+    // (both CTAs at a border work out the same numbers)
+    const int t = min(nt, (int)((float)nt * ((float)(x - at) / (float)c)));
     return t < kChSnap ? 0 : nt - t < kChSnap ? nt : t;
   }
   __device__ bool next(ChunkItem &it) {
     while (seq < a.n_seqs && at < end) {
-      const int64_t c = R > 0 ? upto(r + 1, off) - upto(r, off) : 0;
+      const int64_t c = R > 0 ? upto(r + 1, off, m) - upto(r, off, m) : 0;
       bool own = false;
       if (R > 0) {
         const int tok0 = r * span, ntok = min(span, nq - tok0), p0 = off + tok0;
@@ -314,7 +326,7 @@ struct ChunkSchedule {
           if (!whole && lo > 0) cont = 1;
           if (!whole && lo == 0) {
             // the last CTA that has some of this item
-            int b = (int)min((int64_t)n_cta - 1, (at + c) / max((int64_t)1, total / n_cta));
+            int b = min(n_cta - 1, (int)((float)(at + c) / (float)max((int64_t)1, share)));
             while (b > 0 && border(b) >= at + c) --b;
             while (b + 1 < n_cta && border(b + 1) < at + c) ++b;
             first = make_int4(it.row0, ntok, kvh, b);
@@ -343,7 +355,7 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
   // no static shared memory: the dynamic part starts on the boundary it asks for
   extern __shared__ __align__(1024) unsigned char smem[];
   int *misc = reinterpret_cast<int *>(smem + C::OFF_MISC);
-  volatile int *abort_v = misc, *bad_values = misc + 2;
+  volatile int *abort_v = misc, *missing = misc + 1, *bad_values = misc + 2;
   auto item_of = [&](int k) -> ChunkItem & {
     return *reinterpret_cast<ChunkItem *>(smem + C::OFF_ITEM + (k & 1) * 64);
   };
@@ -359,10 +371,10 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
 
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
   uint64_t *q_full = bars, *q_empty = bars + 1, *mma_done = bars + 2, *full = bars + 3,
-           *empty = full + C::SLOTS, *clean = empty + C::SLOTS, *known = clean + (W8 ? 0 : C::CLEAN),
-           *raw = known + C::NE;
+           *empty = full + C::SLOTS, *clean = empty + C::SLOTS, *raw = clean + (W8 ? 0 : C::CLEAN);
   uint64_t *s_full = raw + 2 * C::TURN, *p_full = s_full + 2, *pv_done = s_full + 4,
-           *o_empty = s_full + 6, *item_full = s_full + 8, *item_empty = s_full + 10;
+           *o_empty = s_full + 6, *item_full = s_full + 8, *item_empty = s_full + 10,
+           *half_in = s_full + 12, *half_read = s_full + 16;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_TMEM);
   if (tid == kChLoad * 32) {
     mbar_init(q_full, 1);
@@ -374,7 +386,6 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
     }
     if (!W8)
       for (int i = 0; i < C::CLEAN; ++i) mbar_init(&clean[i], 1);
-    for (int i = 0; i < C::NE; ++i) mbar_init(&known[i], W8 ? 8 : 1);
     for (int i = 0; i < 2 * C::TURN; ++i) mbar_init(&raw[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
@@ -384,7 +395,11 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
       mbar_init(&item_full[i], 1);
       mbar_init(&item_empty[i], C::THREADS / 32 - 1);  // all warps but the loader's
     }
-    for (int i = 0; i < 4; ++i) misc[i] = 0;
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&half_in[i], 2);
+      mbar_init(&half_read[i], 2);
+      misc[i] = 0;
+    }
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     fence_proxy_async_smem();
   }
@@ -527,11 +542,11 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
           for (int r = 0; r < 4; ++r)
             if (lane + 32 * r < boxes && now.page[r] != INT32_MIN && !there(now.page[r])) {
               page_error(a.err, DC_LOC_RANGE, DHS_SITE_PAGE_CHUNK);
+              *missing = 1;
               for (int x = (lane + 32 * r) * a.box; x < (lane + 32 * r + 1) * a.box; ++x)
                 atomicOr(&e[x >> 5], 1u << (x & 31));
             }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&known[kn % C::NE]);
           fetch_tile(it, &mk, kslot(kn), now);
           ++kn;
         }
@@ -589,9 +604,11 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
         __syncwarp();
         tc_fence_after();
       };
-      // the last piece's O has been read
-      for (int i = 0; i < 2; ++i)
-        if ((dual || (i ? it.n1 : it.n0) > 0) && on[i] > 0) wait(&o_empty[i], (on[i] - 1) & 1u);
+      // (the last piece's O has been read, before the first product over it)
+      auto o_free = [&](int i) {
+        if (on[i] > 0) wait(&o_empty[i], (on[i] - 1) & 1u);
+        ++on[i];
+      };
       wait(q_full, qn & 1u);
       ++qn;
       key_in(kn);
@@ -610,12 +627,10 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
           if ((n & 15) == 15 && given_up()) break;
           values_in();
           auto step = [&](int i) {
+            if (n < 2) o_free(i);
             weights_in(i);
             pv(i, vn, n >> 1);
-            if (n + 2 >= nt) {
-              warp_commit(&pv_done[i]);
-              ++on[i];
-            }
+            if (n + 2 >= nt) warp_commit(&pv_done[i]);
             warp_commit(&empty[vslot(vn)]);
             ++vn;
             if (n + 2 < nt) {
@@ -644,12 +659,10 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
         for (int i = 0; i < 2; ++i) {
           const int ni = i ? it.n1 : it.n0;
           if (n < ni) {
+            if (n == 0) o_free(i);
             weights_in(i);
             pv(i, vn, n);
-            if (n + 1 == ni) {
-              warp_commit(&pv_done[i]);
-              ++on[i];
-            }
+            if (n + 1 == ni) warp_commit(&pv_done[i]);
           }
           if (n + 1 < ni) {
             key_in(kn);
@@ -676,7 +689,6 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
     const uint32_t mine = warp < 20 ? 0 : warp < 22 ? warp - 19 : warp - 21;
     unsigned char *room = smem + C::OFF_RAW + ((v ? C::TURN : 0) + mine) * C::QUARTER;
     uint64_t *landed = &raw[(v ? C::TURN : 0) + mine];
-    const float *scales = v ? a.pg.vs : a.pg.ks;
     const int pitch = D == 64 && a.box == 1 ? 128 : D;
     // 16 codes at a time: chunk y of a row's 64 dims.  8 lanes that go together have rows x and
     // x ^ 5, so that they meet no bank twice, neither among the codes (128-byte rows are swizzled)
@@ -702,11 +714,19 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
           const bool ok = there(page);
           const uint32_t c = g >> 2;
           const int q = g & 3;
-          if (page != INT32_MIN && !ok) page_error(a.err, DC_LOC_RANGE, DHS_SITE_PAGE_CHUNK);
-          const uint32_t bad = __ballot_sync(0xffffffffu, page != INT32_MIN && !ok);
-          if (!v && lane == 0) bad_of(c)[q] = bad;
-          const int64_t row = ok ? ((int64_t)page * a.pg.hkv + it.kvh) * a.pg.rows + in : 0;
-          cp_async_4_or_0(scales_of(c) + (v ? 128 : 0) + 32 * q + lane, scales + row, ok ? 4 : 0);
+          if (!v) {  // (the softmax wants both scales with the keys)
+            const bool gone = page != INT32_MIN && !ok;
+            if (gone) {
+              page_error(a.err, DC_LOC_RANGE, DHS_SITE_PAGE_CHUNK);
+              *missing = 1;
+            }
+            const uint32_t bad = __ballot_sync(0xffffffffu, gone);
+            if (lane == 0) bad_of(c)[q] = bad;
+            const int64_t row = ok ? ((int64_t)page * a.pg.hkv + it.kvh) * a.pg.rows + in : 0;
+            float *to = scales_of(c) + 32 * q + lane;
+            cp_async_4_or_0(to, a.pg.ks + row, ok ? 4 : 0);
+            cp_async_4_or_0(to + 128, a.pg.vs + row, ok ? 4 : 0);
+          }
           // a box is in one page: any of its positions that is there tells which
           const int first = lane & ~(a.box - 1);
           const uint32_t all = a.box == 32 ? ~0u : (1u << a.box) - 1u;
@@ -769,10 +789,7 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
         cp_async_wait_group<1>();  // this quarter's scales are in (the next one's may be under way)
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&full[slot]);
-          mbar_arrive(&known[c % C::NE]);
-        }
+        if (lane == 0) mbar_arrive(&full[slot]);
       }
       tn += max(it.n0, it.n1);
       if (given_up()) break;
@@ -871,23 +888,24 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
     const int i = warp >> 3, hg = (warp >> 2) & 1, m = tid & 127;
     const int tloc = m / a.G, h = m - tloc * a.G;
     const int pair = 1 + i * 4 + (warp & 3);  // barrier of the two warps of these rows
-    const int rows = 9 + (warp & 3);          // of these and the other row tile's
     const uint32_t lrow = (uint32_t)((warp & 3) * 32) << 16;
     // this thread's half of the row's scores, and of its output columns
-    const uint32_t tS = tmem + lrow + i * kChN, tO = tmem + lrow + 2 * kChN + i * D + hg * (D / 2);
+    const uint32_t tS = tmem + lrow + i * kChN + hg * kChH;
+    const uint32_t tP = tmem + lrow + i * kChN + hg * (kChH / 2);
+    const uint32_t tO = tmem + lrow + 2 * kChN + i * D + hg * (D / 2);
     float *red = reinterpret_cast<float *>(smem + C::OFF_RED) + i * 256;
     const float sl2 = a.scale_log2;
     const uint64_t sl22 = pack_f32x2(sl2, sl2);
-    uint32_t sn = 0, on = 0;
+    uint32_t sn = 0, pieces = 0, hn = 0;  // key tiles of this row tile; pieces walked as two halves
     for (int k = 0;; ++k) {
       // the piece stays in shared memory until its rows are written: few of its fields are
       // wanted in the loop, where registers are short
       wait(&item_full[k & 1], item_par(k));
       __syncwarp();
       volatile const ChunkItem &it = item_of(k);
-      // (the warps of these rows leave together: they meet at barriers below, also after a
-      // wait has run out)
-      if (named_or(rows, 128, *abort_v != 0) || it.row0 < 0) break;
+      // (the warps of a pair leave together: they meet at barriers below, also after a wait
+      // has run out)
+      if (named_or(pair, 64, *abort_v != 0) || it.row0 < 0) break;
       // one row tile of several key tiles: row tile 0's threads have the even tiles, row tile
       // 1's the odd ones, of the same rows
       const bool dual = it.n1 == 0 && it.n0 > 1;
@@ -907,17 +925,17 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
       float m_run = -CUDART_INF_F, l = 0.f;
       const int ns = WIN ? it.ns : 0, gap = WIN ? it.gap : 0;
       for (int n = 0; n < ni; ++n, ++sn, en += tstep, tile += tstep) {
-        wait(&known[en % C::NE], (en / C::NE) & 1u);
         wait(&s_full[i], sn & 1u);
         __syncwarp();
         tc_fence_after();
         uint32_t s0[32], s1[32];
-        tmem_ld32(tS + hg * kChH, s0);
-        tmem_ld32(tS + hg * kChH + 32, s1);
+        tmem_ld32(tS, s0);
+        tmem_ld32(tS + 32, s1);
         tmem_wait_ld();
         const int first = (WIN ? tile_of(ns, gap, tile) : tile) * kChN;
         const float *sc = scales_of(en) + hg * kChH;
-        const uint2 out_of = *reinterpret_cast<const uint2 *>(bad_of(en) + hg * 2);
+        uint2 out_of = make_uint2(0u, 0u);  // positions that are not there
+        if (*missing) out_of = *reinterpret_cast<const uint2 *>(bad_of(en) + hg * 2);
         const bool masked = first + kChN > least || (out_of.x | out_of.y) != 0u ||
                             (WIN && first < wend && first + kChN > a.sinks);
         if (W8) {
@@ -1022,9 +1040,9 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
           }
         };
         weights(s0, sc + 128, hid0);
-        tmem_st16(tS + hg * (kChH / 2), p);
+        tmem_st16(tP, p);
         weights(s1, sc + 160, hid1);
-        tmem_st16(tS + hg * (kChH / 2) + 16, p);
+        tmem_st16(tP + 16, p);
         {
           float l0, l1;
           unpack_f32x2(l2, l0, l1);
@@ -1038,8 +1056,7 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
       red[hg * 128 + m] = l;
       bool bad = false;
       if (ni > 0) {
-        wait(&pv_done[i], on & 1u);
-        ++on;
+        wait(&pv_done[i], pieces++ & 1u);
         __syncwarp();
         tc_fence_after();
       }
@@ -1050,8 +1067,11 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
         named_sync(pair, 64);
         red[hg * 128 + m] = hg ? l : m_run;
         tc_fence_before();
-        named_sync(rows, 128);  // they may read
-        named_sync(rows, 128);  // they have read
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&half_in[warp & 3]);
+        wait(&half_read[warp & 3], hn & 1u);
+        ++hn;
+        __syncwarp();
         if (lane == 0) {
           mbar_arrive(&o_empty[1]);
           mbar_arrive(&item_empty[k & 1]);
@@ -1071,7 +1091,10 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
 #pragma unroll
         for (int x = 0; x < D / 2; ++x) o[x] = 0u;
       }
-      if (dual) named_sync(rows, 128);  // the other half is there
+      if (dual) {  // the other half is there
+        wait(&half_in[warp & 3], hn & 1u);
+        ++hn;
+      }
       // Rows of a piece for which a wait ran out (whoever's it was: it is known by the time
       // what it waited for arrives here) are not written, nor half of them.
       const bool lost = named_or(pair, 64, *abort_v != 0);
@@ -1097,7 +1120,8 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
             o[c + e] = __float_as_uint(__uint_as_float(o[c + e]) * f0 + __uint_as_float(x[e]) * f1);
         }
         tc_fence_before();
-        named_sync(rows, 128);  // read
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&half_read[warp & 3]);
       }
       const int tok = ti * a.tpt + tloc, ntok = it.ntok, p0 = it.p0, slot = it.slot;
       const int row0 = it.row0, kvh = it.kvh, seq = it.seq, j0 = it.j0;
@@ -1179,36 +1203,43 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
   if (tid == 0) a.status[blockIdx.x] = *abort_v;
 }
 
-// Joins an item's parts: sum_p w_p O_p / sum_p w_p l_p, w_p = 2^(m_p - max m).  Block (b, y):
-// rows 32 y .. of the item that CTA b begins and others go on with, a row at a time in a warp.
+// Joins the items' parts: sum_p w_p O_p / sum_p w_p l_p, w_p = 2^(m_p - max m).  Every block
+// lists the items that were cut, and all warps share their rows, a row at a time.
+constexpr int kChMostCtas = 256;
 template <int D>
 __global__ void __launch_bounds__(256)
 k_chunk_join(const __grid_constant__ ChunkArgs a, int ctas) {
-  constexpr int V = D / 32;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.x;
+  constexpr int V = D / 32, AHEAD = 8;  // dims of a lane; parts under way at a time
+  __shared__ int begun[kChMostCtas], cut, lost;
+  __shared__ unsigned char goes_on[kChMostCtas];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) cut = lost = 0;
+  __syncthreads();
   pdl_wait();
-  const int4 pl = a.plan[2 * b];
-  const int p0 = a.plan[2 * b + 1].x;
+  if (threadIdx.x < ctas) {
+    const int4 pl = a.plan[2 * threadIdx.x];
+    goes_on[threadIdx.x] = a.plan[2 * threadIdx.x + 1].y != 0;
+    if (pl.w >= 0) begun[atomicAdd(&cut, 1)] = threadIdx.x;
+    if (a.status[threadIdx.x]) lost = 1;
+  }
+  __syncthreads();
   // a wait that ran out in any CTA: no row is joined (which of them are whole is not known)
-  int lost = 0;
-  if (pl.w >= 0)
-    for (int c = threadIdx.x; c < ctas; c += 256) lost |= a.status[c];
-  if (__syncthreads_or(lost) || pl.w < 0) return;
-  for (int x = warp; x < 32; x += 8) {
-    const int w = blockIdx.y * 32 + x, i = w >> 7, m = w & 127;
+  if (lost) return;
+  for (int e = blockIdx.x * 8 + warp; e < cut * 256; e += gridDim.x * 8) {
+    const int w = e % 256, i = w >> 7, m = w & 127, b = begun[e / 256];
+    const int4 pl = a.plan[2 * b];
     const int tloc = m / a.G, h = m - tloc * a.G, tok = i * a.tpt + tloc;
     if (tloc >= a.tpt || tok >= pl.y) continue;
     float top = -CUDART_INF_F, den = 0.f, acc[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.f;
-    // (eight parts' loads are under way at a time)
-    for (int c0 = b; c0 <= pl.w; c0 += 8) {
-      float2 ml[8];
-      float o[8][V];
+    for (int c0 = b; c0 <= pl.w; c0 += AHEAD) {
+      float2 ml[AHEAD];
+      float o[AHEAD][V];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < AHEAD; ++u) {
         const int c = c0 + u;
-        const bool in = c <= pl.w && (c == b || a.plan[2 * min(c, ctas - 1) + 1].y != 0);
+        const bool in = c <= pl.w && (c == b || goes_on[c]);
         const int64_t place = ((int64_t)c * 2 + (c == b ? 1 : 0)) * 256 + w;
         ml[u] = in ? a.ml[place] : make_float2(-CUDART_INF_F, 0.f);
 #pragma unroll
@@ -1221,7 +1252,7 @@ k_chunk_join(const __grid_constant__ ChunkArgs a, int ctas) {
       }
       float now = top;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) now = fmaxf(now, ml[u].x);
+      for (int u = 0; u < AHEAD; ++u) now = fmaxf(now, ml[u].x);
       // (a part that saw nothing weighs nothing; one of NaN scores has m = -inf too)
       const float f0 = top == -CUDART_INF_F ? (den != den ? 1.f : 0.f) : ex2_approx(top - now);
       den *= f0;
@@ -1229,7 +1260,7 @@ k_chunk_join(const __grid_constant__ ChunkArgs a, int ctas) {
       for (int v = 0; v < V; ++v) acc[v] *= f0;
       top = now;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < AHEAD; ++u) {
         const float f = ml[u].x == -CUDART_INF_F ? (ml[u].y != ml[u].y ? 1.f : 0.f)
                                                  : ex2_approx(ml[u].x - now);
         den += ml[u].y * f;
@@ -1238,7 +1269,7 @@ k_chunk_join(const __grid_constant__ ChunkArgs a, int ctas) {
       }
     }
     const int64_t row = (int64_t)(pl.x + tok) * a.hq + pl.z * a.G + h;
-    const bool sees = p0 + tok >= 0;
+    const bool sees = a.plan[2 * b + 1].x + tok >= 0;
     const float inv = 1.f / den;
 #pragma unroll
     for (int v = 0; v < V; v += 2)
@@ -1255,6 +1286,9 @@ bool chunk_args(const dhs_pages *pages, int64_t n_tok, int32_t n_seqs, int32_t h
   return page_view(pages, pg) && n_tok >= 0 && n_tok <= INT32_MAX - 256 && n_seqs >= 0 &&
          n_seqs <= kMaxSeqs && hq >= 1 && hq % pg->hkv == 0 && hq / pg->hkv <= 128;
 }
+
+// CTAs of a call, one on an SM; 0 on failure.
+int chunk_ctas(int dev) { return std::min(device_sms(dev), kChMostCtas); }
 
 // Workspace of n CTAs: parts, their maxima and sums, plan and status; parts start at the next
 // 32-byte boundary.
@@ -1311,8 +1345,8 @@ extern "C" int64_t dhs_page_chunk_workspace(const dhs_pages *pages, int64_t n_to
     cudaGetLastError();
     return -1;
   }
-  const int sms = device_sms(dev);
-  return sms < 1 ? -1 : chunk_bytes(sms, pg.d);
+  const int ctas = chunk_ctas(dev);
+  return ctas < 1 ? -1 : chunk_bytes(ctas, pg.d);
 }
 
 extern "C" int dhs_page_chunk(const dhs_pages *pages, const void *q, const int64_t *q_strides,
@@ -1347,10 +1381,10 @@ extern "C" int dhs_page_chunk(const dhs_pages *pages, const void *q, const int64
     cudaGetLastError();
     return DHS_ERR_CUDA;
   }
-  const int sms = device_sms(dev);
+  const int ctas = chunk_ctas(dev);
   EncodeTiled enc = encoder();
-  if (sms < 1 || !enc) return DHS_ERR_CUDA;
-  if (workspace_bytes < chunk_bytes(sms, (int)d)) return DHS_ERR_INVALID;
+  if (ctas < 1 || !enc) return DHS_ERR_CUDA;
+  if (workspace_bytes < chunk_bytes(ctas, (int)d)) return DHS_ERR_INVALID;
   a.cu = cu;
   a.lens = seq_lens;
   a.table = page_table;
@@ -1358,9 +1392,9 @@ extern "C" int dhs_page_chunk(const dhs_pages *pages, const void *q, const int64
   a.lse = lse;
   unsigned char *w = reinterpret_cast<unsigned char *>(((uintptr_t)workspace + 31) & ~(uintptr_t)31);
   a.parts = reinterpret_cast<float *>(w);
-  a.ml = reinterpret_cast<float2 *>(w + (int64_t)sms * 2 * 256 * d * 4);
-  a.plan = reinterpret_cast<int4 *>(a.ml + (int64_t)sms * 2 * 256);
-  a.status = reinterpret_cast<int32_t *>(a.plan + 2 * sms);
+  a.ml = reinterpret_cast<float2 *>(w + (int64_t)ctas * 2 * 256 * d * 4);
+  a.plan = reinterpret_cast<int4 *>(a.ml + (int64_t)ctas * 2 * 256);
+  a.status = reinterpret_cast<int32_t *>(a.plan + 2 * ctas);
   a.err = err;
   a.n_tok = n_tokens;
   a.n_seqs = n_seqs;
@@ -1394,7 +1428,7 @@ extern "C" int dhs_page_chunk(const dhs_pages *pages, const void *q, const int64
     static DeviceSmem granted;
     cudaError_t e = granted.ensure(kern, C::SMEM, dev);
     if (e == cudaSuccess)
-      e = launch_prio(kern, dim3((unsigned)sms), dim3(C::THREADS), (size_t)C::SMEM, s, mq, mk, mv, a);
+      e = launch_prio(kern, dim3((unsigned)ctas), dim3(C::THREADS), (size_t)C::SMEM, s, mq, mk, mv, a);
     return e;
   };
   auto kinds = [&](auto dim, auto win) -> cudaError_t {
@@ -1407,7 +1441,7 @@ extern "C" int dhs_page_chunk(const dhs_pages *pages, const void *q, const int64
       default: e = run(k_chunk<D, DHS_PAGE_E4M3, W>, ChCfg<D, DHS_PAGE_E4M3>(), win); break;
     }
     if (e == cudaSuccess)
-      e = launch_pdl(k_chunk_join<D>, dim3((unsigned)sms, 8), dim3(256), 0, s, a, sms);
+      e = launch_pdl(k_chunk_join<D>, dim3((unsigned)(4 * ctas)), dim3(256), 0, s, a, ctas);
     return e;
   };
   auto windows = [&](auto dim) -> cudaError_t {
