@@ -68,7 +68,8 @@ constexpr uint32_t dhs_chunk_wait_us = 2000000;
 constexpr float kChRescale = 8.f;
 constexpr uint32_t kChCols = 512;   // tensor memory: S0, S1 (P over them), O0, O1
 constexpr int kChOver = 3 * kChN;   // what an item costs besides its positions
-constexpr int kChLeast = 5 * kChN;  // cost of a CTA's share at least
+constexpr int kChLone = 3;          // quarters of a position's cost where there is one row tile
+constexpr int kChLeast = 3 * kChN;  // cost of a CTA's share at least
 constexpr int kChSnap = 2;          // tiles of a part at least
 
 struct ChunkArgs {
@@ -205,15 +206,16 @@ struct ChunkSchedule {
     const int64_t left = a.cap - 1 - max(o, 0);
     return left < span ? 0 : (int64_t)((uint32_t)left / (uint32_t)span);
   }
-  // cost of a sequence's first j items
-  __device__ int64_t upto(int j, int o, int64_t m) const {
+  // cost of a sequence's first j items; a single row tile has two key tiles at a time
+  __device__ int64_t upto(int j, int n, int o, int64_t m) const {
     const int64_t x = min((int64_t)j, m);
+    if (n <= a.tpt) return j == 0 ? 0 : (x * (max(o, 0) + span) + (j - x) * a.cap) * kChLone / 4 + kChOver;
     return x * max(o, 0) + (int64_t)span * (x * (x + 1) / 2) + (j - x) * a.cap + (int64_t)j * kChOver;
   }
   __device__ int64_t cost_of(int i, bool record) const {
     int x0, n, o;
     if (i >= a.n_seqs || !chunk_seq(a, i, x0, n, o, record)) return 0;
-    return upto((int)((uint32_t)(n + span - 1) / (uint32_t)span), o, below_cap(o)) * hkv;
+    return upto((int)((uint32_t)(n + span - 1) / (uint32_t)span), n, o, below_cap(o)) * hkv;
   }
   __device__ int64_t border(int b) const {
     return share * b + (int64_t)((uint32_t)rest * (uint32_t)b / (uint32_t)n_cta);
@@ -231,7 +233,7 @@ struct ChunkSchedule {
     off = __shfl_sync(0xffffffffu, my_off, i - base);
     R = (int)((uint32_t)(nq + span - 1) / (uint32_t)span);
     m = below_cap(off);
-    per = upto(R, off, m);
+    per = upto(R, nq, off, m);
   }
   __device__ ChunkSchedule(const ChunkArgs &args, int l) : a(args), lane(l) {
     span = 2 * a.tpt;
@@ -279,11 +281,11 @@ struct ChunkSchedule {
     int lo = 0, hi = R - 1;  // the last item that starts at or before `begin`
     while (lo < hi) {
       const int mid = (int)(((int64_t)lo + hi + 1) >> 1);
-      if (at + upto(mid, off, m) <= begin) lo = mid;
+      if (at + upto(mid, nq, off, m) <= begin) lo = mid;
       else hi = mid - 1;
     }
     r = lo;
-    at += upto(r, off, m);
+    at += upto(r, nq, off, m);
   }
   // (of an item of nt tiles that starts at `at` and costs c) the tile at which border x cuts it
   __device__ int cut(int64_t x, int64_t c, int nt) const {
@@ -293,7 +295,7 @@ struct ChunkSchedule {
   }
   __device__ bool next(ChunkItem &it) {
     while (seq < a.n_seqs && at < end) {
-      const int64_t c = R > 0 ? upto(r + 1, off, m) - upto(r, off, m) : 0;
+      const int64_t c = R > 0 ? upto(r + 1, nq, off, m) - upto(r, nq, off, m) : 0;
       bool own = false;
       if (R > 0) {
         const int tok0 = r * span, ntok = min(span, nq - tok0), p0 = off + tok0;
