@@ -1211,7 +1211,7 @@ constexpr int kChMostCtas = 256;
 template <int D>
 __global__ void __launch_bounds__(256)
 k_chunk_join(const __grid_constant__ ChunkArgs a, int ctas) {
-  constexpr int V = D / 32, AHEAD = 8;  // dims of a lane; parts under way at a time
+  constexpr int V = D / 32, AHEAD = 4;  // dims of a lane; parts under way at a time
   __shared__ int begun[kChMostCtas], cut, lost;
   __shared__ unsigned char goes_on[kChMostCtas];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1443,7 +1443,7 @@ extern "C" int dhs_page_chunk(const dhs_pages *pages, const void *q, const int64
       default: e = run(k_chunk<D, DHS_PAGE_E4M3, W>, ChCfg<D, DHS_PAGE_E4M3>(), win); break;
     }
     if (e == cudaSuccess)
-      e = launch_pdl(k_chunk_join<D>, dim3((unsigned)(4 * ctas)), dim3(256), 0, s, a, ctas);
+      e = launch_pdl(k_chunk_join<D>, dim3((unsigned)(8 * ctas)), dim3(256), 0, s, a, ctas);
     return e;
   };
   auto windows = [&](auto dim) -> cudaError_t {
