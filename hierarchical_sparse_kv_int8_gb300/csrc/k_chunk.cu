@@ -1212,21 +1212,28 @@ template <int D>
 __global__ void __launch_bounds__(256)
 k_chunk_join(const __grid_constant__ ChunkArgs a, int ctas) {
   constexpr int V = D / 32, AHEAD = 4;  // dims of a lane; parts under way at a time
-  __shared__ int begun[kChMostCtas], cut, lost;
+  __shared__ int begun[kChMostCtas], counts[8];
   __shared__ unsigned char goes_on[kChMostCtas];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0) cut = lost = 0;
-  __syncthreads();
   pdl_wait();
+  // (in the order of the CTAs: all blocks go by the same list)
+  bool begins = false, lost = false;
   if (threadIdx.x < ctas) {
-    const int4 pl = a.plan[2 * threadIdx.x];
+    begins = a.plan[2 * threadIdx.x].w >= 0;
     goes_on[threadIdx.x] = a.plan[2 * threadIdx.x + 1].y != 0;
-    if (pl.w >= 0) begun[atomicAdd(&cut, 1)] = threadIdx.x;
-    if (a.status[threadIdx.x]) lost = 1;
+    lost = a.status[threadIdx.x] != 0;
   }
-  __syncthreads();
+  const uint32_t some = __ballot_sync(0xffffffffu, begins);
+  if (lane == 0) counts[warp] = __popc(some);
   // a wait that ran out in any CTA: no row is joined (which of them are whole is not known)
-  if (lost) return;
+  if (__syncthreads_or(lost)) return;
+  int cut = 0, at = 0;
+  for (int w = 0; w < 8; ++w) {
+    if (w == warp) at = cut;
+    cut += counts[w];
+  }
+  if (begins) begun[at + __popc(some & ((1u << lane) - 1u))] = threadIdx.x;
+  __syncthreads();
   for (int e = blockIdx.x * 8 + warp; e < cut * 256; e += gridDim.x * 8) {
     const int w = e % 256, i = w >> 7, m = w & 127, b = begun[e / 256];
     const int4 pl = a.plan[2 * b];
