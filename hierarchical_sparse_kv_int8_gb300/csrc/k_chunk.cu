@@ -33,8 +33,7 @@
 // Work split.  An item's cost is taken as the positions it walks and some tiles' worth for its
 // own sake; all items' costs are laid end to end, sequence by sequence, and CTA b of n takes
 // the b-th n-th.  An item cut by such a border is walked in parts by several CTAs, which leave
-// (O, m, l) in the workspace for a join; a border within two tiles of an item's end is moved
-// there.  Every CTA so has the same work whatever the lengths are (one chunk of a long prompt
+// (O, m, l) in the workspace for a join; a border near an item's end is moved there.  Every CTA so has the same work whatever the lengths are (one chunk of a long prompt
 // beside sequences that decode one token), and the sums of costs have a closed form, so that a
 // CTA finds its place by two searches.  Lengths are read on the device, and bits repeat.
 #include "pages_internal.cuh"
@@ -70,7 +69,11 @@ constexpr uint32_t kChCols = 512;   // tensor memory: S0, S1 (P over them), O0, 
 constexpr int kChOver = 3 * kChN;   // what an item costs besides its positions
 constexpr int kChLone = 3;          // quarters of a position's cost where there is one row tile
 constexpr int kChLeast = 3 * kChN;  // cost of a CTA's share at least
-constexpr int kChSnap = 2;          // tiles of a part at least
+// A border this many tiles from an item's end, or fewer, is moved there: an eighth of a share, 2
+// to 8 tiles.  A cut costs what a CTA writes and the join reads for it, so long shares rather
+// differ by as much (4096 and 2485 new
+// tokens in a window of 1024, 32 heads over 8 of 64 dims, bf16: 181 us with 2 tiles at most, 137 with 8), short ones, whose time is the longest share's, do not.
+constexpr int kChSnap = 2, kChSnapMost = 8, kChSnapPart = 8;
 
 struct ChunkArgs {
   PageView pg;
@@ -291,7 +294,8 @@ struct ChunkSchedule {
   __device__ int cut(int64_t x, int64_t c, int nt) const {
     // (both CTAs at a border work out the same numbers)
     const int t = min(nt, (int)((float)nt * ((float)(x - at) / (float)c)));
-    return t < kChSnap ? 0 : nt - t < kChSnap ? nt : t;
+    const int snap = (int)max((int64_t)kChSnap, min((int64_t)kChSnapMost, share / (kChSnapPart * kChN)));
+    return t < snap ? 0 : nt - t < snap ? nt : t;
   }
   __device__ bool next(ChunkItem &it) {
     while (seq < a.n_seqs && at < end) {
