@@ -71,8 +71,9 @@ constexpr int kChLone = 3;          // quarters of a position's cost where there
 constexpr int kChLeast = 3 * kChN;  // cost of a CTA's share at least
 // A border this many tiles from an item's end, or fewer, is moved there: an eighth of a share, 2
 // to 8 tiles.  A cut costs what a CTA writes and the join reads for it, so long shares rather
-// differ by as much (4096 and 2485 new
-// tokens in a window of 1024, 32 heads over 8 of 64 dims, bf16: 181 us with 2 tiles at most, 137 with 8), short ones, whose time is the longest share's, do not.
+// differ by as much (4096 and 2485 new tokens in a window of 1024, 32 heads over 8 of 64 dims,
+// bf16: 181 us with 2 tiles at most, 137 with 8), short ones, whose time is the longest share's,
+// do not.
 constexpr int kChSnap = 2, kChSnapMost = 8, kChSnapPart = 8;
 
 struct ChunkArgs {

@@ -361,3 +361,19 @@ def test_chunk_refuses_tensors_that_do_not_fit(torch, dhs):
         call(q, cu, pc.seq_lens, pc.table, torch.empty_like(q), ws, sinks=3)
     with pytest.raises(ValueError):
         pc.cache.chunk_workspace(4, 1, 3)
+
+
+@pytest.mark.parametrize("kind", [INT8, E4M3])
+def test_chunk_sequences_over_the_same_pages(torch, dhs, kind):
+    """Sequences that share their pages, together longer than the cache."""
+    n, t, new, hq, d = 14, 600, 300, 4, 64
+    pc = Paged(torch, dhs, [t], 32, 1, d, kind)
+    kv = pc.fill()
+    pc.table = pc.table.expand(n, -1).contiguous()
+    pc.seq_lens = pc.seq_lens.expand(n).contiguous()
+    pc.lens = [t] * n
+    _chunk(torch, dhs, pc, kv * n, [new] * n, hq)
+    pc.seq_lens = (pc.seq_lens - torch.arange(n, dtype=torch.int32).cuda() * 7).contiguous()
+    pc.lens = [t - 7 * i for i in range(n)]
+    _chunk(torch, dhs, pc, [[x[:t - 7 * i] for x in kv[0]] for i in range(n)], [new - 9 * i for i in range(n)], hq,
+           window=130, sinks=5)
