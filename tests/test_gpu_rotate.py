@@ -314,3 +314,28 @@ def test_append_captured_follows_lengths_and_on_another_stream(torch, dhs):
         for a, b in ((pc.cache.k, ref.cache.k), (pc.cache.v, ref.cache.v)):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
     pc.cache.check()
+
+
+def test_append_far_pages_and_more_heads_than_a_launch_has_rows_of(torch, dhs):
+    """Pages whose elements lie beyond 2^31, and 70000 heads of queries."""
+    rows, hkv, d = 64, 2, 64
+    pc = Paged(torch, dhs, [130], rows, hkv, d, INT8, huge_pages=2 ** 31 // (rows * hkv * d) + 9)
+    ref = Paged(torch, dhs, [130], rows, hkv, d, INT8)
+    rot = dhs.Rotation(_freqs(32))
+    g = torch.Generator().manual_seed(2)
+    k, v = (torch.randn((3, hkv, d), generator=g).bfloat16().cuda() for _ in range(2))
+    cu = torch.tensor([0, 3], dtype=torch.int32).cuda()
+    for p in (pc, ref):
+        p.cache.append(None, k, v, cu, p.seq_lens, p.table, None, rot)
+        p.cache.check()
+    at, to = pc.table[0, :3].long(), ref.table[0, :3].long()
+    assert int(at.max()) * rows * hkv * d > 2 ** 31
+    for a, b in ((pc.cache.k, ref.cache.k), (pc.cache.v, ref.cache.v), (pc.cache.k_scale, ref.cache.k_scale)):
+        assert torch.equal(a[at].view(torch.uint8), b[to].view(torch.uint8))
+    q = torch.randn((2, 70000, d), generator=g).bfloat16().cuda()
+    pos = torch.tensor([5, 100000], dtype=torch.int32).cuda()
+    out, few = torch.empty_like(q), torch.empty((2, 7, d), dtype=torch.bfloat16, device="cuda")
+    dhs.rotate(q, None, pos, rot, out, None)
+    for h in (0, 35000, 69993):
+        dhs.rotate(q[:, h:h + 7], None, pos, rot, few, None)
+        assert torch.equal(out[:, h:h + 7], few)
