@@ -115,25 +115,30 @@ def _rows(t, name, index):
 
 
 def _strides(name, t, index):
-    """Token and head stride of a packed bf16 tensor; like _rows, sooner for the usual one."""
-    if t.dtype is _BF16 and t.is_contiguous() and t.get_device() == index and t.dim() == 3:
-        _, h, d = t.shape
-        return h * d, d
-    return _rows(t, name, index)[3:]
+    """Shape of a packed bf16 tensor, and its token's and head's stride; like _rows, sooner for
+    the usual one."""
+    shape = t.shape
+    if t.dtype is _BF16 and len(shape) == 3 and t.get_device() == index and t.is_contiguous():
+        d = shape[2]
+        return shape, shape[1] * d, d
+    return (shape, *_rows(t, name, index)[3:])
 
 
 def _heads(name, x, out, norm, index):
-    """A dhs_heads: a tensor's heads, [tokens, heads, head_dim], and where they go."""
-    xt, xh = _strides(name, x, index)
-    shape, at, ot, oh = x.shape, None, 0, 0
-    if out is not None:
-        if out.shape != shape:
-            raise ValueError("%s_out: %s expected, not %s" % (name, tuple(shape), tuple(out.shape)))
-        ot, oh = _strides(name + "_out", out, index)
+    """The shape of a tensor's heads, [tokens, heads, head_dim], and a dhs_heads: they and where
+    they go."""
+    shape, xt, xh = _strides(name, x, index)
+    at = ot = oh = weights = 0
+    if out is x:
+        at, ot, oh = x.data_ptr(), xt, xh
+    elif out is not None:
+        to, ot, oh = _strides(name + "_out", out, index)
+        if to != shape:
+            raise ValueError("%s_out: %s expected, not %s" % (name, tuple(shape), tuple(to)))
         at = out.data_ptr()
-    return _HEADS.pack(x.data_ptr(), at or 0,
-                       0 if norm is None else _plain(norm, name + "_norm", _F32, shape[2:], index),
-                       xt, xh, ot, oh, shape[1])
+    if norm is not None:
+        weights = _plain(norm, name + "_norm", _F32, shape[2:], index)
+    return shape, _HEADS.pack(x.data_ptr(), at, weights, xt, xh, ot, oh, shape[1])
 
 
 def _turns(rotation, index):
@@ -231,11 +236,15 @@ def rotate(q, k, positions, rotation, q_out, k_out, q_norm=None, k_norm=None, ep
     if ix < 0 or _current_device() != ix:
         with _on(ix):
             return rotate(q, k, positions, rotation, q_out, k_out, q_norm, k_norm, eps, stream)
-    hq = None if q is None else _heads("q", q, q_out, q_norm, ix)
-    hk = None if k is None else _heads("k", k, k_out, k_norm, ix)
-    n, _, d = some.shape
-    if hk is not None and (k.shape[0] != n or k.shape[2] != d):
-        raise ValueError("k: [%d, kv_heads, %d] expected, not %s" % (n, d, tuple(k.shape)))
+    hq = hk = None
+    if q is not None:
+        (n, _, d), hq = _heads("q", q, q_out, q_norm, ix)
+    if k is not None:
+        (nk, _, dk), hk = _heads("k", k, k_out, k_norm, ix)
+        if hq is None:
+            n, d = nk, dk
+        elif nk != n or dk != d:
+            raise ValueError("k: [%d, kv_heads, %d] expected, not %s" % (n, d, tuple(k.shape)))
     rc = _lib().dhs_rotate(_turns(rotation, ix), hq, hk, eps, d, n,
                            None if positions is None else _plain(positions, "positions", _I32, (n,), ix),
                            _raw(stream, ix))
@@ -324,16 +333,16 @@ class PageCache:
             with _on(ix):
                 return self.append(q, k, v, cu, seq_lens, page_table, q_out, rotation, q_norm, k_norm,
                                    eps, positions, k_out, stream)
-        hk = _heads("k", k, k_out, k_norm, ix)
-        vt, vh = _strides("v", v, ix)
-        tok, h, d = k.shape
-        if d != self.head_dim or h != self.kv_heads or v.shape != k.shape:
+        ks, hk = _heads("k", k, k_out, k_norm, ix)
+        vs, vt, vh = _strides("v", v, ix)
+        tok, h, d = ks
+        if d != self.head_dim or h != self.kv_heads or vs != ks:
             raise ValueError("k and v: [tokens, %d, %d] expected, not %s and %s" % (
                 self.kv_heads, self.head_dim, tuple(k.shape), tuple(v.shape)))
         hq = None
         if q is not None:
-            hq = _heads("q", q, q_out, q_norm, ix)
-            if q.shape[0] != tok or q.shape[2] != d:
+            (nq, _, dq), hq = _heads("q", q, q_out, q_norm, ix)
+            if nq != tok or dq != d:
                 raise ValueError("q: [%d, q_heads, %d] expected, not %s" % (tok, d, tuple(q.shape)))
         n = seq_lens.shape[0]
         rc = self._lib.dhs_page_append(
@@ -410,8 +419,8 @@ class PageCache:
             with _on(ix):
                 return self.attend_chunk(q, cu, seq_lens, page_table, out, workspace, lse, window,
                                          sinks, scale, stream)
-        qt, qh = _strides("q", q, ix)
-        tok, hq, d = q.shape
+        shape, qt, qh = _strides("q", q, ix)
+        tok, hq, d = shape
         if d != self.head_dim:
             raise ValueError("q: [tokens, q_heads, %d] expected, not %s" % (self.head_dim, tuple(q.shape)))
         n = seq_lens.shape[0]
@@ -420,7 +429,7 @@ class PageCache:
             self._ref, q.data_ptr(), None if qt == hq * d and qh == d else _Strides2(qt, qh), tok,
             _plain(cu, "cu", _I32, (n + 1,), ix), _plain(seq_lens, "seq_lens", _I32, (n,), ix),
             _table(page_table, n, ix), page_table.shape[1], n, hq, window, sinks, scale,
-            _plain(out, "out", _BF16, q.shape, ix),
+            _plain(out, "out", _BF16, shape, ix),
             None if lse is None else _plain(lse, "lse", _F32, (tok, hq), ix), space, nbytes,
             self._err, _raw(stream, ix))
         if rc:
