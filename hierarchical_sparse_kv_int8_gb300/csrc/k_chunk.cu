@@ -367,6 +367,7 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
     return *reinterpret_cast<ChunkItem *>(smem + C::OFF_ITEM + (k & 1) * 64);
   };
   if ((smem_u32(smem) & 1023u) != 0u) {  // (the swizzle pattern follows address bits)
+    pdl_wait();
     if (threadIdx.x == 0) {
       a.status[blockIdx.x] = 1;
       a.plan[2 * blockIdx.x] = make_int4(0, 0, 0, -1);
@@ -416,6 +417,7 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
     tma_prefetch(&mk);
     tma_prefetch(&mv);
   }
+  pdl_wait();     // (what is above needs nothing of the launch before)
   pdl_trigger();  // the join may be placed; it waits for this grid's end
   tc_fence_before();
   __syncthreads();
@@ -1449,7 +1451,7 @@ extern "C" int dhs_page_chunk(const dhs_pages *pages, const void *q, const int64
     static DeviceSmem granted;
     cudaError_t e = granted.ensure(kern, C::SMEM, dev);
     if (e == cudaSuccess)
-      e = launch_prio(kern, dim3((unsigned)ctas), dim3(C::THREADS), (size_t)C::SMEM, s, mq, mk, mv, a);
+      e = launch_pdl(kern, dim3((unsigned)ctas), dim3(C::THREADS), (size_t)C::SMEM, s, mq, mk, mv, a);
     return e;
   };
   auto kinds = [&](auto dim, auto win) -> cudaError_t {

@@ -75,6 +75,7 @@ k_rotate(const PageView pg, const RotateArgs a) {
   constexpr int L = D / 8, TOK = kRoThreads / L, U = kRoAhead;  // lanes of a row, tokens
   __shared__ int64_t dst[TOK];
   __shared__ int at_pos[TOK];
+  pdl_wait();
   const int sub = threadIdx.x % L, mine = threadIdx.x / L;
   const int64_t t0 = (int64_t)blockIdx.x * TOK, tok = t0 + mine;
   const bool there = tok < a.n_tok;
@@ -327,8 +328,8 @@ int launch(const PageView &pg, RotateArgs &a, int d, int kind, dhs_stream stream
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   auto go = [&](auto dim, auto k) {
     constexpr int D = decltype(dim)::value, K = decltype(k)::value;
-    return a.halves ? launch_prio(k_rotate<D, K, true>, grid, dim3(kRoThreads), 0, s, pg, a)
-                    : launch_prio(k_rotate<D, K, false>, grid, dim3(kRoThreads), 0, s, pg, a);
+    return a.halves ? launch_pdl(k_rotate<D, K, true>, grid, dim3(kRoThreads), 0, s, pg, a)
+                    : launch_pdl(k_rotate<D, K, false>, grid, dim3(kRoThreads), 0, s, pg, a);
   };
   auto kinds = [&](auto dim) {
     switch (kind) {
