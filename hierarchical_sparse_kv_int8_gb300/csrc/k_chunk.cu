@@ -33,9 +33,24 @@
 // Work split.  An item's cost is taken as the positions it walks and some tiles' worth for its
 // own sake; all items' costs are laid end to end, sequence by sequence, and CTA b of n takes
 // the b-th n-th.  An item cut by such a border is walked in parts by several CTAs, which leave
-// (O, m, l) in the workspace for a join; a border near an item's end is moved there.  Every CTA so has the same work whatever the lengths are (one chunk of a long prompt
-// beside sequences that decode one token), and the sums of costs have a closed form, so that a
-// CTA finds its place by two searches.  Lengths are read on the device, and bits repeat.
+// (O, m, l) in the workspace for a join; a border near an item's end is moved there.  Every CTA
+// so has the same work whatever the lengths are (one chunk of a long prompt beside sequences
+// that decode one token), and the sums of costs have a closed form, so that a CTA finds its
+// place by two searches.  Lengths are read on the device, and bits repeat.
+//
+// Measured, the two launches inside a captured graph (GB300, 1904 TFLOP/s and 6.77 TB/s
+// measured, 1687 TFLOP/s held for seconds):
+//   8192 new tokens at the end of 32768, 16 heads over 1, 128 dims: bf16 1.13 ms, 1700 TFLOP/s,
+//   the rate held under the power limit; int8 1.68, e4m3 1.75.  With codes the softmax threads
+//   have the scales' products beside their own (a tile's chain is 2700 cycles in bf16, 1400 of
+//   them softmax) and share their issue slots with the warps that turn codes.
+//   64 dims, bf16: 0.91 ms; S = Q K^T takes half the time, the softmax the same.
+//   64 sequences that decode one token each over up to 30000 positions: bf16 5.9 TB/s, 87 %;
+//   int8 2.55 TB/s, bound by turning codes of which one row tile makes use.
+//   4096 and 2485 new tokens in a window of 1024 with 4 sinks, 32 heads over 8, 64 dims: bf16
+//   136 us, e4m3 162: items of some ten tiles, of which an item's start and end take as much
+//   time as four.
+//   600 new tokens of one sequence, 8 heads over 1: 20 us, of which the tiles take 3.
 #include "pages_internal.cuh"
 #include "attn_tc.cuh"
 
@@ -411,13 +426,13 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     fence_proxy_async_smem();
   }
-  if (warp == kChMma) tmem_alloc(tmem_slot, kChCols);
   if (tid == kChLoad * 32 + 1) {
     tma_prefetch(&mq);
     tma_prefetch(&mk);
     tma_prefetch(&mv);
   }
-  pdl_wait();     // (what is above needs nothing of the launch before)
+  pdl_wait();  // (what is above needs nothing of the launch before, nor takes what it may want)
+  if (warp == kChMma) tmem_alloc(tmem_slot, kChCols);
   pdl_trigger();  // the join may be placed; it waits for this grid's end
   tc_fence_before();
   __syncthreads();

@@ -232,6 +232,8 @@ def rotate(q, k, positions, rotation, q_out, k_out, q_norm=None, k_norm=None, ep
     and ``q_out`` may be None.  ``positions`` int32 [tokens]; ``q_norm`` and ``k_norm`` fp32
     [head_dim] or None; ``rotation`` a :class:`Rotation` or None."""
     some = k if q is None else q
+    if some is None:
+        raise ValueError("q or k expected")
     ix = some.get_device()
     if ix < 0 or _current_device() != ix:
         with _on(ix):

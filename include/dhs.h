@@ -780,11 +780,13 @@ int64_t dhs_page_attend_workspace(const dhs_pages *pages, int32_t n_seqs, int32_
  *   workspace  as in dhs_page_attend, of dhs_page_chunk_workspace() bytes
  * A token that sees no position has out = 0 and lse = -inf.  Rows of padding tokens (before
  * cu[0] or from cu[n_seqs] on) and of sequences whose offsets or length are out of range are
- * left as they were; positions on a page outside the cache are left out.  Page table entries
- * of which no new token of the sequence sees a position are not read, so pages behind the
- * window may be given away.  What a token does not see (infinities, NaN) never reaches it;
- * scales of an 8-bit cache as in dhs_page_attend; with the same lengths the result repeats bit
- * by bit.  n_tokens is at most 2^31 - 257, q_heads / kv_heads at most 128. */
+ * left as they were; positions on a page outside the cache are left out (a token that has no
+ * other is NaN with lse = -inf).  Weighted sums are in fp32 before their division, so values
+ * are to be below 2^88.  Page table entries of which no new token of the sequence sees a
+ * position are not read, so pages behind the window may be given away.  What a token does not
+ * see (infinities, NaN) never reaches it; scales of an 8-bit cache as in dhs_page_attend; with
+ * the same lengths the result repeats bit by bit.  n_tokens is at most 2^31 - 257, q_heads /
+ * kv_heads at most 128. */
 int dhs_page_chunk(const dhs_pages *pages, const void *q, const int64_t *q_strides,
                    int64_t n_tokens, const int32_t *cu, const int32_t *seq_lens,
                    const int32_t *page_table, int32_t table_width, int32_t n_seqs, int32_t q_heads,

@@ -130,6 +130,8 @@ def test_binding_refuses_cpu_tensors(dhs):
     with pytest.raises(ValueError):
         dhs.rotate(x, None, None, None, x, None)
     with pytest.raises(ValueError):
+        dhs.rotate(None, None, None, None, None, None)
+    with pytest.raises(ValueError):
         dhs.Rotation(torch.zeros((2, 4), dtype=torch.float64), device="cpu")
     with pytest.raises(ValueError):
         dhs.Rotation(torch.zeros(4, dtype=torch.float64), pairing=2, device="cpu")
