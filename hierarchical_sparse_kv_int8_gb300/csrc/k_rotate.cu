@@ -19,11 +19,11 @@
 // made once and stays in registers over the heads of a chunk.  A lane holds 8 values of a
 // row: 4 and their 4 partners half a rotation away, or 4 pairs of neighbours, so that the
 // rotation needs no exchange between lanes and the norm one reduction over the row.
-// Measured (GB300, 6.77 TB/s copied), 128 dims: 27,309 tokens of 40 heads 89 us, 87 % of the
-// bytes' time; 37,000 tokens of 32 query heads and 8 + 8 heads going into pages, as bf16 209 us
-// (89 %), as e4m3 229 (75 %: four codes a lane are half a sector); 64 tokens 4.8 us, of which
-// the lookup of their places is three loads that wait for one another.  With sines worked out
-// for every row of every head it was 199 and 432 us.
+// Measured (GB300, 6.77 TB/s copied), 128 dims, 32 query heads over 8: 25,638 tokens 89 us,
+// 87 % of the bytes' time; 51,383 tokens on into pages as bf16 208 us (89 %), as e4m3 228 (75 %:
+// 72 % of the issue slots); 64 tokens 4.8 us, of which the lookup of their places is three
+// loads that wait for one another.  With sines worked out for every row of every head it was
+// 199 and 432 us.
 #include "pages_quant.cuh"
 #include "tc_util.cuh"
 
