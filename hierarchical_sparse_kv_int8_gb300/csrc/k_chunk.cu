@@ -482,34 +482,44 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
     in = pos - pg * a.pg.rows;
     return want ? a.table[(int64_t)it.seq * a.width + pg] : INT32_MIN;
   };
-  auto there = [&](int page) { return page >= 0 && page < a.pg.n_pages; };
-  // bf16: the boxes of a key or value tile; a lane has box lane, lane + 32, ...
+  const uint32_t pages = (uint32_t)a.pg.n_pages;
+  auto there = [&](int page) { return (uint32_t)page < pages; };
+  // bf16: the boxes of a key or value tile; a lane has box lane, lane + 32, ...  (One warp has
+  // some 2300 cycles for all that it does for a tile, so the usual case, pages of which no more
+  // than 32 boxes make a tile, passes by the others.)
   const int boxes = kChN / a.box;
   struct Boxes {
     int page[4], in[4];
   };
   auto ask_tile = [&](const ChunkItem &it, int n, Boxes &b) {
-    const int t0 = tile_of(it.ns, it.gap, it.j0 + n) * kChN;
+    const int pos = tile_of(it.ns, it.gap, it.j0 + n) * kChN + lane * a.box;
+    b.page[0] = INT32_MIN;
+    if (lane < boxes) b.page[0] = ask(it, pos, pos + a.box - 1, b.in[0]);
+    if (boxes > 32) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      b.page[r] = INT32_MIN;
-      if (lane + 32 * r < boxes) {
-        const int pos = t0 + (lane + 32 * r) * a.box;
-        b.page[r] = ask(it, pos, pos + a.box - 1, b.in[r]);
+      for (int r = 1; r < 4; ++r) {
+        b.page[r] = INT32_MIN;
+        const int p = pos + 32 * r * a.box;
+        if (lane + 32 * r < boxes) b.page[r] = ask(it, p, p + a.box - 1, b.in[r]);
       }
     }
   };
   auto fetch_tile = [&](const ChunkItem &it, const CUtensorMap *map, uint32_t slot, const Boxes &b) {
     if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)C::TILE);
-    __syncwarp();
+    unsigned char *to = smem + C::OFF_KV + slot * C::TILE + lane * a.box * 128;
+    auto box = [&](int r) {
+      const int page = there(b.page[r]) ? b.page[r] : (int)pages;
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (lane + 32 * r < boxes) {
-        const int page = there(b.page[r]) ? b.page[r] : (int)a.pg.n_pages;
-        for (int h = 0; h < C::HALVES; ++h)
-          tma_load_4d(smem + C::OFF_KV + slot * C::TILE + h * C::HALF + (lane + 32 * r) * a.box * 128,
-                      map, h * 64, b.in[r], it.kvh, page, &full[slot]);
-      }
+      for (int h = 0; h < C::HALVES; ++h)
+        tma_load_4d(to + h * C::HALF + 32 * r * a.box * 128, map, h * 64, b.in[r], it.kvh, page,
+                    &full[slot]);
+    };
+    if (lane < boxes) box(0);
+    if (boxes > 32) {
+#pragma unroll
+      for (int r = 1; r < 4; ++r)
+        if (lane + 32 * r < boxes) box(r);
+    }
     __syncwarp();
   };
 
@@ -560,17 +570,20 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
           if (given_up()) break;
           // wanted positions that are not there
           uint32_t *e = bad_of(kn);
-          if (lane < 4) e[lane] = 0u;
-          __syncwarp();
+          if (lane == 0) *reinterpret_cast<uint4 *>(e) = make_uint4(0u, 0u, 0u, 0u);
+          auto gone = [&](int r) { return now.page[r] != INT32_MIN && !there(now.page[r]); };
+          if (__any_sync(0xffffffffu, gone(0) || (boxes > 32 && (gone(1) || gone(2) || gone(3))))) {
+            __syncwarp();
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (lane + 32 * r < boxes && now.page[r] != INT32_MIN && !there(now.page[r])) {
-              page_error(a.err, DC_LOC_RANGE, DHS_SITE_PAGE_CHUNK);
-              *missing = 1;
-              for (int x = (lane + 32 * r) * a.box; x < (lane + 32 * r + 1) * a.box; ++x)
-                atomicOr(&e[x >> 5], 1u << (x & 31));
-            }
-          __syncwarp();
+            for (int r = 0; r < 4; ++r)
+              if (lane + 32 * r < boxes && gone(r)) {
+                page_error(a.err, DC_LOC_RANGE, DHS_SITE_PAGE_CHUNK);
+                *missing = 1;
+                for (int x = (lane + 32 * r) * a.box; x < (lane + 32 * r + 1) * a.box; ++x)
+                  atomicOr(&e[x >> 5], 1u << (x & 31));
+              }
+            __syncwarp();
+          }
           fetch_tile(it, &mk, kslot(kn), now);
           ++kn;
         }
@@ -767,7 +780,7 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
           __syncwarp();
           if (lane == first)
             tma_load_4d(room + lane * pitch, v ? &mv : &mk, 0, in, it.kvh,
-                        in_box ? of : (int)a.pg.n_pages, landed);
+                        in_box ? of : (int)pages, landed);
           ++issued;
         }
         cp_async_commit();
