@@ -22,7 +22,8 @@
 // TMA fills with zeros, and so nothing is read that the page table does not name.
 //
 // bf16: the boxes go straight into the 128-byte-swizzled tiles that the MMAs read (warps 17
-// and 19: an issued copy takes a warp some 55 cycles); warp 18 sets values to 0 that are not
+// and 19: an issued copy takes a warp some 55 cycles, and every instruction that a tile costs
+// them ten or more beside the softmax); warp 18 sets values to 0 that are not
 // finite and that some row does not see (0 times an infinity is not 0), and the rows that see
 // them get them added at the end.
 // 8 bits: three warps fetch the codes of keys and three those of values, and turn them into
@@ -40,17 +41,18 @@
 //
 // Measured, the two launches inside a captured graph (GB300, 1904 TFLOP/s and 6.77 TB/s
 // measured, 1687 TFLOP/s held for seconds):
-//   8192 new tokens at the end of 32768, 16 heads over 1, 128 dims: bf16 1.13 ms, 1700 TFLOP/s,
-//   the rate held under the power limit; int8 1.68, e4m3 1.75.  With codes the softmax threads
-//   have the scales' products beside their own (a tile's chain is 2700 cycles in bf16, 1400 of
-//   them softmax) and share their issue slots with the warps that turn codes.
-//   64 dims, bf16: 0.91 ms; S = Q K^T takes half the time, the softmax the same.
+//   8192 new tokens at the end of 32768, 16 heads over 1, 128 dims: bf16 1.09 ms, 1757 TFLOP/s,
+//   over the rate held under the power limit; int8 1.69, e4m3 1.76.  With codes the softmax
+//   threads have the scales' products beside their own (a tile's chain is some 2400 cycles in
+//   bf16, 1450 of them softmax) and share their issue slots with the warps that turn codes, which
+//   are busy all the time.
+//   64 dims: bf16 0.89 ms (S = Q K^T takes half the time, the softmax the same), int8 1.43.
 //   64 sequences that decode one token each over up to 8192 positions, 32 heads over 8: bf16
-//   229 us, 5.9 TB/s; int8 270, 2.55 TB/s, bound by turning codes that 4 rows make use of.
+//   218 us, 6.2 TB/s; int8 272, 2.56 TB/s, bound by turning codes that 4 rows make use of.
 //   4096 and 2485 new tokens in a window of 1024 with 4 sinks, 32 heads over 8, 64 dims: bf16
-//   136 us, e4m3 162: items of some ten tiles, of which an item's start and end take as much
-//   time as four.
-//   77 new tokens at the end of 1100, 8 heads over 1: 21 us, latency from end to end.
+//   119 us, e4m3 149: items of some ten tiles, of which an item's start and end take as much
+//   time as two and masks as much as two more.
+//   77 new tokens at the end of 1100, 8 heads over 1: 20.5 us, latency from end to end.
 #include "pages_internal.cuh"
 #include "attn_tc.cuh"
 
@@ -87,7 +89,7 @@ constexpr int kChLeast = 3 * kChN;  // cost of a CTA's share at least
 // A border this many tiles from an item's end, or fewer, is moved there: an eighth of a share, 2
 // to 8 tiles.  A cut costs what a CTA writes and the join reads for it, so long shares rather
 // differ by as much (4096 and 2485 new tokens in a window of 1024, 32 heads over 8 of 64 dims,
-// bf16: 181 us with 2 tiles at most, 137 with 8), short ones, whose time is the longest share's,
+// bf16: 143 us with 2 tiles at most, 119 with 8), short ones, whose time is the longest share's,
 // do not.
 constexpr int kChSnap = 2, kChSnapMost = 8, kChSnapPart = 8;
 
@@ -693,9 +695,9 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
       ++kn;
       for (int n = 0; n < nt; ++n) {
         if ((n & 15) == 15 && given_up()) break;
-        // (bf16: as above.  Two chunks among 30 decoding sequences 210 -> 200 us.  With a warp for
-        // each row tile's MMAs the two tiles' products interleave, and each is there later: 8192
-        // tokens over 32768 1.13 -> 1.49 ms)
+        // (bf16: as above.  8192 tokens over 32768 of 64 dims 0.91 -> 0.89 ms, 128 dims the same.
+        // With a warp for each row tile's MMAs the two tiles' products interleave, and each is there
+        // later: 1.13 -> 1.49 ms)
         values_in();
         if (!W8 && n + 1 < nt) key_in(kn);
         __syncwarp();
@@ -941,9 +943,10 @@ k_chunk(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensor
     const float sl2 = a.scale_log2;
     const uint64_t sl22 = pack_f32x2(sl2, sl2);
     // Whether columns that no row of a warp sees are gone past.  In bf16 the branches cost every
-    // tile more than that saves (8192 tokens over 32768 1.13 -> 1.18 ms, 64 dims 0.91 -> 1.01),
-    // in 8 bits they do so with 128 dims and no window (1.69 -> 1.71); windowed chunks in e4m3
-    // take 150 us instead of 162 with them, long ones of 64 dims in int8 1.43 ms instead of 1.73.
+    // tile more than that saves (8192 tokens over 32768 1.09 -> 1.15 ms, 64 dims 0.89 -> 0.96, in a
+    // window 119 -> 124 us), in 8 bits with 128 dims and no window they save nothing; windowed
+    // chunks in e4m3 take 149 us instead of 155 with them, long ones of 64 dims in int8 1.43 ms
+    // instead of 1.73.
     constexpr bool SKIP = W8 && (WIN || D == 64);
     uint32_t sn = 0, pieces = 0, hn = 0;  // key tiles of this row tile; pieces walked as two halves
     for (int k = 0;; ++k) {
