@@ -7,10 +7,9 @@
 // the sinks and the first query's window costs nothing.  The last q_len - 1 positions before the
 // last query's window are seen by some queries and not by others, as are the newest q_len - 1.
 // Measured (GB300): 128 sequences of up to 102400 positions in a window of 4096 with 4 sinks,
-// int8, 16 rows, 49.5 us, of which the bytes take 21 at the measured copy bandwidth; plain
-// attention over 4100 positions each, the same bytes, takes 45.5.  The way from the lengths
-// through the page table to the first rows takes some 7 us, the join 5.  One sequence, bf16,
-// 9.6 us.
+// int8, 16 rows, 45.9 us, of which the bytes take 21 at the measured copy bandwidth: from the
+// start through the lengths, a CTA's place, the page table and the first rows it takes 7 us,
+// 25 to stream, a second item in a CTA some 7 more, the join 4.  One sequence, bf16, 9.6 us.
 #include "page_attn.cuh"
 
 extern "C" int dhs_page_attend_window(const dhs_pages *pages, const void *q, const int32_t *q_lens,

@@ -267,10 +267,10 @@ __device__ __forceinline__ longlong2 count_blocks(const SeqLens &a, int32_t *err
   return make_longlong2(sum, some);
 }
 // The 32 neighbours (their first) among whom unit `want` is, and the units before them.
-// (chunk: blocks of a unit)
+// (chunk: blocks of a unit; extra: units of a sequence besides)
 template <int BLOCK, bool WIN>
 __device__ __forceinline__ longlong2 find_neighbours(const SeqLens &a, int64_t want,
-                                                     int64_t chunk) {
+                                                     int64_t chunk, int extra) {
   int base = 0;
   bool found = false;
   int64_t at = 0;
@@ -279,7 +279,8 @@ __device__ __forceinline__ longlong2 find_neighbours(const SeqLens &a, int64_t w
     blocks_of_8<BLOCK, WIN>(a, i, n, nullptr);
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const int units = chunk == 1 ? n[u] : (int)idiv(n[u] + chunk - 1, chunk);
+      const int units = chunk == 1 ? n[u] + (WIN && n[u] > 0 ? extra : 0)
+                                   : (int)idiv(n[u] + chunk - 1, chunk);
       const int all = __reduce_add_sync(0xffffffffu, units);
       if (!found && want < at + all) {
         found = true;
@@ -307,7 +308,49 @@ __device__ __noinline__ longlong2 find_neighbours_call(const int32_t *q_lens,
                                                        int n_seqs, int most, int64_t want,
                                                        int64_t chunk) {
   return find_neighbours<BLOCK, false>(SeqLens{q_lens, seq_lens, q_len, n_seqs, most, 0, 0}, want,
-                                       chunk);
+                                       chunk, 0);
+}
+// With a window.  Of up to 256 sequences the first call keeps the counts, [256] of each warp in
+// shared memory, for the second (128 sequences: 1.5 us less than to work them out again).
+template <int BLOCK>
+__device__ __noinline__ longlong2 count_windows_call(const int32_t *q_lens, const int32_t *seq_lens,
+                                                     int q_len, int n_seqs, int most, int window,
+                                                     int sinks, int32_t *err, int *counts) {
+  const SeqLens seqs{q_lens, seq_lens, q_len, n_seqs, most, window, sinks};
+  if (n_seqs > 256) return count_blocks<BLOCK, true>(seqs, err);
+  int n[8], some = 0;
+  int64_t sum = 0;
+  blocks_of_8<BLOCK, true>(seqs, 0, n, err);
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    some += __popc(__ballot_sync(0xffffffffu, n[u] > 0));
+    sum += n[u];
+    counts[32 * u + (threadIdx.x & 31)] = n[u];
+  }
+  return make_longlong2(sum, some);
+}
+template <int BLOCK>
+__device__ __noinline__ longlong2 find_windows_call(const int32_t *q_lens, const int32_t *seq_lens,
+                                                    int q_len, int n_seqs, int most, int window,
+                                                    int sinks, int64_t want, int64_t chunk,
+                                                    int extra, const int *counts) {
+  const SeqLens seqs{q_lens, seq_lens, q_len, n_seqs, most, window, sinks};
+  if (n_seqs > 256 || chunk != 1)
+    return find_neighbours<BLOCK, true>(seqs, want, chunk, extra);
+  int base = 0;
+  int64_t at = 0;
+  bool found = false;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const int n = counts[32 * u + (threadIdx.x & 31)];  // (this lane's own, as above)
+    const int all = __reduce_add_sync(0xffffffffu, n > 0 ? n + extra : 0);
+    if (!found && want < at + all) {
+      found = true;
+      base = 32 * u;
+    }
+    if (!found) at += all;
+  }
+  return make_longlong2(base, at);
 }
 
 template <class C>
@@ -355,6 +398,7 @@ k_page_attn(const PageView pg, const AttnArgs a) {
   // All blocks, and the sequences with any: every warp adds up all of them.
   int64_t sum = 0;
   int some = 0;
+  int *counts = reinterpret_cast<int *>(smem) + warp * 256;  // (the ring is not in use yet)
   if (few) {
     const int n = blocks(0);
     some = __popc(__ballot_sync(0xffffffffu, n > 0));
@@ -362,7 +406,11 @@ k_page_attn(const PageView pg, const AttnArgs a) {
   } else {
     const longlong2 r = kCalls ? count_blocks_call<C::BLOCK>(a.q_lens, a.seq_lens, a.q_len,
                                                              a.n_seqs, (int)most, a.err)
-                               : count_blocks<C::BLOCK, C::WIN>(seqs, a.err);
+                        : C::WIN
+                            ? count_windows_call<C::BLOCK>(a.q_lens, a.seq_lens, a.q_len, a.n_seqs,
+                                                           (int)most, a.window, a.sinks, a.err,
+                                                           counts)
+                            : count_blocks<C::BLOCK, C::WIN>(seqs, a.err);
     sum = r.x;
     some = (int)r.y;
 #pragma unroll
@@ -406,8 +454,19 @@ k_page_attn(const PageView pg, const AttnArgs a) {
   const bool chunked = items > 1 && items * 32 <= n_cta;
   const int64_t most_blocks =
       chunked ? idiv(total + n_cta - items - 1, max((int64_t)1, n_cta - items)) : 1;
-  auto units = [&](int64_t n) { return chunked ? idiv(n + most_blocks - 1, most_blocks) : n; };
-  int64_t total_units = total;
+  // With a window items are short, and one that begins in a CTA costs it lookups, first copies
+  // and a merge, in time as much as some blocks: so many units before its own have no block.
+  // 128 dims, int8, 16 rows, window 4096: 128 sequences 50.0 us with none, 48.2 with 2, 45.3 with
+  // 4, 46.9 with 6; 32 sequences 26.7, 20.9, 20.9, 22.3; window 1024: 29.5, 27.3, 25.4, 27.3.  With
+  // fewer blocks than three to a CTA they cost (one sequence 9.6, 10.3, 10.9; 24 of 4 tokens in
+  // a window of 200 19.7, 21.8, 23.9), with three of them 2 are best (in a window of 1000
+  // 27.3, 25.3, 28.0).
+  const int64_t thrice = 3 * (int64_t)n_cta;
+  const int extra = !C::WIN || chunked || total < thrice ? 0 : total < thrice + n_cta ? 2 : 4;
+  auto units = [&](int64_t n) {
+    return chunked ? idiv(n + most_blocks - 1, most_blocks) : C::WIN && n > 0 ? n + extra : n;
+  };
+  int64_t total_units = total + items * extra;
   if (chunked) {
     int64_t x = 0;
     for (int i = 0; i < a.n_seqs; i += 32) x += units(blocks(i));
@@ -429,15 +488,19 @@ k_page_attn(const PageView pg, const AttnArgs a) {
     const int64_t want = idiv(begin, hkv);  // in units of one head: only the sequence is looked for
     int64_t at = 0;
     int base = 0;  // its 32 neighbours
+    const bool found = C::WIN && !few && !chunked && a.n_seqs <= 256;
     if (!few) {
       const longlong2 r =
           kCalls ? find_neighbours_call<C::BLOCK>(a.q_lens, a.seq_lens, a.q_len, a.n_seqs,
                                                   (int)most, want, most_blocks)
-                 : find_neighbours<C::BLOCK, C::WIN>(seqs, want, most_blocks);
+          : C::WIN
+              ? find_windows_call<C::BLOCK>(a.q_lens, a.seq_lens, a.q_len, a.n_seqs, (int)most,
+                                            a.window, a.sinks, want, most_blocks, extra, counts)
+              : find_neighbours<C::BLOCK, C::WIN>(seqs, want, most_blocks, 0);
       base = (int)r.x;
       at = r.y;
     }
-    const int n = (int)units(blocks(base));
+    const int n = (int)units(found ? counts[base + lane] : blocks(base));
     int x = n;  // inclusive sums
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -448,8 +511,12 @@ k_page_attn(const PageView pg, const AttnArgs a) {
     const int src = max(0, __ffs(here) - 1);
     seq = base + src;
     seq_at = (at + __shfl_sync(0xffffffffu, x - n, src)) * hkv;
-    seq_nq = __shfl_sync(0xffffffffu, my_nq, src);
-    seq_len = __shfl_sync(0xffffffffu, my_len, src);
+    if (found) {
+      shape(seq, seq_nq, seq_len);
+    } else {
+      seq_nq = __shfl_sync(0xffffffffu, my_nq, src);
+      seq_len = __shfl_sync(0xffffffffu, my_len, src);
+    }
   }
   if (tid == 0) {
     sh_flag = 0;
@@ -482,8 +549,16 @@ k_page_attn(const PageView pg, const AttnArgs a) {
     const int64_t item0 = seq_at + kvh * nu, item1 = item0 + nu;
     const int64_t stop = min(end, item1);
     // blocks of this item's part
-    const int b0 = (int)(chunked ? idiv(nb * (pos - item0), nu) : pos - item0);
-    const int nblk = (int)(chunked ? idiv(nb * (stop - item0), nu) : stop - item0) - b0;
+    auto block_of = [&](int64_t unit) {
+      if (chunked) return idiv(nb * unit, nu);
+      return C::WIN ? max((int64_t)0, unit - extra) : unit;
+    };
+    const int b0 = (int)block_of(pos - item0);
+    const int nblk = (int)block_of(stop - item0) - b0;
+    if (C::WIN && nblk == 0) {  // (the next CTA begins the item)
+      pos = stop;
+      continue;
+    }
     const int32_t *tab = a.table + (int64_t)seq * a.width;
 
     // ---- Q fragments of this warp's rows: for 16-bit rows k-step s holds dims 16 s ..;
@@ -1024,8 +1099,9 @@ k_page_attn(const PageView pg, const AttnArgs a) {
     const bool patch = sh_flag != 0;
     const uint32_t late = C::SOME ? sh_late : 0u;
     float *late_w = reinterpret_cast<float *>(smem + C::OFF_LATE);  // a row's weights
-    const bool whole = pos == item0 && stop == item1;
-    const int slot = pos > item0 ? 0 : 1;
+    const bool begins = C::WIN ? b0 == 0 : pos == item0;
+    const bool whole = begins && stop == item1;
+    const int slot = begins ? 1 : 0;
     float *part = a.parts + ((int64_t)blockIdx.x * 2 + slot) * a.R * (D + 4);
     int2 *tab_of = reinterpret_cast<int2 *>(smem + C::OFF_TAB);
     // a row's maximum and sum over the groups; its place (-1: an idle query) and the
@@ -1166,7 +1242,7 @@ k_page_attn(const PageView pg, const AttnArgs a) {
         *reinterpret_cast<float4 *>(part + m * (D + 4) + d4) = acc;
       }
     }
-    if (pos == item0 && tid == 0) {
+    if (begins && tid == 0) {
       // for the join: the CTAs that share the item
       auto owner = [&](int64_t blk) {  // largest b with range(b) <= blk (a unit)
         int b = (int)min((int64_t)n_cta - 1, idiv((blk + 1) * n_cta - 1, total_units));
