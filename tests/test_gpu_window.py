@@ -132,3 +132,31 @@ def test_window_large_scales_that_some_queries_do_not_see(torch, dhs, kind, hq, 
                     continue
                 vmax = np.abs(kv[0][1][keep]).max()
                 _close(_np(out[0, j:j + 1]), None, want, d, t, vmax)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n,hkv,window,sinks,q_len", [
+    (33, 1, 2000, 3, 1), (40, 2, 500, 0, 4), (160, 2, 250, 4, 1), (255, 1, 600, 200, 1), (256, 2, 300, 4, 2),
+    (257, 2, 300, 4, 1), (300, 1, 900, 1, 1), (520, 1, 260, 130, 2)])
+def test_window_of_many_sequences(torch, dhs, kind, n, hkv, window, sinks, q_len):
+    """CTAs' places among many items of some blocks each, empty sequences among them; twice the
+    same bits."""
+    lens = [0 if i % 11 == 5 else (i * 389) % 1400 + 1 for i in range(n)]
+    pc = Paged(torch, dhs, lens, 32, hkv, 64, kind)
+    kv = pc.fill()
+    give_away(pc, [q_len] * n, window, sinks)
+    out, lse = _attend(torch, pc, kv, q_len, 4 * hkv, window, sinks)
+    again, lse2 = _attend(torch, pc, kv, q_len, 4 * hkv, window, sinks)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("kind", [BF16, INT8])
+def test_window_where_every_item_is_cut(torch, dhs, kind):
+    """Few long items beside short ones: parts that begin in the units that an item counts for
+    itself, and items of which a part has no block."""
+    lens = [9000] * 9 + [1, 40, 200, 3000, 5000] * 7
+    pc = Paged(torch, dhs, lens, 64, 1, 128, kind)
+    kv = pc.fill()
+    for window in (100000, 4096, 700):
+        give_away(pc, [1] * len(lens), window, 2)
+        _attend(torch, pc, kv, 1, 8, window, 2)
