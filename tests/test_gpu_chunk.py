@@ -377,3 +377,26 @@ def test_chunk_sequences_over_the_same_pages(torch, dhs, kind):
     pc.lens = [t - 7 * i for i in range(n)]
     _chunk(torch, dhs, pc, [[x[:t - 7 * i] for x in kv[0]] for i in range(n)], [new - 9 * i for i in range(n)], hq,
            window=130, sinks=5)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("window", [0, 200])
+@pytest.mark.parametrize("rows", [1, 2, 3, 12])
+def test_chunk_small_pages_that_are_not_there(torch, dhs, kind, window, rows):
+    """Pages of which more than 32 make a tile: one in every place of a tile's four 32s is gone."""
+    from oracle import dense_oracle as oracle
+    t, new, d, hq = 400, 150, 64, 4
+    pc = Paged(torch, dhs, [t], rows, 1, d, kind)
+    kv = pc.fill()
+    pages = sorted({p // rows for p in (128 + 5, 128 + 40, 128 + 77, 255, 256, 300, 399)})
+    for j, g in enumerate(pages):
+        pc.table[0, g] = (-1, pc.n_pages, 2147483647)[j % 3]
+    gone = {p for g in pages for p in range(g * rows, (g + 1) * rows)}
+    q, cu, out, lse = _chunk(torch, dhs, pc, kv, [new], hq, window=window, check=False)
+    with pytest.raises(dhs.DhsError, match="dhs_page_chunk: a page"):
+        pc.cache.check()
+    for u in list(range(0, new, 7)) + [new - 1]:
+        pos = t - new + u
+        keep = [p for p in range(pos + 1) if p not in gone and (not window or p > pos - window)]
+        want = oracle.attend(_np(q[u:u + 1]), kv[0][0][keep], kv[0][1][keep], 1 / math.sqrt(d))
+        _close(_np(out[u:u + 1]), _np(lse[u:u + 1]), want, d, t)
