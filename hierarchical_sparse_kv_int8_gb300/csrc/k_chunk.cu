@@ -136,7 +136,8 @@ struct ChCfg {
   static constexpr int CLEAN = 4;             // value tiles gone over and not yet used, at most
   static constexpr int BARS = 3 + 2 * SLOTS + (W8 ? 0 : CLEAN) + 2 * TURN + 8 + 4 + 8;
   static constexpr int OFF_TMEM = OFF_BAR + BARS * 8;
-  static constexpr int OFF_MISC = OFF_TMEM + 16;  // int [4]: abort, whether pages were missing, bad values by item parity
+  // int [4]: abort, whether pages were missing, bad values by item parity
+  static constexpr int OFF_MISC = OFF_TMEM + 16;
   static constexpr int OFF_ITEM = OFF_MISC + 16;  // ChunkItem [2]
   static constexpr int SMEM = OFF_ITEM + 2 * 64;
   static_assert(NE >= KS + (W8 ? 3 : 2), "entries of key tiles");
