@@ -812,9 +812,9 @@ k_page_attn(const PageView pg, const AttnArgs a) {
       }
       if (C::W == 1) {
         if (C::SOME && nq > 1 && (p0 + TN > common || behind)) {
-          // Scales that only some rows see (the last q_len - 1) and that are 2^5 times those
-          // that all see, or the first of them: following one would cost the rows that do
-          // not see it their weights.  Where the power of two does not cover them already,
+          // Scales that only some rows see (the last q_len - 1, with a window as many where it
+          // starts) and that are 2^5 times those that all see, or, after those, the first of
+          // them: following one would cost the rows that do not see it their weights.  Where the power of two does not cover them already,
           // their positions' values are left for the merge.  (Each warp of the group does
           // the same.  This costs 1 to 3 %; a power of two of each row's own cost 4 to 16.)
           int e[2] = {-127, -127}, ref = -127;
@@ -827,11 +827,24 @@ k_page_attn(const PageView pg, const AttnArgs a) {
               ref = max(ref, e[u]);
           }
           ref = __reduce_max_sync(0xffffffffu, ref);
-          if (C::WIN && ref == -127) {  // none that all see: the first of those there
-            const uint32_t some0 = __ballot_sync(0xffffffffu, lane < TN && e[0] > -127);
-            const uint32_t some1 = __ballot_sync(0xffffffffu, TN > 32 && e[(TN + 31) / 32 - 1] > -127);
-            ref = __shfl_sync(0xffffffffu, some0 || TN <= 32 ? e[0] : e[(TN + 31) / 32 - 1],
-                              max(0, __ffs(some0 ? some0 : some1) - 1));
+          if (C::WIN && ref == -127) {  // none that all see
+            if (behind) {
+              // Rows that do not see the first of those there see later ones, here and in the
+              // tiles to come.  What every row sees is the first position of the last query's
+              // window; where it is none (a window of fewer positions than queries, a page that
+              // is not there) all of these are left for the merge.
+              if (all_from < common && __any_sync(0xffffffffu, max(e[0], e[(TN + 31) / 32 - 1]) > -127)) {
+                const int64_t row = page_row(pg, tab, all_from, nullptr, 0);
+                const uint32_t b = row < 0 ? 0u : __float_as_uint(pg.vs[row + (int64_t)kvh * pg.rows]);
+                ref = (int)((b < 0x7F800000u ? b : 0u) >> 23) - 127;
+              }
+            } else {
+              // the first of those there: rows that do not see it see nothing after it
+              const uint32_t some0 = __ballot_sync(0xffffffffu, lane < TN && e[0] > -127);
+              const uint32_t some1 = __ballot_sync(0xffffffffu, TN > 32 && e[(TN + 31) / 32 - 1] > -127);
+              ref = __shfl_sync(0xffffffffu, some0 || TN <= 32 ? e[0] : e[(TN + 31) / 32 - 1],
+                                max(0, __ffs(some0 ? some0 : some1) - 1));
+            }
           }
 #pragma unroll
           for (int u = 0; u < (TN + 31) / 32; ++u) {

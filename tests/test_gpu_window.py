@@ -160,3 +160,91 @@ def test_window_where_every_item_is_cut(torch, dhs, kind):
     for window in (100000, 4096, 700):
         give_away(pc, [1] * len(lens), window, 2)
         _attend(torch, pc, kv, 1, 8, window, 2)
+
+
+def _check_scaled(torch, pc, kv, q_len, hq, window, sinks, scaled, gone=()):
+    """One sequence whose values at positions ``scaled`` {position: factor} are that much larger:
+    every query against its own positions, without those of ``gone``."""
+    from oracle import dense_oracle as oracle
+    t, rows, d = pc.lens[0], pc.rows, pc.d
+    kv = [(k, v.copy()) for k, v in kv]
+    before = pc.cache.v_scale.clone()
+    for p, s in scaled.items():
+        pc.cache.v_scale[int(pc.table[0, p // rows]), 0, p % rows] *= s
+        kv[0][1][p] *= s
+    q = torch.randn((1, q_len, hq, d), generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    out = torch.empty_like(q)
+    pc.cache.attend(q, pc.seq_lens, pc.table, out, pc.cache.attend_workspace(1, q_len, hq), window=window,
+                    sinks=sinks)
+    pc.cache.v_scale.copy_(before)
+    for j in range(q_len):
+        pos = t - q_len + j
+        keep = [x for x in range(pos + 1) if (x > pos - window or x < sinks) and x not in gone]
+        want = oracle.attend(_np(q[0, j:j + 1]), kv[0][0][keep], kv[0][1][keep], 1 / math.sqrt(d))
+        _close(_np(out[0, j:j + 1]), None, want, d, t, np.abs(kv[0][1][keep]).max())
+
+
+@pytest.mark.parametrize("kind", [INT8, E4M3])
+@pytest.mark.parametrize("hq,d", [(2, 128), (8, 64), (16, 128)])
+@pytest.mark.parametrize("q_len", [2, 4, 8])
+def test_window_starts_at_a_tile_end(torch, dhs, kind, hq, d, q_len):
+    """The tile in which the first query's window starts holds no position that all queries see:
+    a scale that is large, at a position that the later ones do not see, costs them nothing."""
+    window, rows = 100, 16
+    for start in {128, 128 + q_len // 2}:          # the last query's first position
+        pc = Paged(torch, dhs, [start + window], rows, 1, d, kind)
+        kv = pc.fill()
+        first = start - q_len + 1                  # the first query's
+        for sinks in (0, 2):
+            for p in sorted({first, first + 1, 127, start - 1, start}):
+                for s in (2.0 ** 24, 2.0 ** 40):
+                    _check_scaled(torch, pc, kv, q_len, hq, window, sinks, {p: s})
+            # the first position that all see is small, or none at all
+            _check_scaled(torch, pc, kv, q_len, hq, window, sinks, {start: 2.0 ** -40})
+            _check_scaled(torch, pc, kv, q_len, hq, window, sinks, {start: 0.0, first: 2.0 ** 24})
+        pc.cache.check()
+        # its page is not there
+        gone = range(start // rows * rows, start // rows * rows + rows)
+        pc.table[0, start // rows] = -1
+        _check_scaled(torch, pc, kv, q_len, hq, window, 0, {first: 1.0 if first in gone else 2.0 ** 24}, gone)
+        with pytest.raises(dhs.DhsError):
+            pc.cache.check()
+
+
+@pytest.mark.parametrize("kind", [INT8, E4M3])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (2, 0), (5, 0), (7, 1), (3, 2)])
+@pytest.mark.parametrize("hq,d", [(2, 128), (16, 64)])
+def test_window_of_fewer_positions_than_queries(torch, dhs, kind, window, sinks, hq, d):
+    """No position but the first ones is seen by all queries: a large scale in any query's window
+    costs the others nothing."""
+    for t in (200, 196, 9, 8):
+        pc = Paged(torch, dhs, [t], 16, 1, d, kind)
+        kv = pc.fill()
+        for p in range(max(0, t - 8 - window), t):
+            _check_scaled(torch, pc, kv, 8, hq, window, sinks, {p: 2.0 ** 30})
+        pc.cache.check()
+
+
+@pytest.mark.parametrize("kind", [INT8, E4M3])
+@pytest.mark.parametrize("q_len", [2, 8])
+@pytest.mark.parametrize("hkv,d", [(256, 128), (600, 64)])
+def test_window_starts_at_a_tile_end_and_goes_on(torch, dhs, kind, q_len, hkv, d):
+    """The same where a group of warps goes on to later tiles of an item: they keep their precision
+    after a scale that the first query alone sees."""
+    from oracle import dense_oracle as oracle
+    window, rows, start = 400, 16, 128
+    t, first = start + window, start - q_len + 1
+    pc = Paged(torch, dhs, [t], rows, hkv, d, kind)
+    (k, v), = pc.fill()
+    pc.cache.v_scale[int(pc.table[0, first // rows]), :, first % rows] *= 2.0 ** 30
+    v[first] *= 2.0 ** 30
+    q = torch.randn((1, q_len, hkv, d), generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    out = torch.empty_like(q)
+    pc.cache.attend(q, pc.seq_lens, pc.table, out, pc.cache.attend_workspace(1, q_len, hkv), window=window)
+    pc.cache.check()
+    for j in range(q_len):
+        seen = slice(first + j, first + j + window)
+        for h in list(range(0, hkv, 41)) + [hkv - 1]:
+            one = slice(h, h + 1)
+            want = oracle.attend(_np(q[0, j:j + 1, one]), k[seen, one], v[seen, one], 1 / math.sqrt(d))
+            _close(_np(out[0, j:j + 1, one]), None, want, d, t, np.abs(v[seen, one]).max())
