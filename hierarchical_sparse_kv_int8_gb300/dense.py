@@ -200,17 +200,19 @@ def _found(code, site):
 class Rotation:
     """A position rotation for :func:`rotate` and :meth:`PageCache.append`, laid out once.
 
-    ``freqs``: the angle that pair i of a head's row turns by per position, in radians (fp64,
-    on any device); a multiple of 4 of them, at most half a head's elements, the rest of which
-    stay as they are.  ``pairing``: ``ROTATE_HALVES`` for pairs (i, i + len(freqs)),
+    ``freqs``: the angle that pair i of a head's row turns by per position, in radians (numbers,
+    or an array or tensor on any device, fp64: what has fewer bits is taken as it is, and far
+    positions turn by as many times its error); a multiple of 4 of them, at most half a head's
+    elements, the rest of which stay as they are.  ``pairing``: ``ROTATE_HALVES`` for pairs (i, i + len(freqs)),
     ``ROTATE_NEIGHBOURS`` for (2 i, 2 i + 1).  ``amplitude`` multiplies sines and cosines.
     """
 
     def __init__(self, freqs, pairing: int = ROTATE_HALVES, amplitude: float = 1.0, device=None):
-        host = torch.as_tensor(freqs).detach()
+        # (a list of numbers would become 32 bits by itself)
+        host = torch.as_tensor(freqs, dtype=torch.float64).detach()
         if device is None:
             device = host.device if host.is_cuda else "cuda"
-        host = host.to("cpu", torch.float64).contiguous()
+        host = host.cpu().contiguous()
         if host.dim() != 1 or pairing not in (ROTATE_HALVES, ROTATE_NEIGHBOURS):
             raise ValueError("freqs: [n_pairs], pairing: ROTATE_HALVES or ROTATE_NEIGHBOURS expected")
         turns = torch.empty(host.shape, dtype=torch.int64)

@@ -137,3 +137,23 @@ def test_binding_refuses_cpu_tensors(dhs):
         dhs.Rotation(torch.zeros(4, dtype=torch.float64), pairing=2, device="cpu")
     with pytest.raises(ValueError):
         dhs.Rotation(torch.zeros(4, dtype=torch.float64), device="cpu")
+
+
+@pytest.mark.parametrize("of", [list, tuple, np.asarray, lambda f: [np.float64(x) for x in f]])
+def test_rotation_takes_frequencies_in_64_bits(dhs, of):
+    """Python's numbers keep their 64 bits.  (Without a GPU a Rotation is refused after its turns
+    are made.)"""
+    import torch
+    f = (10000.0 ** (-np.arange(32) / 32)).tolist()
+    want = np.zeros(32, np.uint64)
+    assert dhs.load().dhs_rotation_turns(np.asarray(f).ctypes.data, 32, want.ctypes.data) == 0
+    rot = dhs.Rotation.__new__(dhs.Rotation)
+    with pytest.raises(ValueError):
+        rot.__init__(of(f), device="cpu")
+    assert np.array_equal(rot.turns.numpy().view(np.uint64), want)
+    # a tensor of fewer bits is taken as it is
+    low = torch.tensor(f, dtype=torch.float32)
+    with pytest.raises(ValueError):
+        rot.__init__(low, device="cpu")
+    assert dhs.load().dhs_rotation_turns(low.double().data_ptr(), 32, want.ctypes.data) == 0
+    assert np.array_equal(rot.turns.numpy().view(np.uint64), want)
