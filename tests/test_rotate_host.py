@@ -145,8 +145,8 @@ def test_rotation_takes_frequencies_in_64_bits(dhs, of):
     are made.)"""
     import torch
     f = (10000.0 ** (-np.arange(32) / 32)).tolist()
-    want = np.zeros(32, np.uint64)
-    assert dhs.load().dhs_rotation_turns(np.asarray(f).ctypes.data, 32, want.ctypes.data) == 0
+    want, held = np.zeros(32, np.uint64), np.asarray(f)
+    assert dhs.load().dhs_rotation_turns(held.ctypes.data, 32, want.ctypes.data) == 0
     rot = dhs.Rotation.__new__(dhs.Rotation)
     with pytest.raises(ValueError):
         rot.__init__(of(f), device="cpu")
@@ -155,5 +155,6 @@ def test_rotation_takes_frequencies_in_64_bits(dhs, of):
     low = torch.tensor(f, dtype=torch.float32)
     with pytest.raises(ValueError):
         rot.__init__(low, device="cpu")
-    assert dhs.load().dhs_rotation_turns(low.double().data_ptr(), 32, want.ctypes.data) == 0
+    held = low.double()
+    assert dhs.load().dhs_rotation_turns(held.data_ptr(), 32, want.ctypes.data) == 0
     assert np.array_equal(rot.turns.numpy().view(np.uint64), want)
