@@ -400,3 +400,98 @@ def test_chunk_small_pages_that_are_not_there(torch, dhs, kind, window, rows):
         keep = [p for p in range(pos + 1) if p not in gone and (not window or p > pos - window)]
         want = oracle.attend(_np(q[u:u + 1]), kv[0][0][keep], kv[0][1][keep], 1 / math.sqrt(d))
         _close(_np(out[u:u + 1]), _np(lse[u:u + 1]), want, d, t)
+
+
+def _attend_64(torch, q, k, v, scale, window, sinks):
+    """_window_attend for many rows: in 64 bits on the GPU, a head at a time."""
+    n, hq, d = q.shape
+    t, hkv, _ = k.shape
+    q = q.double()
+    k, v = (torch.from_numpy(x).cuda() for x in (k, v))
+    at = torch.arange(t, device="cuda")
+    p = (t - n + torch.arange(n, device="cuda"))[:, None]
+    hide = at > p
+    if window:
+        hide |= (at <= p - window) & (at >= sinks)
+    got = []
+    for h in range(hq):
+        kh, vh = k[:, h * hkv // hq], v[:, h * hkv // hq]
+        s = (q[:, h] @ kh.T * scale).masked_fill_(hide, -math.inf)
+        lse = torch.logsumexp(s, 1)
+        s = s.sub_(lse[:, None]).exp_()
+        reach = (q[:, h].abs() @ kh.abs().T).masked_fill_(hide, 0).amax(1) * scale
+        got.append((s @ vh, lse, s @ vh.abs(), reach))
+    return tuple(torch.stack([x[j] for x in got], 1).cpu().numpy() for j in range(4))
+
+
+def _tiles_a_border_moves(torch, lens, new, hkv, group, window, sinks):
+    """How far a border between two CTAs' shares is moved at most: an eighth of a share, in tiles
+    of 128 positions, 2 to 8 (the kernel's rule, from the costs of its items)."""
+    tpt = 128 // group
+    cap = window + sinks + 2 * tpt + 256 if window else 1 << 31
+    total = 0
+    for t, a in zip(lens, new):
+        for r in range(-(-a // (2 * tpt))):
+            walked = min(t - a + (r + 1) * 2 * tpt, cap)
+            total += hkv * (384 + (walked * 3 // 4 if a <= tpt else walked))
+    share = total // torch.cuda.get_device_properties(0).multi_processor_count
+    return max(2, min(8, share // 1024))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("lens,new,d,window,sinks,least,most", [
+    ([9000, 6000, 1200, 8000], [3000, 2500, 700, 1], 128, 0, 0, 8, 8),
+    ([9000, 6000, 1200, 8000], [3000, 2500, 700, 1], 64, 6000, 130, 8, 8),
+    ([9000, 6000, 1200], [3000, 2500, 700], 128, 2000, 5, 4, 7),
+    ([5000, 2600] + [3000] * 8, [1500, 800] + [1] * 8, 64, 0, 0, 3, 6),
+    ([12000, 9000], [12000, 9000], 64, 300, 4, 8, 8)])      # many short items to a CTA
+def test_chunk_of_long_shares(torch, dhs, kind, lens, new, d, window, sinks, least, most):
+    """Shares so long that borders are moved by more than two tiles, every row of every item: the
+    CTAs on either side of a border and the join agree on it.  Twice the same bits."""
+    hq, hkv = 16, 4
+    assert least <= _tiles_a_border_moves(torch, lens, new, hkv, hq // hkv, window, sinks) <= most
+    pc = Paged(torch, dhs, lens, 64, hkv, d, kind)
+    kv = pc.fill()
+    give_away(pc, new, window or 1 << 30, sinks)
+    q, cu, out, lse = _chunk(torch, dhs, pc, kv, new, hq, window=window, sinks=sinks, pad=(3, 2), check=False)
+    pc.cache.check()
+    for i, a in enumerate(new):
+        s = slice(int(cu[i]), int(cu[i]) + a)
+        want = _attend_64(torch, q[s], *kv[i], 1 / math.sqrt(d), window, sinks)
+        _close(_np(out[s]), _np(lse[s]), want, d, lens[i])
+    for s in (slice(0, 3), slice(3 + sum(new), None)):
+        assert torch.all(out[s] == 77) and torch.all(lse[s] == 77)
+    _, _, again, lse2 = _chunk(torch, dhs, pc, kv, new, hq, window=window, sinks=sinks, pad=(3, 2), check=False)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (3, 0), (70, 2), (128, 200)])
+@pytest.mark.parametrize("hq,d", [(2, 128), (16, 64)])
+def test_chunk_keys_that_are_not_finite(torch, dhs, window, sinks, hq, d):
+    """bf16: a key of NaN beside values that are not finite: tokens that do not see it have the
+    outputs that they have without it."""
+    from oracle import dense_oracle as oracle
+    t, new, rows = 420, 130, 16
+    first = t - new
+    for p in sorted({first - 1, first + 5, t - 2, first - window + 40, t - window - 1, 1, 200} & set(range(t))):
+        pc = Paged(torch, dhs, [t, 200], rows, 1, d, BF16)
+        kv = pc.fill()
+        page = int(pc.table[0, p // rows])
+        for c, x in ((3, math.inf), (20, math.nan)):
+            pc.cache.v[page, 0, p % rows, c] = x
+            kv[0][1][p, 0, c] = x
+        pc.cache.k[page, 0, p % rows] = math.nan
+        kv[0][0][p] = math.nan
+        q, cu, out, lse = _chunk(torch, dhs, pc, kv, [new, 200], hq, window=window, sinks=sinks, check=False)
+        pc.cache.check()
+        pos = torch.arange(first, t)
+        seen = (p <= pos) & ((pos - p < window) if window and p >= sinks else torch.ones_like(pos, dtype=torch.bool))
+        blind = (~seen).nonzero()[:, 0].tolist()
+        assert torch.isnan(out[:new][seen]).all() and torch.isnan(lse[:new][seen]).all()
+        kv[0][0][p] = kv[0][1][p] = 0.0      # (of no weight below: the oracle's masked places are left out)
+        want = _window_attend(oracle, _np(q[:new]), *kv[0],
+                              1 / math.sqrt(d), window, sinks)
+        _close(_np(out[blind]), _np(lse[blind]), [x[blind] for x in want], d, t)
+        want = _window_attend(oracle, _np(q[new:]), *kv[1],
+                              1 / math.sqrt(d), window, sinks)
+        _close(_np(out[new:]), _np(lse[new:]), want, d, 200)
