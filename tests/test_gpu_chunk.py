@@ -495,3 +495,25 @@ def test_chunk_keys_that_are_not_finite(torch, dhs, window, sinks, hq, d):
         want = _window_attend(oracle, _np(q[new:]), *kv[1],
                               1 / math.sqrt(d), window, sinks)
         _close(_np(out[new:]), _np(lse[new:]), want, d, 200)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("window,sinks", [(2147483647, 2147483647), (2147483647, 0), (1, 2147483647)])
+def test_chunk_windows_and_sinks_of_any_size(torch, dhs, kind, window, sinks):
+    pc = Paged(torch, dhs, [600, 40, 300], 16, 2, 64, kind)
+    _chunk(torch, dhs, pc, pc.fill(), [150, 40, 1], 4, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("window", [0, 90])
+def test_chunk_of_more_than_a_thousand_sequences(torch, dhs, kind, window):
+    """Most of them decode one token, some have none, a few have a chunk."""
+    n = 1100
+    lens = [0 if i % 97 == 5 else (i * 131) % 260 + 1 for i in range(n)]
+    new = [min(t, 0 if i % 13 == 2 else 150 if i % 200 == 77 else 1) for i, t in enumerate(lens)]
+    pc = Paged(torch, dhs, lens, 16, 1, 64, kind)
+    kv = pc.fill()
+    give_away(pc, new, window or 1 << 30, 2 if window else 0)
+    q, cu, out, lse = _chunk(torch, dhs, pc, kv, new, 4, window=window, sinks=2 if window else 0)
+    _, _, again, lse2 = _chunk(torch, dhs, pc, kv, new, 4, window=window, sinks=2 if window else 0, check=False)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
